@@ -230,6 +230,23 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
                           const float* dlogits, void* dx, void* dw_router, void* ws,
                           size_t ws_bytes, void* stream);
 
+/* The whole layer for a few tokens (1 <= T <= 64), forward only: the step of a decoder, where the time
+ * goes into reading the chosen experts' weights once. The same y as moe_fwd (same routing, ties and
+ * expert share; the sums run in another order, and h = w silu(a) b keeps fp32's accuracy up to the
+ * down product, where moe_fwd rounds it to bf16), without `saved`, and in two kernels:
+ *   w_router = NULL  logits [T, E_total] is an input, as in moe_fwd
+ *   w_router given   [E_total, H], elem: logits = x w_router^T first (one more kernel); logits is an output
+ * A token none of whose experts is in the share gets y = 0. Modes FP32 and BF16
+ * (MOE_ERR_UNSUPPORTED_MODE otherwise); T > 64 is MOE_ERR_UNSUPPORTED_SHAPE (moe_fwd takes those).
+ * desc.recompute has no meaning here. 16-byte alignment of every tensor, 4-byte of logits, 256-byte of
+ * ws, whose size is moe_query_few_sizes's and whose contents need not be preserved; calls that share
+ * a workspace must be ordered by the caller. The non-finite values of a token's x reach that
+ * token's y alone. */
+moe_status moe_query_few_sizes(const moe_desc* d, size_t* ws);
+moe_status moe_fwd_few(const moe_desc* d, const void* x, const void* w_router, float* logits,
+                       const void* w_gate, const void* w_up, const void* w_down, void* y, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Byte offsets of the routing results inside `saved`.
  *   idx       int32 [T*k]      chosen experts, slot order (logit desc, index asc)
  *   weight    float [T*k]      renormalised routing weights

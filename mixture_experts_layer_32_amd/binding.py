@@ -80,11 +80,13 @@ def lib():
         L.moe_query_router_sizes.argtypes = [_D, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
         L.moe_router_fwd.argtypes = [_D, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_router_bwd.argtypes = [_D, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.moe_query_few_sizes.argtypes = [_D, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fwd_few.argtypes = [_D, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_profile_enable.argtypes = [ctypes.c_int]
         L.moe_profile_kernel.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                          ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double)]
         for n in ("moe_query_sizes", "moe_route", "moe_route_static", "moe_fwd", "moe_fwd_router", "moe_bwd", "moe_saved_layout", "moe_mx_quantize",
-                  "moe_fp8_block_quantize",
+                  "moe_fp8_block_quantize", "moe_query_few_sizes", "moe_fwd_few",
                   "moe_query_router_sizes", "moe_router_fwd", "moe_router_bwd", "moe_profile_enable",
                   "moe_profile_disable", "moe_profile_collect", "moe_profile_kernel"):
             getattr(L, n).restype = st
@@ -170,6 +172,17 @@ def moe_router_fwd(desc, x, w_router, logits, ws, ws_bytes, stream=None):
 def moe_router_bwd(desc, x, w_router, dlogits, dx, dw_router, ws, ws_bytes, stream=None):
     _check(lib().moe_router_bwd(ctypes.byref(desc), ptr(x), ptr(w_router), ptr(dlogits), ptr(dx), ptr(dw_router),
                                 ptr(ws), ws_bytes, _stream(stream)))
+
+
+def query_few_sizes(desc: Desc):
+    n = ctypes.c_size_t()
+    _check(lib().moe_query_few_sizes(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def moe_fwd_few(desc, x, w_router, logits, w_gate, w_up, w_down, y, ws, ws_bytes, stream=None):
+    _check(lib().moe_fwd_few(ctypes.byref(desc), ptr(x), ptr(w_router), ptr(logits), ptr(w_gate), ptr(w_up),
+                             ptr(w_down), ptr(y), ptr(ws), ws_bytes, _stream(stream)))
 
 
 def moe_mx_quantize(x, rows, cols, axis, q, scales, stream=None):

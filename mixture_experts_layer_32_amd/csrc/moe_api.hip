@@ -949,6 +949,102 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------------------------------------
+// The whole layer for a few tokens
+
+namespace {
+struct FewLayout {
+  size_t nact, off, act, tok, h, hlo, xq, xs, hmax, total;
+};
+
+FewLayout few_layout(const moe_desc& d, bool int8) {
+  FewLayout L{};
+  const size_t n = (size_t)d.T * d.topk, El = (size_t)d.E_local, F = (size_t)d.F;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.nact = take(4);
+  L.off = take((El + 1) * 4);
+  L.act = take(El * 4);
+  L.tok = take(n * 4);
+  const bool split = d.mode != MOE_MODE_FP32 && !int8;   // bf16: high and low parts
+  L.h = take(n * F * (split ? 2 : 4));
+  L.hlo = take(split ? n * F * 2 : 0);
+  L.xq = take(int8 ? (size_t)d.T * d.H : 0);
+  L.xs = take(int8 ? (size_t)d.T * 4 : 0);
+  L.hmax = take(int8 ? n * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+FewParams few_params(const moe_desc& d, const FewLayout& L, const void* x, const void* w_router, float* logits,
+                     const void* w_gate, const void* w_up, const void* w_down, void* y, void* ws) {
+  char* w = static_cast<char*>(ws);
+  FewParams p{};
+  p.x0 = x;
+  p.x = x;
+  p.wr = w_router;
+  p.logits = logits;
+  p.wg = w_gate;
+  p.wu = w_up;
+  p.wd = w_down;
+  p.y = y;
+  p.h = w + L.h;
+  p.hlo = w + L.hlo;
+  p.r_nact = reinterpret_cast<int*>(w + L.nact);
+  p.r_off = reinterpret_cast<int*>(w + L.off);
+  p.r_act = reinterpret_cast<int*>(w + L.act);
+  p.r_tok = reinterpret_cast<int*>(w + L.tok);
+  p.T = (int)d.T;
+  p.H = d.H;
+  p.F = d.F;
+  p.E = d.E_total;
+  p.El = d.E_local;
+  p.e0 = d.expert_offset;
+  p.k = d.topk;
+  return p;
+}
+
+moe_status few_checks(const moe_desc* d) {
+  moe_status st = validate(d);
+  if (st != MOE_OK) return st;
+  if (d->mode != MOE_MODE_FP32 && d->mode != MOE_MODE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED_MODE, "moe_fwd_few takes MOE_MODE_FP32 or MOE_MODE_BF16");
+  if (d->T > kFewTokens) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "moe_fwd_few takes up to 64 tokens (else moe_fwd)");
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_query_few_sizes(const moe_desc* d, size_t* ws) {
+  g_last_error.clear();
+  moe_status st = few_checks(d);
+  if (st != MOE_OK) return st;
+  if (ws) *ws = few_layout(*d, false).total;
+  return MOE_OK;
+}
+
+moe_status moe_fwd_few(const moe_desc* d, const void* x, const void* w_router, float* logits, const void* w_gate,
+                       const void* w_up, const void* w_down, void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status st = few_checks(d);
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs({{x, "x"}, {w_gate, "w_gate"}, {w_up, "w_up"}, {w_down, "w_down"}, {y, "y"}}, 16)) != MOE_OK)
+    return st;
+  if (w_router && (st = check_ptrs({{w_router, "w_router"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{logits, "logits"}}, 4)) != MOE_OK) return st;
+  if ((st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const FewLayout L = few_layout(*d, false);
+  if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "few-token workspace too small");
+  const hipError_t e = launch_few(few_params(*d, L, x, w_router, logits, w_gate, w_up, w_down, y, ws),
+                                  d->mode == MOE_MODE_FP32 ? 4 : 2, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "few-token launch");
+  return MOE_OK;
+}
+
 moe_status moe_mx_quantize(const void* in, int64_t rows, int64_t cols, int axis, uint8_t* q, uint8_t* scales,
                            void* stream) {
   g_last_error.clear();

@@ -191,6 +191,26 @@ hipError_t launch_router_bwd_bf16(const RouterParams& p, int grid, hipStream_t s
 hipError_t launch_router_fwd_f32(const RouterParams& p, hipStream_t s);   // fp32 test mode
 hipError_t launch_router_bwd_f32(const RouterParams& p, hipStream_t s);
 
+// The whole layer for a few tokens (T <= kFewTokens): few.hip.
+constexpr int kFewTokens = 64;      // one 64-bit token mask per expert
+struct FewParams {
+  const void* x0;        // [T, H] bf16 (fp32 mode: fp32)
+  const void* x;         // the gate/up products' rows: x0, or the quantised rows
+  const void* wr;        // [E, H] router weight like x0, or null: the logits are given
+  float* logits;         // [T, E], written when wr is given
+  const void *wg, *wu, *wd;
+  const float *sg, *su, *sd;   // 8-bit weights: scales per output channel [El, F], [El, F], [El, H]
+  void* y;               // [T, H]
+  void *h, *hlo;         // [pairs, F] w silu(a) b: fp32, or bf16 high and low parts
+  uint8_t* xq;           // 8-bit weights: quantised x [T, H], its scales [T], and the magnitude bits of each
+  float* xs;             //   pair's largest |h| [pairs]
+  unsigned* hmax;
+  int *r_nact, *r_off, *r_act, *r_tok;   // routing, from the gate/up kernel to the down kernel
+  int T, H, F, E, El, e0, k;
+};
+// type: bytes of a weight element (4: fp32 mode, 2: bf16, 1: 8-bit weights with bf16 x and y)
+hipError_t launch_few(const FewParams& p, int type, hipStream_t s);
+
 hipError_t launch_forward_gemms_mx(const FwdParams& p, int grid, hipStream_t s, bool recompute = false);
 hipError_t launch_backward_gemms_mx(const BwdParams& p, int grid, hipStream_t s);
 hipError_t launch_quant_rows(const void* in, uint8_t* q, uint8_t* sc, int64_t n, const char* name, hipStream_t s,

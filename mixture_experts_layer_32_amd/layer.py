@@ -26,6 +26,13 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _device(device):
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
 class MoELayer:
     def __init__(self, T, H, F, E_total, topk, mode="bf16", E_local=None, expert_offset=0, device="cuda",
                  recompute=False):
@@ -34,9 +41,7 @@ class MoELayer:
         self.desc = binding.Desc.make(T, H, F, E_total, topk, mode, E_local, expert_offset, recompute)
         self.mode = mode
         self.dtype = torch.float32 if mode == "fp32" else torch.bfloat16
-        self.device = torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _device(device)
         self.fwd_ws_bytes, self.bwd_ws_bytes, self.saved_bytes = binding.query_sizes(self.desc)
         u8 = dict(dtype=torch.uint8, device=self.device)
         self.ws = torch.empty(max(self.fwd_ws_bytes, self.bwd_ws_bytes), **u8)
@@ -141,3 +146,44 @@ class MoELayer:
                     weight=view("weight", rows, torch.float32).view(d.T, d.topk),
                     counts=view("counts", d.E_local, torch.int32), offsets=offsets,
                     perm=view("perm", rows, torch.int32)[:P], pair_pos=view("pair_pos", rows, torch.int32))
+
+
+class FewTokenLayer:
+    """The layer's forward for 1 to 64 tokens through moe_fwd_few: holds the workspace of one shape. Calls
+    of one object share it: order them, or give concurrent streams an object each."""
+
+    def __init__(self, T, H, F, E_total, topk, mode="bf16", E_local=None, expert_offset=0, device="cuda"):
+        self.desc = d = binding.Desc.make(T, H, F, E_total, topk, mode, E_local, expert_offset)
+        self.mode = mode
+        self.dtype = torch.float32 if mode == "fp32" else torch.bfloat16
+        self.device = _device(device)
+        self.ws = torch.empty(binding.query_few_sizes(d), dtype=torch.uint8, device=self.device)
+        self._x, self._logits, self._wr = (d.T, d.H), (d.T, d.E_total), (d.E_total, d.H)
+        self._w_in, self._w_out = (d.E_local, d.F, d.H), (d.E_local, d.H, d.F)
+
+    def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
+        el, dev = self.dtype, self.device
+        if y is None:
+            y = torch.empty(self._x, dtype=el, device=dev)
+        else:
+            _expect(y, "y", self._x, el, dev)
+        _expect(x, "x", self._x, el, dev)
+        _expect(w_gate, "w_gate", self._w_in, el, dev)
+        _expect(w_up, "w_up", self._w_in, el, dev)
+        _expect(w_down, "w_down", self._w_out, el, dev)
+        binding.moe_fwd_few(self.desc, x, w_router, logits, w_gate, w_up, w_down, y, self.ws, self.ws.numel(), stream)
+        return y
+
+    def forward(self, x, logits, w_gate, w_up, w_down, y=None, stream=None):
+        """y of x and the router's logits [T, E_total] fp32."""
+        _expect(logits, "logits", self._logits, torch.float32, self.device)
+        return self._run(x, None, logits, w_gate, w_up, w_down, y, stream)
+
+    def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
+        """The forward from x and w_router [E_total, H]; returns (y, logits)."""
+        if logits is None:
+            logits = torch.empty(self._logits, dtype=torch.float32, device=self.device)
+        else:
+            _expect(logits, "logits", self._logits, torch.float32, self.device)
+        _expect(w_router, "w_router", self._wr, self.dtype, self.device)
+        return self._run(x, w_router, logits, w_gate, w_up, w_down, y, stream), logits

@@ -1,0 +1,240 @@
+"""GPU: the whole layer for a few tokens (moe_fwd_few) against the float64 oracle.
+
+Bars, relative Frobenius. bf16: y is rounded once, by at most half a step (2^-8 of each value), and
+what comes before it (w h as high and low bf16 parts, off by 2^-16; fp32 sums of up to 2048 terms) adds
+less than 1e-4. fp32: sums of up to n terms of random sign, each rounded by 2^-24, sqrt(n) 2^-24 < 5e-6
+for n <= 4096, twice in a row. Router logits: products of bf16 values are exact in fp32, one such sum.
+"""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mixture_experts_layer_32_amd import inputs
+from mixture_experts_layer_32_amd.layer import FewTokenLayer, MoELayer
+from gpu_util import to_dev
+
+pytestmark = pytest.mark.gpu
+
+TOL = {"bf16": 2.0 ** -8 + 1e-4, "fp32": 1e-5}
+LOGITS_TOL = 1e-5
+
+
+class Case:
+    def __init__(self, T, H, F, E, k, mode="bf16", seed=301, E_local=-1, e0=0, zipf_s=0.0):
+        self.cfg, self.L = inputs.custom_layer(T=T, H=H, F=F, E=E, k=k, dtype=mode, seed=seed, E_local=E_local, e0=e0,
+                                               zipf_s=zipf_s)
+        self.dt = torch.float32 if mode == "fp32" else torch.bfloat16
+        L = self.L
+        self.x, self.lg = to_dev(L["x"], self.dt), to_dev(L["logits"], torch.float32)
+        self.wg, self.wu, self.wd = (to_dev(L[n], self.dt) for n in ("wg", "wu", "wd"))
+        wr = inputs.router_weight(self.cfg)
+        self.wr_np, self.wr = wr, to_dev(wr, self.dt)
+        self.layer = FewTokenLayer(T, H, F, E, k, mode, self.cfg.el, e0)
+        self.layer.ws.fill_(0xFF)                       # NaN patterns and wild indices in every scratch byte
+        self.y = torch.full((T, H), float("nan"), dtype=self.dt, device="cuda")
+        self.mode = mode
+
+    def run(self, logits=None, **kw):
+        return self.layer.forward(self.x, self.lg if logits is None else logits, self.wg, self.wu, self.wd, self.y, **kw)
+
+    def ref(self, logits=None, x=None):
+        L, c = self.L, self.cfg
+        return oracle.forward(L["x"] if x is None else x, L["logits"] if logits is None else logits, L["wg"], L["wu"],
+                              L["wd"], c.k, c.e0, c.el)[0]
+
+    def check(self, y, ref):
+        got = y.float().cpu().numpy()
+        assert np.isfinite(got).all()
+        err = oracle.rel_frobenius(got, ref)
+        assert err <= TOL[self.mode], err
+        for t in range(len(ref)):                       # a fault in one token's row
+            assert oracle.rel_frobenius(got[t], ref[t]) <= 2 * TOL[self.mode], t
+
+
+CASES = [
+    dict(T=1, H=256, F=128, E=1, k=1),                  # one dense expert
+    dict(T=1, H=2048, F=768, E=128, k=8),
+    dict(T=2, H=256, F=128, E=8, k=2, mode="fp32"),
+    dict(T=3, H=768, F=640, E=5, k=5),                  # every expert for every token
+    dict(T=5, H=512, F=384, E=40, k=3, mode="fp32"),
+    dict(T=8, H=1024, F=256, E=16, k=4),
+    dict(T=16, H=256, F=256, E=4, k=4),                 # 16 tokens on every expert
+    dict(T=17, H=512, F=128, E=6, k=6),                 # 17: two column groups
+    dict(T=33, H=256, F=384, E=3, k=3),                 # 33: four column groups
+    dict(T=64, H=512, F=256, E=9, k=9),                 # 64 tokens on every expert
+    dict(T=64, H=256, F=128, E=4, k=4, mode="fp32"),
+    dict(T=64, H=512, F=256, E=64, k=6, zipf_s=2.5),    # a few popular experts
+    dict(T=40, H=256, F=128, E=512, k=32),              # the most experts and slots
+    dict(T=64, H=256, F=128, E=512, k=32, E_local=511, e0=1),
+    dict(T=31, H=512, F=256, E=24, k=4, E_local=5, e0=19),
+    dict(T=13, H=256, F=128, E=8, k=2, E_local=3, e0=2, mode="fp32"),
+    dict(T=7, H=4096, F=1536, E=12, k=8, zipf_s=1.1),
+    dict(T=9, H=7168, F=128, E=6, k=2),
+]
+
+
+def name(c):
+    return "-".join(f"{k}{v}" for k, v in c.items())
+
+
+@pytest.mark.parametrize("c", CASES, ids=name)
+def test_few_matches_the_oracle(c):
+    print("case few", c, flush=True)
+    k = Case(**c)
+    y = k.run()
+    torch.cuda.synchronize()
+    k.check(y, k.ref())
+    first = y.clone()
+    k.layer.ws.fill_(0x55)                              # no state between calls, the same bits again
+    y.fill_(float("nan"))
+    k.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("c", [c for i, c in enumerate(CASES) if i % 2 == 0], ids=name)
+def test_few_with_the_router(c):
+    print("case few router", c, flush=True)
+    k = Case(**c)
+    logits = torch.full((k.cfg.T, k.cfg.E), float("nan"), device="cuda")
+    y, lg = k.layer.forward_router(k.x, k.wr, k.wg, k.wu, k.wd, k.y, logits)
+    torch.cuda.synchronize()
+    assert lg is logits and y is k.y
+    got = lg.cpu().numpy()
+    assert oracle.rel_frobenius(got, oracle.router_forward(k.L["x"], k.wr_np)) <= LOGITS_TOL
+    k.check(y, k.ref(logits=got))                       # routed on the logits it returned
+
+
+def test_few_sweep():
+    rng = np.random.default_rng(77)
+    for i in range(24):
+        E = int(rng.integers(1, 200))
+        el = int(rng.integers(1, E + 1)) if rng.random() < 0.4 else E
+        c = dict(T=int(rng.integers(1, 65)), H=256 * int(rng.integers(1, 6)), F=128 * int(rng.integers(1, 7)), E=E,
+                 k=int(rng.integers(1, min(E, 32) + 1)), mode=("bf16", "fp32")[i % 2], seed=400 + i, E_local=el,
+                 e0=int(rng.integers(0, E - el + 1)), zipf_s=float(rng.choice([0.0, 1.1, 2.5])))
+        print("case few sweep", c, flush=True)
+        k = Case(**c)
+        y = k.run()
+        torch.cuda.synchronize()
+        k.check(y, k.ref())
+
+
+@pytest.mark.parametrize("mode", ["bf16", "fp32"])
+def test_a_share_without_tokens_is_zero(mode):
+    print("case few empty share", mode, flush=True)
+    k = Case(T=6, H=256, F=128, E=8, k=2, mode=mode, E_local=2, e0=6)
+    lg = k.lg.clone()
+    lg[:, 6:] = -torch.finfo(torch.float32).max        # masked by the type's lowest value
+    y = k.run(logits=lg)
+    torch.cuda.synchronize()
+    assert torch.count_nonzero(y) == 0 and torch.isfinite(y).all()
+
+
+def test_ties_and_lowest_values():
+    """Equal logits choose the lower experts with equal weights, also where all are the lowest value."""
+    print("case few ties", flush=True)
+    k = Case(T=4, H=256, F=128, E=12, k=3)
+    lg = np.zeros((4, 12), np.float32)
+    lg[1] = -np.finfo(np.float32).max
+    lg[2, ::2] = -0.0
+    lg[3] = -np.finfo(np.float32).max
+    lg[3, 7] = 1.5
+    y = k.run(logits=to_dev(lg, torch.float32))
+    torch.cuda.synchronize()
+    k.check(y, k.ref(logits=lg))
+
+
+def test_nan_token_stays_alone():
+    print("case few nan token", flush=True)
+    k = Case(T=20, H=256, F=128, E=4, k=4)
+    y0 = k.run().clone()
+    k.x[7, 3] = float("nan")
+    k.x[11, 0] = float("inf")
+    y1 = k.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(y1[7]).all() and not torch.isfinite(y1[11]).all()
+    rest = [t for t in range(20) if t not in (7, 11)]
+    assert torch.equal(y0[rest], y1[rest])
+
+
+def test_prompt_then_tokens():
+    """A prompt through the training forward, then its tokens again a few at a time: the same layer, each
+    output rounded (moe_fwd also rounds w h and the experts' outputs to bf16: 3 roundings of 2^-8)."""
+    print("case few after prompt", flush=True)
+    T, H, F, E, k = 130, 512, 256, 16, 4
+    cfg, L = inputs.custom_layer(T=T, H=H, F=F, E=E, k=k, seed=33)
+    x, lg = to_dev(L["x"], torch.bfloat16), to_dev(L["logits"], torch.float32)
+    w = [to_dev(L[n], torch.bfloat16) for n in ("wg", "wu", "wd")]
+    y = MoELayer(T, H, F, E, k).forward(x, lg, *w)
+    out, t = [], 0
+    for n in (64, 1, 33, 32):
+        out.append(FewTokenLayer(n, H, F, E, k).forward(x[t:t + n], lg[t:t + n], *w))
+        t += n
+    torch.cuda.synchronize()
+    got = torch.cat(out).float().cpu().numpy()
+    ref = oracle.forward(L["x"], L["logits"], L["wg"], L["wu"], L["wd"], k)[0]
+    assert oracle.rel_frobenius(got, ref) <= TOL["bf16"]
+    assert oracle.rel_frobenius(got, y.float().cpu().numpy()) <= 4 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("router", [False, True])
+def test_graph_replays(router):
+    print("case few graph", router, flush=True)
+    k = Case(T=9, H=512, F=256, E=16, k=4)
+    lg = torch.empty(9, 16, device="cuda")
+
+    def step():
+        if router:
+            k.layer.forward_router(k.x, k.wr, k.wg, k.wu, k.wd, k.y, lg)
+        else:
+            k.run()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x0 = k.x.clone()
+    for r in range(4):
+        k.x.copy_(x0 * (1 + r))                         # new inputs in the captured buffers
+        step()
+        torch.cuda.synchronize()
+        want = k.y.clone()
+        k.y.fill_(float("nan"))
+        k.layer.ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want.view(torch.uint8), k.y.view(torch.uint8)), r
+
+
+def test_two_threads_on_their_own_streams():
+    print("case few threads", flush=True)
+    cases = [Case(T=11, H=512, F=256, E=16, k=4, seed=51), Case(T=64, H=256, F=384, E=8, k=2, seed=52)]
+    want = []
+    for c in cases:
+        want.append(c.run().clone())
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                cases[i].y.fill_(float("nan"))
+                cases[i].run()
+                if not torch.equal(cases[i].y, want[i]):
+                    bad.append(i)
+
+    th = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in th]
+    [t.join() for t in th]
+    assert not bad
