@@ -247,6 +247,55 @@ moe_status moe_fwd_few(const moe_desc* d, const void* x, const void* w_router, f
                        const void* w_gate, const void* w_up, const void* w_down, void* y, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* 8-bit integer rows, products and layer, for serving: weights quantised once, activations on the fly.
+ *
+ * A quantised row of n elements v has one fp32 scale s and n signed bytes q, and stands for q * s:
+ *   D = max(max_i |v_i|, 127 * 2^-126),  s = D / 127 in fp32,
+ *   q_i = the whole number nearest to the real quotient 127 v_i / D, ties to even (|q_i| <= 127).
+ * A row of zeros has s = 2^-126. A row that holds a NaN or an infinity has s = NaN and q = 0, so that
+ * whatever is computed from it is NaN. */
+typedef enum { MOE_TYPE_FP32 = 0, MOE_TYPE_BF16 = 1 } moe_type;
+
+/* Quantises the rows of in [rows, cols] (row-major, `type`) into q [rows, cols] and scales [rows]:
+ * tokens along their features, or a weight [N, K] (or [E, N, K] as E*N rows) along its contraction
+ * axis, which gives one scale an output channel. cols a multiple of 16 and <= 131072, rows < 2^31
+ * (MOE_ERR_UNSUPPORTED_SHAPE); an unknown type is MOE_ERR_UNSUPPORTED_MODE. in and q need 16-byte
+ * alignment, scales 4-byte. */
+moe_status moe_int8_quantize(const void* in, int type, int64_t rows, int64_t cols, int8_t* q, float* scales,
+                             void* stream);
+
+/* The product of 8-bit rows with 8-bit weights, each with its scales:
+ *   y[m, n] = (sum_k x[m, k] w[g, n, k]) * (x_scales[m] * w_scales[g, n])
+ * with the sum exact in 32-bit integers (bytes of -127..127), the scales applied once in fp32, and y
+ * rounded to `type` last. x [M, K], w [G, N, K], w_scales [G, N], y [M, N].
+ *   offsets = NULL (G = 1): every row is multiplied by the one weight.
+ *   offsets [G + 1] int32 (device): rows offsets[g] .. offsets[g+1]-1 belong to group g, as moe_route's
+ *     `offsets` give them for rows sorted by expert. Groups may be empty. Offsets ascend; values outside
+ *     0..M are taken as the nearest of the two. Rows of y before offsets[0] and from offsets[G] on are left
+ *     as they were.
+ * K a multiple of 16 and <= 131072, N <= 2^20, G <= 512, M < 2^31, M*N < 2^40. x and w need 16-byte
+ * alignment, the scales and offsets 4-byte, y its type's (16 bytes and N % 8 = 0 write faster). */
+moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales,
+                           int64_t M, int64_t N, int64_t K, int G, const int32_t* offsets, void* y, int type,
+                           void* stream);
+
+/* The whole layer with 8-bit weights, forward only, any T: x rows quantised, both products' sums exact,
+ * h = w silu(a) b in fp32, its rows (one a pair) quantised, the down product, the combine. Mode BF16
+ * (x, y and w_router; MOE_ERR_UNSUPPORTED_MODE otherwise). Weights and scales as moe_int8_quantize
+ * gives them for each matrix along its last axis: w_gate, w_up [E_local, F, H] with s_gate, s_up
+ * [E_local, F], w_down [E_local, H, F] with s_down [E_local, H].
+ * Up to 64 tokens run on the kernels of moe_fwd_few (y summed in fp32), more on the grouped products
+ * (each pair's output rounded to bf16 before the combine, as in moe_fwd).
+ * logits and w_router as in moe_fwd_few, but with w_router, more than 64 tokens need E_total <= 256
+ * (MOE_ERR_UNSUPPORTED_SHAPE: moe_router_fwd, then the call without). desc.recompute has no meaning here.
+ * 16-byte alignment of every tensor, 4-byte of logits and scales, 256-byte of ws
+ * (moe_query_int8_sizes; contents need not be preserved). */
+moe_status moe_query_int8_sizes(const moe_desc* d, size_t* ws);
+moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, float* logits,
+                        const int8_t* w_gate, const float* s_gate, const int8_t* w_up, const float* s_up,
+                        const int8_t* w_down, const float* s_down, void* y, void* ws, size_t ws_bytes,
+                        void* stream);
+
 /* Byte offsets of the routing results inside `saved`.
  *   idx       int32 [T*k]      chosen experts, slot order (logit desc, index asc)
  *   weight    float [T*k]      renormalised routing weights

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 MODES = {"fp32": 0, "bf16": 1, "mxfp8": 2, "fp8_bwd": 3, "fp8": 4}
+TYPES = {"fp32": 0, "bf16": 1}
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
           3: "MOE_ERR_UNSUPPORTED_MODE", 4: "MOE_ERR_WORKSPACE_TOO_SMALL", 5: "MOE_ERR_HIP"}
 
@@ -82,11 +83,17 @@ def lib():
         L.moe_router_bwd.argtypes = [_D, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_query_few_sizes.argtypes = [_D, ctypes.POINTER(ctypes.c_size_t)]
         L.moe_fwd_few.argtypes = [_D, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        i64 = ctypes.c_int64
+        L.moe_int8_quantize.argtypes = [_P, ctypes.c_int, i64, i64, _P, _P, _P]
+        L.moe_int8_matmul.argtypes = [_P, _P, _P, _P, i64, i64, i64, ctypes.c_int, _P, _P, ctypes.c_int, _P]
+        L.moe_query_int8_sizes.argtypes = [_D, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fwd_int8.argtypes = [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_profile_enable.argtypes = [ctypes.c_int]
         L.moe_profile_kernel.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                          ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double)]
         for n in ("moe_query_sizes", "moe_route", "moe_route_static", "moe_fwd", "moe_fwd_router", "moe_bwd", "moe_saved_layout", "moe_mx_quantize",
-                  "moe_fp8_block_quantize", "moe_query_few_sizes", "moe_fwd_few",
+                  "moe_fp8_block_quantize", "moe_query_few_sizes", "moe_fwd_few", "moe_int8_quantize",
+                  "moe_int8_matmul", "moe_query_int8_sizes", "moe_fwd_int8",
                   "moe_query_router_sizes", "moe_router_fwd", "moe_router_bwd", "moe_profile_enable",
                   "moe_profile_disable", "moe_profile_collect", "moe_profile_kernel"):
             getattr(L, n).restype = st
@@ -183,6 +190,27 @@ def query_few_sizes(desc: Desc):
 def moe_fwd_few(desc, x, w_router, logits, w_gate, w_up, w_down, y, ws, ws_bytes, stream=None):
     _check(lib().moe_fwd_few(ctypes.byref(desc), ptr(x), ptr(w_router), ptr(logits), ptr(w_gate), ptr(w_up),
                              ptr(w_down), ptr(y), ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_int8_quantize(x, type, rows, cols, q, scales, stream=None):
+    _check(lib().moe_int8_quantize(ptr(x), type, rows, cols, ptr(q), ptr(scales), _stream(stream)))
+
+
+def moe_int8_matmul(x, x_scales, w, w_scales, M, N, K, G, offsets, y, type, stream=None):
+    _check(lib().moe_int8_matmul(ptr(x), ptr(x_scales), ptr(w), ptr(w_scales), M, N, K, G, ptr(offsets), ptr(y), type,
+                                 _stream(stream)))
+
+
+def query_int8_sizes(desc: Desc):
+    n = ctypes.c_size_t()
+    _check(lib().moe_query_int8_sizes(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def moe_fwd_int8(desc, x, w_router, logits, w_gate, s_gate, w_up, s_up, w_down, s_down, y, ws, ws_bytes, stream=None):
+    _check(lib().moe_fwd_int8(ctypes.byref(desc), ptr(x), ptr(w_router), ptr(logits), ptr(w_gate), ptr(s_gate),
+                              ptr(w_up), ptr(s_up), ptr(w_down), ptr(s_down), ptr(y), ptr(ws), ws_bytes,
+                              _stream(stream)))
 
 
 def moe_mx_quantize(x, rows, cols, axis, q, scales, stream=None):

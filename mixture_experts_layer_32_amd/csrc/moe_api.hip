@@ -1045,6 +1045,203 @@ moe_status moe_fwd_few(const moe_desc* d, const void* x, const void* w_router, f
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------------------------------------
+// 8-bit integer rows, products and layer
+
+static moe_status check_type(int type) {
+  if (type != MOE_TYPE_FP32 && type != MOE_TYPE_BF16) return fail(MOE_ERR_UNSUPPORTED_MODE, "unknown type");
+  return MOE_OK;
+}
+
+moe_status moe_int8_quantize(const void* in, int type, int64_t rows, int64_t cols, int8_t* q, float* scales,
+                             void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(type)) != MOE_OK) return st;
+  if (rows < 1 || cols < 1) return fail(MOE_ERR_INVALID_ARG, "rows and cols must be positive");
+  if (cols % 16 != 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "cols must be a multiple of 16");
+  if (cols > kInt8MaxK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "cols must be <= 131072");
+  if (rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rows must be < 2^31");
+  if ((st = check_ptrs({{in, "in"}, {q, "q"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{scales, "scales"}}, 4)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const hipError_t e = launch_int8_quant(in, type == MOE_TYPE_FP32, rows, (int)cols, nullptr,
+                                         reinterpret_cast<uint8_t*>(q), scales, "int8_quant",
+                                         static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int8 quantise launch");
+  return MOE_OK;
+}
+
+moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales, int64_t M,
+                           int64_t N, int64_t K, int G, const int32_t* offsets, void* y, int type, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(type)) != MOE_OK) return st;
+  if (M < 1 || N < 1 || K < 1 || G < 1) return fail(MOE_ERR_INVALID_ARG, "M, N, K and G must be positive");
+  if (!offsets && G != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is null with more than one group");
+  if (K % 16 != 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be a multiple of 16");
+  if (K > kInt8MaxK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be <= 131072");
+  if (G > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "G must be <= 512");
+  if (M > INT32_MAX || N > (1 << 20) || M * N >= (int64_t(1) << 40))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be < 2^31, N <= 2^20 and M*N < 2^40");
+  if ((st = check_ptrs({{x, "x"}, {w, "w"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{x_scales, "x_scales"}, {w_scales, "w_scales"}}, 4)) != MOE_OK) return st;
+  if (offsets && (st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;
+  if ((st = check_ptrs({{y, "y"}}, type == MOE_TYPE_FP32 ? 4 : 2)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  I8Params p{};
+  p.x = reinterpret_cast<const uint8_t*>(x);
+  p.xs = x_scales;
+  p.w = reinterpret_cast<const uint8_t*>(w);
+  p.ws = w_scales;
+  p.offsets = offsets;
+  p.y = y;
+  p.M = M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.G = G;
+  p.f32 = type == MOE_TYPE_FP32;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = M <= kFewTokens ? launch_int8_rows(p, s) : launch_int8_matmul(p, persistent_grid(1), "int8_matmul", s);
+  if (e != hipSuccess) return hip_fail(e, "int8 product launch");
+  return MOE_OK;
+}
+
+namespace {
+// Workspace of moe_fwd_int8 beyond kFewTokens tokens: the routing's buffers (as the bf16 layer without
+// activations lays them out), then the 8-bit operands.
+struct Int8Layout {
+  Layout route;
+  size_t saved, scratch, xq, xs, h, hq, hs, o, total;
+};
+
+Int8Layout int8_layout(moe_desc d) {
+  Int8Layout L{};
+  d.recompute = 1;   // `saved` holds the routing alone
+  L.route = make_layout(d);
+  const size_t n = (size_t)L.route.rows, H = (size_t)d.H, F = (size_t)d.F;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.saved = take(L.route.saved_total);
+  L.scratch = take(L.route.o);   // the forward workspace up to its first activation
+  L.xq = take((size_t)d.T * H);
+  L.xs = take((size_t)d.T * 4);
+  L.h = take(n * F * 4);
+  L.hq = take(n * F);
+  L.hs = take(n * 4);
+  L.o = take(n * H * 2);
+  L.total = off;
+  return L;
+}
+
+moe_status int8_checks(const moe_desc* d) {
+  moe_status st = validate(d);
+  if (st != MOE_OK) return st;
+  if (d->mode != MOE_MODE_BF16) return fail(MOE_ERR_UNSUPPORTED_MODE, "moe_fwd_int8 takes MOE_MODE_BF16 (its x and y)");
+  if (d->H > kInt8MaxK || d->F > kInt8MaxK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "H and F must be <= 131072");
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_query_int8_sizes(const moe_desc* d, size_t* ws) {
+  g_last_error.clear();
+  moe_status st = int8_checks(d);
+  if (st != MOE_OK) return st;
+  if (ws) *ws = d->T <= kFewTokens ? few_layout(*d, true).total : int8_layout(*d).total;
+  return MOE_OK;
+}
+
+moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, float* logits, const int8_t* w_gate,
+                        const float* s_gate, const int8_t* w_up, const float* s_up, const int8_t* w_down,
+                        const float* s_down, void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status st = int8_checks(d);
+  if (st != MOE_OK) return st;
+  const bool few = d->T <= kFewTokens;
+  if (w_router && !few && d->E_total > 256)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "moe_fwd_int8 with w_router and more than 64 tokens needs E_total <= 256 "
+                                           "(else moe_router_fwd first)");
+  if ((st = check_ptrs({{x, "x"}, {w_gate, "w_gate"}, {w_up, "w_up"}, {w_down, "w_down"}, {y, "y"}}, 16)) != MOE_OK)
+    return st;
+  if (w_router && (st = check_ptrs({{w_router, "w_router"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{s_gate, "s_gate"}, {s_up, "s_up"}, {s_down, "s_down"}, {logits, "logits"}}, 4)) != MOE_OK)
+    return st;
+  if ((st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  char* w = static_cast<char*>(ws);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (few) {
+    const FewLayout L = few_layout(*d, true);
+    if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "8-bit layer workspace too small");
+    FewParams p = few_params(*d, L, x, w_router, logits, w_gate, w_up, w_down, y, ws);
+    p.sg = s_gate;
+    p.su = s_up;
+    p.sd = s_down;
+    p.xq = reinterpret_cast<uint8_t*>(w + L.xq);
+    p.xs = reinterpret_cast<float*>(w + L.xs);
+    p.hmax = reinterpret_cast<unsigned*>(w + L.hmax);
+    p.x = p.xq;
+    if ((e = launch_few(p, 1, s)) != hipSuccess) return hip_fail(e, "few-token launch");
+    return MOE_OK;
+  }
+  const Int8Layout L = int8_layout(*d);
+  if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "8-bit layer workspace too small");
+  const RouteParams rp = route_params(*d, L.route, logits, w + L.saved, w + L.scratch);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(w + L.xq);
+  float* xs = reinterpret_cast<float*>(w + L.xs);
+  if ((e = launch_int8_quant(x, false, d->T, d->H, nullptr, xq, xs, "int8_quant_x", s)) != hipSuccess)
+    return hip_fail(e, "int8 quantise launch");
+  if (w_router && d->topk <= 8) {
+    e = launch_router_route_bf16(rp, x, w_router, logits, d->H, s);
+  } else {
+    e = w_router ? launch_router_logits_bf16(x, w_router, logits, d->T, d->H, d->E_total, s) : hipSuccess;
+    if (e == hipSuccess) e = launch_route(rp, s);
+  }
+  if (e != hipSuccess) return hip_fail(e, "route launch");
+  I8LayerParams gp{};
+  gp.xq = xq;
+  gp.xs = xs;
+  gp.wg = reinterpret_cast<const uint8_t*>(w_gate);
+  gp.wu = reinterpret_cast<const uint8_t*>(w_up);
+  gp.sg = s_gate;
+  gp.su = s_up;
+  gp.weight = rp.weight;
+  gp.perm = rp.perm;
+  gp.ptok = rp.ptok;
+  gp.offsets = rp.offsets;
+  gp.mtile2 = rp.mtile2;
+  gp.num_mtiles2 = rp.num_mtiles2;
+  gp.h = reinterpret_cast<float*>(w + L.h);
+  gp.H = d->H;
+  gp.F = d->F;
+  if ((e = launch_gateup_i8(gp, persistent_grid(1), s)) != hipSuccess) return hip_fail(e, "gate/up launch");
+  I8Params dp{};
+  dp.x = reinterpret_cast<const uint8_t*>(w + L.hq);
+  dp.xs = reinterpret_cast<const float*>(w + L.hs);
+  dp.w = reinterpret_cast<const uint8_t*>(w_down);
+  dp.ws = s_down;
+  dp.offsets = rp.offsets;
+  dp.y = w + L.o;
+  dp.M = L.route.rows;
+  dp.N = d->H;
+  dp.K = d->F;
+  dp.G = d->E_local;
+  if ((e = launch_int8_quant(gp.h, true, L.route.rows, d->F, rp.offsets + d->E_local,
+                             reinterpret_cast<uint8_t*>(w + L.hq), reinterpret_cast<float*>(w + L.hs), "int8_quant_h",
+                             s)) != hipSuccess)
+    return hip_fail(e, "int8 quantise launch");
+  if ((e = launch_int8_matmul(dp, persistent_grid(1), "int8_down", s)) != hipSuccess) return hip_fail(e, "down launch");
+  if ((e = launch_combine<bf16>(w + L.o, rp.pair_pos, y, d->T, d->topk, d->H,
+                                combine_tpw(d->topk, d->E_local, d->E_total), s)) != hipSuccess)
+    return hip_fail(e, "combine launch");
+  return MOE_OK;
+}
+
 moe_status moe_mx_quantize(const void* in, int64_t rows, int64_t cols, int axis, uint8_t* q, uint8_t* scales,
                            void* stream) {
   g_last_error.clear();

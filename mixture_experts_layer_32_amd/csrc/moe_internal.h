@@ -211,6 +211,36 @@ struct FewParams {
 // type: bytes of a weight element (4: fp32 mode, 2: bf16, 1: 8-bit weights with bf16 x and y)
 hipError_t launch_few(const FewParams& p, int type, hipStream_t s);
 
+// 8-bit integer rows and products: int8.hip, gemm_i8.hip.
+constexpr int kInt8MaxK = 131072;   // 127^2 K < 2^31: int32 sums are exact
+struct I8Params {
+  const uint8_t* x;      // [M, K] signed bytes
+  const float* xs;       // [M]
+  const uint8_t* w;      // [G, N, K]
+  const float* ws;       // [G, N]
+  const int* offsets;    // [G + 1] first row of each group, or null (G = 1: all rows)
+  void* y;               // [M, N] fp32 (f32) or bf16
+  int64_t M;
+  int N, K, G;
+  bool f32;
+};
+// rows of x [rows, cols] (fp32 or bf16) as signed bytes with a scale each; nrows: the row count on the
+// device, or null
+hipError_t launch_int8_quant(const void* x, bool f32, int64_t rows, int cols, const int* nrows, uint8_t* q,
+                             float* scales, const char* name, hipStream_t s);
+hipError_t launch_int8_rows(const I8Params& p, hipStream_t s);                                    // M <= 64
+hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hipStream_t s);      // any M
+// gate/up of the 8-bit layer over the routing's tiles
+struct I8LayerParams {
+  const uint8_t *xq, *wg, *wu;
+  const float *xs, *sg, *su, *weight;
+  const int *perm, *ptok, *offsets, *num_mtiles2;
+  const int2* mtile2;
+  float* h;              // [pairs, F]
+  int H, F;
+};
+hipError_t launch_gateup_i8(const I8LayerParams& p, int grid, hipStream_t s);
+
 hipError_t launch_forward_gemms_mx(const FwdParams& p, int grid, hipStream_t s, bool recompute = false);
 hipError_t launch_backward_gemms_mx(const BwdParams& p, int grid, hipStream_t s);
 hipError_t launch_quant_rows(const void* in, uint8_t* q, uint8_t* sc, int64_t n, const char* name, hipStream_t s,

@@ -26,6 +26,12 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _current(device):
+    """Raises ValueError unless `device` is the calling thread's current GPU, whose streams the library uses."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"{device} is not the current GPU (torch.cuda.set_device)")
+
+
 def _device(device):
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
@@ -163,6 +169,7 @@ class FewTokenLayer:
 
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         el, dev = self.dtype, self.device
+        _current(dev)
         if y is None:
             y = torch.empty(self._x, dtype=el, device=dev)
         else:
@@ -186,4 +193,102 @@ class FewTokenLayer:
         else:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, self.dtype, self.device)
+        return self._run(x, w_router, logits, w_gate, w_up, w_down, y, stream), logits
+
+
+_INT8_TYPES = {torch.float32: binding.TYPES["fp32"], torch.bfloat16: binding.TYPES["bf16"]}
+
+
+def _int8_type(dtype):
+    if dtype not in _INT8_TYPES:
+        raise ValueError(f"expected dtype torch.float32 or torch.bfloat16, got {dtype}")
+    return _INT8_TYPES[dtype]
+
+
+def int8_quantize(x, q=None, scales=None, stream=None):
+    """x [.., K] (bf16 or fp32) as signed bytes with one scale for each row of K: (q, scales), as activations
+    or as the (weight, scales) pair of int8_matmul and Int8Layer."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected a tensor of at least one dimension")
+    t, dev, lead = _int8_type(x.dtype), x.device, x.shape[:-1]
+    if not x.is_contiguous():
+        raise ValueError("x: expected a contiguous tensor")
+    _current(dev)
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    else:
+        _expect(q, "q", x.shape, torch.int8, dev)
+    if scales is None:
+        scales = torch.empty(lead, dtype=torch.float32, device=dev)
+    else:
+        _expect(scales, "scales", lead, torch.float32, dev)
+    binding.moe_int8_quantize(x, t, lead.numel(), x.shape[-1], q, scales, stream)
+    return q, scales
+
+
+def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bfloat16, stream=None):
+    """y [M, N] of 8-bit rows x [M, K] and weights w [N, K], or w [G, N, K] with offsets [G + 1] int32: rows
+    offsets[g] .. offsets[g+1]-1 are multiplied by w[g]. A y that is given sets the dtype, and its rows
+    outside the groups are left as they were (a y made here holds anything there)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (2 if offsets is None else 3):
+        raise ValueError("expected x [M, K] and w [N, K], or w [G, N, K] with offsets")
+    dev, (M, K), N = x.device, x.shape, w.shape[-2]
+    G = 1 if offsets is None else w.shape[0]
+    _current(dev)
+    _expect(x, "x", (M, K), torch.int8, dev)
+    _expect(w, "w", (N, K) if offsets is None else (G, N, K), torch.int8, dev)
+    _expect(x_scales, "x_scales", (M,), torch.float32, dev)
+    _expect(w_scales, "w_scales", (N,) if offsets is None else (G, N), torch.float32, dev)
+    if offsets is not None:
+        _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
+    if y is None:
+        t = _int8_type(dtype)
+        y = torch.empty(M, N, dtype=dtype, device=dev)
+    else:
+        t = _int8_type(y.dtype)
+        _expect(y, "y", (M, N), y.dtype, dev)
+    binding.moe_int8_matmul(x, x_scales, w, w_scales, M, N, K, G, offsets, y, t, stream)
+    return y
+
+
+class Int8Layer:
+    """The layer's forward with 8-bit weights through moe_fwd_int8, for any number of tokens: holds the workspace
+    of one shape. Each weight is the (bytes, scales) pair of int8_quantize on the bf16 or fp32 matrix. Calls of
+    one object share the workspace: order them, or give concurrent streams an object each."""
+
+    def __init__(self, T, H, F, E_total, topk, E_local=None, expert_offset=0, device="cuda"):
+        self.desc = d = binding.Desc.make(T, H, F, E_total, topk, "bf16", E_local, expert_offset)
+        self.device = _device(device)
+        self.ws = torch.empty(binding.query_int8_sizes(d), dtype=torch.uint8, device=self.device)
+        self._x, self._logits, self._wr = (d.T, d.H), (d.T, d.E_total), (d.E_total, d.H)
+        self._w_in, self._w_out = (d.E_local, d.F, d.H), (d.E_local, d.H, d.F)
+
+    def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
+        dev = self.device
+        _current(dev)
+        if y is None:
+            y = torch.empty(self._x, dtype=torch.bfloat16, device=dev)
+        else:
+            _expect(y, "y", self._x, torch.bfloat16, dev)
+        _expect(x, "x", self._x, torch.bfloat16, dev)
+        for name, (w, s), shape in (("w_gate", w_gate, self._w_in), ("w_up", w_up, self._w_in),
+                                    ("w_down", w_down, self._w_out)):
+            _expect(w, name, shape, torch.int8, dev)
+            _expect(s, name + " scales", shape[:2], torch.float32, dev)
+        binding.moe_fwd_int8(self.desc, x, w_router, logits, w_gate[0], w_gate[1], w_up[0], w_up[1], w_down[0],
+                             w_down[1], y, self.ws, self.ws.numel(), stream)
+        return y
+
+    def forward(self, x, logits, w_gate, w_up, w_down, y=None, stream=None):
+        """y of x and the router's logits [T, E_total] fp32; w_gate, w_up, w_down: (bytes, scales)."""
+        _expect(logits, "logits", self._logits, torch.float32, self.device)
+        return self._run(x, None, logits, w_gate, w_up, w_down, y, stream)
+
+    def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
+        """The forward from x and w_router [E_total, H] bf16; returns (y, logits)."""
+        if logits is None:
+            logits = torch.empty(self._logits, dtype=torch.float32, device=self.device)
+        else:
+            _expect(logits, "logits", self._logits, torch.float32, self.device)
+        _expect(w_router, "w_router", self._wr, torch.bfloat16, self.device)
         return self._run(x, w_router, logits, w_gate, w_up, w_down, y, stream), logits
