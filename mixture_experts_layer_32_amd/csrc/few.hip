@@ -1,17 +1,25 @@
 // The whole layer for a few tokens (T <= 64), forward only, in bf16, fp32 or with 8-bit weights.
 //
 // At a few tokens the layer reads the weights of the experts that were chosen, once, and does little
-// else: 6 H F flops against 3 H F elements per pair. These kernels are built to keep those reads in
-// flight on every CU, with the arithmetic on MFMA tiles whose 16 columns are an expert's tokens.
+// else: 6 H F flops against 3 H F elements per pair. These kernels are built around that read. One wave
+// instruction takes 256 bytes of each of 4 weight rows (whole cache lines, non-temporal), and the
+// arithmetic is v_mfma_*_4x4x4_16b: sixteen independent 4 x 4 products, here 4 rows by 4 tokens for
+// sixteen 16-byte pieces of the rows, whose sums are added over the lanes at the end of a row. An expert's
+// tokens are taken in sets of 4, up to 4 sets at a time, so that little of the matrix work is padding.
+// Reads alone, 320 MB on 256 CUs: 4 rows x 256 B 6.5 TB/s (5.7 without the non-temporal hint), 16 rows x
+// 64 B, the form a 16 x 16 MFMA would take, 5.2 TB/s either way.
 //
-//   k_few_prep    logits = x W_r^T (16 experts per workgroup) and, with 8-bit weights, the quantised rows
+//   k_few_prep    logits = x W_r^T (4 experts by 16 tokens per workgroup) and, with 8-bit weights, the quantised rows
 //                 of x. Only launched where one of the two is asked for.
-//   k_few_gateup  every workgroup routes the tokens for itself (a few hundred cycles), then takes
-//                 (expert, 16 rows of F) tasks: both weights' rows times the expert's tokens, split
-//                 along H over the waves, h = w silu(a) b into the workspace.
-//   k_few_down    a workgroup owns 16 rows of H for every expert: its waves share the (expert, F) axis,
+//   k_few_topk    the tokens' experts and weights; only launched for more than 8 tokens.
+//   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 8 tokens, chooses them); then its
+//                 waves take (expert, 4 rows of F) units, each on its own, and write h = w silu(a) b into
+//                 the workspace.
+//   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
 //                 each keeping its own sum per token, and the sums are added in a fixed order. No
 //                 partial sums in memory, no atomics on sums: repeated calls give the same bits.
+// Experts of more than 16 tokens ("heavy") take 16 x 16 MFMA tiles in both, 16 tokens a column group, so that
+// their weights too are read once.
 //
 // h is kept in fp32's accuracy: as fp32, or in bf16 mode as the pair hi = bf16(h), lo = bf16(h - hi),
 // whose two products cost matrix time that a read-bound kernel does not miss.
@@ -27,140 +35,233 @@
 namespace moe {
 namespace {
 
-constexpr int kGW = 8;      // waves of k_few_gateup
-constexpr int kDW = 16;     // waves of k_few_down and k_few_prep
-constexpr int kStep = 64;   // bytes of one weight row per MFMA step
+constexpr int kGW = 8;       // waves of k_few_gateup
+constexpr int kDW = 16;      // waves of k_few_down
+constexpr int kPW = 8;       // waves of k_few_prep
+constexpr int kSeg = 256;    // bytes of one weight row per wave instruction
+constexpr int kSets = 4;     // sets of 4 tokens taken at once
 
-template <class T> struct Mma;   // one 16x16 MFMA step over 64 bytes of contraction
-template <> struct Mma<bf16> {
+// Sixteen 4x4 products over 16 bytes of contraction. Lane l supplies row l & 3 of A and column l & 3 of
+// B, piece l >> 2; accumulator element i of lane l is row i, column l & 3 of block l >> 2.
+template <class T> struct Mma4;
+template <> struct Mma4<bf16> {
   typedef f32x4 Acc;
-  typedef float Sum;
-  static __device__ __forceinline__ void go(Acc& c, const uint4& a, const uint4& b) { mma16<bf16>(c, a, b); }
-};
-template <> struct Mma<float> {
-  typedef f32x4 Acc;
-  typedef float Sum;
-  static __device__ __forceinline__ void go(Acc& c, const uint4& a, const uint4& b) { mma16<float>(c, a, b); }
-};
-template <> struct Mma<int8_t> {
-  typedef i32x4 Acc;
-  typedef int Sum;
   static __device__ __forceinline__ void go(Acc& c, const uint4& a, const uint4& b) {
-    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    c = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, make_uint2(a.x, a.y)),
+                                               __builtin_bit_cast(s16x4, make_uint2(b.x, b.y)), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, make_uint2(a.z, a.w)),
+                                               __builtin_bit_cast(s16x4, make_uint2(b.z, b.w)), c, 0, 0, 0);
   }
 };
+template <> struct Mma4<float> {
+  typedef f32x4 Acc;
+  static __device__ __forceinline__ void go(Acc& c, const uint4& a, const uint4& b) {
+    c = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  }
+};
+template <> struct Mma4<int8_t> {
+  typedef i32x4 Acc;
+  static __device__ __forceinline__ void go(Acc& c, const uint4& a, const uint4& b) {
+    c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)a.x, (int)b.x, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)a.y, (int)b.y, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)a.z, (int)b.z, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)a.w, (int)b.w, c, 0, 0, 0);
+  }
+};
+
+// One 16x16 product over 64 bytes of contraction: lane l supplies row (column) l & 15, 16-byte piece
+// l >> 4; accumulator element i of lane l is row 4 (l >> 4) + i, column l & 15. For heavy experts.
+__device__ __forceinline__ void mma16x16(f32x4& c, const uint4& a, const uint4& b, bf16) { mma16<bf16>(c, a, b); }
+__device__ __forceinline__ void mma16x16(f32x4& c, const uint4& a, const uint4& b, float) { mma16<float>(c, a, b); }
+__device__ __forceinline__ void mma16x16(i32x4& c, const uint4& a, const uint4& b, int8_t) {
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+constexpr int kStep = 64;    // bytes of a row per such step
+
+// sum over the sixteen blocks (the lanes with equal l & 3), in every lane
+__device__ __forceinline__ float block_sum(float v) {
+  v += dpp_mov<0x124>(v);   // row_ror:4
+  v += dpp_mov<0x128>(v);   // row_ror:8
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ int block_sum(int v) {
+  v += (int)dpp_mov<0x124>((unsigned)v);
+  v += (int)dpp_mov<0x128>((unsigned)v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
 
 // ------------------------------------------------------------------------------------------------
 // routing of the few tokens inside a workgroup
 
-// the k best experts of a token by one wave: lane j < k ends with the j-th key
-__device__ __forceinline__ unsigned long long wave_topk(const float* row, int E, int k, int lane) {
-  unsigned long long key[kMaxExperts / 64], mine = 0ull;
-  const int per = (E + 63) >> 6;
+// The k best experts of a token by one wave (E <= 64 PER): lane j < k ends with the j-th expert and its
+// logit. A round takes the largest of the order-preserving 32-bit keys over the wave (DPP), and of the
+// lanes that hold it the lowest expert (ballots, experts 0..63 first).
+template <int PER>
+__device__ __forceinline__ void wave_topk(const float* row, int E, int k, int lane, int& my_e, float& my_v) {
+  unsigned key[PER];
 #pragma unroll
-  for (int i = 0; i < kMaxExperts / 64; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    key[i] = i < per && e < E ? topk_key(row[e], e) : 0ull;
+    key[i] = e < E ? max((unsigned)(topk_key(row[e], 0) >> 32), 1u) : 0u;   // 0: no expert
   }
+#pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    unsigned long long b = key[0];
+    unsigned m = key[0];
 #pragma unroll
-    for (int i = 1; i < kMaxExperts / 64; ++i)
-      if (i < per) b = key[i] > b ? key[i] : b;
-    auto step = [&](unsigned long long o) { b = o > b ? o : b; };
-    step(((unsigned long long)dpp_mov<kDppXor1>((unsigned)(b >> 32)) << 32) | dpp_mov<kDppXor1>((unsigned)b));
-    step(((unsigned long long)dpp_mov<kDppXor2>((unsigned)(b >> 32)) << 32) | dpp_mov<kDppXor2>((unsigned)b));
-    step(((unsigned long long)dpp_mov<kDppHalfMirror>((unsigned)(b >> 32)) << 32) | dpp_mov<kDppHalfMirror>((unsigned)b));
-    step(((unsigned long long)dpp_mov<kDppMirror>((unsigned)(b >> 32)) << 32) | dpp_mov<kDppMirror>((unsigned)b));
-    unsigned long long best = 0ull;
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    m = wave_max_u32(m);
+    int e = -1;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {   // one lane of each 16-lane row
-      const unsigned long long o = ((unsigned long long)(unsigned)__builtin_amdgcn_readlane((int)(b >> 32), 16 * q) << 32) |
-                                   (unsigned)__builtin_amdgcn_readlane((int)b, 16 * q);
-      best = o > best ? o : best;
+    for (int i = 0; i < PER; ++i)
+      if (e < 0) {
+        const unsigned long long at = __ballot(key[i] == m);
+        if (at) {
+          const int l = __ffsll(at) - 1;
+          e = 64 * i + l;
+          key[i] = lane == l ? 0u : key[i];
+        }
+      }
+    if (lane == j) {
+      my_e = e;
+      my_v = key_value((unsigned long long)m << 32);
     }
-    if (lane == j) mine = best;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 64; ++i) key[i] = key[i] == best ? 0ull : key[i];
   }
-  return mine;
 }
+
+// Experts with pairs, in classes by their number of tokens: more than 16 ("heavy"), 9-16, 5-8, 1-4.
+constexpr int kClasses = 4;
+__device__ __forceinline__ int few_class(int n) { return n > 16 ? 0 : n > 8 ? 1 : n > 4 ? 2 : 3; }
 
 // The routing of all T tokens in a workgroup's LDS, pairs sorted by (local expert, token).
 struct FewRoute {
   unsigned long long* mask;   // [El] tokens that chose the expert
+  int4* ent;                  // [El] active experts by class: expert, first pair, pairs
+  int* cls;                   // [kClasses + 1] first entry of each class
   int* off;                   // [El + 1] first pair of each expert
-  int* act;                   // [El] experts with pairs, ascending; nact of them
-  int* nact;                  // [1]
   int* el;                    // [T k] local expert of pair t k + j, -1: not local
   float* wt;                  // [T k] its weight
   int* stok;                  // [T k] token of sorted pair p
   float* swt;                 // [T k] its weight
   static __host__ __device__ size_t bytes(int El, int n) {
-    return (size_t)El * 8 + (size_t)(El + 1) * 4 + (size_t)El * 4 + 4 + (size_t)n * 16;
+    return (size_t)El * 24 + (kClasses + 1) * 4 + (size_t)(El + 1) * 4 + (size_t)n * 16 + 16;
   }
   __device__ __forceinline__ FewRoute(char* s, int El, int n) {
-    mask = reinterpret_cast<unsigned long long*>(s);
-    off = reinterpret_cast<int*>(mask + El);
-    act = off + El + 1;
-    nact = act + El;
-    el = nact + 1;
+    ent = reinterpret_cast<int4*>(s);
+    mask = reinterpret_cast<unsigned long long*>(ent + El);
+    cls = reinterpret_cast<int*>(mask + El);
+    off = cls + kClasses + 1;
+    el = off + El + 1;
     wt = reinterpret_cast<float*>(el + n);
     stok = reinterpret_cast<int*>(wt + n);
     swt = reinterpret_cast<float*>(stok + n);
   }
 };
 
+// the k chosen experts of token t and their weights, by one wave: lane j < k returns slot j's
+__device__ __forceinline__ void choose(const FewParams& p, int t, int lane, int& e, float& wt) {
+  const float* row = p.logits + (size_t)t * p.E;
+  float v = 0.f;
+  e = 0;
+  if (p.E <= 64) wave_topk<1>(row, p.E, p.k, lane, e, v);
+  else if (p.E <= 128) wave_topk<2>(row, p.E, p.k, lane, e, v);
+  else if (p.E <= 256) wave_topk<4>(row, p.E, p.k, lane, e, v);
+  else wave_topk<8>(row, p.E, p.k, lane, e, v);
+  const float top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 0));
+  const float z = lane < p.k ? expf(v - top) : 0.f;
+  float s = 0.f;   // summed in slot order
+  for (int j = 0; j < p.k; ++j) s += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), j));
+  wt = z / s;
+}
+
+// More than kRouteHere tokens: one wave a token, ahead of the kernels that use the choice (in every
+// workgroup of k_few_gateup, 64 tokens' choices took 20 us).
+constexpr int kRouteHere = 8;
+__global__ __launch_bounds__(64) void k_few_topk(FewParams p) {
+  int e;
+  float wt;
+  choose(p, blockIdx.x, threadIdx.x, e, wt);
+  if ((int)threadIdx.x < p.k) {
+    p.r_idx[blockIdx.x * p.k + threadIdx.x] = e;
+    p.r_wt[blockIdx.x * p.k + threadIdx.x] = wt;
+  }
+}
+
 template <int NW>
 __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = p.T * p.k;
   for (int e = tid; e < p.El; e += NW * 64) R.mask[e] = 0ull;
   __syncthreads();
-  for (int t = w; t < p.T; t += NW) {
-    const unsigned long long key = wave_topk(p.logits + (size_t)t * p.E, p.E, p.k, lane);
-    const float v = key_value(key);
-    const float top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 0));
-    const float z = lane < p.k ? expf(v - top) : 0.f;
-    float s = 0.f;   // summed in slot order
-    for (int j = 0; j < p.k; ++j) s += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), j));
-    if (lane < p.k) {
-      const int e = key_expert(key) - p.e0;
-      const bool here = e >= 0 && e < p.El;
-      R.el[t * p.k + lane] = here ? e : -1;
-      R.wt[t * p.k + lane] = z / s;
-      if (here) atomicOr(&R.mask[e], 1ull << t);
+  auto put = [&](int i, int e, float wt) {   // pair i = t k + j
+    const bool here = e >= 0 && e < p.El;
+    R.el[i] = here ? e : -1;
+    R.wt[i] = wt;
+    if (here) atomicOr(&R.mask[e], 1ull << (i / p.k));
+  };
+  if (p.T > kRouteHere) {
+    for (int i = tid; i < n; i += NW * 64) put(i, p.r_idx[i] - p.e0, p.r_wt[i]);
+  } else {
+    for (int t = w; t < p.T; t += NW) {
+      int e;
+      float wt;
+      choose(p, t, lane, e, wt);
+      if (lane < p.k) put(t * p.k + lane, e - p.e0, wt);
     }
   }
   __syncthreads();
-  if (w == 0) {   // lane's experts: a contiguous run
+  if (w == 0) {   // lane's experts: a contiguous run; counts of pairs, and of experts by class (16 bits each)
     const int per = (p.El + 63) >> 6, e0 = lane * per;
-    int c = 0, a = 0;
+    int c = 0;
+    unsigned long long a = 0ull;
     for (int i = 0; i < per; ++i) {
       const int m = e0 + i < p.El ? __popcll(R.mask[e0 + i]) : 0;
       c += m;
-      a += m > 0;
+      if (m > 0) a += 1ull << (16 * few_class(m));
     }
-    int ic = c, ia = a;
+    int ic = c;
+    unsigned long long ia = a;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int nc = __shfl_up(ic, d), na = __shfl_up(ia, d);
+      const int nc = __shfl_up(ic, d);
+      const unsigned long long na = __shfl_up(ia, d);
       if (lane >= d) {
         ic += nc;
         ia += na;
       }
     }
-    int o = ic - c, q = ia - a;
+    const unsigned long long all = __shfl(ia, 63);
+    unsigned long long at = ia - a;   // class q's next entry, 16 bits each
+#pragma unroll
+    for (int q = 0; q < kClasses; ++q)
+#pragma unroll
+      for (int r = 0; r < q; ++r) at += ((all >> (16 * r)) & 0xffff) << (16 * q);
+    int o = ic - c;
     for (int i = 0; i < per; ++i) {
       const int e = e0 + i;
       if (e >= p.El) break;
       const int m = __popcll(R.mask[e]);
       R.off[e] = o;
-      if (m > 0) R.act[q++] = e;
+      if (m > 0) {
+        const int q = 16 * few_class(m);
+        R.ent[(at >> q) & 0xffff] = make_int4(e, o, m, 0);
+        at += 1ull << q;
+      }
       o += m;
     }
-    if (lane == 63) {
-      R.off[p.El] = ic;
-      *R.nact = ia;
+    if (lane == 63) R.off[p.El] = ic;
+    if (lane == 0) {
+      int first = 0;
+#pragma unroll
+      for (int q = 0; q < kClasses; ++q) {
+        R.cls[q] = first;
+        first += (int)((all >> (16 * q)) & 0xffff);
+      }
+      R.cls[kClasses] = first;
     }
   }
   __syncthreads();
@@ -175,19 +276,190 @@ __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p)
   __syncthreads();
 }
 
+__device__ __forceinline__ int4 uniform4(const int4& v) {
+  return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                   __builtin_amdgcn_readfirstlane(v.z), 0);
+}
+
 // ------------------------------------------------------------------------------------------------
-// weight rows times tokens: NM weight matrices, NG groups of 16 columns, steps [s0, s1) of 64 bytes.
-// U steps' loads are issued before their MFMAs (the last step's again where the run ends inside them).
-template <class T, int NM, int NG, int U>
-__device__ __forceinline__ void dot_rows(const char* const (&pw)[NM], const char* const (&px)[NG], int s0, int s1,
-                                         typename Mma<T>::Acc (&acc)[NM][NG]) {
-  for (int s = s0; s < s1; s += U) {
-    uint4 a[NM][U], b[NG][U];
+// NQ times 4 weight rows times NS sets of 4 tokens, segments [s0, s1) of 256 bytes. Each lane's pointers
+// are at its own 16-byte piece of the rows. Two buffers of U segments: the next one's loads are issued
+// before the MFMAs of the current (past the run's end, the last segment again). 8-bit rows may end inside a
+// segment: its missing pieces (from byte `rowb` on) count as zero.
+template <class T, int NQ, int NS, int U>
+__device__ __forceinline__ void dot4(const char* const (&pw)[NQ], const char* const (&px)[NS], int s0, int s1, int rowb,
+                                     typename Mma4<T>::Acc (&acc)[NQ][NS]) {
+  const int piece = 16 * ((threadIdx.x & 63) >> 2);
+  struct Buf {
+    uint4 a[NQ][U], b[NS][U];
+  };
+  auto load = [&](Buf& v, int s) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const size_t o = (size_t)min(s + i, s1 - 1) * kStep;
+      const int o = min(s + i, s1 - 1) * kSeg;
+      const bool in = sizeof(T) > 1 || o + piece < rowb;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) a[m][i] = ld16(pw[m] + o);
+      for (int q = 0; q < NQ; ++q) v.a[q][i] = in ? ld16_nt(pw[q] + o) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < NS; ++t) v.b[t][i] = in ? ld16(px[t] + o) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto mul = [&](const Buf& v, int s) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (s + i < s1)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int t = 0; t < NS; ++t) Mma4<T>::go(acc[q][t], v.a[q][i], v.b[t][i]);
+  };
+  if (s0 >= s1) return;
+  Buf u, v;
+  load(u, s0);
+  for (int s = s0; s < s1; s += 2 * U) {
+    if (s + U < s1) load(v, s + U);
+    mul(u, s);
+    if (s + 2 * U < s1) load(u, s + 2 * U);
+    if (s + U < s1) mul(v, s + U);
+  }
+}
+
+template <class A, int NQ, int NS>
+__device__ __forceinline__ void clear(A (&acc)[NQ][NS]) {
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int t = 0; t < NS; ++t) acc[q][t] = A{0, 0, 0, 0};
+}
+
+__device__ __forceinline__ float4 ld4f(const float* p) { return make_float4(p[0], p[1], p[2], p[3]); }
+
+// h of rows f0 .. f0+3 and pair pos (of token t, weight wt) from the products' sums; 8-bit weights: times
+// the scales of the token's row and of the 4 gate and up rows
+template <class T>
+__device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, float wt, int f0,
+                                        const typename Mma4<T>::Acc& sa, const typename Mma4<T>::Acc& sb, const float4& sg,
+                                        const float4& su) {
+  const float g[4] = {sg.x, sg.y, sg.z, sg.w}, u[4] = {su.x, su.y, su.z, su.w};
+  const float xs = sizeof(T) == 1 ? p.xs[t] : 1.f;
+  float h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = (float)sa[i], b = (float)sb[i];
+    if constexpr (sizeof(T) == 1) {
+      a *= xs * g[i];
+      b *= xs * u[i];
+    }
+    h[i] = wt * (a / (1.0f + expf(-a)) * b);
+  }
+  const size_t at = (size_t)pos * p.F + f0;
+  if constexpr (sizeof(T) == 2) {
+    float lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = h[i] - (float)(bf16)h[i];
+    eng::st8(static_cast<bf16*>(p.h) + at, eng::pack4(h[0], h[1], h[2], h[3]));
+    eng::st8(static_cast<bf16*>(p.hlo) + at, eng::pack4(lo[0], lo[1], lo[2], lo[3]));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.h) + at) = make_float4(h[0], h[1], h[2], h[3]);
+  }
+  if (sizeof(T) == 1 && p.hmax)   // 4 rows' largest: k_few_down takes the pair's (one atomic maximum a pair
+                                  // from every unit, on the same few cache lines, took 15 us for one token)
+    p.hmax[(size_t)pos * (p.F / 4) + f0 / 4] =
+        max(max(mag_bits(h[0]), mag_bits(h[1])), max(mag_bits(h[2]), mag_bits(h[3])));
+}
+
+// LDS of gateup_heavy's and gateup_unit's partial sums; only more than 16 tokens can make an expert heavy
+__host__ __device__ inline int few_red_bytes(int T) { return T > 16 ? kGW * 2 * 64 * 16 : kGW * 32 * 16; }
+
+// One unit of the gate/up products by a wave: rows f0 .. f0+3 of expert e, pairs base .. base+cnt-1
+// (cnt <= 4 NS). PART: only part kp of ks of H, whose sums go to red [16][2] of the wave instead.
+template <class T, int NS, bool PART>
+__device__ __forceinline__ void gateup_unit(const FewParams& p, const FewRoute& R, typename Mma4<T>::Acc* red, int e,
+                                            int base, int cnt, int f0, int ks, int kp) {
+  typedef typename Mma4<T>::Acc Acc;
+  constexpr int ES = sizeof(T);
+  const int lane = threadIdx.x & 63, j = lane & 3, piece = 16 * (lane >> 2);
+  const size_t rowb = (size_t)p.H * ES, wo = ((size_t)e * p.F + f0 + j) * rowb + piece;
+  const char* pw[2] = {static_cast<const char*>(p.wg) + wo, static_cast<const char*>(p.wu) + wo};
+  const char* px[NS];
+#pragma unroll
+  for (int t = 0; t < NS; ++t)
+    px[t] = static_cast<const char*>(p.x) + R.stok[base + min(4 * t + j, cnt - 1)] * rowb + piece;
+  float4 sg = {}, su = {};
+  if constexpr (ES == 1 && !PART) {   // asked for before the products, used after them
+    sg = ld4f(p.sg + (size_t)e * p.F + f0);
+    su = ld4f(p.su + (size_t)e * p.F + f0);
+  }
+  Acc acc[2][NS];
+  clear(acc);
+  const int S = (int)(rowb / kSeg), s0 = PART ? kp * S / ks : 0, s1 = PART ? (kp + 1) * S / ks : S;
+  dot4<T, 2, NS, NS == 1 ? (ES == 1 ? 2 : 4) : NS == 2 ? 2 : 1>(pw, px, s0, s1, (int)rowb, acc);
+#pragma unroll
+  for (int t = 0; t < NS; ++t) {
+    Acc a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = block_sum(acc[0][t][i]);
+      b[i] = block_sum(acc[1][t][i]);
+    }
+    if constexpr (PART) {
+      if (lane < 4) {
+        red[2 * (4 * t + j)] = a;
+        red[2 * (4 * t + j) + 1] = b;
+      }
+    } else if (lane < 4 && 4 * t + j < cnt) {
+      const int pos = base + 4 * t + j;
+      store_h<T>(p, pos, R.stok[pos], R.swt[pos], f0, a, b, sg, su);
+    }
+  }
+}
+
+// the parts' sums of a unit, added in order, and its h; red: the first part's wave's
+template <class T>
+__device__ __forceinline__ void gateup_join(const FewParams& p, const FewRoute& R, const typename Mma4<T>::Acc* red, int e,
+                                            int base, int cnt, int f0, int ks) {
+  const int lane = threadIdx.x & 63;
+  if (lane < cnt) {
+    float4 sg = {}, su = {};
+    if constexpr (sizeof(T) == 1) {
+      sg = ld4f(p.sg + (size_t)e * p.F + f0);
+      su = ld4f(p.su + (size_t)e * p.F + f0);
+    }
+    typename Mma4<T>::Acc a = red[2 * lane], b = red[2 * lane + 1];
+    for (int k = 1; k < ks; ++k) {
+      a += red[32 * k + 2 * lane];
+      b += red[32 * k + 2 * lane + 1];
+    }
+    const int pos = base + lane;
+    store_h<T>(p, pos, R.stok[pos], R.swt[pos], f0, a, b, sg, su);
+  }
+}
+
+// rows f0 .. f0+15 of a heavy expert by the whole workgroup, on 16 x 16 tiles with the weights read once for
+// all its tokens (up to 16 NG): the waves split H, red: [kGW][2][64] accumulators
+template <class T, int NG>
+__device__ __forceinline__ void gateup_heavy(const FewParams& p, const FewRoute& R, char* red_, int e, int base, int cnt,
+                                             int f0) {
+  typedef typename Mma4<T>::Acc Acc;
+  constexpr int ES = sizeof(T);
+  const int lane = threadIdx.x & 63, w = eng::wave_id();
+  const size_t rowb = (size_t)p.H * ES, wo = ((size_t)e * p.F + f0 + (lane & 15)) * rowb + 16 * (lane >> 4);
+  const char *pg = static_cast<const char*>(p.wg) + wo, *pu = static_cast<const char*>(p.wu) + wo;
+  const char* px[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+    px[g] = static_cast<const char*>(p.x) + R.stok[base + min(16 * g + (lane & 15), cnt - 1)] * rowb + 16 * (lane >> 4);
+  const int S = (int)(rowb / kStep), s0 = w * S / kGW, s1 = (w + 1) * S / kGW;
+  Acc acc[2][NG];
+  clear(acc);
+  constexpr int U = NG == 4 ? 2 : 4;
+  for (int s = s0; s < s1; s += U) {
+    uint4 a[2][U], b[NG][U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int o = min(s + i, s1 - 1) * kStep;
+      a[0][i] = ld16(pg + o);
+      a[1][i] = ld16(pu + o);
 #pragma unroll
       for (int g = 0; g < NG; ++g) b[g][i] = ld16(px[g] + o);
     }
@@ -195,38 +467,11 @@ __device__ __forceinline__ void dot_rows(const char* const (&pw)[NM], const char
     for (int i = 0; i < U; ++i)
       if (s + i < s1)
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) Mma<T>::go(acc[m][g], a[m][i], b[g][i]);
+        for (int g = 0; g < NG; ++g) {
+          mma16x16(acc[0][g], a[0][i], b[g][i], T());
+          mma16x16(acc[1][g], a[1][i], b[g][i], T());
+        }
   }
-}
-
-template <class A, int NM, int NG>
-__device__ __forceinline__ void clear(A (&acc)[NM][NG]) {
-#pragma unroll
-  for (int m = 0; m < NM; ++m)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[m][g] = A{0, 0, 0, 0};
-}
-
-// one (expert e, rows f0 .. f0+15) task of the gate/up products; red: [kGW][2][64] accumulators
-template <class T, int NG>
-__device__ __forceinline__ void gateup_task(const FewParams& p, const FewRoute& R, char* red_, int e, int f0) {
-  typedef typename Mma<T>::Acc Acc;
-  constexpr int ES = sizeof(T);
-  const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id();
-  const int base = R.off[e], cnt = R.off[e + 1] - base;
-  const size_t rowb = (size_t)p.H * ES;
-  const size_t wo = ((size_t)e * p.F + f0 + (lane & 15)) * rowb + 16 * (lane >> 4);
-  const char* pw[2] = {static_cast<const char*>(p.wg) + wo, static_cast<const char*>(p.wu) + wo};
-  const char* px[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-    px[g] = static_cast<const char*>(p.x) + R.stok[base + min(16 * g + (lane & 15), cnt - 1)] * rowb + 16 * (lane >> 4);
-  const int S = (int)(rowb / kStep);
-  Acc acc[2][NG];
-  clear(acc);
-  dot_rows<T, 2, NG, NG == 4 ? 2 : 4>(pw, px, w * S / kGW, (w + 1) * S / kGW, acc);
   Acc* red = reinterpret_cast<Acc*>(red_);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
@@ -234,42 +479,22 @@ __device__ __forceinline__ void gateup_task(const FewParams& p, const FewRoute& 
     red[(2 * w) * 64 + lane] = acc[0][g];
     red[(2 * w + 1) * 64 + lane] = acc[1][g];
     __syncthreads();
-    // thread i of the first 256: row f0 + i % 16 of column i / 16
-    if (tid < 256) {
-      const int f = tid & 15, c = 16 * g + (tid >> 4), src = (f >> 2) * 16 + (tid >> 4);
-      if (c < cnt) {
-        typedef typename Mma<T>::Sum Sum;
-        const Sum* rs = reinterpret_cast<const Sum*>(red) + src * 4 + (f & 3);
-        Sum sa = rs[0], sb = rs[256];
+    if (w == 0) {   // lane: rows f0 + 4 (lane / 16) .. + 3 of column lane % 16
+      const int c = 16 * g + (lane & 15), f = f0 + 4 * (lane >> 4);
+      Acc sa = red[lane], sb = red[64 + lane];
 #pragma unroll
-        for (int v = 1; v < kGW; ++v) {
-          sa += rs[2 * v * 256];
-          sb += rs[(2 * v + 1) * 256];
-        }
+      for (int v = 1; v < kGW; ++v) {
+        sa += red[2 * v * 64 + lane];
+        sb += red[(2 * v + 1) * 64 + lane];
+      }
+      if (c < cnt) {
         const int pos = base + c;
-        float a = (float)sa, b = (float)sb;
+        float4 sg = {}, su = {};
         if constexpr (ES == 1) {
-          const float xs = p.xs[R.stok[pos]];
-          a *= xs * p.sg[(size_t)e * p.F + f0 + f];
-          b *= xs * p.su[(size_t)e * p.F + f0 + f];
+          sg = ld4f(p.sg + (size_t)e * p.F + f);
+          su = ld4f(p.su + (size_t)e * p.F + f);
         }
-        const float h = R.swt[pos] * (a / (1.0f + expf(-a)) * b);
-        const size_t at = (size_t)pos * p.F + f0 + f;
-        if constexpr (ES == 2) {
-          const bf16 hi = (bf16)h;
-          static_cast<bf16*>(p.h)[at] = hi;
-          static_cast<bf16*>(p.hlo)[at] = (bf16)(h - (float)hi);
-        } else {
-          static_cast<float*>(p.h)[at] = h;
-        }
-        if constexpr (ES == 1) {
-          unsigned m = mag_bits(h);   // over the column's 16 rows: one 16-lane row
-          m = max(m, dpp_mov<kDppXor1>(m));
-          m = max(m, dpp_mov<kDppXor2>(m));
-          m = max(m, dpp_mov<kDppHalfMirror>(m));
-          m = max(m, dpp_mov<kDppMirror>(m));
-          if (f == 0) atomicMax(p.hmax + pos, m);   // a maximum: any order gives the same bits
-        }
+        store_h<T>(p, pos, R.stok[pos], R.swt[pos], f, sa, sb, sg, su);
       }
     }
     __syncthreads();
@@ -280,217 +505,372 @@ template <class T>
 __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, n = p.T * p.k;
-  char* red = smem;
-  const FewRoute R(smem + kGW * 2 * 64 * 16, p.El, n);
+  const FewRoute R(smem + few_red_bytes(p.T), p.El, n);
   few_route<kGW>(R, p);
-  const int nact = *R.nact;
+  const int nact = R.cls[kClasses], heavy = R.cls[1];
   if (blockIdx.x == 0) {   // the routing for k_few_down
-    for (int i = tid; i <= p.El; i += kGW * 64) p.r_off[i] = R.off[i];
-    for (int i = tid; i < nact; i += kGW * 64) p.r_act[i] = R.act[i];
-    for (int i = tid; i < R.off[p.El]; i += kGW * 64) p.r_tok[i] = R.stok[i];
-    if (tid == 0) *p.r_nact = nact;
+    if (tid <= kClasses) p.r_cls[tid] = R.cls[tid];
+    if (tid == 0) p.r_cls[kClasses + 1] = R.off[p.El];
+    for (int i = tid; i < nact; i += kGW * 64) p.r_ent[i] = R.ent[i];
+    for (int i = tid; i < n; i += kGW * 64) p.r_tok[i] = i < R.off[p.El] ? R.stok[i] : 0;
   }
-  const int nf = p.F / 16, ntask = nact * nf;
+  const int nh = p.F / 16, ntask = heavy * nh;
   for (int task = blockIdx.x; task < ntask; task += gridDim.x) {
-    const int a = task / nf, e = __builtin_amdgcn_readfirstlane(R.act[a]), f0 = (task - a * nf) * 16;
-    const int cnt = __builtin_amdgcn_readfirstlane(R.off[e + 1] - R.off[e]);
-    if (cnt <= 16) gateup_task<T, 1>(p, R, red, e, f0);
-    else if (cnt <= 32) gateup_task<T, 2>(p, R, red, e, f0);
-    else gateup_task<T, 4>(p, R, red, e, f0);
+    const int a = task / nh, f0 = (task - a * nh) * 16;
+    const int4 x = uniform4(R.ent[a]);
+    if (x.z <= 32) gateup_heavy<T, 2>(p, R, smem, x.x, x.y, x.z, f0);
+    else gateup_heavy<T, 4>(p, R, smem, x.x, x.y, x.z, f0);
+  }
+  // Consecutive units go to different workgroups: a few units still spread over all CUs. Where the waves
+  // outnumber the units, two or four share a unit, so that more of its loads are in flight at once.
+  typedef typename Mma4<T>::Acc Acc;
+  const int nf = p.F / 4, units = (nact - heavy) * nf, w = eng::wave_id(), waves = kGW * gridDim.x;
+  const int ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
+  if (ks == 1) {
+    for (int u = w * gridDim.x + blockIdx.x; u < units; u += waves) {
+      const int a = u / nf, f0 = (u - a * nf) * 4;
+      const int4 x = uniform4(R.ent[heavy + a]);
+      if (x.z <= 4) gateup_unit<T, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+      else if (x.z <= 8) gateup_unit<T, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+      else gateup_unit<T, kSets, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    }
+  } else {   // one round; a heavy task's last barrier is behind its reads of smem
+    const int kp = w & (ks - 1), u = (w / ks) * gridDim.x + blockIdx.x, a = u / nf, f0 = (u - a * nf) * 4;
+    Acc* red = reinterpret_cast<Acc*>(smem) + 32 * w;   // [16 tokens][gate, up]
+    int4 x = make_int4(0, 0, 0, 0);
+    if (u < units) {
+      x = uniform4(R.ent[heavy + a]);
+      if (x.z <= 4) gateup_unit<T, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else if (x.z <= 8) gateup_unit<T, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else gateup_unit<T, kSets, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+    }
+    __syncthreads();
+    if (u < units && kp == 0) gateup_join<T>(p, R, red, x.x, x.y, x.z, f0, ks);
   }
 }
 
 // ------------------------------------------------------------------------------------------------
-// rows h0 .. h0+15 of W_down[e] times the h of pairs base .. base+cnt-1 (cnt <= 16 NG), steps [s0, s1) of 64 bytes of weight row, added to
-// the wave's sums ya [T][16]
-template <class T, int NG>
-__device__ __forceinline__ void down_part(const FewParams& p, const int* stok, float* ya, int e, int base, int cnt,
-                                          int h0, int s0, int s1) {
-  typedef typename Mma<T>::Acc Acc;
-  constexpr int ES = sizeof(T);
-  const int lane = threadIdx.x & 63;
+// Rows h0 .. h0 + 4 NQ - 1 of W_down for the experts ent[0 .. na) of one class (up to 4 NS pairs each),
+// segments [c, end) of their (expert, 256-byte segment) axis, S segments an expert; added to the wave's
+// sums ya [T][4 NQ]. The stages of U segments run through expert boundaries: the next stage's loads, of
+// weights and h, are in flight while the current one is multiplied (DB; without it the registers of the
+// second stage would spill).
+// FLY (8-bit weights, T <= 4): h is fp32 and quantised here, with the pairs' maxima hm.
+template <class T, int NQ, int NS, int U, bool DB, bool FLY>
+__device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent, const int* stok, const unsigned* hm,
+                                            float* ya, int h0, int S, int c, int end) {
+  typedef typename Mma4<T>::Acc Acc;
+  constexpr int ES = sizeof(T), NB = FLY ? 4 : ES == 2 ? 2 : 1;   // 16-byte pieces of h a lane loads
+  static_assert(!FLY || (NS == 1 && ES == 1 && U == 1), "quantising on the fly");
+  const int lane = threadIdx.x & 63, j = lane & 3, blk = lane >> 2, piece = 16 * blk;
+  const int q4 = min(blk, NQ - 1);   // lane (blk, j) adds rows 4 q4 .. 4 q4 + 3 of token j
   const size_t rowb = (size_t)p.F * ES;
-  const char* pw = static_cast<const char*>(p.wd) + ((size_t)e * p.H + h0 + (lane & 15)) * rowb + 16 * (lane >> 4);
-  Acc acc[1][NG];
+  if (c >= end) return;
+  struct Stage {
+    uint4 a[NQ][U], b[NS][U][NB];
+    int4 x;       // its expert
+    int n;        // segments in it
+    bool last;    // the wave's last of this expert
+  };
+  int a = c / S, s = c - a * S;
+  auto load = [&](Stage& v) {   // the stage at (a, s), and on to the next
+    v.x = uniform4(ent[a]);
+    v.n = min(min(U, S - s), end - c);
+    const char* pw = static_cast<const char*>(p.wd) + ((size_t)v.x.x * p.H + h0 + j) * rowb + piece;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int o = min(s + i, s + v.n - 1) * kSeg;
+      const bool in = ES > 1 || o + piece < (int)rowb;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) v.a[q][i] = in ? ld16_nt(pw + (size_t)(4 * q) * rowb + o) : zero;
+#pragma unroll
+      for (int t = 0; t < NS; ++t) {
+        const size_t pos = v.x.y + min(4 * t + j, v.x.z - 1);
+        if constexpr (FLY) {
+          const float* ph = static_cast<const float*>(p.h) + pos * p.F + (in ? o + piece : 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v.b[t][i][r] = ld16(ph + 4 * r);
+        } else if constexpr (ES == 1) {
+          v.b[t][i][0] = in ? ld16(p.hq + pos * rowb + o + piece) : zero;
+        } else {
+          v.b[t][i][0] = ld16(static_cast<const char*>(p.h) + pos * rowb + o + piece);
+          if constexpr (ES == 2) v.b[t][i][1] = ld16(static_cast<const char*>(p.hlo) + pos * rowb + o + piece);
+        }
+      }
+    }
+    s += v.n;
+    c += v.n;
+    v.last = s == S || c == end;
+    if (s == S) {
+      s = 0;
+      ++a;
+    }
+  };
+  Acc acc[NQ][NS];
   clear(acc);
-  float hs[NG];
-  if constexpr (ES == 1) {
-    static_assert(NG == 1, "a lane quantises one column's h");
-    const int pos = base + min(lane & 15, cnt - 1);
-    const Q8Row qr(p.hmax[pos]);
-    hs[0] = qr.scale;
-    const float* ph = static_cast<const float*>(p.h) + (size_t)pos * p.F + 16 * (lane >> 4);
-    constexpr int U = 2;
-    for (int s = s0; s < s1; s += U) {
-      uint4 a[U];
-      float b[U][16];
+  auto use = [&](const Stage& v) {
+    const int base = v.x.y, cnt = v.x.z;
+    Q8Row qr;
+    if constexpr (FLY) qr = Q8Row(hm[base + min(j, cnt - 1)]);
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int si = min(s + i, s1 - 1);
-        a[i] = ld16(pw + (size_t)si * kStep);
+    for (int i = 0; i < U; ++i)
+      if (i < v.n)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float4 f = *reinterpret_cast<const float4*>(ph + si * 64 + 4 * v);
-          b[i][4 * v] = f.x; b[i][4 * v + 1] = f.y; b[i][4 * v + 2] = f.z; b[i][4 * v + 3] = f.w;
-        }
-      }
+        for (int t = 0; t < NS; ++t) {
+          uint4 b = v.b[t][i][0];
+          if constexpr (FLY) {
+            float f[16];
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (s + i < s1) {
-          unsigned q[4];
-          q8_pack<true>(b[i], qr, q);
-          Mma<T>::go(acc[0][0], a[i], make_uint4(q[0], q[1], q[2], q[3]));
-        }
-    }
-  } else {
-    const char *ph[NG], *pl[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const size_t o = (size_t)(base + min(16 * g + (lane & 15), cnt - 1)) * rowb + 16 * (lane >> 4);
-      ph[g] = static_cast<const char*>(p.h) + o;
-      pl[g] = ES == 2 ? static_cast<const char*>(p.hlo) + o : nullptr;
-    }
-    constexpr int U = NG == 4 ? 2 : 4;
-    for (int s = s0; s < s1; s += U) {
-      uint4 a[U], b[U][NG], c[U][NG];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const size_t o = (size_t)min(s + i, s1 - 1) * kStep;
-        a[i] = ld16(pw + o);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          b[i][g] = ld16(ph[g] + o);
-          if constexpr (ES == 2) c[i][g] = ld16(pl[g] + o);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (s + i < s1)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            Mma<T>::go(acc[0][g], a[i], b[i][g]);
-            if constexpr (ES == 2) Mma<T>::go(acc[0][g], a[i], c[i][g]);
+            for (int r = 0; r < 4; ++r) {
+              f[4 * r] = __uint_as_float(v.b[t][i][r].x);
+              f[4 * r + 1] = __uint_as_float(v.b[t][i][r].y);
+              f[4 * r + 2] = __uint_as_float(v.b[t][i][r].z);
+              f[4 * r + 3] = __uint_as_float(v.b[t][i][r].w);
+            }
+            unsigned o[4];
+            q8_pack<true>(f, qr, o);
+            b = make_uint4(o[0], o[1], o[2], o[3]);
           }
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            Mma4<T>::go(acc[q][t], v.a[q][i], b);
+            if constexpr (ES == 2) Mma4<T>::go(acc[q][t], v.a[q][i], v.b[t][i][NB - 1]);
+          }
+        }
+    if (!v.last) return;
+    float4 sd = make_float4(1.f, 1.f, 1.f, 1.f);
+    if constexpr (ES == 1) sd = ld4f(p.sd + (size_t)v.x.x * p.H + h0 + 4 * q4);
+#pragma unroll
+    for (int t = 0; t < NS; ++t) {
+      float r[4] = {};
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float sum = (float)block_sum(acc[q][t][i]);
+          r[i] = q == q4 ? sum : r[i];
+        }
+      if (blk < NQ && 4 * t + j < cnt) {
+        if constexpr (ES == 1) {
+          const float hs = FLY ? qr.scale : p.hs[base + 4 * t + j];
+          r[0] *= hs * sd.x;
+          r[1] *= hs * sd.y;
+          r[2] *= hs * sd.z;
+          r[3] *= hs * sd.w;
+        }
+        float4* y = reinterpret_cast<float4*>(ya + (stok[base + 4 * t + j] * NQ + blk) * 4);
+        const float4 o = *y;
+        *y = make_float4(o.x + r[0], o.y + r[1], o.z + r[2], o.w + r[3]);
+      }
     }
+    clear(acc);
+  };
+  Stage u;
+  if constexpr (!DB) {
+    while (c < end) {
+      load(u);
+      use(u);
+    }
+    return;
   }
-  float4 sd = make_float4(1.f, 1.f, 1.f, 1.f);
-  if constexpr (ES == 1) {
-    const float* q = p.sd + (size_t)e * p.H + h0 + 4 * (lane >> 4);
-    sd = make_float4(q[0], q[1], q[2], q[3]);
+  Stage v;
+  load(u);
+  for (;;) {
+    const bool more = c < end;
+    if (more) load(v);
+    use(u);
+    if (!more) break;
+    const bool more2 = c < end;
+    if (more2) load(u);
+    use(v);
+    if (!more2) break;
   }
+}
+
+// the same for a pair run of up to 16 NG on 16 x 16 tiles (rows from 4 NQ on repeat and are dropped), so
+// that a heavy expert's weights are read once; steps [s0, s1) of 64 bytes
+template <class T, int NQ, int NG>
+__device__ __forceinline__ void down_heavy(const FewParams& p, const int* stok, float* ya, int e, int base, int cnt,
+                                           int h0, int s0, int s1) {
+  typedef typename Mma4<T>::Acc Acc;
+  constexpr int ES = sizeof(T), NR = 4 * NQ;
+  const int lane = threadIdx.x & 63, piece = 16 * (lane >> 4);
+  const size_t rowb = (size_t)p.F * ES;
+  const char* pw = static_cast<const char*>(p.wd) + ((size_t)e * p.H + h0 + (lane & (NR - 1))) * rowb + piece;
+  const char *ph[NG], *pl[NG];
+  float hs[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const int c = 16 * g + (lane & 15);
-    if (c < cnt) {
-      float4* y = reinterpret_cast<float4*>(ya + stok[base + c] * 16 + 4 * (lane >> 4));
-      float4 v = *y;
-      if constexpr (ES == 1) {
-        v.x += (float)acc[0][g][0] * (hs[g] * sd.x);
-        v.y += (float)acc[0][g][1] * (hs[g] * sd.y);
-        v.z += (float)acc[0][g][2] * (hs[g] * sd.z);
-        v.w += (float)acc[0][g][3] * (hs[g] * sd.w);
-      } else {
-        v.x += acc[0][g][0];
-        v.y += acc[0][g][1];
-        v.z += acc[0][g][2];
-        v.w += acc[0][g][3];
+    const int pos = base + min(16 * g + (lane & 15), cnt - 1);
+    ph[g] = (ES == 1 ? reinterpret_cast<const char*>(p.hq) : static_cast<const char*>(p.h)) + (size_t)pos * rowb + piece;
+    pl[g] = ES == 2 ? static_cast<const char*>(p.hlo) + (size_t)pos * rowb + piece : nullptr;
+    hs[g] = ES == 1 ? p.hs[pos] : 1.f;
+  }
+  Acc acc[1][NG];
+  clear(acc);
+  constexpr int U = 2;
+  for (int s = s0; s < s1; s += U) {
+    uint4 a[U], b[NG][U], c[NG][U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int o = min(s + i, s1 - 1) * kStep;
+      a[i] = ld16(pw + o);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        b[g][i] = ld16(ph[g] + o);
+        if constexpr (ES == 2) c[g][i] = ld16(pl[g] + o);
       }
-      *y = v;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (s + i < s1)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          mma16x16(acc[0][g], a[i], b[g][i], T());
+          if constexpr (ES == 2) mma16x16(acc[0][g], a[i], c[g][i], T());
+        }
+  }
+  const int q4 = lane >> 4;   // rows 4 q4 .. + 3 of column lane % 16
+  if (q4 < NQ) {
+    float4 sd = make_float4(1.f, 1.f, 1.f, 1.f);
+    if constexpr (ES == 1) sd = ld4f(p.sd + (size_t)e * p.H + h0 + 4 * q4);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int c = 16 * g + (lane & 15);
+      if (c < cnt) {
+        float4* y = reinterpret_cast<float4*>(ya + (stok[base + c] * NQ + q4) * 4);
+        const float4 o = *y;
+        *y = make_float4(o.x + (float)acc[0][g][0] * (hs[g] * sd.x), o.y + (float)acc[0][g][1] * (hs[g] * sd.y),
+                         o.z + (float)acc[0][g][2] * (hs[g] * sd.z), o.w + (float)acc[0][g][3] * (hs[g] * sd.w));
+      }
     }
   }
 }
 
-template <class T>
+// FLY (8-bit weights, T <= 4): h is quantised where it is read, with the maxima the gate/up kernel left;
+// otherwise the quantiser has run between the two.
+template <class T, int NQ, bool FLY>
 __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int tid = threadIdx.x, w = eng::wave_id(), h0 = blockIdx.x * 16;
-  float* ya = reinterpret_cast<float*>(smem);   // [kDW][T][16]
-  int* off = reinterpret_cast<int*>(ya + kDW * p.T * 16);
-  int* act = off + p.El + 1;
-  int* stok = act + p.El;
-  const int nact = *p.r_nact;
-  for (int i = tid; i < kDW * p.T * 16; i += kDW * 64) ya[i] = 0.f;
-  for (int i = tid; i <= p.El; i += kDW * 64) off[i] = p.r_off[i];
-  for (int i = tid; i < nact; i += kDW * 64) act[i] = p.r_act[i];
-  __syncthreads();
-  for (int i = tid; i < off[p.El]; i += kDW * 64) stok[i] = p.r_tok[i];
-  __syncthreads();
-  constexpr int ES = sizeof(T);
-  const int S = p.F * ES / kStep, N = nact * S;
-  float* mine = ya + w * p.T * 16;
-  for (int c = (int)((int64_t)w * N / kDW), end = (int)((int64_t)(w + 1) * N / kDW); c < end;) {
-    const int a = c / S, s0 = c - a * S, s1 = min(S, s0 + end - c);
-    const int e = __builtin_amdgcn_readfirstlane(act[a]);
-    const int base = __builtin_amdgcn_readfirstlane(off[e]), cnt = __builtin_amdgcn_readfirstlane(off[e + 1]) - base;
-    if constexpr (ES == 1) {   // more than 16 tokens: the weight rows again, from the caches
-      for (int q = 0; q < cnt; q += 16) down_part<T, 1>(p, stok, mine, e, base + q, min(16, cnt - q), h0, s0, s1);
-    } else {
-      if (cnt <= 16) down_part<T, 1>(p, stok, mine, e, base, cnt, h0, s0, s1);
-      else if (cnt <= 32) down_part<T, 2>(p, stok, mine, e, base, cnt, h0, s0, s1);
-      else down_part<T, 4>(p, stok, mine, e, base, cnt, h0, s0, s1);
+  constexpr int NR = 4 * NQ, ES = sizeof(T);
+  const int tid = threadIdx.x, w = eng::wave_id(), h0 = blockIdx.x * NR, n = p.T * p.k;
+  float* ya = reinterpret_cast<float*>(smem);   // [kDW][T][NR]
+  int4* ent = reinterpret_cast<int4*>(ya + kDW * p.T * NR);
+  int* stok = reinterpret_cast<int*>(ent + min(n, p.El));
+  unsigned* hm = reinterpret_cast<unsigned*>(stok + n);
+  int cls[kClasses + 1];
+#pragma unroll
+  for (int q = 0; q <= kClasses; ++q) cls[q] = __builtin_amdgcn_readfirstlane(p.r_cls[q]);
+  for (int i = tid; i < kDW * p.T * NR; i += kDW * 64) ya[i] = 0.f;
+  for (int i = tid; i < min(n, p.El); i += kDW * 64) ent[i] = p.r_ent[i];   // entries past the last are not used
+  for (int i = tid; i < n; i += kDW * 64) stok[i] = p.r_tok[i];
+  if constexpr (FLY) {   // each pair's largest |h|, a wave a pair
+    const int lane = tid & 63, nf = p.F / 4;
+    for (int i = w; i < p.r_cls[kClasses + 1]; i += kDW) {
+      unsigned m = 0u;
+      for (int f = lane; f < nf; f += 64) m = max(m, p.hmax[(size_t)i * nf + f]);
+      m = wave_max_u32(m);
+      if (lane == 0) hm[i] = m;
     }
-    c += s1 - s0;
   }
   __syncthreads();
-  for (int i = tid; i < p.T * 16; i += kDW * 64) {
+  const int S = (p.F * ES + kSeg - 1) / kSeg;
+  float* mine = ya + w * p.T * NR;
+  // class by class, the waves sharing each class's (expert, segment) axis
+  auto part = [&](int q, int& c, int& end) {
+    const int64_t N = (int64_t)(cls[q + 1] - cls[q]) * S;
+    c = (int)(w * N / kDW);
+    end = (int)((w + 1) * N / kDW);
+  };
+  int c, end;
+  if constexpr (!FLY) {
+    part(0, c, end);
+    for (; c < end;) {
+      const int a = c / S, s0 = c - a * S, s1 = min(S, s0 + end - c);
+      // a 256-byte segment is four 64-byte steps; an 8-bit row may end in the middle of its last one
+      const int t0 = 4 * s0, t1 = min(4 * s1, p.F * ES / kStep);
+      const int4 x = uniform4(ent[a]);
+      if (x.z <= 32) down_heavy<T, NQ, 2>(p, stok, mine, x.x, x.y, x.z, h0, t0, t1);
+      else down_heavy<T, NQ, 4>(p, stok, mine, x.x, x.y, x.z, h0, t0, t1);
+      c += s1 - s0;
+    }
+    part(1, c, end);
+    if constexpr (NQ < 4) {
+      down_stream<T, NQ, 4, 1, ES == 1 || NQ == 1, false>(p, ent + cls[1], stok, hm, mine, h0, S, c, end);
+    } else {   // 16 rows by 16 tokens in 4 x 4 form would spill
+      for (; c < end;) {
+        const int a = c / S, s0 = c - a * S, s1 = min(S, s0 + end - c);
+        const int4 x = uniform4(ent[cls[1] + a]);
+        down_heavy<T, NQ, 1>(p, stok, mine, x.x, x.y, x.z, h0, 4 * s0, min(4 * s1, p.F * ES / kStep));
+        c += s1 - s0;
+      }
+    }
+    part(2, c, end);
+    down_stream<T, NQ, 2, 1, ES != 2 || NQ < 4, false>(p, ent + cls[2], stok, hm, mine, h0, S, c, end);
+  }
+  part(3, c, end);
+  down_stream<T, NQ, 1, FLY || NQ == 4 ? 1 : 2, !FLY, FLY>(p, ent + cls[3], stok, hm, mine, h0, S, c, end);
+  __syncthreads();
+  for (int i = tid; i < p.T * NR; i += kDW * 64) {
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < kDW; ++v) s += ya[v * p.T * 16 + i];
-    const size_t at = (size_t)(i >> 4) * p.H + h0 + (i & 15);
+    for (int v = 0; v < kDW; ++v) s += ya[v * p.T * NR + i];
+    const size_t at = (size_t)(i / NR) * p.H + h0 + i % NR;
     if constexpr (ES == 4) static_cast<float*>(p.y)[at] = s;
     else static_cast<bf16*>(p.y)[at] = (bf16)s;
   }
 }
 
 // ------------------------------------------------------------------------------------------------
-// router projection: experts 16 b .. 16 b + 15 for every token; red: [kDW][64] accumulators per group
-template <class T, int NG>
-__device__ __forceinline__ void router_tile(const FewParams& p, char* red_) {
-  const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), e0 = blockIdx.x * 16;
-  const size_t rowb = (size_t)p.H * sizeof(T);
-  const char* pw[1] = {static_cast<const char*>(p.wr) + min(e0 + (lane & 15), p.E - 1) * rowb + 16 * (lane >> 4)};
-  const char* px[NG];
+// router projection: experts e0 .. e0 + 3 for tokens t0 .. t0 + 4 NS - 1, the waves splitting H
+template <class T, int NS>
+__device__ __forceinline__ void router_tile(const FewParams& p, float* red, int e0, int t0) {
+  const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), j = lane & 3;
+  const size_t rowb = (size_t)p.H * sizeof(T), piece = 16 * (lane >> 2);
+  const char* pw[1] = {static_cast<const char*>(p.wr) + min(e0 + j, p.E - 1) * rowb + piece};
+  const char* px[NS];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
-    px[g] = static_cast<const char*>(p.x0) + min(16 * g + (lane & 15), p.T - 1) * rowb + 16 * (lane >> 4);
-  const int S = (int)(rowb / kStep);
-  f32x4 acc[1][NG];
+  for (int t = 0; t < NS; ++t)
+    px[t] = static_cast<const char*>(p.x0) + min(t0 + 4 * t + j, p.T - 1) * rowb + piece;
+  const int S = (int)(rowb / kSeg);
+  f32x4 acc[1][NS];
   clear(acc);
-  dot_rows<T, 1, NG, NG == 4 ? 2 : 4>(pw, px, w * S / kDW, (w + 1) * S / kDW, acc);
-  f32x4* red = reinterpret_cast<f32x4*>(red_);
+  dot4<T, 1, NS, NS == 4 ? 1 : 2>(pw, px, w * S / kPW, (w + 1) * S / kPW, (int)rowb, acc);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    red[w * 64 + lane] = acc[0][g];
-    __syncthreads();
-    if (tid < 256) {
-      const int f = tid & 15, t = 16 * g + (tid >> 4), src = (f >> 2) * 16 + (tid >> 4);
-      const float* rs = reinterpret_cast<const float*>(red) + src * 4 + (f & 3);
-      float s = 0.f;
+  for (int t = 0; t < NS; ++t)
 #pragma unroll
-      for (int v = 0; v < kDW; ++v) s += rs[v * 256];
-      if (t < p.T && e0 + f < p.E) p.logits[(size_t)t * p.E + e0 + f] = s;
+    for (int i = 0; i < 4; ++i) {
+      const float s = block_sum(acc[0][t][i]);
+      if (lane < 4) red[(w * NS * 4 + 4 * t + j) * 4 + i] = s;   // [wave][token][expert]
     }
-    __syncthreads();
+  __syncthreads();
+  if (tid < 16 * NS) {
+    const int t = t0 + tid / 4, e = e0 + tid % 4;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < kPW; ++v) s += red[v * NS * 16 + tid];
+    if (t < p.T && e < p.E) p.logits[(size_t)t * p.E + e] = s;
   }
 }
 
 template <class T>
-__global__ __launch_bounds__(kDW * 64, 4) void k_few_prep(FewParams p, int router_blocks) {
-  __shared__ __attribute__((aligned(16))) char smem[kDW * 64 * 16];
+__global__ __launch_bounds__(kPW * 64, 4) void k_few_prep(FewParams p, int router_blocks) {
+  __shared__ float smem[kPW * 16 * kSets];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   if ((int)blockIdx.x < router_blocks) {
-    if (p.T <= 16) router_tile<T, 1>(p, smem);
-    else if (p.T <= 32) router_tile<T, 2>(p, smem);
-    else router_tile<T, 4>(p, smem);
+    const int ne = (p.E + 3) / 4, e0 = 4 * (blockIdx.x % ne), t0 = 4 * kSets * (blockIdx.x / ne);
+    if (p.T - t0 <= 4) router_tile<T, 1>(p, smem, e0, t0);
+    else if (p.T - t0 <= 8) router_tile<T, 2>(p, smem, e0, t0);
+    else router_tile<T, kSets>(p, smem, e0, t0);
     return;
   }
-  if constexpr (sizeof(T) == 2) {   // with 8-bit weights: quantise row t of x, clear its pairs' maxima
+  if constexpr (sizeof(T) == 2) {   // with 8-bit weights: quantise row t of x
     const int t = blockIdx.x - router_blocks;
     unsigned* sm = reinterpret_cast<unsigned*>(smem);
-    for (int j = tid; j < p.k; j += kDW * 64) p.hmax[t * p.k + j] = 0u;
     const bf16* row = static_cast<const bf16*>(p.x0) + (size_t)t * p.H;
     unsigned m = 0u;
-    for (int c = tid; c < p.H / 8; c += kDW * 64) {
+    for (int c = tid; c < p.H / 8; c += kPW * 64) {
       float v[8];
       eng::unpack8(ld16(row + 8 * c), v);
 #pragma unroll
@@ -501,9 +881,9 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_prep(FewParams p, int route
     __syncthreads();
     m = 0u;
 #pragma unroll
-    for (int v = 0; v < kDW; ++v) m = max(m, sm[v]);
+    for (int v = 0; v < kPW; ++v) m = max(m, sm[v]);
     const Q8Row r(m);
-    for (int c = tid; c < p.H / 8; c += kDW * 64) {
+    for (int c = tid; c < p.H / 8; c += kPW * 64) {
       float v[8];
       unsigned q[2];
       eng::unpack8(ld16(row + 8 * c), v);
@@ -516,34 +896,50 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_prep(FewParams p, int route
 
 template <class T>
 hipError_t launch_prep(const FewParams& p, hipStream_t s, bool quant) {
-  const int nr = p.wr ? (p.E + 15) / 16 : 0;
+  const int nr = p.wr ? (p.E + 3) / 4 * ((p.T + 4 * kSets - 1) / (4 * kSets)) : 0;
   if (nr == 0 && !quant) return hipSuccess;
   prof_mark_begin("few_prep", s);
-  k_few_prep<T><<<nr + (quant ? p.T : 0), kDW * 64, 0, s>>>(p, nr);
+  k_few_prep<T><<<nr + (quant ? p.T : 0), kPW * 64, 0, s>>>(p, nr);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;
 }
 
-template <class T>
-hipError_t launch_layer(const FewParams& p, hipStream_t s) {
-  const int n = p.T * p.k, tasks = std::min(n, p.El) * (p.F / 16);
-  const int grid = std::min(tasks, persistent_grid(2));
-  const size_t lds_g = (size_t)kGW * 2 * 64 * 16 + FewRoute::bytes(p.El, n);
-  const size_t lds_d = (size_t)kDW * p.T * 64 + ((size_t)2 * p.El + 1 + n) * 4;
+template <class T, int NQ, bool FLY>
+hipError_t launch_down(const FewParams& p, hipStream_t s) {
+  const size_t n = (size_t)p.T * p.k, lds = kDW * p.T * 16 * NQ + std::min<size_t>(n, p.El) * 16 + n * (FLY ? 8 : 4);
   hipError_t err;
-  if (lds_d > 65536 && (err = hipFuncSetAttribute(reinterpret_cast<const void*>(k_few_down<T>),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds_d)) != hipSuccess)
+  if (lds > 65536 && (err = hipFuncSetAttribute(reinterpret_cast<const void*>(k_few_down<T, NQ, FLY>),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)
     return err;
-  prof_mark_begin("few_gateup", s);
-  k_few_gateup<T><<<grid, kGW * 64, lds_g, s>>>(p);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
-  prof_mark_end(s);
   prof_mark_begin("few_down", s);
-  k_few_down<T><<<p.H / 16, kDW * 64, lds_d, s>>>(p);
+  k_few_down<T, NQ, FLY><<<p.H / (4 * NQ), kDW * 64, lds, s>>>(p);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   prof_mark_end(s);
   return hipSuccess;
+}
+
+template <class T, bool FLY = false>
+hipError_t launch_layer(const FewParams& p, hipStream_t s) {
+  const int n = p.T * p.k, units = std::min(n, p.El) * (p.F / 4);
+  const int grid = std::min(units, persistent_grid(2));
+  hipError_t err;
+  if (p.T > kRouteHere) {
+    prof_mark_begin("few_topk", s);
+    k_few_topk<<<p.T, 64, 0, s>>>(p);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+  }
+  prof_mark_begin("few_gateup", s);
+  k_few_gateup<T><<<grid, kGW * 64, few_red_bytes(p.T) + FewRoute::bytes(p.El, n), s>>>(p);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
+  prof_mark_end(s);
+  if (sizeof(T) == 1 && !FLY &&
+      (err = launch_int8_quant(p.h, true, n, p.F, p.r_cls + kClasses + 1, p.hq, p.hs, "int8_quant_h", s)) != hipSuccess)
+    return err;
+  // as many rows per workgroup (each read of h serves them all) as leave every CU one
+  if (p.H >= 4096) return launch_down<T, 4, FLY>(p, s);
+  return p.H >= 2048 ? launch_down<T, 2, FLY>(p, s) : launch_down<T, 1, FLY>(p, s);
 }
 
 }  // namespace
@@ -552,7 +948,8 @@ hipError_t launch_few(const FewParams& p, int type, hipStream_t s) {
   hipError_t err;
   if (type == 4) return (err = launch_prep<float>(p, s, false)) != hipSuccess ? err : launch_layer<float>(p, s);
   if (type == 2) return (err = launch_prep<bf16>(p, s, false)) != hipSuccess ? err : launch_layer<bf16>(p, s);
-  return (err = launch_prep<bf16>(p, s, true)) != hipSuccess ? err : launch_layer<int8_t>(p, s);
+  if ((err = launch_prep<bf16>(p, s, true)) != hipSuccess) return err;
+  return p.hmax ? launch_layer<int8_t, true>(p, s) : launch_layer<int8_t>(p, s);
 }
 
 }  // namespace moe

@@ -954,7 +954,7 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
 
 namespace {
 struct FewLayout {
-  size_t nact, off, act, tok, h, hlo, xq, xs, hmax, total;
+  size_t cls, ent, tok, idx, wt, h, hlo, xq, xs, hq, hs, hmax, total;
 };
 
 FewLayout few_layout(const moe_desc& d, bool int8) {
@@ -966,16 +966,19 @@ FewLayout few_layout(const moe_desc& d, bool int8) {
     off = align256(off + bytes);
     return at;
   };
-  L.nact = take(4);
-  L.off = take((El + 1) * 4);
-  L.act = take(El * 4);
+  L.cls = take(32);
+  L.ent = take(El * 16);
   L.tok = take(n * 4);
+  L.idx = take(n * 4);
+  L.wt = take(n * 4);
   const bool split = d.mode != MOE_MODE_FP32 && !int8;   // bf16: high and low parts
   L.h = take(n * F * (split ? 2 : 4));
   L.hlo = take(split ? n * F * 2 : 0);
   L.xq = take(int8 ? (size_t)d.T * d.H : 0);
   L.xs = take(int8 ? (size_t)d.T * 4 : 0);
-  L.hmax = take(int8 ? n * 4 : 0);
+  L.hq = take(int8 ? n * F : 0);
+  L.hs = take(int8 ? n * 4 : 0);
+  L.hmax = take(int8 && d.T <= 4 ? n * F : 0);
   L.total = off;
   return L;
 }
@@ -994,10 +997,11 @@ FewParams few_params(const moe_desc& d, const FewLayout& L, const void* x, const
   p.y = y;
   p.h = w + L.h;
   p.hlo = w + L.hlo;
-  p.r_nact = reinterpret_cast<int*>(w + L.nact);
-  p.r_off = reinterpret_cast<int*>(w + L.off);
-  p.r_act = reinterpret_cast<int*>(w + L.act);
+  p.r_cls = reinterpret_cast<int*>(w + L.cls);
+  p.r_ent = reinterpret_cast<int4*>(w + L.ent);
   p.r_tok = reinterpret_cast<int*>(w + L.tok);
+  p.r_idx = reinterpret_cast<int*>(w + L.idx);
+  p.r_wt = reinterpret_cast<float*>(w + L.wt);
   p.T = (int)d.T;
   p.H = d.H;
   p.F = d.F;
@@ -1184,7 +1188,9 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
     p.sd = s_down;
     p.xq = reinterpret_cast<uint8_t*>(w + L.xq);
     p.xs = reinterpret_cast<float*>(w + L.xs);
-    p.hmax = reinterpret_cast<unsigned*>(w + L.hmax);
+    p.hq = reinterpret_cast<uint8_t*>(w + L.hq);
+    p.hs = reinterpret_cast<float*>(w + L.hs);
+    p.hmax = d->T <= 4 ? reinterpret_cast<unsigned*>(w + L.hmax) : nullptr;
     p.x = p.xq;
     if ((e = launch_few(p, 1, s)) != hipSuccess) return hip_fail(e, "few-token launch");
     return MOE_OK;

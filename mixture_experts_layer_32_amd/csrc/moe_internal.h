@@ -202,10 +202,14 @@ struct FewParams {
   const float *sg, *su, *sd;   // 8-bit weights: scales per output channel [El, F], [El, F], [El, H]
   void* y;               // [T, H]
   void *h, *hlo;         // [pairs, F] w silu(a) b: fp32, or bf16 high and low parts
-  uint8_t* xq;           // 8-bit weights: quantised x [T, H], its scales [T], and the magnitude bits of each
-  float* xs;             //   pair's largest |h| [pairs]
-  unsigned* hmax;
-  int *r_nact, *r_off, *r_act, *r_tok;   // routing, from the gate/up kernel to the down kernel
+  uint8_t *xq, *hq;      // 8-bit weights: quantised x [T, H] and h [pairs, F], and their scales
+  float *xs, *hs;
+  unsigned* hmax;        // T <= 4: magnitude bits of the largest |h| of each 4 of a pair's row [pairs, F / 4]
+                         //   (h is then quantised in the down kernel); null otherwise
+  int* r_idx;            // [T k] chosen experts and their weights, of more than 8 tokens
+  float* r_wt;
+  int *r_cls, *r_tok;    // routing, from the gate/up kernel to the down kernel
+  int4* r_ent;
   int T, H, F, E, El, e0, k;
 };
 // type: bytes of a weight element (4: fp32 mode, 2: bf16, 1: 8-bit weights with bf16 x and y)
