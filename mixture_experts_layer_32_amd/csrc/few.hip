@@ -11,8 +11,8 @@
 //
 //   k_few_prep    logits = x W_r^T (4 experts by 16 tokens per workgroup) and, with 8-bit weights, the quantised rows
 //                 of x. Only launched where one of the two is asked for.
-//   k_few_topk    the tokens' experts and weights; only launched for more than 8 tokens.
-//   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 8 tokens, chooses them); then its
+//   k_few_topk    the tokens' experts and weights; only launched for more than 16 tokens.
+//   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 16 tokens, chooses them); then its
 //                 waves take (expert, 4 rows of F) units, each on its own, and write h = w silu(a) b into
 //                 the workspace.
 //   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
@@ -181,7 +181,7 @@ __device__ __forceinline__ void choose(const FewParams& p, int t, int lane, int&
 
 // More than kRouteHere tokens: one wave a token, ahead of the kernels that use the choice (in every
 // workgroup of k_few_gateup, 64 tokens' choices took 20 us).
-constexpr int kRouteHere = 8;
+constexpr int kRouteHere = 16;
 __global__ __launch_bounds__(64) void k_few_topk(FewParams p) {
   int e;
   float wt;

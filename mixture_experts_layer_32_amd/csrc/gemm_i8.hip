@@ -3,14 +3,27 @@
 // Products and sums are exact: |q p| <= 127^2, and K <= 131072 keeps the int32 sums below 2^31. The
 // scales of a row and of a channel multiply the finished sum in fp32, once.
 //
-// The engine is the K-major one of engine.h: a workgroup of 4 waves computes a 256 x 256 tile, a wave
-// 128 x 128 of it as 4 x 4 blocks of 32 x 32 (256 accumulators). A K-tile is 128 elements, 128 bytes a
-// row (whole lines), loaded straight into LDS through a ring of two 64 KB stages. It is four
-// MFMA steps of 32 elements; each step's fragments (8 reads of 1 KB per wave) are read while the
-// previous step's 16 MFMAs run. Four waves of 128 x 128 read 64 bytes of LDS per clock at the full MFMA
-// rate, eight waves of 64 x 128 would read 96 beside the 32 the loads write, of 128 in all.
+// Two engines, both on K-major operands in K-tiles of 128 elements (128 bytes a row: whole lines) that
+// reach LDS by direct-to-LDS loads:
+//
+//  k_i8_256   a persistent workgroup of 8 waves computes 256 x 256 tiles. A wave owns 64 x 128 of one as
+//             2 x 4 blocks of 32 x 32 (128 accumulators). A ring of two 64 KB stages; a K-tile is four
+//             MFMA steps of 32 elements, each step's fragments (6 reads of 1 KB per wave) read while the
+//             previous step's 8 MFMAs run. The next tile's first two K-tiles (and the scales of its rows and channels) are issued
+//             before the epilogue, whose stores stay in flight into the next main loop.
+//  k_i8_tile  one 64 x 64 or 128 x 128 tile per workgroup, for products with too few tiles of 256 x 256
+//             to fill the chip.
+//
+// Epilogues store straight from the accumulators, in whole lines and without LDS: the B rows of a tile are
+// placed in LDS so that the 4 column blocks of a lane are 4 neighbouring channels of one row (256 bytes of
+// bf16 per row and instruction). Staging the rows in LDS instead took 68 us of the 239 us of the down product
+// of 65536 pairs, the matrix cores idle.
+//
 // The contraction may end inside a K-tile (K is a multiple of 16): the missing 16-byte chunks of A are
 // read from a page of zeros, those of B from the row's start (their products are zero).
+#include <algorithm>
+#include <type_traits>
+
 #include "engine.h"
 #include "int8_device.h"
 #include "moe_internal.h"
@@ -23,136 +36,70 @@ using namespace eng;
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int KT8 = 128;                       // elements (bytes) of a row per K-tile
-typedef KRows<128> KOp;
-constexpr int LOADS = KOp::LOADS;              // 8 loads per lane per operand per K-tile
-constexpr int OPB = 32768;                     // bytes per operand per stage
+constexpr int OPB = 32768;                     // bytes per operand per stage (256 rows)
 constexpr int STB = 2 * OPB;
-constexpr int SMEM_I8 = 2 * STB > 4 * SLAB * 4 ? 2 * STB : 4 * SLAB * 4;
+constexpr int RING = 2 * STB;
+
+// What a kernel computes: y = sums times scales as bf16 or fp32, or the gate/up half of the layer,
+// h = w silu(a) b in fp32 (the row quantiser reads it next: its scale needs the whole row) from tiles of
+// half as many gate rows and the same up rows of the weights, with gathered x rows.
+enum Out { kBf16, kF32, kGateUp };
 
 __device__ __attribute__((aligned(128))) unsigned g_zero16[4];   // never written
 
-// a K-major operand whose last K-tile holds `tail` bytes a row (0: whole)
+// lane i copies 4 bytes from g into lds + 4 i (lds wave-uniform); see gl2lds
+__device__ __forceinline__ void gl2lds4(const void* g, char* lds) {
+  const unsigned off = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(off), "v"(g) : "memory", "m0");
+}
+
+// 16-byte chunk c of row r of a staged K-tile (engine.h's layout for 128-byte rows)
+__device__ __forceinline__ int swz8(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ const char* at8(const char* tile, int r, int c) { return tile + r * KT8 + ((c ^ swz8(r)) << 4); }
+
+// A K-major operand of ROWS rows loaded by NW waves: this lane moves chunk slot lane % 8 of rows
+// (w LOADS + j) 8 + lane / 8.
+template <int ROWS, int NW>
 struct Op8 {
-  KOp k;
-  const char* past;   // read in place of chunks past the row's end; null: the row's first chunk
-  __device__ __forceinline__ void issue(char* tile, int kt, int nk, int tail) const {
+  static constexpr int LOADS = ROWS / (8 * NW);
+  const char* p[LOADS];   // the lane's chunk of K-tile 0
+  static __device__ __forceinline__ int row_of(int j) { return (wave_id() * LOADS + j) * 8 + (threadIdx.x & 63) / 8; }
+  static __device__ __forceinline__ int chunk_of(int j) { return (threadIdx.x & 7) ^ swz8(row_of(j)); }
+  // K-tile kt of nk; the last one holds `tail` bytes a row (0: whole), of whose missing chunks `past` is
+  // read in place (null: the row's first chunk)
+  __device__ __forceinline__ void issue(char* tile, int kt, int nk, int tail, const char* past) const {
+    const int w = wave_id();
     if (tail == 0 || kt + 1 < nk) {
-      k.issue(tile, kt);
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) gl2lds(p[j] + (size_t)kt * KT8, tile + (w * LOADS + j) * 1024);
       return;
     }
-    const int w = wave_id();
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int c = 16 * KOp::chunk_of(j);
-      const char* p = c < tail ? k.p[j] + (size_t)kt * KT8 : past ? past : k.p[j] - c;
-      gl2lds(p, tile + (w * LOADS + j) * 1024);
+      const int c = 16 * chunk_of(j);
+      gl2lds(c < tail ? p[j] + (size_t)kt * KT8 : past ? past : p[j] - c, tile + (w * LOADS + j) * 1024);
     }
   }
 };
 
-struct Frag8 {
-  i32x4 a[4], b[4];
-};
-
-// step s (32 elements) of the K-tile staged at st
-__device__ __forceinline__ void read_frags8(Frag8& f, const char* st, int s, int am0, const int (&bn)[4], int lane) {
-  const int c = 2 * s + (lane >> 5);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(KOp::at(st, am0 + 32 * i + (lane & 31), c));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(KOp::at(st + OPB, bn[j] + (lane & 31), c));
-}
-
-// the step's 16 MFMAs (B fragment first: a block holds the transposed 32 x 32 product), each of the
-// first eight followed in issue order by one of the LDS reads around it
-__device__ __forceinline__ void mma8(i32x16 (&acc)[4][4], const Frag8& f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
-}
-
-// nk K-tiles. Per K-tile: the four steps, each after the reads of the next one's fragments; before the
-// last step every wave waits for the next K-tile's loads and passes the barrier, and the stage just
-// read is refilled with the K-tile two ahead.
-__device__ __forceinline__ void mainloop8(i32x16 (&acc)[4][4], char* smem, const Op8& la, const Op8& lb, int nk, int tail,
-                                          int am0, const int (&bn)[4]) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  wait_vm<0>();   // the previous tile's epilogue stores do not count against the ring below
-  block_sync();   // and every wave is done reading its staging slab
-  auto issue = [&](int kt) {
-    char* st = smem + (kt & 1) * STB;
-    la.issue(st, kt, nk, tail);
-    lb.issue(st + OPB, kt, nk, tail);
-  };
-  issue(0);
-  if (nk > 1) issue(1);
-  if (nk > 1) wait_vm<2 * LOADS>();
-  else wait_vm<0>();
-  block_sync();
-  Frag8 f0, f1;
-  read_frags8(f0, smem, 0, am0, bn, lane);
-  for (int kt = 0; kt < nk; ++kt) {
-    const char* cur = smem + (kt & 1) * STB;
-    read_frags8(f1, cur, 1, am0, bn, lane);
-    mma8(acc, f0);
-    read_frags8(f0, cur, 2, am0, bn, lane);
-    mma8(acc, f1);
-    read_frags8(f1, cur, 3, am0, bn, lane);
-    mma8(acc, f0);
-    wait_vm<0>();
-    block_sync();
-    if (kt + 2 < nk) issue(kt + 2);
-    read_frags8(f0, smem + ((kt + 1) & 1) * STB, 0, am0, bn, lane);   // past the last K-tile: unused
-    mma8(acc, f1);
-  }
-  block_sync();
-}
-
-// rows 32 i .. 32 i + 31 of the wave's blocks into its slab, as integers
-__device__ __forceinline__ void stage8(int* slab, const i32x16 (&acc)[4][4], int i, int lane) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-      *reinterpret_cast<int4*>(slab + (lane & 31) * SLD + 32 * j + acc_n(a, lane)) =
-          make_int4(acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]);
-}
-
-__device__ __forceinline__ void read8i(const int* slab, int row, int col, float (&v)[8]) {
-  const int4 x = *reinterpret_cast<const int4*>(slab + row * SLD + col);
-  const int4 y = *reinterpret_cast<const int4*>(slab + row * SLD + col + 4);
-  v[0] = (float)x.x; v[1] = (float)x.y; v[2] = (float)x.z; v[3] = (float)x.w;
-  v[4] = (float)y.x; v[5] = (float)y.y; v[6] = (float)y.z; v[7] = (float)y.w;
-}
-
 // ------------------------------------------------------------------------------------------------
-// tiles of the groups: LDS prefix sums of the groups' 256-row tile counts
+// tiles of the groups: LDS prefix sums of the groups' tile counts
 struct Groups {
-  int* tile0;   // [G + 1]
-  int* row0;    // [G + 1] clamped offsets
+  int tile0[kMaxExperts + 1];
+  int row0[kMaxExperts + 1];   // clamped offsets
 };
 
 __device__ __forceinline__ int clamped_offset(const I8Params& p, int g) { return min(max(p.offsets[g], 0), (int)p.M); }
 
-__device__ __forceinline__ void group_tiles(const I8Params& p, const Groups& s) {
+// fills s and returns the number of M-tiles of BM rows
+template <int BM>
+__device__ __forceinline__ int group_tiles(const I8Params& p, Groups& s) {
+  if (!p.offsets) return (int)((p.M + BM - 1) / BM);
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x, per = (p.G + 63) >> 6, g0 = lane * per;
     int t = 0;
     for (int i = 0; i < per; ++i)
-      if (g0 + i < p.G) t += (max(clamped_offset(p, g0 + i + 1) - clamped_offset(p, g0 + i), 0) + TILE - 1) / TILE;
+      if (g0 + i < p.G) t += (max(clamped_offset(p, g0 + i + 1) - clamped_offset(p, g0 + i), 0) + BM - 1) / BM;
     int inc = t;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -166,91 +113,148 @@ __device__ __forceinline__ void group_tiles(const I8Params& p, const Groups& s) 
       const int a = clamped_offset(p, g), b = max(clamped_offset(p, g + 1), a);
       s.tile0[g] = at;
       s.row0[g] = a;
-      at += (b - a + TILE - 1) / TILE;
+      at += (b - a + BM - 1) / BM;
     }
-    if (lane == 63) s.tile0[p.G] = inc;
+    if (lane == 63) {
+      s.tile0[p.G] = inc;
+      s.row0[p.G] = clamped_offset(p, p.G);
+    }
   }
   __syncthreads();
+  return s.tile0[p.G];
 }
 
-template <bool F32>
-__global__ __launch_bounds__(NTHR, 1) void k_int8_matmul(I8Params p) {
-  __shared__ __attribute__((aligned(1024))) char smem[SMEM_I8];
-  __shared__ int tile0[kMaxExperts + 1], row0[kMaxExperts + 1];
-  const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
-  const int ntn = (p.N + TILE - 1) / TILE, nk = (p.K + KT8 - 1) / KT8, tail = p.K % KT8;
-  int mtiles = (int)((p.M + TILE - 1) / TILE);
-  if (p.offsets) {
-    group_tiles(p, Groups{tile0, row0});
-    mtiles = tile0[p.G];
+// M-tile mt: its group g, first row r0 and the group's last row + 1
+template <int BM>
+__device__ __forceinline__ void find_tile(const I8Params& p, const Groups& s, int mt, int& g, int& r0, int& end) {
+  g = 0;
+  r0 = mt * BM;
+  end = (int)p.M;
+  if (!p.offsets) return;
+  int lo = 0, hi = p.G;   // the last group whose first tile is not past mt
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.tile0[mid] <= mt) lo = mid;
+    else hi = mid;
   }
-  const XcdRange xr = xcd_range(mtiles * ntn);
-  const int bn[4] = {128 * wn, 128 * wn + 32, 128 * wn + 64, 128 * wn + 96};
-  const bool wide = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
-  for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
-    const int mt = tile / ntn, n0 = (tile - mt * ntn) * TILE;
-    int g = 0, r0 = mt * TILE, seg_end = (int)p.M;
-    if (p.offsets) {   // the last group whose first tile is not past mt
-      int lo = 0, hi = p.G;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tile0[mid] <= mt) lo = mid;
-        else hi = mid;
+  g = __builtin_amdgcn_readfirstlane(lo);
+  r0 = __builtin_amdgcn_readfirstlane(s.row0[g] + (mt - s.tile0[g]) * BM);
+  end = __builtin_amdgcn_readfirstlane(max(s.row0[g + 1], s.row0[g]));
+}
+
+// Which channel of the tile the B row rho of LDS holds. A wave's NJ column blocks are rows 32 NJ wn + 32 j + l
+// of LDS (l = lane % 32): channel 32 NJ wn + NJ l + j, so that a lane's blocks are neighbours. kGateUp: the
+// first half of the blocks is gate rows and the second the same up rows (one block: lanes 16-31 are the up
+// rows of lanes 0-15); `up` says which.
+template <Out OUT, int NJ>
+__device__ __forceinline__ int channel_of(int rho, bool& up) {
+  const int wn = rho / (32 * NJ), j = rho % (32 * NJ) / 32, l = rho % 32;
+  up = false;
+  if constexpr (OUT != kGateUp) return 32 * NJ * wn + NJ * l + j;
+  if constexpr (NJ == 1) {
+    up = l >= 16;
+    return 16 * wn + (l & 15);
+  }
+  constexpr int HJ = NJ > 1 ? NJ / 2 : 1;
+  up = j >= HJ;
+  return 32 * HJ * wn + HJ * l + j % HJ;
+}
+
+// The operand pointers of a tile of BM rows from r0 and BN weight rows from channel n0 (kGateUp: half of them
+// gate, half up rows) of group g; NJ column blocks per wave.
+template <Out OUT, int NJ, int BM, int BN, int NW>
+__device__ __forceinline__ void tile_operands(const I8Params& p, int g, int r0, int end, int n0, Op8<BM, NW>& la,
+                                              Op8<BN, NW>& lb) {
+#pragma unroll
+  for (int j = 0; j < Op8<BM, NW>::LOADS; ++j) {
+    const int r = min(r0 + Op8<BM, NW>::row_of(j), end - 1);
+    const size_t row = OUT == kGateUp ? (size_t)p.ptok[r] : (size_t)r;
+    la.p[j] = reinterpret_cast<const char*>(p.x + row * p.K) + 16 * Op8<BM, NW>::chunk_of(j);
+  }
+#pragma unroll
+  for (int j = 0; j < Op8<BN, NW>::LOADS; ++j) {
+    bool up;
+    const int n = min(n0 + channel_of<OUT, NJ>(Op8<BN, NW>::row_of(j), up), p.N - 1);
+    const uint8_t* w = OUT == kGateUp && up ? p.wu : p.w;
+    lb.p[j] = reinterpret_cast<const char*>(w + ((size_t)g * p.N + n) * p.K) + 16 * Op8<BN, NW>::chunk_of(j);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Epilogue of a tile: rows r0 .. end-1 (block i of the wave: rows AST i + 32 wm of the tile, element 4 a + b of
+// lane l its row 8 a + 4 (l / 32) + b), channels from n0. sx, wt: the tile rows' scales and routing weights,
+// sw: the channels' scales (kGateUp: half of them gate, then as many up), all in LDS.
+// WIDE (N a multiple of 8, y 16-byte aligned): vector stores through a buffer whose range ends behind the
+// tile's last row, so that the hardware drops the rows past it, and channels past N at an offset outside. Every
+// lane issues every store: no branch between them, and their number is known.
+template <Out OUT, bool WIDE, int AST, int MI, int NJ>
+__device__ __forceinline__ void epilogue(const I8Params& p, const i32x16 (&acc)[MI][NJ], int r0, int end, int n0,
+                                         const float* sx, const float* sw, const float* wt, int wm, int wn, int lane) {
+  constexpr int VW = OUT != kGateUp ? NJ : NJ == 4 ? 2 : 1;   // neighbouring channels a lane stores
+  constexpr unsigned ES = OUT == kBf16 ? 2 : 4;
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  const int l = lane & 31, h4 = 4 * (lane >> 5);
+  const int c = OUT == kGateUp && NJ == 1 ? 16 * wn + (l & 15) : 32 * VW * wn + VW * l, n = n0 + c;
+  float g[VW], u[VW];
+#pragma unroll
+  for (int v = 0; v < VW; ++v) {
+    g[v] = sw[c + v];
+    u[v] = OUT == kGateUp ? sw[32 * NJ + c + v] : 0.f;
+  }
+  const bool mine = n < p.N && (OUT != kGateUp || NJ > 1 || l < 16);
+  char* base = static_cast<char*>(p.y) + ((size_t)r0 * p.N + n0) * ES;   // uniform; a tile spans less than 4 GB
+  const unsigned ldb = (unsigned)p.N * ES, rows_in = (unsigned)min(end - r0, AST * MI);
+  __amdgpu_buffer_rsrc_t rsrc;
+  if constexpr (WIDE) rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, rows_in * ldb, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int rl = AST * i + 32 * wm + h4, rows = end - r0 - rl;   // the lane's row 8 a + b is stored if below
+    const unsigned off0 = (unsigned)rl * ldb + (unsigned)c * ES;
+    unsigned off = WIDE && !mine ? 0xf0000000u : off0;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      __builtin_amdgcn_sched_barrier(0);   // (the scales of every row read ahead would spill)
+      const float4 s4 = *reinterpret_cast<const float4*>(sx + rl + 8 * a);
+      const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+      float w[4] = {};
+      if constexpr (OUT == kGateUp) {
+        const float4 w4 = *reinterpret_cast<const float4*>(wt + rl + 8 * a);
+        w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
       }
-      g = __builtin_amdgcn_readfirstlane(lo);
-      r0 = __builtin_amdgcn_readfirstlane(row0[g] + (mt - tile0[g]) * TILE);
-      seg_end = __builtin_amdgcn_readfirstlane(max(clamped_offset(p, g + 1), row0[g]));
-    }
-    Op8 la, lb;
-    la.past = reinterpret_cast<const char*>(g_zero16);
-    lb.past = nullptr;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int row = KOp::row_of(j), c = KOp::chunk_of(j);
-      la.k.p[j] = reinterpret_cast<const char*>(p.x + (size_t)min(r0 + row, seg_end - 1) * p.K) + 16 * c;
-      lb.k.p[j] = reinterpret_cast<const char*>(p.w + ((size_t)g * p.N + min(n0 + row, p.N - 1)) * p.K) + 16 * c;
-    }
-    i32x16 acc[4][4];
-    mainloop8(acc, smem, la, lb, nk, tail, 128 * wm, bn);
-    // epilogue: 32 rows at a time through the wave's slab, then 8 columns of a row per lane
-    int* slab = reinterpret_cast<int*>(wave_slab(smem));
-    const int c0 = (lane & 15) * 8, n = n0 + 128 * wn + c0;
-    float sw[8];
+      for (int b = 0; b < 4; ++b) {
+        const int q = 4 * a + b;
+        float o[VW];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sw[e] = p.ws[(size_t)g * p.N + min(n + e, p.N - 1)];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      stage8(slab, acc, i, lane);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int rl = (lane >> 4) + 4 * s, r = r0 + 128 * wm + 32 * i + rl;
-        if (r < seg_end && n < p.N) {
-          float v[8];
-          read8i(slab, rl, c0, v);
-          const float sx = p.xs[r];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= sx * sw[e];
-          const size_t at = (size_t)r * p.N + n;
-          if constexpr (F32) {
-            float* o = static_cast<float*>(p.y) + at;
-            if (wide) {
-              st16_nt(o, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-              st16_nt(o + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < p.N) o[e] = v[e];
-            }
+        for (int v = 0; v < VW; ++v) {
+          if constexpr (OUT != kGateUp) {
+            o[v] = (float)acc[i][v][q] * (s[b] * g[v]);
           } else {
-            bf16* o = static_cast<bf16*>(p.y) + at;
-            if (wide) {
-              st16_nt(o, pack8(v));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < p.N) o[e] = (bf16)v[e];
-            }
+            const int us = NJ == 1 ? __shfl_xor(acc[i][0][q], 16) : acc[i][NJ == 1 ? 0 : NJ / 2 + v][q];
+            const float ga = (float)acc[i][v][q] * (s[b] * g[v]), up = (float)us * (s[b] * u[v]);
+            o[v] = w[b] * (ga * sigmoidf_(ga) * up);
           }
+        }
+        if constexpr (WIDE) {   // aux 2: non-temporal
+          if constexpr (OUT == kBf16 && VW == 4) {
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4(o[0], o[1], o[2], o[3])), rsrc, off, 0, 2);
+          } else if constexpr (VW == 4) {
+            const u32x4 f = {__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])};
+            __builtin_amdgcn_raw_buffer_store_b128(f, rsrc, off, 0, 2);
+          } else {
+            const u32x2 f = {__float_as_uint(o[0]), __float_as_uint(o[1])};
+            __builtin_amdgcn_raw_buffer_store_b64(f, rsrc, off, 0, 2);
+          }
+          off += b < 3 ? ldb : 5 * ldb;   // rows 8 a + b, then 8 (a + 1)
+        } else if (mine && 8 * a + b < rows) {
+          char* y = base + off + (unsigned)(8 * a + b) * ldb;
+#pragma unroll
+          for (int v = 0; v < VW; ++v)
+            if (n + v < p.N) {
+              if constexpr (OUT == kBf16) reinterpret_cast<bf16*>(y)[v] = (bf16)o[v];
+              else reinterpret_cast<float*>(y)[v] = o[v];
+            }
         }
       }
     }
@@ -258,63 +262,211 @@ __global__ __launch_bounds__(NTHR, 1) void k_int8_matmul(I8Params p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// gate/up of the 8-bit layer: a tile is 256 pairs of an expert by 128 columns of F (128 gate rows and the
-// same 128 up rows of the weights); x rows are gathered through the routing's token list. The epilogue
-// writes h = w silu(a) b in fp32, which the row quantiser then reads: its scale needs the whole row.
-__global__ __launch_bounds__(NTHR, 1) void k_gateup_i8(I8LayerParams p) {
-  __shared__ __attribute__((aligned(1024))) char smem[SMEM_I8];
-  const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
-  const int H = p.H, F = p.F, ntn = F / 128;
-  const XcdRange xr = xcd_range(*p.num_mtiles2 * ntn);
-  const int bn[4] = {64 * wn, 64 * wn + 32, 128 + 64 * wn, 128 + 64 * wn + 32};
+// k_i8_256
+constexpr int NT256 = 512;                     // 8 waves: 64 x 128 of the tile each
+typedef Op8<TILE, 8> Op256;
+struct Frag8 {
+  i32x4 a[2], b[4];
+};
+
+// step s (32 elements) of the K-tile staged at st; row blocks of the wave at am0 and am0 + 128, columns from bn0
+__device__ __forceinline__ void read_frags8(Frag8& f, const char* st, int s, int am0, int bn0, int lane) {
+  const int c = 2 * s + (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(at8(st, am0 + 128 * i + (lane & 31), c));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(at8(st + OPB, bn0 + 32 * j + (lane & 31), c));
+}
+
+// the step's 8 MFMAs, each of the first six followed in issue order by one of the LDS reads around it
+__device__ __forceinline__ void mma8(i32x16 (&acc)[2][4], const Frag8& f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+  for (int q = 0; q < 6; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+}
+
+// K-tiles 0 .. nk-1, of which 0 (landed, published) and 1 are issued. Per K-tile: the four steps, each after
+// the reads of the next one's fragments; before the last step every wave waits for the next K-tile's
+// loads and passes the barrier, and the stage just read is refilled with the K-tile two ahead.
+template <class Issue>
+__device__ __forceinline__ void ktiles8(i32x16 (&acc)[2][4], const char* smem, Issue issue, int nk, int am0, int bn0,
+                                        int lane) {
+  Frag8 f0, f1;
+  read_frags8(f0, smem, 0, am0, bn0, lane);
+  for (int kt = 0; kt < nk; ++kt) {
+    const char* cur = smem + (kt & 1) * STB;
+    read_frags8(f1, cur, 1, am0, bn0, lane);
+    mma8(acc, f0);
+    read_frags8(f0, cur, 2, am0, bn0, lane);
+    mma8(acc, f1);
+    read_frags8(f1, cur, 3, am0, bn0, lane);
+    mma8(acc, f0);
+    wait_vm<0>();
+    block_sync();
+    if (kt + 2 < nk) issue(kt + 2);
+    read_frags8(f0, smem + ((kt + 1) & 1) * STB, 0, am0, bn0, lane);   // past the last K-tile: unused
+    mma8(acc, f1);
+  }
+  block_sync();
+}
+
+template <Out OUT>
+__global__ __launch_bounds__(NT256, 1) void k_i8_256(I8Params p) {
+  __shared__ __attribute__((aligned(1024))) char smem[RING];
+  __shared__ __attribute__((aligned(16))) float scales[2][3 * TILE];   // by tile parity: rows, channels, routing weights
+  __shared__ Groups groups;
+  constexpr int BN = OUT == kGateUp ? TILE / 2 : TILE;   // output columns of a tile
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
+  const int ntn = (p.N + BN - 1) / BN, nk = (p.K + KT8 - 1) / KT8, tail = p.K % KT8;
+  const int mtiles = group_tiles<TILE>(p, groups);
+  const XcdRange xr = xcd_range(mtiles * ntn);
+  if (xr.first >= xr.end) return;
+  Op256 la, lb;
+  int r0 = 0, end = 0, n0 = 0, par = 0;
+  auto issue = [&](int kt) {
+    char* st = smem + (kt & 1) * STB;
+    la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
+    lb.issue(st + OPB, kt, nk, tail, nullptr);
+  };
+  // tile `tile`: its operands, its scales into scales[par] and its first two K-tiles
+  auto begin = [&](int tile) {
+    const int mt = tile / ntn;
+    int g;
+    n0 = (tile - mt * ntn) * BN;
+    find_tile<TILE>(p, groups, mt, g, r0, end);
+    tile_operands<OUT, 4, TILE, TILE, 8>(p, g, r0, end, n0, la, lb);
+    char* sc = reinterpret_cast<char*>(scales[par]) + (w & 3) * 256;
+    const int t = tid & 255;
+    if (w < 4) {
+      const int r = min(r0 + t, end - 1);
+      if constexpr (OUT == kGateUp) gl2lds4(p.weight + p.perm[r], sc + 8 * TILE);
+      gl2lds4(p.xs + (OUT == kGateUp ? p.ptok[r] : r), sc);
+    } else {
+      const bool up = OUT == kGateUp && t >= BN;
+      gl2lds4((up ? p.wsu : p.ws) + (size_t)g * p.N + min(n0 + (up ? t - BN : t), p.N - 1), sc + 4 * TILE);
+    }
+    issue(0);
+    if (nk > 1) issue(1);
+  };
+  begin(xr.first);
+  bool after_stores = false;
   for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
-    const int mt = tile / ntn, nt = tile - mt * ntn;
-    const int2 me = p.mtile2[mt];
-    const int e = me.x, r0 = me.y, seg_end = p.offsets[e + 1];
-    Op8 la, lb;
-    la.past = lb.past = nullptr;
+    i32x16 acc[2][4];
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int row = KOp::row_of(j), c = KOp::chunk_of(j);
-      const int r = min(r0 + row, seg_end - 1);
-      la.k.p[j] = reinterpret_cast<const char*>(p.xq + (size_t)p.ptok[r] * H) + 16 * c;
-      const uint8_t* wrow = row < 128 ? p.wg + ((size_t)e * F + nt * 128 + row) * H
-                                      : p.wu + ((size_t)e * F + nt * 128 + row - 128) * H;
-      lb.k.p[j] = reinterpret_cast<const char*>(wrow) + 16 * c;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+    // The vector-memory counter completes in order: the two K-tiles, older than a tile's 32 epilogue stores, have
+    // landed once at most those are outstanding.
+    if (after_stores) wait_vm<32>();
+    else wait_vm<0>();
+    block_sync();
+    ktiles8(acc, smem, issue, nk, 32 * wm, 128 * wn, lane);
+    // this tile's place, then the next tile's first loads: every wave is past the last barrier, the ring is free
+    const int cr0 = r0, cend = end, cn0 = n0;
+    const float* sc = scales[par];
+    par ^= 1;
+    if (tile + xr.stride < xr.end) begin(tile + xr.stride);
+    epilogue<OUT, true, 128>(p, acc, cr0, cend, cn0, sc, sc + TILE, sc + 2 * TILE, wm, wn, lane);
+    after_stores = true;
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// k_i8_tile: MI x NJ blocks per wave, 2 x 2 waves, a ring of S stages with one barrier each: after it the
+// stage read in the previous K-tile is refilled with the K-tile S - 1 ahead.
+template <Out OUT, int MI, int NJ, int S>
+__global__ __launch_bounds__(NTHR, 2) void k_i8_tile(I8Params p) {
+  constexpr int BM = 64 * MI, BN = 64 * NJ, ST = (BM + BN) * KT8, NL = Op8<BM, 4>::LOADS + Op8<BN, 4>::LOADS;
+  constexpr int BC = OUT == kGateUp ? BN / 2 : BN;   // output columns of a tile
+  __shared__ __attribute__((aligned(1024))) char smem[S * ST];
+  __shared__ __attribute__((aligned(16))) float sx[BM], sw[BN], wt[BM];
+  __shared__ Groups groups;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
+  const int ntn = (p.N + BC - 1) / BC, nk = (p.K + KT8 - 1) / KT8, tail = p.K % KT8;
+  const int mtiles = group_tiles<BM>(p, groups);
+  const int tile = xcd_logical_block(gridDim.x);
+  if (tile >= mtiles * ntn) return;
+  const int mt = tile / ntn, n0 = (tile - mt * ntn) * BC;
+  int g, r0, end;
+  find_tile<BM>(p, groups, mt, g, r0, end);
+  Op8<BM, 4> la;
+  Op8<BN, 4> lb;
+  tile_operands<OUT, NJ>(p, g, r0, end, n0, la, lb);
+  auto issue = [&](int kt) {
+    char* st = smem + (kt % S) * ST;
+    la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
+    lb.issue(st + BM * KT8, kt, nk, tail, nullptr);
+  };
+  if (tid < BM) {
+    const int r = min(r0 + tid, end - 1);
+    sx[tid] = p.xs[OUT == kGateUp ? p.ptok[r] : r];
+    if constexpr (OUT == kGateUp) wt[tid] = p.weight[p.perm[r]];
+  }
+  if (tid < BN) sw[tid] = (OUT == kGateUp && tid >= BC ? p.wsu : p.ws)[(size_t)g * p.N + min(n0 + tid % BC, p.N - 1)];
+  wait_vm<0>();   // the compiler's own loads do not count against the ring below
+#pragma unroll
+  for (int q = 0; q < S - 1; ++q)
+    if (q < nk) issue(q);
+  i32x16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    const int younger = min(S - 2, nk - 1 - kt);   // K-tiles issued after kt
+    if (S > 3 && younger >= 2) wait_vm<2 * NL>();
+    else if (S > 2 && younger == 1) wait_vm<NL>();
+    else wait_vm<0>();
+    block_sync();
+    if (kt + S - 1 < nk) issue(kt + S - 1);
+    const char* st = smem + (kt % S) * ST;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int c = 2 * s + (lane >> 5);
+      i32x4 fa[MI], fb[NJ];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const i32x4*>(at8(st, 64 * i + 32 * wm + (lane & 31), c));
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        fb[j] = *reinterpret_cast<const i32x4*>(at8(st + BM * KT8, 32 * (NJ * wn + j) + (lane & 31), c));
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
     }
-    i32x16 acc[4][4];
-    mainloop8(acc, smem, la, lb, H / KT8, 0, 128 * wm, bn);
-    int* slab = reinterpret_cast<int*>(wave_slab(smem));
-    const int c0 = (lane & 7) * 8, f = nt * 128 + 64 * wn + c0;
-    float sg[8], su[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      sg[q] = p.sg[(size_t)e * F + f + q];
-      su[q] = p.su[(size_t)e * F + f + q];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      stage8(slab, acc, i, lane);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int rl = (lane >> 3) + 8 * s, r = r0 + 128 * wm + 32 * i + rl;
-        if (r < seg_end) {
-          float a[8], b[8], h[8];
-          read8i(slab, rl, c0, a);
-          read8i(slab, rl, 64 + c0, b);
-          const float sx = p.xs[p.ptok[r]], wt = p.weight[p.perm[r]];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            a[q] *= sx * sg[q];
-            b[q] *= sx * su[q];
-            h[q] = wt * (a[q] / (1.0f + expf(-a[q])) * b[q]);
-          }
-          float* o = p.h + (size_t)r * F + f;
-          st16_nt(o, make_uint4(__float_as_uint(h[0]), __float_as_uint(h[1]), __float_as_uint(h[2]), __float_as_uint(h[3])));
-          st16_nt(o + 4, make_uint4(__float_as_uint(h[4]), __float_as_uint(h[5]), __float_as_uint(h[6]), __float_as_uint(h[7])));
-        }
-      }
-    }
+  }
+  epilogue<OUT, false, 64>(p, acc, r0, end, n0, sx, sw, wt, wm, wn, lane);
+}
+
+// The most tiles of bm rows by bn columns the product can have.
+int64_t tiles(const I8Params& p, int bm, int bn) {
+  const int64_t m = p.M / bm + (p.offsets ? std::min<int64_t>(p.G, p.M) : 1);
+  return std::min<int64_t>(m, p.M) * ((p.N + bn - 1) / bn);
+}
+
+template <Out OUT>
+void launch_i8(const I8Params& p, int grid, hipStream_t s) {
+  constexpr int half = OUT == kGateUp ? 2 : 1;
+  // 256 x 256 tiles once they fill three quarters of the CUs, else 128 x 128 ones if they do, else 64 x 64
+  const bool wide = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+  if (wide && 4 * tiles(p, 256, 256 / half) >= 3 * grid) {
+    k_i8_256<OUT><<<grid, NT256, 0, s>>>(p);
+  } else if (4 * tiles(p, 128, 128 / half) >= 3 * grid) {
+    k_i8_tile<OUT, 2, 2, 2><<<(unsigned)tiles(p, 128, 128 / half), NTHR, 0, s>>>(p);
+  } else {
+    k_i8_tile<OUT, 1, 1, 4><<<(unsigned)tiles(p, 64, 64 / half), NTHR, 0, s>>>(p);
   }
 }
 
@@ -322,16 +474,9 @@ __global__ __launch_bounds__(NTHR, 1) void k_gateup_i8(I8LayerParams p) {
 
 hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hipStream_t s) {
   prof_mark_begin(name, s);
-  if (p.f32) k_int8_matmul<true><<<grid, NTHR, 0, s>>>(p);
-  else k_int8_matmul<false><<<grid, NTHR, 0, s>>>(p);
-  const hipError_t err = hipGetLastError();
-  if (err == hipSuccess) prof_mark_end(s);
-  return err;
-}
-
-hipError_t launch_gateup_i8(const I8LayerParams& p, int grid, hipStream_t s) {
-  prof_mark_begin("int8_gateup", s);
-  k_gateup_i8<<<grid, NTHR, 0, s>>>(p);
+  if (p.wu) launch_i8<kGateUp>(p, grid, s);
+  else if (p.f32) launch_i8<kF32>(p, grid, s);
+  else launch_i8<kBf16>(p, grid, s);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;

@@ -1209,23 +1209,25 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
     if (e == hipSuccess) e = launch_route(rp, s);
   }
   if (e != hipSuccess) return hip_fail(e, "route launch");
-  I8LayerParams gp{};
-  gp.xq = xq;
+  float* h = reinterpret_cast<float*>(w + L.h);
+  I8Params gp{};
+  gp.x = xq;
   gp.xs = xs;
-  gp.wg = reinterpret_cast<const uint8_t*>(w_gate);
+  gp.w = reinterpret_cast<const uint8_t*>(w_gate);
   gp.wu = reinterpret_cast<const uint8_t*>(w_up);
-  gp.sg = s_gate;
-  gp.su = s_up;
+  gp.ws = s_gate;
+  gp.wsu = s_up;
   gp.weight = rp.weight;
   gp.perm = rp.perm;
   gp.ptok = rp.ptok;
   gp.offsets = rp.offsets;
-  gp.mtile2 = rp.mtile2;
-  gp.num_mtiles2 = rp.num_mtiles2;
-  gp.h = reinterpret_cast<float*>(w + L.h);
-  gp.H = d->H;
-  gp.F = d->F;
-  if ((e = launch_gateup_i8(gp, persistent_grid(1), s)) != hipSuccess) return hip_fail(e, "gate/up launch");
+  gp.y = h;
+  gp.M = L.route.rows;
+  gp.N = d->F;
+  gp.K = d->H;
+  gp.G = d->E_local;
+  if ((e = launch_int8_matmul(gp, persistent_grid(1), "int8_gateup", s)) != hipSuccess)
+    return hip_fail(e, "gate/up launch");
   I8Params dp{};
   dp.x = reinterpret_cast<const uint8_t*>(w + L.hq);
   dp.xs = reinterpret_cast<const float*>(w + L.hs);
@@ -1237,7 +1239,7 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
   dp.N = d->H;
   dp.K = d->F;
   dp.G = d->E_local;
-  if ((e = launch_int8_quant(gp.h, true, L.route.rows, d->F, rp.offsets + d->E_local,
+  if ((e = launch_int8_quant(h, true, L.route.rows, d->F, rp.offsets + d->E_local,
                              reinterpret_cast<uint8_t*>(w + L.hq), reinterpret_cast<float*>(w + L.hs), "int8_quant_h",
                              s)) != hipSuccess)
     return hip_fail(e, "int8 quantise launch");

@@ -206,7 +206,7 @@ struct FewParams {
   float *xs, *hs;
   unsigned* hmax;        // T <= 4: magnitude bits of the largest |h| of each 4 of a pair's row [pairs, F / 4]
                          //   (h is then quantised in the down kernel); null otherwise
-  int* r_idx;            // [T k] chosen experts and their weights, of more than 8 tokens
+  int* r_idx;            // [T k] chosen experts and their weights, of more than 16 tokens
   float* r_wt;
   int *r_cls, *r_tok;    // routing, from the gate/up kernel to the down kernel
   int4* r_ent;
@@ -227,6 +227,11 @@ struct I8Params {
   int64_t M;
   int N, K, G;
   bool f32;
+  // gate/up of the 8-bit layer (wu not null): w and ws are the gate's, y is h = weight silu(a) b in fp32, and
+  // row r of the product is row ptok[r] of x, routing weight weight[perm[r]]
+  const uint8_t* wu;
+  const float *wsu, *weight;
+  const int *ptok, *perm;
 };
 // rows of x [rows, cols] (fp32 or bf16) as signed bytes with a scale each; nrows: the row count on the
 // device, or null
@@ -234,16 +239,6 @@ hipError_t launch_int8_quant(const void* x, bool f32, int64_t rows, int cols, co
                              float* scales, const char* name, hipStream_t s);
 hipError_t launch_int8_rows(const I8Params& p, hipStream_t s);                                    // M <= 64
 hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hipStream_t s);      // any M
-// gate/up of the 8-bit layer over the routing's tiles
-struct I8LayerParams {
-  const uint8_t *xq, *wg, *wu;
-  const float *xs, *sg, *su, *weight;
-  const int *perm, *ptok, *offsets, *num_mtiles2;
-  const int2* mtile2;
-  float* h;              // [pairs, F]
-  int H, F;
-};
-hipError_t launch_gateup_i8(const I8LayerParams& p, int grid, hipStream_t s);
 
 hipError_t launch_forward_gemms_mx(const FwdParams& p, int grid, hipStream_t s, bool recompute = false);
 hipError_t launch_backward_gemms_mx(const BwdParams& p, int grid, hipStream_t s);
