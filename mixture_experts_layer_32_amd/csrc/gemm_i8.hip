@@ -9,9 +9,8 @@
 //  k_i8_256   a persistent workgroup of 8 waves computes 256 x 256 tiles. A wave owns 64 x 128 of one as
 //             2 x 4 blocks of 32 x 32 (128 accumulators). A ring of two 64 KB stages; a K-tile is four
 //             MFMA steps of 32 elements, each step's fragments (6 reads of 1 KB per wave) read while the
-//             previous step's 8 MFMAs run. The next tile's first two K-tiles (and the scales of its rows and channels) are issued
-//             before the epilogue, whose stores stay in flight into the next main loop.
-//  k_i8_tile  one 64 x 64 or 128 x 128 tile per workgroup, for products with too few tiles of 256 x 256
+//             previous step's 8 MFMAs run. A tile of up to 128 rows runs half of them.
+//  k_i8_tile  64 x 64 or 128 x 128 tiles, two workgroups of 4 waves a CU, for products with too few tiles of 256 x 256
 //             to fill the chip.
 //
 // Epilogues store straight from the accumulators, in whole lines and without LDS: the B rows of a tile are
@@ -270,49 +269,51 @@ struct Frag8 {
 };
 
 // step s (32 elements) of the K-tile staged at st; row blocks of the wave at am0 and am0 + 128, columns from bn0
+template <int MI>
 __device__ __forceinline__ void read_frags8(Frag8& f, const char* st, int s, int am0, int bn0, int lane) {
   const int c = 2 * s + (lane >> 5);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(at8(st, am0 + 128 * i + (lane & 31), c));
+  for (int i = 0; i < MI; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(at8(st, am0 + 128 * i + (lane & 31), c));
 #pragma unroll
   for (int j = 0; j < 4; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(at8(st + OPB, bn0 + 32 * j + (lane & 31), c));
 }
 
-// the step's 8 MFMAs, each of the first six followed in issue order by one of the LDS reads around it
+// the step's 4 MI MFMAs, each of the first followed in issue order by one of the LDS reads around it
+template <int MI>
 __device__ __forceinline__ void mma8(i32x16 (&acc)[2][4], const Frag8& f) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
 #pragma unroll
-  for (int q = 0; q < 6; ++q) {
+  for (int q = 0; q < (MI == 2 ? 6 : 4); ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  if (MI == 2) __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
 }
 
 // K-tiles 0 .. nk-1, of which 0 (landed, published) and 1 are issued. Per K-tile: the four steps, each after
 // the reads of the next one's fragments; before the last step every wave waits for the next K-tile's
 // loads and passes the barrier, and the stage just read is refilled with the K-tile two ahead.
-template <class Issue>
+template <int MI, class Issue>
 __device__ __forceinline__ void ktiles8(i32x16 (&acc)[2][4], const char* smem, Issue issue, int nk, int am0, int bn0,
                                         int lane) {
   Frag8 f0, f1;
-  read_frags8(f0, smem, 0, am0, bn0, lane);
+  read_frags8<MI>(f0, smem, 0, am0, bn0, lane);
   for (int kt = 0; kt < nk; ++kt) {
     const char* cur = smem + (kt & 1) * STB;
-    read_frags8(f1, cur, 1, am0, bn0, lane);
-    mma8(acc, f0);
-    read_frags8(f0, cur, 2, am0, bn0, lane);
-    mma8(acc, f1);
-    read_frags8(f1, cur, 3, am0, bn0, lane);
-    mma8(acc, f0);
+    read_frags8<MI>(f1, cur, 1, am0, bn0, lane);
+    mma8<MI>(acc, f0);
+    read_frags8<MI>(f0, cur, 2, am0, bn0, lane);
+    mma8<MI>(acc, f1);
+    read_frags8<MI>(f1, cur, 3, am0, bn0, lane);
+    mma8<MI>(acc, f0);
     wait_vm<0>();
     block_sync();
     if (kt + 2 < nk) issue(kt + 2);
-    read_frags8(f0, smem + ((kt + 1) & 1) * STB, 0, am0, bn0, lane);   // past the last K-tile: unused
-    mma8(acc, f1);
+    read_frags8<MI>(f0, smem + ((kt + 1) & 1) * STB, 0, am0, bn0, lane);   // past the last K-tile: unused
+    mma8<MI>(acc, f1);
   }
   block_sync();
 }
@@ -320,7 +321,7 @@ __device__ __forceinline__ void ktiles8(i32x16 (&acc)[2][4], const char* smem, I
 template <Out OUT>
 __global__ __launch_bounds__(NT256, 1) void k_i8_256(I8Params p) {
   __shared__ __attribute__((aligned(1024))) char smem[RING];
-  __shared__ __attribute__((aligned(16))) float scales[2][3 * TILE];   // by tile parity: rows, channels, routing weights
+  __shared__ __attribute__((aligned(16))) float scales[3 * TILE];   // of rows and channels, and routing weights
   __shared__ Groups groups;
   constexpr int BN = OUT == kGateUp ? TILE / 2 : TILE;   // output columns of a tile
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
@@ -329,20 +330,22 @@ __global__ __launch_bounds__(NT256, 1) void k_i8_256(I8Params p) {
   const XcdRange xr = xcd_range(mtiles * ntn);
   if (xr.first >= xr.end) return;
   Op256 la, lb;
-  int r0 = 0, end = 0, n0 = 0, par = 0;
+  int r0 = 0, end = 0, n0 = 0;
+  bool half = false;   // up to 128 rows: the second row blocks, and the loads of waves 4-7's A rows, are left out
   auto issue = [&](int kt) {
     char* st = smem + (kt & 1) * STB;
-    la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
+    if (!half || w < 4) la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
     lb.issue(st + OPB, kt, nk, tail, nullptr);
   };
-  // tile `tile`: its operands, its scales into scales[par] and its first two K-tiles
+  // tile `tile`: its operands, its scales into LDS and its first two K-tiles
   auto begin = [&](int tile) {
     const int mt = tile / ntn;
     int g;
     n0 = (tile - mt * ntn) * BN;
     find_tile<TILE>(p, groups, mt, g, r0, end);
+    half = end - r0 <= 128;
     tile_operands<OUT, 4, TILE, TILE, 8>(p, g, r0, end, n0, la, lb);
-    char* sc = reinterpret_cast<char*>(scales[par]) + (w & 3) * 256;
+    char* sc = reinterpret_cast<char*>(scales) + (w & 3) * 256;
     const int t = tid & 255;
     if (w < 4) {
       const int r = min(r0 + t, end - 1);
@@ -355,8 +358,6 @@ __global__ __launch_bounds__(NT256, 1) void k_i8_256(I8Params p) {
     issue(0);
     if (nk > 1) issue(1);
   };
-  begin(xr.first);
-  bool after_stores = false;
   for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
     i32x16 acc[2][4];
 #pragma unroll
@@ -365,24 +366,19 @@ __global__ __launch_bounds__(NT256, 1) void k_i8_256(I8Params p) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-    // The vector-memory counter completes in order: the two K-tiles, older than a tile's 32 epilogue stores, have
-    // landed once at most those are outstanding.
-    if (after_stores) wait_vm<32>();
-    else wait_vm<0>();
+    begin(tile);
+    wait_vm<0>();
     block_sync();
-    ktiles8(acc, smem, issue, nk, 32 * wm, 128 * wn, lane);
-    // this tile's place, then the next tile's first loads: every wave is past the last barrier, the ring is free
-    const int cr0 = r0, cend = end, cn0 = n0;
-    const float* sc = scales[par];
-    par ^= 1;
-    if (tile + xr.stride < xr.end) begin(tile + xr.stride);
-    epilogue<OUT, true, 128>(p, acc, cr0, cend, cn0, sc, sc + TILE, sc + 2 * TILE, wm, wn, lane);
-    after_stores = true;
+    if (half) ktiles8<1>(acc, smem, issue, nk, 32 * wm, 128 * wn, lane);
+    else ktiles8<2>(acc, smem, issue, nk, 32 * wm, 128 * wn, lane);
+    const float* sc = scales;
+    epilogue<OUT, true, 128>(p, acc, r0, end, n0, sc, sc + TILE, sc + 2 * TILE, wm, wn, lane);
+    block_sync();   // every wave has read its scales
   }
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_i8_tile: MI x NJ blocks per wave, 2 x 2 waves, a ring of S stages with one barrier each: after it the
+// k_i8_tile: persistent, MI x NJ blocks per wave, 2 x 2 waves, a ring of S stages with one barrier each: after it the
 // stage read in the previous K-tile is refilled with the K-tile S - 1 ahead.
 template <Out OUT, int MI, int NJ, int S>
 __global__ __launch_bounds__(NTHR, 2) void k_i8_tile(I8Params p) {
@@ -394,79 +390,85 @@ __global__ __launch_bounds__(NTHR, 2) void k_i8_tile(I8Params p) {
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), wm = w >> 1, wn = w & 1;
   const int ntn = (p.N + BC - 1) / BC, nk = (p.K + KT8 - 1) / KT8, tail = p.K % KT8;
   const int mtiles = group_tiles<BM>(p, groups);
-  const int tile = xcd_logical_block(gridDim.x);
-  if (tile >= mtiles * ntn) return;
-  const int mt = tile / ntn, n0 = (tile - mt * ntn) * BC;
-  int g, r0, end;
-  find_tile<BM>(p, groups, mt, g, r0, end);
-  Op8<BM, 4> la;
-  Op8<BN, 4> lb;
-  tile_operands<OUT, NJ>(p, g, r0, end, n0, la, lb);
-  auto issue = [&](int kt) {
-    char* st = smem + (kt % S) * ST;
-    la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
-    lb.issue(st + BM * KT8, kt, nk, tail, nullptr);
-  };
-  if (tid < BM) {
-    const int r = min(r0 + tid, end - 1);
-    sx[tid] = p.xs[OUT == kGateUp ? p.ptok[r] : r];
-    if constexpr (OUT == kGateUp) wt[tid] = p.weight[p.perm[r]];
-  }
-  if (tid < BN) sw[tid] = (OUT == kGateUp && tid >= BC ? p.wsu : p.ws)[(size_t)g * p.N + min(n0 + tid % BC, p.N - 1)];
-  wait_vm<0>();   // the compiler's own loads do not count against the ring below
+  const XcdRange xr = xcd_range(mtiles * ntn);
+  for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
+    const int mt = tile / ntn, n0 = (tile - mt * ntn) * BC;
+    int g, r0, end;
+    find_tile<BM>(p, groups, mt, g, r0, end);
+    Op8<BM, 4> la;
+    Op8<BN, 4> lb;
+    tile_operands<OUT, NJ>(p, g, r0, end, n0, la, lb);
+    auto issue = [&](int kt) {
+      char* st = smem + (kt % S) * ST;
+      la.issue(st, kt, nk, tail, reinterpret_cast<const char*>(g_zero16));
+      lb.issue(st + BM * KT8, kt, nk, tail, nullptr);
+    };
+    block_sync();   // every wave is done with the previous tile's scales
+    if (tid < BM) {
+      const int r = min(r0 + tid, end - 1);
+      sx[tid] = p.xs[OUT == kGateUp ? p.ptok[r] : r];
+      if constexpr (OUT == kGateUp) wt[tid] = p.weight[p.perm[r]];
+    }
+    if (tid < BN) sw[tid] = (OUT == kGateUp && tid >= BC ? p.wsu : p.ws)[(size_t)g * p.N + min(n0 + tid % BC, p.N - 1)];
+    wait_vm<0>();   // the compiler's own loads, and the previous tile's stores, do not count against the ring below
 #pragma unroll
-  for (int q = 0; q < S - 1; ++q)
-    if (q < nk) issue(q);
-  i32x16 acc[MI][NJ];
+    for (int q = 0; q < S - 1; ++q)
+      if (q < nk) issue(q);
+    i32x16 acc[MI][NJ];
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    const int younger = min(S - 2, nk - 1 - kt);   // K-tiles issued after kt
-    if (S > 3 && younger >= 2) wait_vm<2 * NL>();
-    else if (S > 2 && younger == 1) wait_vm<NL>();
-    else wait_vm<0>();
-    block_sync();
-    if (kt + S - 1 < nk) issue(kt + S - 1);
-    const char* st = smem + (kt % S) * ST;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int c = 2 * s + (lane >> 5);
-      i32x4 fa[MI], fb[NJ];
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const i32x4*>(at8(st, 64 * i + 32 * wm + (lane & 31), c));
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        fb[j] = *reinterpret_cast<const i32x4*>(at8(st + BM * KT8, 32 * (NJ * wn + j) + (lane & 31), c));
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+      const int younger = min(S - 2, nk - 1 - kt);   // K-tiles issued after kt
+      if (S > 3 && younger >= 2) wait_vm<2 * NL>();
+      else if (S > 2 && younger == 1) wait_vm<NL>();
+      else wait_vm<0>();
+      block_sync();
+      if (kt + S - 1 < nk) issue(kt + S - 1);
+      const char* st = smem + (kt % S) * ST;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      for (int s = 0; s < 4; ++s) {
+        const int c = 2 * s + (lane >> 5);
+        i32x4 fa[MI], fb[NJ];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const i32x4*>(at8(st, 64 * i + 32 * wm + (lane & 31), c));
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          fb[j] = *reinterpret_cast<const i32x4*>(at8(st + BM * KT8, 32 * (NJ * wn + j) + (lane & 31), c));
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      }
     }
+    epilogue<OUT, false, 64>(p, acc, r0, end, n0, sx, sw, wt, wm, wn, lane);
+    block_sync();   // every wave is done reading the ring
   }
-  epilogue<OUT, false, 64>(p, acc, r0, end, n0, sx, sw, wt, wm, wn, lane);
 }
 
-// The most tiles of bm rows by bn columns the product can have.
-int64_t tiles(const I8Params& p, int bm, int bn) {
-  const int64_t m = p.M / bm + (p.offsets ? std::min<int64_t>(p.G, p.M) : 1);
-  return std::min<int64_t>(m, p.M) * ((p.N + bn - 1) / bn);
+// Tiles of bm rows by bn columns for `rows` rows in as many groups as the product may have.
+int64_t tiles(const I8Params& p, int64_t rows, int bm, int bn) {
+  const int64_t m = rows / bm + (p.offsets ? std::min<int64_t>(p.G, rows) : 1);
+  return std::min<int64_t>(m, rows) * ((p.N + bn - 1) / bn);
 }
 
+// 256 x 256 tiles once the expected rows make enough to fill three quarters of the CUs, else 128 x 128 ones if
+// they do, else 64 x 64. 1117 x 777 x 1104 in 9 groups: 55 us on 256 x 256, 10 us on 64 x 64. The products of
+// 1333 tokens on 16 of 128 experts (2048 x 768): 28 and 14 us on 256 x 256, 18 and 12 us on 128 x 128.
 template <Out OUT>
 void launch_i8(const I8Params& p, int grid, hipStream_t s) {
   constexpr int half = OUT == kGateUp ? 2 : 1;
-  // 256 x 256 tiles once they fill three quarters of the CUs, else 128 x 128 ones if they do, else 64 x 64
+  const int64_t rows = std::max<int64_t>(1, p.expect);
   const bool wide = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
-  if (wide && 4 * tiles(p, 256, 256 / half) >= 3 * grid) {
+  if (wide && 4 * tiles(p, rows, 256, 256 / half) >= 3 * grid) {
     k_i8_256<OUT><<<grid, NT256, 0, s>>>(p);
-  } else if (4 * tiles(p, 128, 128 / half) >= 3 * grid) {
-    k_i8_tile<OUT, 2, 2, 2><<<(unsigned)tiles(p, 128, 128 / half), NTHR, 0, s>>>(p);
+  } else if (4 * tiles(p, rows, 128, 128 / half) >= 3 * grid) {
+    k_i8_tile<OUT, 2, 2, 3><<<grid, NTHR, 0, s>>>(p);
   } else {
-    k_i8_tile<OUT, 1, 1, 4><<<(unsigned)tiles(p, 64, 64 / half), NTHR, 0, s>>>(p);
+    k_i8_tile<OUT, 1, 1, 4><<<2 * grid, NTHR, 0, s>>>(p);
   }
 }
 

@@ -1101,6 +1101,7 @@ moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t*
   p.offsets = offsets;
   p.y = y;
   p.M = M;
+  p.expect = M;
   p.N = (int)N;
   p.K = (int)K;
   p.G = G;
@@ -1223,6 +1224,7 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
   gp.offsets = rp.offsets;
   gp.y = h;
   gp.M = L.route.rows;
+  gp.expect = L.route.rows * d->E_local / d->E_total;   // a share's pairs, of evenly used experts
   gp.N = d->F;
   gp.K = d->H;
   gp.G = d->E_local;
@@ -1236,6 +1238,7 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
   dp.offsets = rp.offsets;
   dp.y = w + L.o;
   dp.M = L.route.rows;
+  dp.expect = gp.expect;
   dp.N = d->H;
   dp.K = d->F;
   dp.G = d->E_local;

@@ -225,6 +225,7 @@ struct I8Params {
   const int* offsets;    // [G + 1] first row of each group, or null (G = 1: all rows)
   void* y;               // [M, N] fp32 (f32) or bf16
   int64_t M;
+  int64_t expect;        // rows in the groups, as far as the host knows (chooses the tiles)
   int N, K, G;
   bool f32;
   // gate/up of the 8-bit layer (wu not null): w and ws are the gate's, y is h = weight silu(a) b in fp32, and

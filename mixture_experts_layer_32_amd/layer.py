@@ -14,6 +14,8 @@ from . import binding
 def _expect(t, name, shape, dtype, device):
     """Raises ValueError unless t is a contiguous tensor of this shape and dtype on this device: the
     C ABI receives bare pointers and cannot check any of it."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != device:
@@ -26,10 +28,14 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _current(device):
-    """Raises ValueError unless `device` is the calling thread's current GPU, whose streams the library uses."""
+def _on(device, stream):
+    """The stream handle for a call on `device`: the given stream's, or the current one's. Raises ValueError
+    unless `device` is the calling thread's current GPU, whose streams the library uses."""
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"{device} is not the current GPU (torch.cuda.set_device)")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _device(device):
@@ -169,7 +175,7 @@ class FewTokenLayer:
 
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         el, dev = self.dtype, self.device
-        _current(dev)
+        stream = _on(dev, stream)
         if y is None:
             y = torch.empty(self._x, dtype=el, device=dev)
         else:
@@ -210,19 +216,19 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     or as the (weight, scales) pair of int8_matmul and Int8Layer."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a tensor of at least one dimension")
-    t, dev, lead = _int8_type(x.dtype), x.device, x.shape[:-1]
+    t, shape, dev = _int8_type(x.dtype), x.shape, x.device
     if not x.is_contiguous():
         raise ValueError("x: expected a contiguous tensor")
-    _current(dev)
+    stream = _on(dev, stream)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        q = torch.empty(shape, dtype=torch.int8, device=dev)
     else:
-        _expect(q, "q", x.shape, torch.int8, dev)
+        _expect(q, "q", shape, torch.int8, dev)
     if scales is None:
-        scales = torch.empty(lead, dtype=torch.float32, device=dev)
+        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     else:
-        _expect(scales, "scales", lead, torch.float32, dev)
-    binding.moe_int8_quantize(x, t, lead.numel(), x.shape[-1], q, scales, stream)
+        _expect(scales, "scales", shape[:-1], torch.float32, dev)
+    binding.moe_int8_quantize(x, t, scales.numel(), shape[-1], q, scales, stream)
     return q, scales
 
 
@@ -232,18 +238,22 @@ def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bflo
     outside the groups are left as they were (a y made here holds anything there)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (2 if offsets is None else 3):
         raise ValueError("expected x [M, K] and w [N, K], or w [G, N, K] with offsets")
-    dev, (M, K), N = x.device, x.shape, w.shape[-2]
-    G = 1 if offsets is None else w.shape[0]
-    _current(dev)
+    dev, (M, K) = x.device, x.shape
+    stream = _on(dev, stream)
     _expect(x, "x", (M, K), torch.int8, dev)
-    _expect(w, "w", (N, K) if offsets is None else (G, N, K), torch.int8, dev)
     _expect(x_scales, "x_scales", (M,), torch.float32, dev)
-    _expect(w_scales, "w_scales", (N,) if offsets is None else (G, N), torch.float32, dev)
-    if offsets is not None:
+    if offsets is None:
+        G, N = 1, w.shape[0]
+        _expect(w, "w", (N, K), torch.int8, dev)
+        _expect(w_scales, "w_scales", (N,), torch.float32, dev)
+    else:
+        G, N = w.shape[0], w.shape[1]
+        _expect(w, "w", (G, N, K), torch.int8, dev)
+        _expect(w_scales, "w_scales", (G, N), torch.float32, dev)
         _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
     if y is None:
         t = _int8_type(dtype)
-        y = torch.empty(M, N, dtype=dtype, device=dev)
+        y = torch.empty((M, N), dtype=dtype, device=dev)
     else:
         t = _int8_type(y.dtype)
         _expect(y, "y", (M, N), y.dtype, dev)
@@ -265,7 +275,7 @@ class Int8Layer:
 
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         dev = self.device
-        _current(dev)
+        stream = _on(dev, stream)
         if y is None:
             y = torch.empty(self._x, dtype=torch.bfloat16, device=dev)
         else:
