@@ -18,8 +18,9 @@
 //   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
 //                 each keeping its own sum per token, and the sums are added in a fixed order. No
 //                 partial sums in memory, no atomics on sums: repeated calls give the same bits.
-// Experts of more than 16 tokens ("heavy") take 16 x 16 MFMA tiles in both, 16 tokens a column group, so that
-// their weights too are read once.
+// Experts of more than 8 tokens ("heavy") take 16 x 16 MFMA tiles with their tokens' rows in LDS, so that
+// their weights too are read once: in k_few_gateup and, of more than 16 tokens in all, in k_few_heavy ahead of
+// k_few_down (of 9 to 16, another launch would cost more than it gives).
 //
 // h is kept in fp32's accuracy: as fp32, or in bf16 mode as the pair hi = bf16(h), lo = bf16(h - hi),
 // whose two products cost matrix time that a read-bound kernel does not miss.
@@ -134,7 +135,7 @@ __device__ __forceinline__ void wave_topk(const float* row, int E, int k, int la
   }
 }
 
-// Experts with pairs, in classes by their number of tokens: more than 16 ("heavy"), 9-16, 5-8, 1-4.
+// Experts with pairs, in classes by their number of tokens: more than 16, 9-16 (both "heavy"), 5-8, 1-4.
 constexpr int kClasses = 4;
 __device__ __forceinline__ int few_class(int n) { return n > 16 ? 0 : n > 8 ? 1 : n > 4 ? 2 : 3; }
 
@@ -284,12 +285,10 @@ __device__ __forceinline__ int4 uniform4(const int4& v) {
 // ------------------------------------------------------------------------------------------------
 // NQ times 4 weight rows times NS sets of 4 tokens, segments [s0, s1) of 256 bytes. Each lane's pointers
 // are at its own 16-byte piece of the rows. Two buffers of U segments: the next one's loads are issued
-// before the MFMAs of the current (past the run's end, the last segment again). 8-bit rows may end inside a
-// segment: its missing pieces (from byte `rowb` on) count as zero.
+// before the MFMAs of the current (past the run's end, the last segment again).
 template <class T, int NQ, int NS, int U>
-__device__ __forceinline__ void dot4(const char* const (&pw)[NQ], const char* const (&px)[NS], int s0, int s1, int rowb,
+__device__ __forceinline__ void dot4(const char* const (&pw)[NQ], const char* const (&px)[NS], int s0, int s1,
                                      typename Mma4<T>::Acc (&acc)[NQ][NS]) {
-  const int piece = 16 * ((threadIdx.x & 63) >> 2);
   struct Buf {
     uint4 a[NQ][U], b[NS][U];
   };
@@ -297,11 +296,10 @@ __device__ __forceinline__ void dot4(const char* const (&pw)[NQ], const char* co
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int o = min(s + i, s1 - 1) * kSeg;
-      const bool in = sizeof(T) > 1 || o + piece < rowb;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) v.a[q][i] = in ? ld16_nt(pw[q] + o) : make_uint4(0, 0, 0, 0);
+      for (int q = 0; q < NQ; ++q) v.a[q][i] = ld16_nt(pw[q] + o);
 #pragma unroll
-      for (int t = 0; t < NS; ++t) v.b[t][i] = in ? ld16(px[t] + o) : make_uint4(0, 0, 0, 0);
+      for (int t = 0; t < NS; ++t) v.b[t][i] = ld16(px[t] + o);
     }
   };
   auto mul = [&](const Buf& v, int s) {
@@ -368,8 +366,8 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
         max(max(mag_bits(h[0]), mag_bits(h[1])), max(mag_bits(h[2]), mag_bits(h[3])));
 }
 
-// LDS of gateup_heavy's and gateup_unit's partial sums; only more than 16 tokens can make an expert heavy
-__host__ __device__ inline int few_red_bytes(int T) { return T > 16 ? kGW * 2 * 64 * 16 : kGW * 32 * 16; }
+// LDS of heavy_task's stages and gateup_unit's partial sums; more than 8 tokens can make an expert heavy
+__host__ __device__ inline int few_red_bytes(int T) { return T > 16 ? 2 * 64 * kSeg : T > 8 ? 2 * 16 * kSeg : kGW * 32 * 16; }
 
 // One unit of the gate/up products by a wave: rows f0 .. f0+3 of expert e, pairs base .. base+cnt-1
 // (cnt <= 4 NS). PART: only part kp of ks of H, whose sums go to red [16][2] of the wave instead.
@@ -393,7 +391,7 @@ __device__ __forceinline__ void gateup_unit(const FewParams& p, const FewRoute& 
   Acc acc[2][NS];
   clear(acc);
   const int S = (int)(rowb / kSeg), s0 = PART ? kp * S / ks : 0, s1 = PART ? (kp + 1) * S / ks : S;
-  dot4<T, 2, NS, NS == 1 ? (ES == 1 ? 2 : 4) : NS == 2 ? 2 : 1>(pw, px, s0, s1, (int)rowb, acc);
+  dot4<T, 2, NS, NS == 1 ? (ES == 1 ? 2 : 4) : NS == 2 ? 2 : 1>(pw, px, s0, s1, acc);
 #pragma unroll
   for (int t = 0; t < NS; ++t) {
     Acc a, b;
@@ -435,70 +433,166 @@ __device__ __forceinline__ void gateup_join(const FewParams& p, const FewRoute& 
   }
 }
 
-// rows f0 .. f0+15 of a heavy expert by the whole workgroup, on 16 x 16 tiles with the weights read once for
-// all its tokens (up to 16 NG): the waves split H, red: [kGW][2][64] accumulators
-template <class T, int NG>
-__device__ __forceinline__ void gateup_heavy(const FewParams& p, const FewRoute& R, char* red_, int e, int base, int cnt,
-                                             int f0) {
+// ------------------------------------------------------------------------------------------------
+// 128 weight rows of an expert with up to 16 NG tokens by a workgroup of 8 waves, on 16 x 16 tiles. The
+// expert's rows of x (DOWN: of h) go through LDS 256 bytes of contraction at a time, so that each is read
+// once per 128 weight rows; a wave takes 32 of those rows straight from memory, two chunks of 256 bytes ahead.
+// Waves w and w + 4 take the same rows and each half of a chunk (16 rows a wave and whole chunks: twice the LDS
+// reads, which then bound it, 70 us for 64 tokens on 8 experts of 4096 x 1536), and add their sums at the end.
+// Not DOWN: gate and up rows r0 .. r0+63, a wave's 16 of each. DOWN: rows r0 .. r0+127 of W_down, and the
+// products (8-bit: with their scales) go to oh [pairs, H].
+// LDS: [2 stages][planes][16 NG rows][256 bytes], 16-byte piece c of row r at slot c ^ (r & 15); at the end
+// [4 waves][2][NG][64] sums.
+constexpr int heavy_lds(int ng, int planes) { return 2 * planes * 16 * ng * kSeg; }
+template <class T, int NG, bool DOWN>
+__device__ __forceinline__ void heavy_task(const FewParams& p, const int* stok, const float* swt, char* lds, int e, int base,
+                                           int cnt, int r0) {
   typedef typename Mma4<T>::Acc Acc;
-  constexpr int ES = sizeof(T);
-  const int lane = threadIdx.x & 63, w = eng::wave_id();
-  const size_t rowb = (size_t)p.H * ES, wo = ((size_t)e * p.F + f0 + (lane & 15)) * rowb + 16 * (lane >> 4);
-  const char *pg = static_cast<const char*>(p.wg) + wo, *pu = static_cast<const char*>(p.wu) + wo;
-  const char* px[NG];
+  constexpr int ES = sizeof(T), NP = DOWN && ES == 2 ? 2 : 1, BL = (NG + 1) / 2, PLANE = 16 * NG * kSeg;
+  const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), rg = w & 3, kh = w >> 2;
+  const int rowb = (DOWN ? p.F : p.H) * ES, nc = (rowb + kSeg - 1) / kSeg;
+  // this thread's pieces of the staged rows (one column group: the first half of the threads)
+  const bool puts = NG > 1 || tid < 256;
+  const char* pb[NP][BL];
+  int at[BL];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
-    px[g] = static_cast<const char*>(p.x) + R.stok[base + min(16 * g + (lane & 15), cnt - 1)] * rowb + 16 * (lane >> 4);
-  const int S = (int)(rowb / kStep), s0 = w * S / kGW, s1 = (w + 1) * S / kGW;
+  for (int j = 0; j < BL; ++j) {
+    const int i = (tid + 512 * j) % (256 * NG), r = i >> 4, c = i & 15, pos = base + min(r, cnt - 1);
+    at[j] = r * kSeg + ((c ^ (r & 15)) << 4);
+    if constexpr (DOWN) {
+      pb[0][j] = (ES == 1 ? reinterpret_cast<const char*>(p.hq) : static_cast<const char*>(p.h)) + (size_t)pos * rowb + 16 * c;
+      if constexpr (NP == 2) pb[1][j] = static_cast<const char*>(p.hlo) + (size_t)pos * rowb + 16 * c;
+    } else {
+      pb[0][j] = static_cast<const char*>(p.x) + (size_t)stok[pos] * rowb + 16 * c;
+    }
+  }
+  // this lane's two weight rows, at its 16-byte piece of its half of a chunk
+  const int wr = lane & 15, q4 = lane >> 4;
+  const char* pa[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const size_t row = DOWN ? (size_t)e * p.H + r0 + 32 * rg + 16 * m + wr : (size_t)e * p.F + r0 + 16 * rg + wr;
+    pa[m] = static_cast<const char*>(DOWN ? p.wd : m == 0 ? p.wg : p.wu) + row * rowb + 2 * kStep * kh + 16 * q4;
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  struct Rows {
+    uint4 a[2][2];
+  };
+  uint4 bb[NP][BL];
+  // The chunks are taken from a place of the workgroup's own on: in step, the workgroups' rows, a power of two
+  // apart, would meet on the same memory channels (8 % of the time).
+  const int rot = (blockIdx.x * 7) % nc;
+  auto at_chunk = [&](int c) { return (c + rot < nc ? c + rot : c + rot - nc) * kSeg; };
+  // 8-bit rows of W_down may end in the middle of the last 256 bytes: the wave of the missing half takes the first
+  // half again, against staged rows of zeros
+  constexpr bool TAIL = DOWN && ES == 1;
+  auto load_a = [&](Rows& v, int c) {
+    int o = at_chunk(c);
+    if (TAIL && o + 2 * kStep * kh >= rowb) o -= 2 * kStep * kh;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) v.a[m][s] = ld16(pa[m] + o + kStep * s);
+  };
+  auto load_b = [&](int c) {
+    const int o = at_chunk(c);
+#pragma unroll
+    for (int j = 0; j < BL; ++j) {
+      const bool in = !TAIL || o + 16 * (tid & 15) < rowb;
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        bb[q][j] = ld16(pb[q][j] + (in ? o : 0));
+        if (!in) bb[q][j] = zero;
+      }
+    }
+  };
+  auto put_b = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < BL; ++j)
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+        if (puts) st16(lds + ((c & 1) * NP + q) * PLANE + at[j], bb[q][j]);
+    __syncthreads();
+  };
   Acc acc[2][NG];
   clear(acc);
-  constexpr int U = NG == 4 ? 2 : 4;
-  for (int s = s0; s < s1; s += U) {
-    uint4 a[2][U], b[NG][U];
+  // chunk c: the next one's staged rows and the weights of the one after it are asked for first
+  auto step = [&](const Rows& cur, Rows& fill, int c) {
+    if (c + 1 < nc) load_b(c + 1);
+    if (c + 2 < nc) load_a(fill, c + 2);
+    const char* st = lds + (c & 1) * NP * PLANE;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int o = min(s + i, s1 - 1) * kStep;
-      a[0][i] = ld16(pg + o);
-      a[1][i] = ld16(pu + o);
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) b[g][i] = ld16(px[g] + o);
-    }
+      for (int g = 0; g < NG; ++g) {
+        const int r = 16 * g + wr, o = r * kSeg + (((4 * (2 * kh + s) + q4) ^ (r & 15)) << 4);
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (s + i < s1)
+        for (int q = 0; q < NP; ++q) {
+          const uint4 b = ld16(st + q * PLANE + o);
+          mma16x16(acc[0][g], cur.a[0][s], b, T());
+          mma16x16(acc[1][g], cur.a[1][s], b, T());
+        }
+      }
+    if (c + 1 < nc) put_b(c + 1);
+  };
+  Rows a0, a1, a2;
+  load_b(0);
+  load_a(a0, 0);
+  if (nc > 1) load_a(a1, 1);
+  put_b(0);
+  for (int c = 0; c < nc; c += 3) {
+    step(a0, a2, c);
+    if (c + 1 < nc) step(a1, a0, c + 1);
+    if (c + 2 < nc) step(a2, a1, c + 2);
+  }
+  __syncthreads();   // the stages are free
+  Acc* sums = reinterpret_cast<Acc*>(lds) + rg * 2 * NG * 64 + lane;
+  static_assert(4 * 2 * NG * 64 * 16 <= heavy_lds(NG, 1), "the sums fit the stages");
+  if (kh == 1) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sums[(m * NG + g) * 64] = acc[m][g];
+  }
+  __syncthreads();
+  if (kh == 0) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) acc[m][g] += sums[(m * NG + g) * 64];
+    // rows 4 q4 .. + 3 of the tile, column wr
+    if constexpr (DOWN) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int h = r0 + 32 * rg + 16 * m + 4 * q4;
+        float4 sd = make_float4(1.f, 1.f, 1.f, 1.f);
+        if constexpr (ES == 1) sd = ld4f(p.sd + (size_t)e * p.H + h);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          mma16x16(acc[0][g], a[0][i], b[g][i], T());
-          mma16x16(acc[1][g], a[1][i], b[g][i], T());
+          const int c = 16 * g + wr;
+          if (c < cnt) {
+            const float hs = ES == 1 ? p.hs[base + c] : 1.f;
+            *reinterpret_cast<float4*>(p.oh + (size_t)(base + c) * p.H + h) =
+                make_float4((float)acc[m][g][0] * (hs * sd.x), (float)acc[m][g][1] * (hs * sd.y),
+                            (float)acc[m][g][2] * (hs * sd.z), (float)acc[m][g][3] * (hs * sd.w));
+          }
         }
-  }
-  Acc* red = reinterpret_cast<Acc*>(red_);
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    if (16 * g >= cnt) break;
-    red[(2 * w) * 64 + lane] = acc[0][g];
-    red[(2 * w + 1) * 64 + lane] = acc[1][g];
-    __syncthreads();
-    if (w == 0) {   // lane: rows f0 + 4 (lane / 16) .. + 3 of column lane % 16
-      const int c = 16 * g + (lane & 15), f = f0 + 4 * (lane >> 4);
-      Acc sa = red[lane], sb = red[64 + lane];
-#pragma unroll
-      for (int v = 1; v < kGW; ++v) {
-        sa += red[2 * v * 64 + lane];
-        sb += red[(2 * v + 1) * 64 + lane];
       }
-      if (c < cnt) {
-        const int pos = base + c;
-        float4 sg = {}, su = {};
-        if constexpr (ES == 1) {
-          sg = ld4f(p.sg + (size_t)e * p.F + f);
-          su = ld4f(p.su + (size_t)e * p.F + f);
-        }
-        store_h<T>(p, pos, R.stok[pos], R.swt[pos], f, sa, sb, sg, su);
+    } else {
+      const int f = r0 + 16 * rg + 4 * q4;
+      float4 sg = {}, su = {};
+      if constexpr (ES == 1) {
+        sg = ld4f(p.sg + (size_t)e * p.F + f);
+        su = ld4f(p.su + (size_t)e * p.F + f);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int c = 16 * g + wr;
+        if (c < cnt) store_h<T>(p, base + c, stok[base + c], swt[base + c], f, acc[0][g], acc[1][g], sg, su);
       }
     }
-    __syncthreads();
   }
+  __syncthreads();   // the next task's stages
 }
 
 template <class T>
@@ -507,33 +601,43 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
   const int tid = threadIdx.x, n = p.T * p.k;
   const FewRoute R(smem + few_red_bytes(p.T), p.El, n);
   few_route<kGW>(R, p);
-  const int nact = R.cls[kClasses], heavy = R.cls[1];
+  const int nact = R.cls[kClasses], heavy = R.cls[2];   // more than 8 tokens
   if (blockIdx.x == 0) {   // the routing for k_few_down
     if (tid <= kClasses) p.r_cls[tid] = R.cls[tid];
     if (tid == 0) p.r_cls[kClasses + 1] = R.off[p.El];
     for (int i = tid; i < nact; i += kGW * 64) p.r_ent[i] = R.ent[i];
     for (int i = tid; i < n; i += kGW * 64) p.r_tok[i] = i < R.off[p.El] ? R.stok[i] : 0;
   }
-  const int nh = p.F / 16, ntask = heavy * nh;
+  static_assert(kGW == 8, "heavy_task");
+  const int nh = p.F / 64, ntask = heavy * nh;
   for (int task = blockIdx.x; task < ntask; task += gridDim.x) {
-    const int a = task / nh, f0 = (task - a * nh) * 16;
+    const int a = task / nh, f0 = (task - a * nh) * 64;
     const int4 x = uniform4(R.ent[a]);
-    if (x.z <= 32) gateup_heavy<T, 2>(p, R, smem, x.x, x.y, x.z, f0);
-    else gateup_heavy<T, 4>(p, R, smem, x.x, x.y, x.z, f0);
+    if (x.z <= 16) heavy_task<T, 1, false>(p, R.stok, R.swt, smem, x.x, x.y, x.z, f0);
+    else if (x.z <= 32) heavy_task<T, 2, false>(p, R.stok, R.swt, smem, x.x, x.y, x.z, f0);
+    else heavy_task<T, 4, false>(p, R.stok, R.swt, smem, x.x, x.y, x.z, f0);
   }
   // Consecutive units go to different workgroups: a few units still spread over all CUs. Where the waves
   // outnumber the units, two or four share a unit, so that more of its loads are in flight at once.
   typedef typename Mma4<T>::Acc Acc;
   const int nf = p.F / 4, units = (nact - heavy) * nf, w = eng::wave_id(), waves = kGW * gridDim.x;
   const int ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
+  auto light = [&](int u) {
+    const int a = u / nf, f0 = (u - a * nf) * 4;
+    const int4 x = uniform4(R.ent[heavy + a]);
+    if (x.z <= 4) gateup_unit<T, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    else gateup_unit<T, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+  };
   if (ks == 1) {
-    for (int u = w * gridDim.x + blockIdx.x; u < units; u += waves) {
-      const int a = u / nf, f0 = (u - a * nf) * 4;
-      const int4 x = uniform4(R.ent[heavy + a]);
-      if (x.z <= 4) gateup_unit<T, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
-      else if (x.z <= 8) gateup_unit<T, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
-      else gateup_unit<T, kSets, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
-    }
+    // a heavy task (16 units' weights) is about three rounds of a workgroup's units: the workgroups without one
+    // take those rounds' units first
+    const int nb = gridDim.x, hb = ntask % nb, early = hb ? 3 * kGW * (nb - hb) : 0;
+    if (hb && (int)blockIdx.x >= hb)
+      for (int r = 0; r < 3; ++r) {
+        const int u = (r * kGW + w) * (nb - hb) + blockIdx.x - hb;
+        if (u < units) light(u);
+      }
+    for (int u = early + w * nb + blockIdx.x; u < units; u += waves) light(u);
   } else {   // one round; a heavy task's last barrier is behind its reads of smem
     const int kp = w & (ks - 1), u = (w / ks) * gridDim.x + blockIdx.x, a = u / nf, f0 = (u - a * nf) * 4;
     Acc* red = reinterpret_cast<Acc*>(smem) + 32 * w;   // [16 tokens][gate, up]
@@ -541,8 +645,7 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
     if (u < units) {
       x = uniform4(R.ent[heavy + a]);
       if (x.z <= 4) gateup_unit<T, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
-      else if (x.z <= 8) gateup_unit<T, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
-      else gateup_unit<T, kSets, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else gateup_unit<T, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
     }
     __syncthreads();
     if (u < units && kp == 0) gateup_join<T>(p, R, red, x.x, x.y, x.z, f0, ks);
@@ -568,6 +671,7 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
   if (c >= end) return;
   struct Stage {
     uint4 a[NQ][U], b[NS][U][NB];
+    bool in;      // 8-bit: the row has this lane's piece of the last segment (else the row's first piece is in a and b)
     int4 x;       // its expert
     int n;        // segments in it
     bool last;    // the wave's last of this expert
@@ -579,20 +683,20 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
     const char* pw = static_cast<const char*>(p.wd) + ((size_t)v.x.x * p.H + h0 + j) * rowb + piece;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int o = min(s + i, s + v.n - 1) * kSeg;
-      const bool in = ES > 1 || o + piece < (int)rowb;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
+      int o = min(s + i, s + v.n - 1) * kSeg;
+      v.in = ES > 1 || o + piece < (int)rowb;
+      if (!v.in) o = -piece;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) v.a[q][i] = in ? ld16_nt(pw + (size_t)(4 * q) * rowb + o) : zero;
+      for (int q = 0; q < NQ; ++q) v.a[q][i] = ld16_nt(pw + (ptrdiff_t)(4 * q) * (ptrdiff_t)rowb + o);
 #pragma unroll
       for (int t = 0; t < NS; ++t) {
         const size_t pos = v.x.y + min(4 * t + j, v.x.z - 1);
         if constexpr (FLY) {
-          const float* ph = static_cast<const float*>(p.h) + pos * p.F + (in ? o + piece : 0);
+          const float* ph = static_cast<const float*>(p.h) + pos * p.F + (o + piece);
 #pragma unroll
           for (int r = 0; r < 4; ++r) v.b[t][i][r] = ld16(ph + 4 * r);
         } else if constexpr (ES == 1) {
-          v.b[t][i][0] = in ? ld16(p.hq + pos * rowb + o + piece) : zero;
+          v.b[t][i][0] = ld16(p.hq + pos * rowb + (o + piece));
         } else {
           v.b[t][i][0] = ld16(static_cast<const char*>(p.h) + pos * rowb + o + piece);
           if constexpr (ES == 2) v.b[t][i][1] = ld16(static_cast<const char*>(p.hlo) + pos * rowb + o + piece);
@@ -618,7 +722,7 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
       if (i < v.n)
 #pragma unroll
         for (int t = 0; t < NS; ++t) {
-          uint4 b = v.b[t][i][0];
+          uint4 b = v.b[t][i][0];   // 8-bit: of a missing piece, zero (only the last segment can miss any)
           if constexpr (FLY) {
             float f[16];
 #pragma unroll
@@ -632,6 +736,8 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
             q8_pack<true>(f, qr, o);
             b = make_uint4(o[0], o[1], o[2], o[3]);
           }
+          if constexpr (ES == 1)
+            if (i == v.n - 1 && !v.in) b = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             Mma4<T>::go(acc[q][t], v.a[q][i], b);
@@ -688,8 +794,8 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
   }
 }
 
-// the same for a pair run of up to 16 NG on 16 x 16 tiles (rows from 4 NQ on repeat and are dropped), so
-// that a heavy expert's weights are read once; steps [s0, s1) of 64 bytes
+// the same for a pair run of up to 16 NG on 16 x 16 tiles (rows from 4 NQ on repeat and are dropped); steps
+// [s0, s1) of 64 bytes
 template <class T, int NQ, int NG>
 __device__ __forceinline__ void down_heavy(const FewParams& p, const int* stok, float* ya, int e, int base, int cnt,
                                            int h0, int s0, int s1) {
@@ -785,18 +891,21 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   };
   int c, end;
   if constexpr (!FLY) {
-    part(0, c, end);
-    for (; c < end;) {
-      const int a = c / S, s0 = c - a * S, s1 = min(S, s0 + end - c);
-      // a 256-byte segment is four 64-byte steps; an 8-bit row may end in the middle of its last one
-      const int t0 = 4 * s0, t1 = min(4 * s1, p.F * ES / kStep);
+    // heavy experts: k_few_heavy's products, a wave an expert (whose pairs are of different tokens)
+    const int done = p.T > 16 ? cls[2] : 0;
+    for (int a = w; a < done; a += kDW) {
       const int4 x = uniform4(ent[a]);
-      if (x.z <= 32) down_heavy<T, NQ, 2>(p, stok, mine, x.x, x.y, x.z, h0, t0, t1);
-      else down_heavy<T, NQ, 4>(p, stok, mine, x.x, x.y, x.z, h0, t0, t1);
-      c += s1 - s0;
+      for (int i = tid & 63; i < x.z * NQ; i += 64) {   // (pair, 4 rows)
+        const int c = i / NQ, q = i % NQ;
+        const float4 o = *reinterpret_cast<const float4*>(p.oh + (size_t)(x.y + c) * p.H + h0 + 4 * q);
+        float4* y = reinterpret_cast<float4*>(mine + (stok[x.y + c] * NQ + q) * 4);
+        const float4 v = *y;
+        *y = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      }
     }
     part(1, c, end);
-    if constexpr (NQ < 4) {
+    if (done) {
+    } else if constexpr (NQ < 4) {
       down_stream<T, NQ, 4, 1, ES == 1 || NQ == 1, false>(p, ent + cls[1], stok, hm, mine, h0, S, c, end);
     } else {   // 16 rows by 16 tokens in 4 x 4 form would spill
       for (; c < end;) {
@@ -810,7 +919,7 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
     down_stream<T, NQ, 2, 1, ES != 2 || NQ < 4, false>(p, ent + cls[2], stok, hm, mine, h0, S, c, end);
   }
   part(3, c, end);
-  down_stream<T, NQ, 1, FLY || NQ == 4 ? 1 : 2, !FLY, FLY>(p, ent + cls[3], stok, hm, mine, h0, S, c, end);
+  down_stream<T, NQ, 1, FLY || NQ == 4 ? 1 : ES == 1 ? 3 : 2, !FLY, FLY>(p, ent + cls[3], stok, hm, mine, h0, S, c, end);
   __syncthreads();
   for (int i = tid; i < p.T * NR; i += kDW * 64) {
     float s = 0.f;
@@ -819,6 +928,20 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
     const size_t at = (size_t)(i / NR) * p.H + h0 + i % NR;
     if constexpr (ES == 4) static_cast<float*>(p.y)[at] = s;
     else static_cast<bf16*>(p.y)[at] = (bf16)s;
+  }
+}
+
+// the down products of the heavy experts, into oh
+template <class T>
+__global__ __launch_bounds__(512, 4) void k_few_heavy(FewParams p) {
+  __shared__ __attribute__((aligned(16))) char smem[heavy_lds(4, sizeof(T) == 2 ? 2 : 1)];
+  const int heavy = __builtin_amdgcn_readfirstlane(p.r_cls[2]), nh = p.H / 128;
+  for (int task = blockIdx.x; task < heavy * nh; task += gridDim.x) {
+    const int a = task / nh;
+    const int4 x = uniform4(p.r_ent[a]);
+    if (x.z <= 16) heavy_task<T, 1, true>(p, nullptr, nullptr, smem, x.x, x.y, x.z, (task - a * nh) * 128);
+    else if (x.z <= 32) heavy_task<T, 2, true>(p, nullptr, nullptr, smem, x.x, x.y, x.z, (task - a * nh) * 128);
+    else heavy_task<T, 4, true>(p, nullptr, nullptr, smem, x.x, x.y, x.z, (task - a * nh) * 128);
   }
 }
 
@@ -836,7 +959,7 @@ __device__ __forceinline__ void router_tile(const FewParams& p, float* red, int 
   const int S = (int)(rowb / kSeg);
   f32x4 acc[1][NS];
   clear(acc);
-  dot4<T, 1, NS, NS == 4 ? 1 : 2>(pw, px, w * S / kPW, (w + 1) * S / kPW, (int)rowb, acc);
+  dot4<T, 1, NS, NS == 4 ? 1 : 2>(pw, px, w * S / kPW, (w + 1) * S / kPW, acc);
 #pragma unroll
   for (int t = 0; t < NS; ++t)
 #pragma unroll
@@ -930,13 +1053,23 @@ hipError_t launch_layer(const FewParams& p, hipStream_t s) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
     prof_mark_end(s);
   }
+  const size_t lds = few_red_bytes(p.T) + FewRoute::bytes(p.El, n);
+  if (lds > 65536 && (err = hipFuncSetAttribute(reinterpret_cast<const void*>(k_few_gateup<T>),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)
+    return err;
   prof_mark_begin("few_gateup", s);
-  k_few_gateup<T><<<grid, kGW * 64, few_red_bytes(p.T) + FewRoute::bytes(p.El, n), s>>>(p);
+  k_few_gateup<T><<<grid, kGW * 64, lds, s>>>(p);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   prof_mark_end(s);
   if (sizeof(T) == 1 && !FLY &&
       (err = launch_int8_quant(p.h, true, n, p.F, p.r_cls + kClasses + 1, p.hq, p.hs, "int8_quant_h", s)) != hipSuccess)
     return err;
+  if (!FLY && p.T > 16) {
+    prof_mark_begin("few_heavy", s);
+    k_few_heavy<T><<<std::min(n / 9 * (p.H / 128), persistent_grid(2)), 512, 0, s>>>(p);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+  }
   // as many rows per workgroup (each read of h serves them all) as leave every CU one
   if (p.H >= 4096) return launch_down<T, 4, FLY>(p, s);
   return p.H >= 2048 ? launch_down<T, 2, FLY>(p, s) : launch_down<T, 1, FLY>(p, s);

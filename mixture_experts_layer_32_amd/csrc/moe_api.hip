@@ -954,7 +954,7 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
 
 namespace {
 struct FewLayout {
-  size_t cls, ent, tok, idx, wt, h, hlo, xq, xs, hq, hs, hmax, total;
+  size_t cls, ent, tok, idx, wt, h, hlo, xq, xs, hq, hs, hmax, oh, total;
 };
 
 FewLayout few_layout(const moe_desc& d, bool int8) {
@@ -979,6 +979,7 @@ FewLayout few_layout(const moe_desc& d, bool int8) {
   L.hq = take(int8 ? n * F : 0);
   L.hs = take(int8 ? n * 4 : 0);
   L.hmax = take(int8 && d.T <= 4 ? n * F : 0);
+  L.oh = take(d.T > 16 ? n * d.H * 4 : 0);
   L.total = off;
   return L;
 }
@@ -1000,6 +1001,7 @@ FewParams few_params(const moe_desc& d, const FewLayout& L, const void* x, const
   p.r_cls = reinterpret_cast<int*>(w + L.cls);
   p.r_ent = reinterpret_cast<int4*>(w + L.ent);
   p.r_tok = reinterpret_cast<int*>(w + L.tok);
+  p.oh = reinterpret_cast<float*>(w + L.oh);
   p.r_idx = reinterpret_cast<int*>(w + L.idx);
   p.r_wt = reinterpret_cast<float*>(w + L.wt);
   p.T = (int)d.T;
