@@ -31,10 +31,11 @@ def _expect(t, name, shape, dtype, device):
 def _on(device, stream):
     """The stream handle for a call on `device`: the given stream's, or the current one's. Raises ValueError
     unless `device` is the calling thread's current GPU, whose streams the library uses."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    i = device.index
+    if device.type != "cuda" or i != torch.cuda.current_device():
         raise ValueError(f"{device} is not the current GPU (torch.cuda.set_device)")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(i)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -206,9 +207,10 @@ _INT8_TYPES = {torch.float32: binding.TYPES["fp32"], torch.bfloat16: binding.TYP
 
 
 def _int8_type(dtype):
-    if dtype not in _INT8_TYPES:
+    t = _INT8_TYPES.get(dtype)
+    if t is None:
         raise ValueError(f"expected dtype torch.float32 or torch.bfloat16, got {dtype}")
-    return _INT8_TYPES[dtype]
+    return t
 
 
 def int8_quantize(x, q=None, scales=None, stream=None):
@@ -221,14 +223,15 @@ def int8_quantize(x, q=None, scales=None, stream=None):
         raise ValueError("x: expected a contiguous tensor")
     stream = _on(dev, stream)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8)
     else:
         _expect(q, "q", shape, torch.int8, dev)
     if scales is None:
         scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     else:
         _expect(scales, "scales", shape[:-1], torch.float32, dev)
-    binding.moe_int8_quantize(x, t, scales.numel(), shape[-1], q, scales, stream)
+    K = shape[-1]
+    binding.moe_int8_quantize(x, t, x.numel() // K if K else 0, K, q, scales, stream)
     return q, scales
 
 
