@@ -13,7 +13,7 @@
 //                 of x. Only launched where one of the two is asked for.
 //   k_few_topk    the tokens' experts and weights; only launched for more than 16 tokens.
 //   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 16 tokens, chooses them); then its
-//                 waves take (expert, 4 rows of F) units, each on its own, and write h = w silu(a) b into
+//                 waves take (expert, 4 or 8 rows of F) units, each on its own, and write h = w silu(a) b into
 //                 the workspace.
 //   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
 //                 each keeping its own sum per token, and the sums are added in a fixed order. No
@@ -369,67 +369,76 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
 // LDS of heavy_task's stages and gateup_unit's partial sums; more than 8 tokens can make an expert heavy
 __host__ __device__ inline int few_red_bytes(int T) { return T > 16 ? 2 * 64 * kSeg : T > 8 ? 2 * 16 * kSeg : kGW * 32 * 16; }
 
-// One unit of the gate/up products by a wave: rows f0 .. f0+3 of expert e, pairs base .. base+cnt-1
-// (cnt <= 4 NS). PART: only part kp of ks of H, whose sums go to red [16][2] of the wave instead.
-template <class T, int NS, bool PART>
+// One unit of the gate/up products by a wave: rows f0 .. f0 + 4 QR - 1 of expert e, pairs base .. base+cnt-1
+// (cnt <= 4 NS). QR = 2 with 5 to 8 tokens: their rows of x are read once for 8 rows of F (8 experts of 8 tokens,
+// 4096 x 1536: 59 -> 49 us). PART: only part kp of ks of H, whose sums go to red [token][QR][2] of the wave instead.
+template <class T, int QR, int NS, bool PART>
 __device__ __forceinline__ void gateup_unit(const FewParams& p, const FewRoute& R, typename Mma4<T>::Acc* red, int e,
                                             int base, int cnt, int f0, int ks, int kp) {
   typedef typename Mma4<T>::Acc Acc;
   constexpr int ES = sizeof(T);
   const int lane = threadIdx.x & 63, j = lane & 3, piece = 16 * (lane >> 2);
-  const size_t rowb = (size_t)p.H * ES, wo = ((size_t)e * p.F + f0 + j) * rowb + piece;
-  const char* pw[2] = {static_cast<const char*>(p.wg) + wo, static_cast<const char*>(p.wu) + wo};
+  const size_t rowb = (size_t)p.H * ES;
+  const char* pw[2 * QR];
+  float4 sg[QR] = {}, su[QR] = {};
+#pragma unroll
+  for (int q = 0; q < QR; ++q) {
+    const size_t wo = ((size_t)e * p.F + f0 + 4 * q + j) * rowb + piece;
+    pw[2 * q] = static_cast<const char*>(p.wg) + wo;
+    pw[2 * q + 1] = static_cast<const char*>(p.wu) + wo;
+    if constexpr (ES == 1 && !PART) {   // asked for before the products, used after them
+      sg[q] = ld4f(p.sg + (size_t)e * p.F + f0 + 4 * q);
+      su[q] = ld4f(p.su + (size_t)e * p.F + f0 + 4 * q);
+    }
+  }
   const char* px[NS];
 #pragma unroll
   for (int t = 0; t < NS; ++t)
     px[t] = static_cast<const char*>(p.x) + R.stok[base + min(4 * t + j, cnt - 1)] * rowb + piece;
-  float4 sg = {}, su = {};
-  if constexpr (ES == 1 && !PART) {   // asked for before the products, used after them
-    sg = ld4f(p.sg + (size_t)e * p.F + f0);
-    su = ld4f(p.su + (size_t)e * p.F + f0);
-  }
-  Acc acc[2][NS];
+  Acc acc[2 * QR][NS];
   clear(acc);
   const int S = (int)(rowb / kSeg), s0 = PART ? kp * S / ks : 0, s1 = PART ? (kp + 1) * S / ks : S;
-  dot4<T, 2, NS, NS == 1 ? (ES == 1 ? 2 : 4) : NS == 2 ? 2 : 1>(pw, px, s0, s1, acc);
+  dot4<T, 2 * QR, NS, (QR > 1 ? 1 : ES == 1 ? 2 : 4)>(pw, px, s0, s1, acc);
 #pragma unroll
-  for (int t = 0; t < NS; ++t) {
-    Acc a, b;
+  for (int t = 0; t < NS; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = block_sum(acc[0][t][i]);
-      b[i] = block_sum(acc[1][t][i]);
-    }
-    if constexpr (PART) {
-      if (lane < 4) {
-        red[2 * (4 * t + j)] = a;
-        red[2 * (4 * t + j) + 1] = b;
+    for (int q = 0; q < QR; ++q) {
+      Acc a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = block_sum(acc[2 * q][t][i]);
+        b[i] = block_sum(acc[2 * q + 1][t][i]);
       }
-    } else if (lane < 4 && 4 * t + j < cnt) {
-      const int pos = base + 4 * t + j;
-      store_h<T>(p, pos, R.stok[pos], R.swt[pos], f0, a, b, sg, su);
+      if constexpr (PART) {
+        if (lane < 4) {
+          red[2 * ((4 * t + j) * QR + q)] = a;
+          red[2 * ((4 * t + j) * QR + q) + 1] = b;
+        }
+      } else if (lane < 4 && 4 * t + j < cnt) {
+        const int pos = base + 4 * t + j;
+        store_h<T>(p, pos, R.stok[pos], R.swt[pos], f0 + 4 * q, a, b, sg[q], su[q]);
+      }
     }
-  }
 }
 
-// the parts' sums of a unit, added in order, and its h; red: the first part's wave's
-template <class T>
+// the parts' sums of a unit, added in order, and its h; red: the first part's wave's, 32 sums a wave
+template <class T, int QR>
 __device__ __forceinline__ void gateup_join(const FewParams& p, const FewRoute& R, const typename Mma4<T>::Acc* red, int e,
                                             int base, int cnt, int f0, int ks) {
-  const int lane = threadIdx.x & 63;
-  if (lane < cnt) {
+  const int lane = threadIdx.x & 63;   // (token, quad)
+  if (lane < cnt * QR) {
+    const int f = f0 + 4 * (lane % QR), pos = base + lane / QR;
     float4 sg = {}, su = {};
     if constexpr (sizeof(T) == 1) {
-      sg = ld4f(p.sg + (size_t)e * p.F + f0);
-      su = ld4f(p.su + (size_t)e * p.F + f0);
+      sg = ld4f(p.sg + (size_t)e * p.F + f);
+      su = ld4f(p.su + (size_t)e * p.F + f);
     }
     typename Mma4<T>::Acc a = red[2 * lane], b = red[2 * lane + 1];
     for (int k = 1; k < ks; ++k) {
       a += red[32 * k + 2 * lane];
       b += red[32 * k + 2 * lane + 1];
     }
-    const int pos = base + lane;
-    store_h<T>(p, pos, R.stok[pos], R.swt[pos], f0, a, b, sg, su);
+    store_h<T>(p, pos, R.stok[pos], R.swt[pos], f, a, b, sg, su);
   }
 }
 
@@ -620,13 +629,22 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
   // Consecutive units go to different workgroups: a few units still spread over all CUs. Where the waves
   // outnumber the units, two or four share a unit, so that more of its loads are in flight at once.
   typedef typename Mma4<T>::Acc Acc;
-  const int nf = p.F / 4, units = (nact - heavy) * nf, w = eng::wave_id(), waves = kGW * gridDim.x;
-  const int ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
+  // rows of a unit of an expert with 5 to 8 tokens; of 8 rows of 8-bit weights the scales and sums spill
+  constexpr int WF = sizeof(T) == 1 ? 4 : 8;
+  const int wide_units = (R.cls[3] - heavy) * (p.F / WF), units = wide_units + (nact - R.cls[3]) * (p.F / 4);
+  const int w = eng::wave_id(), waves = kGW * gridDim.x, ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
+  // unit u: of an expert with 5 to 8 tokens, then of one with 1 to 4
+  auto find = [&](int u, int& f0) {
+    const bool wide = u < wide_units;
+    const int v = wide ? u : u - wide_units, nf = p.F / (wide ? WF : 4), a = v / nf;
+    f0 = (v - a * nf) * (wide ? WF : 4);
+    return uniform4(R.ent[(wide ? heavy : R.cls[3]) + a]);
+  };
   auto light = [&](int u) {
-    const int a = u / nf, f0 = (u - a * nf) * 4;
-    const int4 x = uniform4(R.ent[heavy + a]);
-    if (x.z <= 4) gateup_unit<T, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
-    else gateup_unit<T, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    int f0;
+    const int4 x = find(u, f0);
+    if (x.z <= 4) gateup_unit<T, 1, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    else gateup_unit<T, WF / 4, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
   };
   if (ks == 1) {
     // a heavy task (16 units' weights) is about three rounds of a workgroup's units: the workgroups without one
@@ -639,16 +657,20 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
       }
     for (int u = early + w * nb + blockIdx.x; u < units; u += waves) light(u);
   } else {   // one round; a heavy task's last barrier is behind its reads of smem
-    const int kp = w & (ks - 1), u = (w / ks) * gridDim.x + blockIdx.x, a = u / nf, f0 = (u - a * nf) * 4;
-    Acc* red = reinterpret_cast<Acc*>(smem) + 32 * w;   // [16 tokens][gate, up]
+    const int kp = w & (ks - 1), u = (w / ks) * gridDim.x + blockIdx.x;
+    Acc* red = reinterpret_cast<Acc*>(smem) + 32 * w;
     int4 x = make_int4(0, 0, 0, 0);
+    int f0 = 0;
     if (u < units) {
-      x = uniform4(R.ent[heavy + a]);
-      if (x.z <= 4) gateup_unit<T, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
-      else gateup_unit<T, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      x = find(u, f0);
+      if (x.z <= 4) gateup_unit<T, 1, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else gateup_unit<T, WF / 4, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
     }
     __syncthreads();
-    if (u < units && kp == 0) gateup_join<T>(p, R, red, x.x, x.y, x.z, f0, ks);
+    if (u < units && kp == 0) {
+      if (x.z <= 4) gateup_join<T, 1>(p, R, red, x.x, x.y, x.z, f0, ks);
+      else gateup_join<T, WF / 4>(p, R, red, x.x, x.y, x.z, f0, ks);
+    }
   }
 }
 
