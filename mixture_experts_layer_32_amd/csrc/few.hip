@@ -9,9 +9,10 @@
 // Reads alone, 320 MB on 256 CUs: 4 rows x 256 B 6.5 TB/s (5.7 without the non-temporal hint), 16 rows x
 // 64 B, the form a 16 x 16 MFMA would take, 5.2 TB/s either way.
 //
-//   k_few_prep    logits = x W_r^T (4 experts by 16 tokens per workgroup) and, with 8-bit weights, the quantised rows
-//                 of x. Only launched where one of the two is asked for.
-//   k_few_topk    the tokens' experts and weights; only launched for more than 16 tokens.
+//   k_few_prep    logits = x W_r^T (4 experts by 16 tokens per workgroup) and, with 8-bit weights, the quantised
+//                 rows of x. Only launched where one of the two is asked for.
+//   k_few_topk    the tokens' experts and weights; only launched for more than 16 tokens (with 8-bit weights and
+//                 given logits k_few_prep does it).
 //   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 16 tokens, chooses them); then its
 //                 waves take (expert, 4 or 8 rows of F) units, each on its own, and write h = w silu(a) b into
 //                 the workspace.
@@ -183,15 +184,16 @@ __device__ __forceinline__ void choose(const FewParams& p, int t, int lane, int&
 // More than kRouteHere tokens: one wave a token, ahead of the kernels that use the choice (in every
 // workgroup of k_few_gateup, 64 tokens' choices took 20 us).
 constexpr int kRouteHere = 16;
-__global__ __launch_bounds__(64) void k_few_topk(FewParams p) {
+__device__ __forceinline__ void choose_store(const FewParams& p, int t, int lane) {
   int e;
   float wt;
-  choose(p, blockIdx.x, threadIdx.x, e, wt);
-  if ((int)threadIdx.x < p.k) {
-    p.r_idx[blockIdx.x * p.k + threadIdx.x] = e;
-    p.r_wt[blockIdx.x * p.k + threadIdx.x] = wt;
+  choose(p, t, lane, e, wt);
+  if (lane < p.k) {
+    p.r_idx[t * p.k + lane] = e;
+    p.r_wt[t * p.k + lane] = wt;
   }
 }
+__global__ __launch_bounds__(64) void k_few_topk(FewParams p) { choose_store(p, blockIdx.x, threadIdx.x); }
 
 template <int NW>
 __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p) {
@@ -1012,6 +1014,11 @@ __global__ __launch_bounds__(kPW * 64, 4) void k_few_prep(FewParams p, int route
   }
   if constexpr (sizeof(T) == 2) {   // with 8-bit weights: quantise row t of x
     const int t = blockIdx.x - router_blocks;
+    if (t >= p.T) {   // a token's experts by each wave
+      const int c = (t - p.T) * kPW + w;
+      if (c < p.T) choose_store(p, c, lane);
+      return;
+    }
     unsigned* sm = reinterpret_cast<unsigned*>(smem);
     const bf16* row = static_cast<const bf16*>(p.x0) + (size_t)t * p.H;
     unsigned m = 0u;
@@ -1039,12 +1046,16 @@ __global__ __launch_bounds__(kPW * 64, 4) void k_few_prep(FewParams p, int route
   }
 }
 
+bool topk_in_prep(const FewParams& p, bool quant) { return quant && !p.wr && p.T > kRouteHere; }
+
 template <class T>
 hipError_t launch_prep(const FewParams& p, hipStream_t s, bool quant) {
   const int nr = p.wr ? (p.E + 3) / 4 * ((p.T + 4 * kSets - 1) / (4 * kSets)) : 0;
   if (nr == 0 && !quant) return hipSuccess;
+  // rows to quantise and, with given logits, the choice of experts: one launch for both (4.5 us of 114 at 32 tokens of 128 experts)
+  const int nq = quant ? p.T + (topk_in_prep(p, quant) ? (p.T + kPW - 1) / kPW : 0) : 0;
   prof_mark_begin("few_prep", s);
-  k_few_prep<T><<<nr + (quant ? p.T : 0), kPW * 64, 0, s>>>(p, nr);
+  k_few_prep<T><<<nr + nq, kPW * 64, 0, s>>>(p, nr);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;
@@ -1069,7 +1080,7 @@ hipError_t launch_layer(const FewParams& p, hipStream_t s) {
   const int n = p.T * p.k, units = std::min(n, p.El) * (p.F / 4);
   const int grid = std::min(units, persistent_grid(2));
   hipError_t err;
-  if (p.T > kRouteHere) {
+  if (p.T > kRouteHere && !topk_in_prep(p, sizeof(T) == 1)) {
     prof_mark_begin("few_topk", s);
     k_few_topk<<<p.T, 64, 0, s>>>(p);
     if ((err = hipGetLastError()) != hipSuccess) return err;
