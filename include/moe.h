@@ -233,7 +233,8 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
 /* The whole layer for a few tokens (1 <= T <= 64), forward only: the step of a decoder, where the time
  * goes into reading the chosen experts' weights once. The same y as moe_fwd (same routing, ties and
  * expert share; the sums run in another order, and h = w silu(a) b keeps fp32's accuracy up to the
- * down product, where moe_fwd rounds it to bf16), without `saved`, and in two kernels:
+ * down product, where moe_fwd rounds it to bf16), without `saved`, in two kernels up to 16 tokens and four
+ * beyond:
  *   w_router = NULL  logits [T, E_total] is an input, as in moe_fwd
  *   w_router given   [E_total, H], elem: logits = x w_router^T first (one more kernel); logits is an output
  * A token none of whose experts is in the share gets y = 0. Modes FP32 and BF16
@@ -273,7 +274,7 @@ moe_status moe_int8_quantize(const void* in, int type, int64_t rows, int64_t col
  *     `offsets` give them for rows sorted by expert. Groups may be empty. Offsets ascend; values outside
  *     0..M are taken as the nearest of the two. Rows of y before offsets[0] and from offsets[G] on are left
  *     as they were.
- * K a multiple of 16 and <= 131072, N <= 2^20, G <= 512, M < 2^31, M*N < 2^40. x and w need 16-byte
+ * K a multiple of 16 and <= 131072, N <= 2^20, G <= 512, M <= 2^31 - 512, M*N < 2^40. x and w need 16-byte
  * alignment, the scales and offsets 4-byte, y its type's (16 bytes and N % 8 = 0 write faster). */
 moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales,
                            int64_t M, int64_t N, int64_t K, int G, const int32_t* offsets, void* y, int type,

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int
                                                     float* __restrict__ scales) {
   constexpr bool F32 = sizeof(T) == 4;
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), n = nrows ? min(rows, (int64_t)*nrows) : rows;
+  const int64_t r = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6), n = nrows ? min(rows, (int64_t)*nrows) : rows;
   if (r >= n) return;
   const T* row = x + (size_t)r * cols;
   uint8_t* out = q + (size_t)r * cols;
@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int
 template <class T>
 void launch_quant_t(const void* x, int64_t rows, int cols, const int* nrows, uint8_t* q, float* scales, hipStream_t s) {
   const T* p = static_cast<const T*>(x);
-  const unsigned g = (unsigned)((rows + 3) / 4);
+  const int64_t b = (rows + 3) / 4;   // a dimension of a grid holds less than 2^32 threads: 2^22 blocks, then more rows of them
+  const dim3 g((unsigned)std::min<int64_t>(b, 1 << 22), (unsigned)((b + (1 << 22) - 1) >> 22));
   if (cols <= 512) k_int8_quant<T, 1><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
   else if (cols <= 1024) k_int8_quant<T, 2><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
   else if (cols <= 2048) k_int8_quant<T, 4><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
@@ -156,8 +157,7 @@ __device__ __forceinline__ void rows_task(const I8Params& p, char* red_, int g, 
 
 __global__ __launch_bounds__(kRW * 64, 4) void k_int8_rows(I8Params p) {
   __shared__ __attribute__((aligned(16))) char red[kRW * 64 * 16];
-  const int nt = (p.N + 15) / 16;
-  const int g = blockIdx.x / nt, n0 = (blockIdx.x - g * nt) * 16;
+  const int g = blockIdx.y, n0 = blockIdx.x * 16;
   int r0 = 0, cnt = (int)p.M;
   if (p.offsets) {
     r0 = min(max(p.offsets[g], 0), (int)p.M);
@@ -185,7 +185,7 @@ hipError_t launch_int8_quant(const void* x, bool f32, int64_t rows, int cols, co
 
 hipError_t launch_int8_rows(const I8Params& p, hipStream_t s) {
   prof_mark_begin("int8_rows", s);
-  k_int8_rows<<<(unsigned)((p.N + 15) / 16 * p.G), kRW * 64, 0, s>>>(p);
+  k_int8_rows<<<dim3((p.N + 15) / 16, p.G), kRW * 64, 0, s>>>(p);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;

@@ -1088,8 +1088,8 @@ moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t*
   if (K % 16 != 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be a multiple of 16");
   if (K > kInt8MaxK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be <= 131072");
   if (G > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "G must be <= 512");
-  if (M > INT32_MAX || N > (1 << 20) || M * N >= (int64_t(1) << 40))
-    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be < 2^31, N <= 2^20 and M*N < 2^40");
+  if (M > INT32_MAX - 511 || N > (1 << 20) || M * N >= (int64_t(1) << 40))   // a tile's rows are counted in 32 bits
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be <= 2^31 - 512, N <= 2^20 and M*N < 2^40");
   if ((st = check_ptrs({{x, "x"}, {w, "w"}}, 16)) != MOE_OK) return st;
   if ((st = check_ptrs({{x_scales, "x_scales"}, {w_scales, "w_scales"}}, 4)) != MOE_OK) return st;
   if (offsets && (st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;

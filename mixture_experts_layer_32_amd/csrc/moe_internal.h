@@ -206,7 +206,7 @@ struct FewParams {
   float *xs, *hs;
   unsigned* hmax;        // T <= 4: magnitude bits of the largest |h| of each 4 of a pair's row [pairs, F / 4]
                          //   (h is then quantised in the down kernel); null otherwise
-  float* oh;             // [pairs, H] down products of experts with more than 16 tokens
+  float* oh;             // [pairs, H] down products of experts with more than 8 tokens, of more than 16 tokens in all
   int* r_idx;            // [T k] chosen experts and their weights, of more than 16 tokens
   float* r_wt;
   int *r_cls, *r_tok;    // routing, from the gate/up kernel to the down kernel

@@ -1,8 +1,9 @@
 """Device-memory plumbing around the C ABI: torch allocates the caller-owned buffers.
 
 MoELayer holds the workspace and saved buffers for one layer shape, and calls moe_fwd/moe_bwd (and
-the router projection's moe_router_fwd/moe_router_bwd) through the binding. No arithmetic happens
-here.
+the router projection's moe_router_fwd/moe_router_bwd) through the binding. For serving, FewTokenLayer
+(up to 64 tokens), Int8Layer (8-bit weights, any number of tokens), int8_quantize and int8_matmul. No
+arithmetic happens here.
 """
 from __future__ import annotations
 
@@ -37,6 +38,17 @@ def _on(device, stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(i)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new output for a call on `stream`, from that stream's memory: memory of the current stream may still be
+    written by work of its own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _device(device):
@@ -163,7 +175,8 @@ class MoELayer:
 
 class FewTokenLayer:
     """The layer's forward for 1 to 64 tokens through moe_fwd_few: holds the workspace of one shape. Calls
-    of one object share it: order them, or give concurrent streams an object each."""
+    of one object share it: order them, or give concurrent streams an object each, and keep an object until its
+    calls have run."""
 
     def __init__(self, T, H, F, E_total, topk, mode="bf16", E_local=None, expert_offset=0, device="cuda"):
         self.desc = d = binding.Desc.make(T, H, F, E_total, topk, mode, E_local, expert_offset)
@@ -176,16 +189,16 @@ class FewTokenLayer:
 
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         el, dev = self.dtype, self.device
-        stream = _on(dev, stream)
+        handle = _on(dev, stream)
         if y is None:
-            y = torch.empty(self._x, dtype=el, device=dev)
+            y = _empty(self._x, el, dev, stream)
         else:
             _expect(y, "y", self._x, el, dev)
         _expect(x, "x", self._x, el, dev)
         _expect(w_gate, "w_gate", self._w_in, el, dev)
         _expect(w_up, "w_up", self._w_in, el, dev)
         _expect(w_down, "w_down", self._w_out, el, dev)
-        binding.moe_fwd_few(self.desc, x, w_router, logits, w_gate, w_up, w_down, y, self.ws, self.ws.numel(), stream)
+        binding.moe_fwd_few(self.desc, x, w_router, logits, w_gate, w_up, w_down, y, self.ws, self.ws.numel(), handle)
         return y
 
     def forward(self, x, logits, w_gate, w_up, w_down, y=None, stream=None):
@@ -196,7 +209,7 @@ class FewTokenLayer:
     def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
         """The forward from x and w_router [E_total, H]; returns (y, logits)."""
         if logits is None:
-            logits = torch.empty(self._logits, dtype=torch.float32, device=self.device)
+            logits = _empty(self._logits, torch.float32, self.device, stream)
         else:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, self.dtype, self.device)
@@ -221,17 +234,17 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     t, shape, dev = _int8_type(x.dtype), x.shape, x.device
     if not x.is_contiguous():
         raise ValueError("x: expected a contiguous tensor")
-    stream = _on(dev, stream)
+    handle = _on(dev, stream)
     if q is None:
-        q = torch.empty_like(x, dtype=torch.int8)
+        q = _empty(shape, torch.int8, dev, stream)
     else:
         _expect(q, "q", shape, torch.int8, dev)
     if scales is None:
-        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        scales = _empty(shape[:-1], torch.float32, dev, stream)
     else:
         _expect(scales, "scales", shape[:-1], torch.float32, dev)
     K = shape[-1]
-    binding.moe_int8_quantize(x, t, x.numel() // K if K else 0, K, q, scales, stream)
+    binding.moe_int8_quantize(x, t, x.numel() // K if K else 0, K, q, scales, handle)
     return q, scales
 
 
@@ -242,7 +255,7 @@ def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bflo
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (2 if offsets is None else 3):
         raise ValueError("expected x [M, K] and w [N, K], or w [G, N, K] with offsets")
     dev, (M, K) = x.device, x.shape
-    stream = _on(dev, stream)
+    handle = _on(dev, stream)
     _expect(x, "x", (M, K), torch.int8, dev)
     _expect(x_scales, "x_scales", (M,), torch.float32, dev)
     if offsets is None:
@@ -256,18 +269,19 @@ def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bflo
         _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
     if y is None:
         t = _int8_type(dtype)
-        y = torch.empty((M, N), dtype=dtype, device=dev)
+        y = _empty((M, N), dtype, dev, stream)
     else:
         t = _int8_type(y.dtype)
         _expect(y, "y", (M, N), y.dtype, dev)
-    binding.moe_int8_matmul(x, x_scales, w, w_scales, M, N, K, G, offsets, y, t, stream)
+    binding.moe_int8_matmul(x, x_scales, w, w_scales, M, N, K, G, offsets, y, t, handle)
     return y
 
 
 class Int8Layer:
     """The layer's forward with 8-bit weights through moe_fwd_int8, for any number of tokens: holds the workspace
     of one shape. Each weight is the (bytes, scales) pair of int8_quantize on the bf16 or fp32 matrix. Calls of
-    one object share the workspace: order them, or give concurrent streams an object each."""
+    one object share the workspace: order them, or give concurrent streams an object each, and keep an object until its
+    calls have run."""
 
     def __init__(self, T, H, F, E_total, topk, E_local=None, expert_offset=0, device="cuda"):
         self.desc = d = binding.Desc.make(T, H, F, E_total, topk, "bf16", E_local, expert_offset)
@@ -278,9 +292,9 @@ class Int8Layer:
 
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         dev = self.device
-        stream = _on(dev, stream)
+        handle = _on(dev, stream)
         if y is None:
-            y = torch.empty(self._x, dtype=torch.bfloat16, device=dev)
+            y = _empty(self._x, torch.bfloat16, dev, stream)
         else:
             _expect(y, "y", self._x, torch.bfloat16, dev)
         _expect(x, "x", self._x, torch.bfloat16, dev)
@@ -289,7 +303,7 @@ class Int8Layer:
             _expect(w, name, shape, torch.int8, dev)
             _expect(s, name + " scales", shape[:2], torch.float32, dev)
         binding.moe_fwd_int8(self.desc, x, w_router, logits, w_gate[0], w_gate[1], w_up[0], w_up[1], w_down[0],
-                             w_down[1], y, self.ws, self.ws.numel(), stream)
+                             w_down[1], y, self.ws, self.ws.numel(), handle)
         return y
 
     def forward(self, x, logits, w_gate, w_up, w_down, y=None, stream=None):
@@ -300,7 +314,7 @@ class Int8Layer:
     def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
         """The forward from x and w_router [E_total, H] bf16; returns (y, logits)."""
         if logits is None:
-            logits = torch.empty(self._logits, dtype=torch.float32, device=self.device)
+            logits = _empty(self._logits, torch.float32, self.device, stream)
         else:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, torch.bfloat16, self.device)

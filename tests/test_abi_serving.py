@@ -111,6 +111,7 @@ def test_int8_quantize_refusals(args, code, msg):
     (dict(K=131088), "MOE_ERR_UNSUPPORTED_SHAPE", "131072"),
     (dict(G=513, offsets=FAKE), "MOE_ERR_UNSUPPORTED_SHAPE", "512"),
     (dict(M=1 << 31), "MOE_ERR_UNSUPPORTED_SHAPE", "M must be"),
+    (dict(M=(1 << 31) - 511, N=8, K=16), "MOE_ERR_UNSUPPORTED_SHAPE", "M must be"),
     (dict(N=(1 << 20) + 1), "MOE_ERR_UNSUPPORTED_SHAPE", "N <= 2"),
     (dict(M=1 << 21, N=1 << 20), "MOE_ERR_UNSUPPORTED_SHAPE", r"M\*N"),
     (dict(type=5), "MOE_ERR_UNSUPPORTED_MODE", "type"),

@@ -73,6 +73,13 @@ CASES = [
     dict(T=13, H=256, F=128, E=8, k=2, E_local=3, e0=2, mode="fp32"),
     dict(T=7, H=4096, F=1536, E=12, k=8, zipf_s=1.1),
     dict(T=9, H=7168, F=128, E=6, k=2),
+    dict(T=7, H=512, F=128, E=3, k=3),                  # 5 to 8 tokens an expert, units shared by waves
+    dict(T=8, H=256, F=1536, E=24, k=24),               # the same, units enough for every wave
+    dict(T=8, H=1024, F=128, E=16, k=5, mode="fp32"),   # experts of up to 4 and of 5 to 8 tokens
+    dict(T=12, H=2048, F=256, E=3, k=3),                # 9 to 16 tokens an expert
+    dict(T=16, H=4096, F=384, E=3, k=3),
+    dict(T=16, H=4096, F=128, E=20, k=9, mode="fp32"),  # every class of an expert's tokens up to 16
+    dict(T=50, H=4096, F=256, E=24, k=6, zipf_s=1.1),
 ]
 
 
@@ -148,6 +155,26 @@ def test_ties_and_lowest_values():
     k.check(y, k.ref(logits=lg))
 
 
+@pytest.mark.parametrize("T", [5, 40])
+def test_masked_logits(T):
+    """Experts masked by minus infinity: fewer left than slots give weights of zero, none left gives NaN in that
+    token's y alone, as in moe_fwd."""
+    print("case few masked", T, flush=True)
+    k = Case(T=T, H=256, F=128, E=6, k=3)
+    lg = k.lg.clone()
+    y0 = k.run().clone()
+    lg[1, 2:] = float("-inf")
+    lg[3] = float("-inf")
+    y = k.run(logits=lg).clone()
+    full = MoELayer(T, 256, 128, 6, 3).forward(k.x, lg, k.wg, k.wu, k.wd)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[3]).all() and torch.isnan(full[3]).all()
+    rest = [t for t in range(T) if t not in (1, 3)]
+    assert torch.equal(y[rest], y0[rest])
+    two = oracle.forward(k.L["x"][1:2], k.L["logits"][1:2, :2], k.L["wg"][:2], k.L["wu"][:2], k.L["wd"][:2], 2)[0]
+    assert oracle.rel_frobenius(y[1:2].float().cpu().numpy(), two) <= 2 * TOL["bf16"]
+
+
 def test_nan_token_stays_alone():
     print("case few nan token", flush=True)
     k = Case(T=20, H=256, F=128, E=4, k=4)
@@ -181,11 +208,29 @@ def test_prompt_then_tokens():
     assert oracle.rel_frobenius(got, y.float().cpu().numpy()) <= 4 * 2.0 ** -8
 
 
-@pytest.mark.parametrize("router", [False, True])
-def test_graph_replays(router):
-    print("case few graph", router, flush=True)
-    k = Case(T=9, H=512, F=256, E=16, k=4)
-    lg = torch.empty(9, 16, device="cuda")
+def test_a_new_output_on_another_stream():
+    """An output made for a call on a side stream is no memory that the current stream still writes."""
+    print("case few side stream", flush=True)
+    k = Case(T=20, H=4096, F=256, E=8, k=2)
+    want = k.run().clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)
+        old.fill_(5)
+        del old                                         # freed while the current stream has yet to write it
+        got = k.layer.forward(k.x, k.lg, k.wg, k.wu, k.wd, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("router,c", [(False, dict(T=9, H=512, F=256, E=16, k=4)), (True, dict(T=9, H=512, F=256, E=16, k=4)),
+                                      (True, dict(T=64, H=256, F=128, E=512, k=32))], ids=["given", "router", "most"])
+def test_graph_replays(router, c):
+    print("case few graph", router, c, flush=True)
+    k = Case(**c)
+    lg = torch.empty(c["T"], c["E"], device="cuda")
 
     def step():
         if router:

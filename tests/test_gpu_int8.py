@@ -91,6 +91,21 @@ def test_quantise_ties_swept():
         check_quant(x, dt)
 
 
+def test_quantise_many_short_rows():
+    """More rows than one dimension of a grid takes (2^32 threads at a wavefront a row)."""
+    print("case int8 quant rows", flush=True)
+    rows = (1 << 26) + 9
+    x = torch.arange(16, device="cuda").to(torch.bfloat16).repeat(rows, 1)
+    x[-3:, 0] = torch.tensor([20.0, 30.0, -40.0], device="cuda")
+    q, s = int8_quantize(x)
+    torch.cuda.synchronize()
+    for at in (slice(0, 5), slice((1 << 24) - 2, (1 << 24) + 3), slice(rows - 12, rows)):
+        rq, rs = quant_ref(x[at].float().cpu().numpy())
+        assert np.array_equal(s[at].cpu().numpy(), rs) and np.array_equal(q[at].cpu().numpy(), rq)
+    changed = int((s != s[0]).sum()), int((q != q[0]).any(1).sum())
+    assert changed == (3, 3)
+
+
 # ------------------------------------------------------------------------------------------------ product
 
 def matmul_ref(q, s, w, ws, offsets, dt, M, N):
@@ -150,6 +165,46 @@ def test_grouped_product_bit_exact(offsets, N, K, dt):
         M = 64
     print("case int8 grouped", offsets[:9], N, K, dt, flush=True)
     run_matmul(M, N, K, dt, offsets=offsets, seed=len(offsets) + N)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K,offsets", [(6300, 2104, 144, None), (6300, 2104, 400, [3, 3, 1000, 1100, 3660, 6271]),
+                                           (20000, 520, 64, [0, 128, 257, 19900])], ids=["plain", "groups", "short"])
+def test_large_product_bit_exact(M, N, K, offsets, dt):
+    """Enough tiles for the 256 x 256 engine: ends inside a tile, tiles of up to 128 rows, one to four K-tiles."""
+    print("case int8 large tiles", M, N, K, offsets, dt, flush=True)
+    run_matmul(M, N, K, dt, offsets=offsets, seed=M)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_product_into_an_odd_address(dt):
+    print("case int8 odd address", dt, flush=True)
+    for M, N, K in ((20, 40, 64), (300, 128, 144), (6300, 2104, 32)):
+        rng = np.random.default_rng(M)
+        q, w = (torch.from_numpy(rng.integers(-127, 128, s, dtype=np.int8)).cuda() for s in ((M, K), (N, K)))
+        s, ws = torch.rand(M + 1, device="cuda")[1:], torch.rand(N + 3, device="cuda")[3:]
+        room = torch.full((M * N + 9,), float("nan"), dtype=dt, device="cuda")
+        int8_matmul(q, s, w, ws, y=room[1:1 + M * N].view(M, N))
+        want = int8_matmul(q, s, w, ws, dtype=dt)
+        torch.cuda.synchronize()
+        assert torch.equal(room[1:1 + M * N].view(M, N), want), M
+        assert torch.isnan(room[0]) and torch.isnan(room[1 + M * N:]).all(), M
+
+
+def test_many_groups_of_many_channels():
+    """512 groups of 2^17 channels over 60 rows: more workgroups than one dimension of a grid takes."""
+    print("case int8 channels", flush=True)
+    M, N, K, G = 60, 1 << 17, 16, 512
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-127, 128, (G, N, K), dtype=torch.int8, device="cuda", generator=g)
+    s, ws = torch.rand(M, device="cuda", generator=g), torch.rand(G, N, device="cuda", generator=g)
+    off = [0] * 200 + [31] * 312 + [60]
+    y = int8_matmul(q, s, w, ws, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    for a, b, e in ((0, 31, 199), (31, 60, 511)):
+        ref = (q[a:b].double() @ w[e].double().T).float() * (s[a:b, None] * ws[e])
+        assert torch.equal(y[a:b], ref.to(torch.bfloat16))
 
 
 def test_offsets_outside_the_rows_are_clamped():
@@ -264,6 +319,11 @@ LAYERS = [
     dict(T=333, H=1024, F=640, E=16, k=4, E_local=4, e0=8),
     dict(T=700, H=2048, F=768, E=10, k=1),
     dict(T=1500, H=512, F=256, E=12, k=3, zipf_s=1.1),
+    dict(T=2100, H=256, F=1024, E=8, k=4),              # the 256 x 256 engine for the gate/up products
+    dict(T=8, H=512, F=384, E=5, k=5),                  # few tokens: 5 to 8 an expert, rows of h that end in half
+    dict(T=12, H=2048, F=384, E=3, k=3),                # 256 bytes; 9 to 16 an expert
+    dict(T=16, H=4096, F=128, E=20, k=9),
+    dict(T=40, H=4096, F=640, E=24, k=6, zipf_s=1.1),
 ]
 
 
@@ -352,7 +412,27 @@ def test_prompt_then_tokens_with_one_set_of_weights():
     assert oracle.rel_frobenius(few[:64].cpu().numpy(), bf.float().cpu().numpy()) <= 0.05
 
 
-@pytest.mark.parametrize("T,router", [(9, False), (9, True), (130, False), (130, True)])
+def test_new_outputs_on_another_stream():
+    """Outputs made for calls on a side stream are no memory that the current stream still writes."""
+    print("case int8 side stream", flush=True)
+    x = torch.randn(512, 1024, device="cuda")
+    want = int8_quantize(x)
+    y = int8_matmul(*want, *want, dtype=torch.float32)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.empty_like(t) for t in (*want, y)]
+        torch.cuda._sleep(20_000_000)
+        [t.fill_(5) for t in old]
+        del old                                         # freed while the current stream has yet to write them
+        for stream in (side, side.cuda_stream):
+            got = int8_quantize(x, stream=stream)
+            z = int8_matmul(*got, *got, dtype=torch.float32, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("T,router", [(9, False), (9, True), (40, False), (130, False), (130, True)])
 def test_layer_graph_replays(T, router):
     print("case int8 graph", T, router, flush=True)
     k = Case(T=T, H=512, F=256, E=16, k=4)
