@@ -136,9 +136,10 @@ __device__ __forceinline__ void wave_topk(const float* row, int E, int k, int la
   }
 }
 
-// Experts with pairs, in classes by their number of tokens: more than 16, 9-16 (both "heavy"), 5-8, 1-4.
-constexpr int kClasses = 4;
-__device__ __forceinline__ int few_class(int n) { return n > 16 ? 0 : n > 8 ? 1 : n > 4 ? 2 : 3; }
+// Experts with pairs, in classes by their number of tokens: more than 16, 9-16 (both "heavy"), 5-8, 3-4, 1-2.
+constexpr int kClasses = 5;
+constexpr int kClassBits = 12, kClassMask = (1 << kClassBits) - 1;   // of a count of experts by class, up to 512; five in 64 bits
+__device__ __forceinline__ int few_class(int n) { return n > 16 ? 0 : n > 8 ? 1 : n > 4 ? 2 : n > 2 ? 3 : 4; }
 
 // The routing of all T tokens in a workgroup's LDS, pairs sorted by (local expert, token).
 struct FewRoute {
@@ -217,14 +218,14 @@ __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p)
     }
   }
   __syncthreads();
-  if (w == 0) {   // lane's experts: a contiguous run; counts of pairs, and of experts by class (16 bits each)
+  if (w == 0) {   // lane's experts: a contiguous run; counts of pairs, and of experts by class
     const int per = (p.El + 63) >> 6, e0 = lane * per;
     int c = 0;
     unsigned long long a = 0ull;
     for (int i = 0; i < per; ++i) {
       const int m = e0 + i < p.El ? __popcll(R.mask[e0 + i]) : 0;
       c += m;
-      if (m > 0) a += 1ull << (16 * few_class(m));
+      if (m > 0) a += 1ull << (kClassBits * few_class(m));
     }
     int ic = c;
     unsigned long long ia = a;
@@ -238,11 +239,11 @@ __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p)
       }
     }
     const unsigned long long all = __shfl(ia, 63);
-    unsigned long long at = ia - a;   // class q's next entry, 16 bits each
+    unsigned long long at = ia - a;   // class q's next entry
 #pragma unroll
     for (int q = 0; q < kClasses; ++q)
 #pragma unroll
-      for (int r = 0; r < q; ++r) at += ((all >> (16 * r)) & 0xffff) << (16 * q);
+      for (int r = 0; r < q; ++r) at += ((all >> (kClassBits * r)) & kClassMask) << (kClassBits * q);
     int o = ic - c;
     for (int i = 0; i < per; ++i) {
       const int e = e0 + i;
@@ -250,8 +251,8 @@ __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p)
       const int m = __popcll(R.mask[e]);
       R.off[e] = o;
       if (m > 0) {
-        const int q = 16 * few_class(m);
-        R.ent[(at >> q) & 0xffff] = make_int4(e, o, m, 0);
+        const int q = kClassBits * few_class(m);
+        R.ent[(at >> q) & kClassMask] = make_int4(e, o, m, 0);
         at += 1ull << q;
       }
       o += m;
@@ -262,7 +263,7 @@ __device__ __forceinline__ void few_route(const FewRoute& R, const FewParams& p)
 #pragma unroll
       for (int q = 0; q < kClasses; ++q) {
         R.cls[q] = first;
-        first += (int)((all >> (16 * q)) & 0xffff);
+        first += (int)((all >> (kClassBits * q)) & kClassMask);
       }
       R.cls[kClasses] = first;
     }
@@ -400,7 +401,7 @@ __device__ __forceinline__ void gateup_unit(const FewParams& p, const FewRoute& 
   Acc acc[2 * QR][NS];
   clear(acc);
   const int S = (int)(rowb / kSeg), s0 = PART ? kp * S / ks : 0, s1 = PART ? (kp + 1) * S / ks : S;
-  dot4<T, 2 * QR, NS, (QR > 1 ? 1 : ES == 1 ? 2 : 4)>(pw, px, s0, s1, acc);
+  dot4<T, 2 * QR, NS, (QR * NS > 2 ? 1 : QR > 1 || ES == 1 ? 2 : 4)>(pw, px, s0, s1, acc);
 #pragma unroll
   for (int t = 0; t < NS; ++t)
 #pragma unroll
@@ -631,33 +632,36 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
   // Consecutive units go to different workgroups: a few units still spread over all CUs. Where the waves
   // outnumber the units, two or four share a unit, so that more of its loads are in flight at once.
   typedef typename Mma4<T>::Acc Acc;
-  // rows of a unit of an expert with 5 to 8 tokens; of 8 rows of 8-bit weights the scales and sums spill
-  constexpr int WF = sizeof(T) == 1 ? 4 : 8;
-  const int wide_units = (R.cls[3] - heavy) * (p.F / WF), units = wide_units + (nact - R.cls[3]) * (p.F / 4);
+  // rows of a unit of an expert with 3 to 8 tokens; of 8 rows of 8-bit weights the scales and sums spill
+  constexpr int WF = sizeof(T) == 1 ? 4 : 8, WQ = WF / 4;
+  const int few = R.cls[4], wide_units = (few - heavy) * (p.F / WF), units = wide_units + (nact - few) * (p.F / 4);
   const int w = eng::wave_id(), waves = kGW * gridDim.x, ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
-  // unit u: of an expert with 5 to 8 tokens, then of one with 1 to 4
+  // unit u: of an expert with 3 to 8 tokens, then of one with 1 or 2
   auto find = [&](int u, int& f0) {
     const bool wide = u < wide_units;
     const int v = wide ? u : u - wide_units, nf = p.F / (wide ? WF : 4), a = v / nf;
     f0 = (v - a * nf) * (wide ? WF : 4);
-    return uniform4(R.ent[(wide ? heavy : R.cls[3]) + a]);
+    return uniform4(R.ent[(wide ? heavy : few) + a]);
   };
   auto light = [&](int u) {
     int f0;
     const int4 x = find(u, f0);
-    if (x.z <= 4) gateup_unit<T, 1, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
-    else gateup_unit<T, WF / 4, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    if (x.z > 4) gateup_unit<T, WQ, 2, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    else if (WQ > 1 && x.z > 2) gateup_unit<T, WQ, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
+    else gateup_unit<T, 1, 1, false>(p, R, nullptr, x.x, x.y, x.z, f0, 1, 0);
   };
   if (ks == 1) {
-    // a heavy task (16 units' weights) is about three rounds of a workgroup's units: the workgroups without one
-    // take those rounds' units first
-    const int nb = gridDim.x, hb = ntask % nb, early = hb ? 3 * kGW * (nb - hb) : 0;
-    if (hb && (int)blockIdx.x >= hb)
-      for (int r = 0; r < 3; ++r) {
+    // A heavy task costs one to two rounds of units: the workgroups without one take a round ahead of the others, or
+    // two where these hold all units. 48 skewed tokens of 64 experts, 4096 x 1536 (240 tasks, 2.9 rounds on 512
+    // workgroups), none/one/two/three ahead: 200/197/206/220 us; 64 of 128, 2048 x 768 (192 tasks, one round)
+    // 67/57/54/54 us.
+    const int nb = gridDim.x, hb = ntask % nb, ahead = hb == 0 ? 0 : units > 2 * kGW * (nb - hb) ? 1 : 2;
+    if ((int)blockIdx.x >= hb)
+      for (int r = 0; r < ahead; ++r) {
         const int u = (r * kGW + w) * (nb - hb) + blockIdx.x - hb;
         if (u < units) light(u);
       }
-    for (int u = early + w * nb + blockIdx.x; u < units; u += waves) light(u);
+    for (int u = ahead * kGW * (nb - hb) + w * nb + blockIdx.x; u < units; u += waves) light(u);
   } else {   // one round; a heavy task's last barrier is behind its reads of smem
     const int kp = w & (ks - 1), u = (w / ks) * gridDim.x + blockIdx.x;
     Acc* red = reinterpret_cast<Acc*>(smem) + 32 * w;
@@ -665,13 +669,14 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
     int f0 = 0;
     if (u < units) {
       x = find(u, f0);
-      if (x.z <= 4) gateup_unit<T, 1, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
-      else gateup_unit<T, WF / 4, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      if (x.z > 4) gateup_unit<T, WQ, 2, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else if (WQ > 1 && x.z > 2) gateup_unit<T, WQ, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
+      else gateup_unit<T, 1, 1, true>(p, R, red, x.x, x.y, x.z, f0, ks, kp);
     }
     __syncthreads();
     if (u < units && kp == 0) {
-      if (x.z <= 4) gateup_join<T, 1>(p, R, red, x.x, x.y, x.z, f0, ks);
-      else gateup_join<T, WF / 4>(p, R, red, x.x, x.y, x.z, f0, ks);
+      if (x.z > 2) gateup_join<T, WQ>(p, R, red, x.x, x.y, x.z, f0, ks);
+      else gateup_join<T, 1>(p, R, red, x.x, x.y, x.z, f0, ks);
     }
   }
 }
@@ -908,8 +913,8 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   const int S = (p.F * ES + kSeg - 1) / kSeg;
   float* mine = ya + w * p.T * NR;
   // class by class, the waves sharing each class's (expert, segment) axis
-  auto part = [&](int q, int& c, int& end) {
-    const int64_t N = (int64_t)(cls[q + 1] - cls[q]) * S;
+  auto part = [&](int q, int q1, int& c, int& end) {
+    const int64_t N = (int64_t)(cls[q1] - cls[q]) * S;
     c = (int)(w * N / kDW);
     end = (int)((w + 1) * N / kDW);
   };
@@ -927,7 +932,7 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
         *y = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
       }
     }
-    part(1, c, end);
+    part(1, 2, c, end);
     if (done) {
     } else if constexpr (NQ < 4) {
       down_stream<T, NQ, 4, 1, ES == 1 || NQ == 1, false>(p, ent + cls[1], stok, hm, mine, h0, S, c, end);
@@ -939,10 +944,10 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
         c += s1 - s0;
       }
     }
-    part(2, c, end);
+    part(2, 3, c, end);
     down_stream<T, NQ, 2, 1, ES != 2 || NQ < 4, false>(p, ent + cls[2], stok, hm, mine, h0, S, c, end);
   }
-  part(3, c, end);
+  part(3, 5, c, end);
   down_stream<T, NQ, 1, FLY || NQ == 4 ? 1 : ES == 1 ? 3 : 2, !FLY, FLY>(p, ent + cls[3], stok, hm, mine, h0, S, c, end);
   __syncthreads();
   for (int i = tid; i < p.T * NR; i += kDW * 64) {
