@@ -15,13 +15,20 @@
 //                 given logits k_few_prep does it).
 //   k_few_gateup  every workgroup sorts the pairs for itself (and, up to 16 tokens, chooses them); then its
 //                 waves take (expert, 4 or 8 rows of F) units, each on its own, and write h = w silu(a) b into
-//                 the workspace.
+//                 the workspace. Bound by the read of the gate and up rows.
 //   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
 //                 each keeping its own sum per token, and the sums are added in a fixed order. No
-//                 partial sums in memory, no atomics on sums: repeated calls give the same bits.
+//                 partial sums in memory, no atomics on sums: repeated calls give the same bits. Bound by the
+//                 read of the down rows.
 // Experts of more than 8 tokens ("heavy") take 16 x 16 MFMA tiles with their tokens' rows in LDS, so that
-// their weights too are read once: in k_few_gateup and, of more than 16 tokens in all, in k_few_heavy ahead of
-// k_few_down (of 9 to 16, another launch would cost more than it gives).
+// their weights too are read once: in k_few_gateup and, mostly, in k_few_heavy ahead of k_few_down (heavy_ahead).
+//
+// Measured, one launch, median us (2048 x 768 and 4096 x 1536, 128 experts, top-8, bf16; read rate of the weights):
+//                    1 token 2048     8 tokens 2048     64 skewed tokens 4096
+//   k_few_gateup     15               61-65 (5.3 TB/s)  303 (6.0 TB/s)
+//   k_few_heavy                                         61 (4.6 TB/s)
+//   k_few_down       9                32 (5.4 TB/s)     117 (6.1 TB/s)
+// About 5 us of the one-token k_few_gateup are its launch and the choice of experts, which it must wait for.
 //
 // h is kept in fp32's accuracy: as fp32, or in bf16 mode as the pair hi = bf16(h), lo = bf16(h - hi),
 // whose two products cost matrix time that a read-bound kernel does not miss.
@@ -41,6 +48,7 @@ constexpr int kGW = 8;       // waves of k_few_gateup
 constexpr int kDW = 16;      // waves of k_few_down
 constexpr int kPW = 8;       // waves of k_few_prep
 constexpr int kSeg = 256;    // bytes of one weight row per wave instruction
+constexpr int kDown4 = 4096; // H from which a workgroup of k_few_down owns 16 rows
 constexpr int kSets = 4;     // sets of 4 tokens taken at once
 
 // Sixteen 4x4 products over 16 bytes of contraction. Lane l supplies row l & 3 of A and column l & 3 of
@@ -182,8 +190,8 @@ __device__ __forceinline__ void choose(const FewParams& p, int t, int lane, int&
   wt = z / s;
 }
 
-// More than kRouteHere tokens: one wave a token, ahead of the kernels that use the choice (in every
-// workgroup of k_few_gateup, 64 tokens' choices took 20 us).
+// More than kRouteHere tokens: one wave a token, ahead of the kernels that use the choice, for 4.5 us. In every
+// workgroup of k_few_gateup the choices of 9 tokens take 3 us, of 16 4, of 32 9 and of 64 20.
 constexpr int kRouteHere = 16;
 __device__ __forceinline__ void choose_store(const FewParams& p, int t, int lane) {
   int e;
@@ -373,8 +381,9 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
 __host__ __device__ inline int few_red_bytes(int T) { return T > 16 ? 2 * 64 * kSeg : T > 8 ? 2 * 16 * kSeg : kGW * 32 * 16; }
 
 // One unit of the gate/up products by a wave: rows f0 .. f0 + 4 QR - 1 of expert e, pairs base .. base+cnt-1
-// (cnt <= 4 NS). QR = 2 with 5 to 8 tokens: their rows of x are read once for 8 rows of F (8 experts of 8 tokens,
-// 4096 x 1536: 59 -> 49 us). PART: only part kp of ks of H, whose sums go to red [token][QR][2] of the wave instead.
+// (cnt <= 4 NS). QR = 2 with 3 to 8 tokens: their rows of x are read once for 8 rows of F (64 tokens of 128 experts,
+// 4096 x 1536: 600 us with 4 rows, 534 with 8; with 1 or 2 tokens 8 rows are no better, 39 -> 42 us for 4 tokens of
+// the 2048 x 768 layer). PART: only part kp of ks of H, whose sums go to red [token][QR][2] of the wave instead.
 template <class T, int QR, int NS, bool PART>
 __device__ __forceinline__ void gateup_unit(const FewParams& p, const FewRoute& R, typename Mma4<T>::Acc* red, int e,
                                             int base, int cnt, int f0, int ks, int kp) {
@@ -632,7 +641,8 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
   // Consecutive units go to different workgroups: a few units still spread over all CUs. Where the waves
   // outnumber the units, two or four share a unit, so that more of its loads are in flight at once.
   typedef typename Mma4<T>::Acc Acc;
-  // rows of a unit of an expert with 3 to 8 tokens; of 8 rows of 8-bit weights the scales and sums spill
+  // rows of a unit of an expert with 3 to 8 tokens; of 8 rows of 8-bit weights the scales and sums spill (68 -> 83 us
+  // for 32 tokens of 128 experts of 2048 x 768)
   constexpr int WF = sizeof(T) == 1 ? 4 : 8, WQ = WF / 4;
   const int few = R.cls[4], wide_units = (few - heavy) * (p.F / WF), units = wide_units + (nact - few) * (p.F / 4);
   const int w = eng::wave_id(), waves = kGW * gridDim.x, ks = 4 * units <= waves ? 4 : 2 * units <= waves ? 2 : 1;
@@ -687,7 +697,7 @@ __global__ __launch_bounds__(kGW * 64, 4) void k_few_gateup(FewParams p) {
 // sums ya [T][4 NQ]. The stages of U segments run through expert boundaries: the next stage's loads, of
 // weights and h, are in flight while the current one is multiplied (DB; without it the registers of the
 // second stage would spill).
-// FLY (8-bit weights, T <= 4): h is fp32 and quantised here, with the pairs' maxima hm.
+// FLY (8-bit weights): h is fp32 and quantised here, with the pairs' maxima hm.
 template <class T, int NQ, int NS, int U, bool DB, bool FLY>
 __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent, const int* stok, const unsigned* hm,
                                             float* ya, int h0, int S, int c, int end) {
@@ -823,67 +833,12 @@ __device__ __forceinline__ void down_stream(const FewParams& p, const int4* ent,
   }
 }
 
-// the same for a pair run of up to 16 NG on 16 x 16 tiles (rows from 4 NQ on repeat and are dropped); steps
-// [s0, s1) of 64 bytes
-template <class T, int NQ, int NG>
-__device__ __forceinline__ void down_heavy(const FewParams& p, const int* stok, float* ya, int e, int base, int cnt,
-                                           int h0, int s0, int s1) {
-  typedef typename Mma4<T>::Acc Acc;
-  constexpr int ES = sizeof(T), NR = 4 * NQ;
-  const int lane = threadIdx.x & 63, piece = 16 * (lane >> 4);
-  const size_t rowb = (size_t)p.F * ES;
-  const char* pw = static_cast<const char*>(p.wd) + ((size_t)e * p.H + h0 + (lane & (NR - 1))) * rowb + piece;
-  const char *ph[NG], *pl[NG];
-  float hs[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int pos = base + min(16 * g + (lane & 15), cnt - 1);
-    ph[g] = (ES == 1 ? reinterpret_cast<const char*>(p.hq) : static_cast<const char*>(p.h)) + (size_t)pos * rowb + piece;
-    pl[g] = ES == 2 ? static_cast<const char*>(p.hlo) + (size_t)pos * rowb + piece : nullptr;
-    hs[g] = ES == 1 ? p.hs[pos] : 1.f;
-  }
-  Acc acc[1][NG];
-  clear(acc);
-  constexpr int U = 2;
-  for (int s = s0; s < s1; s += U) {
-    uint4 a[U], b[NG][U], c[NG][U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int o = min(s + i, s1 - 1) * kStep;
-      a[i] = ld16(pw + o);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        b[g][i] = ld16(ph[g] + o);
-        if constexpr (ES == 2) c[g][i] = ld16(pl[g] + o);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (s + i < s1)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          mma16x16(acc[0][g], a[i], b[g][i], T());
-          if constexpr (ES == 2) mma16x16(acc[0][g], a[i], c[g][i], T());
-        }
-  }
-  const int q4 = lane >> 4;   // rows 4 q4 .. + 3 of column lane % 16
-  if (q4 < NQ) {
-    float4 sd = make_float4(1.f, 1.f, 1.f, 1.f);
-    if constexpr (ES == 1) sd = ld4f(p.sd + (size_t)e * p.H + h0 + 4 * q4);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int c = 16 * g + (lane & 15);
-      if (c < cnt) {
-        float4* y = reinterpret_cast<float4*>(ya + (stok[base + c] * NQ + q4) * 4);
-        const float4 o = *y;
-        *y = make_float4(o.x + (float)acc[0][g][0] * (hs[g] * sd.x), o.y + (float)acc[0][g][1] * (hs[g] * sd.y),
-                         o.z + (float)acc[0][g][2] * (hs[g] * sd.z), o.w + (float)acc[0][g][3] * (hs[g] * sd.w));
-      }
-    }
-  }
-}
+// Whether k_few_heavy takes the down products of the experts of more than 8 tokens ahead of k_few_down: of 9 to 16
+// tokens only where k_few_down's 16 rows a wave leave no registers for 16 tokens. 16 tokens on 8 experts of 4096 x
+// 1536: 33 us in two kernels, 48 in one (on 16 x 16 tiles); 12 skewed tokens of 128 experts of 2048 x 768: 35 and 30.
+__host__ __device__ inline bool heavy_ahead(const FewParams& p) { return p.T > 16 || (p.T > 8 && p.H >= kDown4); }
 
-// FLY (8-bit weights, T <= 4): h is quantised where it is read, with the maxima the gate/up kernel left;
+// FLY (8-bit weights, up to 4 tokens): h is quantised where it is read, with the maxima the gate/up kernel left;
 // otherwise the quantiser has run between the two.
 template <class T, int NQ, bool FLY>
 __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
@@ -921,7 +876,7 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   int c, end;
   if constexpr (!FLY) {
     // heavy experts: k_few_heavy's products, a wave an expert (whose pairs are of different tokens)
-    const int done = p.T > 16 ? cls[2] : 0;
+    const int done = heavy_ahead(p) ? cls[2] : 0;
     for (int a = w; a < done; a += kDW) {
       const int4 x = uniform4(ent[a]);
       for (int i = tid & 63; i < x.z * NQ; i += 64) {   // (pair, 4 rows)
@@ -932,16 +887,10 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
         *y = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
       }
     }
-    part(1, 2, c, end);
-    if (done) {
-    } else if constexpr (NQ < 4) {
-      down_stream<T, NQ, 4, 1, ES == 1 || NQ == 1, false>(p, ent + cls[1], stok, hm, mine, h0, S, c, end);
-    } else {   // 16 rows by 16 tokens in 4 x 4 form would spill
-      for (; c < end;) {
-        const int a = c / S, s0 = c - a * S, s1 = min(S, s0 + end - c);
-        const int4 x = uniform4(ent[cls[1] + a]);
-        down_heavy<T, NQ, 1>(p, stok, mine, x.x, x.y, x.z, h0, 4 * s0, min(4 * s1, p.F * ES / kStep));
-        c += s1 - s0;
+    if constexpr (NQ < 4) {
+      if (!done) {
+        part(1, 2, c, end);
+        down_stream<T, NQ, 4, 1, ES == 1 || NQ == 1, false>(p, ent + cls[1], stok, hm, mine, h0, S, c, end);
       }
     }
     part(2, 3, c, end);
@@ -960,7 +909,7 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   }
 }
 
-// the down products of the heavy experts, into oh
+// the down products of the heavy experts, into oh: 64 tokens on 8 experts, 4096 x 1536, 36 us (101 MB of weights)
 template <class T>
 __global__ __launch_bounds__(512, 4) void k_few_heavy(FewParams p) {
   __shared__ __attribute__((aligned(16))) char smem[heavy_lds(4, sizeof(T) == 2 ? 2 : 1)];
@@ -975,7 +924,8 @@ __global__ __launch_bounds__(512, 4) void k_few_heavy(FewParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// router projection: experts e0 .. e0 + 3 for tokens t0 .. t0 + 4 NS - 1, the waves splitting H
+// router projection: experts e0 .. e0 + 3 for tokens t0 .. t0 + 4 NS - 1, the waves splitting H. Bound by its launch:
+// 128 experts x 2048, 4 us for one token, 4.7 for 8.
 template <class T, int NS>
 __device__ __forceinline__ void router_tile(const FewParams& p, float* red, int e0, int t0) {
   const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), j = lane & 3;
@@ -1057,7 +1007,7 @@ template <class T>
 hipError_t launch_prep(const FewParams& p, hipStream_t s, bool quant) {
   const int nr = p.wr ? (p.E + 3) / 4 * ((p.T + 4 * kSets - 1) / (4 * kSets)) : 0;
   if (nr == 0 && !quant) return hipSuccess;
-  // rows to quantise and, with given logits, the choice of experts: one launch for both (4.5 us of 114 at 32 tokens of 128 experts)
+  // rows to quantise and, with given logits, the choice of experts: one launch for both (4.5 us of 114 at 32 tokens)
   const int nq = quant ? p.T + (topk_in_prep(p, quant) ? (p.T + kPW - 1) / kPW : 0) : 0;
   prof_mark_begin("few_prep", s);
   k_few_prep<T><<<nr + nq, kPW * 64, 0, s>>>(p, nr);
@@ -1102,14 +1052,15 @@ hipError_t launch_layer(const FewParams& p, hipStream_t s) {
   if (sizeof(T) == 1 && !FLY &&
       (err = launch_int8_quant(p.h, true, n, p.F, p.r_cls + kClasses + 1, p.hq, p.hs, "int8_quant_h", s)) != hipSuccess)
     return err;
-  if (!FLY && p.T > 16) {
+  if (!FLY && heavy_ahead(p)) {
     prof_mark_begin("few_heavy", s);
-    k_few_heavy<T><<<std::min(n / 9 * (p.H / 128), persistent_grid(2)), 512, 0, s>>>(p);
+    k_few_heavy<T><<<std::min(std::max(1, n / 9) * (p.H / 128), persistent_grid(2)), 512, 0, s>>>(p);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     prof_mark_end(s);
   }
-  // as many rows per workgroup (each read of h serves them all) as leave every CU one
-  if (p.H >= 4096) return launch_down<T, 4, FLY>(p, s);
+  // as many rows per workgroup (each read of h serves them all) as leave every CU one. Half as many: 64 tokens of 128
+  // experts, 4096 x 1536 281 -> 370 us, 2048 x 768 102 -> 145; one token 23 -> 25 and 11.5 -> 15.
+  if (p.H >= kDown4) return launch_down<T, 4, FLY>(p, s);
   return p.H >= 2048 ? launch_down<T, 2, FLY>(p, s) : launch_down<T, 1, FLY>(p, s);
 }
 

@@ -10,8 +10,14 @@
 //             2 x 4 blocks of 32 x 32 (128 accumulators). A ring of two 64 KB stages; a K-tile is four
 //             MFMA steps of 32 elements, each step's fragments (6 reads of 1 KB per wave) read while the
 //             previous step's 8 MFMAs run. A tile of up to 128 rows runs half of them.
-//  k_i8_tile  64 x 64 or 128 x 128 tiles, two workgroups of 4 waves a CU, for products with too few tiles of 256 x 256
-//             to fill the chip.
+//             16384 x 4096 x 2048 in 128-140 us, 2.0-2.1 Pop/s, the matrix cores busy half of the cycles at 1.95 GHz;
+//             the products of 65536 pairs with K = 768 in 172-185 us, 1.15 Pop/s. Bound by the main loop (2.4 Pop/s
+//             alone) and the stores, which run at the write rate and which nothing overlaps: without them 114 and
+//             138 us, without the loads 120 and 154. Tried against that: the next tile's first K-tiles ahead of the
+//             stores (no gain); two workgroups of 4 waves a CU on 128 x 256 tiles (148 and 208 us: half as many
+//             rows again to load); starting the CUs at different times (133 and 182 us).
+//  k_i8_tile  64 x 64 or 128 x 128 tiles, one or two workgroups of 4 waves a CU, for products with too few tiles of
+//             256 x 256 to fill the chip. Bound by latency: 10 us for 1117 x 777 x 1104.
 //
 // Epilogues store straight from the accumulators, in whole lines and without LDS: the B rows of a tile are
 // placed in LDS so that the 4 column blocks of a lane are 4 neighbouring channels of one row (256 bytes of

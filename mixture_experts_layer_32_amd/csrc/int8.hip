@@ -2,10 +2,14 @@
 //
 // k_int8_quant       one wavefront per row. Rows of up to 4096 elements are held in registers between
 //                    the maximum and the conversion, longer ones are read twice (the second time from
-//                    L2). Bound by HBM: 2 (4) bytes read and 1 written per bf16 (fp32) element.
+//                    L2). Bound by HBM: 2 (4) bytes read and 1 written per bf16 (fp32) element. 65536 x 512
+//                    bf16 20.6 us (4.9 TB/s, a copy's rate), 131072 x 768 fp32 88 us (5.7 TB/s), 65536 x 768
+//                    bf16 37 us (a quarter of its lanes idle). Two or four short rows a wave: 26 us for 512
+//                    columns, 39 us for 768; several rows a wave in a loop and non-temporal loads: slower too.
 // k_int8_rows        y = diag(s) (q p^T) diag(t) for M <= 64: a workgroup takes 16 output channels of one
 //                    group, its waves split K, so that the weight is read once with every load of a
-//                    workgroup in flight at the same time. Bound by reading the weight.
+//                    workgroup in flight at the same time. Bound by reading the weight, and below some MB of it
+//                    by the launch: 4.1 us for one row, 4096 channels and K = 2048; 6.7 us for 16 rows and K = 4096.
 #include <algorithm>
 
 #include "engine.h"
@@ -34,7 +38,8 @@ __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int
                                                     float* __restrict__ scales) {
   constexpr bool F32 = sizeof(T) == 4;
   const int lane = threadIdx.x & 63;
-  const int64_t r = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6), n = nrows ? min(rows, (int64_t)*nrows) : rows;
+  const int64_t r = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t n = nrows ? min(rows, (int64_t)*nrows) : rows;
   if (r >= n) return;
   const T* row = x + (size_t)r * cols;
   uint8_t* out = q + (size_t)r * cols;
@@ -86,7 +91,8 @@ __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int
 template <class T>
 void launch_quant_t(const void* x, int64_t rows, int cols, const int* nrows, uint8_t* q, float* scales, hipStream_t s) {
   const T* p = static_cast<const T*>(x);
-  const int64_t b = (rows + 3) / 4;   // a dimension of a grid holds less than 2^32 threads: 2^22 blocks, then more rows of them
+  // a dimension of a grid holds less than 2^32 threads: 2^22 workgroups, then more rows of them
+  const int64_t b = (rows + 3) / 4;
   const dim3 g((unsigned)std::min<int64_t>(b, 1 << 22), (unsigned)((b + (1 << 22) - 1) >> 22));
   if (cols <= 512) k_int8_quant<T, 1><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
   else if (cols <= 1024) k_int8_quant<T, 2><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
@@ -181,6 +187,14 @@ hipError_t launch_int8_quant(const void* x, bool f32, int64_t rows, int cols, co
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;
+}
+
+// One weight is read through LDS tiles instead where many channels times many rows would read the rows of x too often:
+// K = 4096, 64 rows of 4096 channels 13.1 us here, 13.5 on tiles; 16 and 32 rows of 8192 11.3 and 16.1, 14.0 and
+// 14.4; 16 rows of 16384 22.2, 19.1. Groups are better off here at any size (64 rows in 2 to 16 groups: 6.5-8.7 us,
+// 9.2-9.7 on tiles, mostly of rows that are not there).
+bool int8_rows_fit(const I8Params& p) {
+  return p.M <= kFewTokens && (p.offsets || p.N * ((p.M + 15) / 16) <= 12288);
 }
 
 hipError_t launch_int8_rows(const I8Params& p, hipStream_t s) {

@@ -957,6 +957,11 @@ struct FewLayout {
   size_t cls, ent, tok, idx, wt, h, hlo, xq, xs, hq, hs, hmax, oh, total;
 };
 
+// 8-bit weights: h is quantised by the down kernel's workgroups, each for itself, instead of in a launch of its own.
+// For up to 4 tokens (one set) and few values: one token, top-8, F = 768 23.7 us against 24.1; 4 tokens, top-2,
+// F = 256 14.1 against 15.8; but 2 tokens, top-8, F = 768 30.3 against 28.4.
+bool quantise_in_down(const moe_desc& d) { return d.T <= 4 && d.T * d.topk * d.F <= 8192; }
+
 FewLayout few_layout(const moe_desc& d, bool int8) {
   FewLayout L{};
   const size_t n = (size_t)d.T * d.topk, El = (size_t)d.E_local, F = (size_t)d.F;
@@ -978,8 +983,8 @@ FewLayout few_layout(const moe_desc& d, bool int8) {
   L.xs = take(int8 ? (size_t)d.T * 4 : 0);
   L.hq = take(int8 ? n * F : 0);
   L.hs = take(int8 ? n * 4 : 0);
-  L.hmax = take(int8 && d.T <= 4 ? n * F : 0);
-  L.oh = take(d.T > 16 ? n * d.H * 4 : 0);
+  L.hmax = take(int8 && quantise_in_down(d) ? n * F : 0);
+  L.oh = take(d.T > 8 ? n * d.H * 4 : 0);
   L.total = off;
   return L;
 }
@@ -1109,7 +1114,7 @@ moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t*
   p.G = G;
   p.f32 = type == MOE_TYPE_FP32;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = M <= kFewTokens ? launch_int8_rows(p, s) : launch_int8_matmul(p, persistent_grid(1), "int8_matmul", s);
+  const hipError_t e = int8_rows_fit(p) ? launch_int8_rows(p, s) : launch_int8_matmul(p, persistent_grid(1), "int8_matmul", s);
   if (e != hipSuccess) return hip_fail(e, "int8 product launch");
   return MOE_OK;
 }
@@ -1193,7 +1198,7 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
     p.xs = reinterpret_cast<float*>(w + L.xs);
     p.hq = reinterpret_cast<uint8_t*>(w + L.hq);
     p.hs = reinterpret_cast<float*>(w + L.hs);
-    p.hmax = d->T <= 4 ? reinterpret_cast<unsigned*>(w + L.hmax) : nullptr;
+    p.hmax = quantise_in_down(*d) ? reinterpret_cast<unsigned*>(w + L.hmax) : nullptr;
     p.x = p.xq;
     if ((e = launch_few(p, 1, s)) != hipSuccess) return hip_fail(e, "few-token launch");
     return MOE_OK;

@@ -204,9 +204,9 @@ struct FewParams {
   void *h, *hlo;         // [pairs, F] w silu(a) b: fp32, or bf16 high and low parts
   uint8_t *xq, *hq;      // 8-bit weights: quantised x [T, H] and h [pairs, F], and their scales
   float *xs, *hs;
-  unsigned* hmax;        // T <= 4: magnitude bits of the largest |h| of each 4 of a pair's row [pairs, F / 4]
-                         //   (h is then quantised in the down kernel); null otherwise
-  float* oh;             // [pairs, H] down products of experts with more than 8 tokens, of more than 16 tokens in all
+  unsigned* hmax;        // magnitude bits of the largest |h| of each 4 of a pair's row [pairs, F / 4], where the
+                         //   down kernel quantises h (8-bit weights, up to 4 tokens); null otherwise
+  float* oh;             // [pairs, H] down products of the experts of more than 8 tokens (k_few_heavy)
   int* r_idx;            // [T k] chosen experts and their weights, of more than 16 tokens
   float* r_wt;
   int *r_cls, *r_tok;    // routing, from the gate/up kernel to the down kernel
@@ -239,6 +239,7 @@ struct I8Params {
 // device, or null
 hipError_t launch_int8_quant(const void* x, bool f32, int64_t rows, int cols, const int* nrows, uint8_t* q,
                              float* scales, const char* name, hipStream_t s);
+bool int8_rows_fit(const I8Params& p);                                                            // launch_int8_rows is the faster
 hipError_t launch_int8_rows(const I8Params& p, hipStream_t s);                                    // M <= 64
 hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hipStream_t s);      // any M
 

@@ -142,7 +142,7 @@ def run_matmul(M, N, K, dt, offsets=None, seed=0, lo=-127):
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 2048, 768), (3, 17, 80), (16, 100, 2048), (17, 33, 112), (33, 256, 64),
                                    (64, 777, 1104), (64, 16, 4096), (65, 1, 16), (65, 256, 128), (100, 300, 144),
-                                   (256, 256, 256), (257, 264, 2048), (700, 1000, 400), (1300, 2048, 768)])
+                                   (16, 9000, 272), (33, 8192, 128), (64, 4100, 80), (256, 256, 256), (257, 264, 2048), (700, 1000, 400), (1300, 2048, 768)])
 def test_product_bit_exact(M, N, K, dt):
     print("case int8 product", M, N, K, dt, flush=True)
     run_matmul(M, N, K, dt, seed=M + N + K)
@@ -320,6 +320,8 @@ LAYERS = [
     dict(T=700, H=2048, F=768, E=10, k=1),
     dict(T=1500, H=512, F=256, E=12, k=3, zipf_s=1.1),
     dict(T=2100, H=256, F=1024, E=8, k=4),              # the 256 x 256 engine for the gate/up products
+    dict(T=4, H=512, F=256, E=4, k=4),                  # h quantised by the down kernel, four tokens an expert
+    dict(T=2, H=2048, F=768, E=128, k=8),               # and by a launch of its own
     dict(T=8, H=512, F=384, E=5, k=5),                  # few tokens: 5 to 8 an expert, rows of h that end in half
     dict(T=12, H=2048, F=384, E=3, k=3),                # 256 bytes; 9 to 16 an expert
     dict(T=16, H=4096, F=128, E=20, k=9),
