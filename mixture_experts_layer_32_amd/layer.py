@@ -40,15 +40,16 @@ def _on(device, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
-    """A new output for a call on `stream`, from that stream's memory: memory of the current stream may still be
-    written by work of its own."""
+def _empty(shape, dtype, like, stream):
+    """A new output for a call on `stream`, on the device of the tensor `like`, from that stream's memory: memory of
+    the current stream may still be written by work of its own."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        # the cheapest of torch's calls for it: 0.9 us against 1.4 of torch.empty
+        return torch.empty_like(like, dtype=dtype) if like.shape == shape else like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _device(device):
@@ -190,11 +191,11 @@ class FewTokenLayer:
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         el, dev = self.dtype, self.device
         handle = _on(dev, stream)
+        _expect(x, "x", self._x, el, dev)
         if y is None:
-            y = _empty(self._x, el, dev, stream)
+            y = _empty(self._x, el, x, stream)
         else:
             _expect(y, "y", self._x, el, dev)
-        _expect(x, "x", self._x, el, dev)
         _expect(w_gate, "w_gate", self._w_in, el, dev)
         _expect(w_up, "w_up", self._w_in, el, dev)
         _expect(w_down, "w_down", self._w_out, el, dev)
@@ -209,7 +210,7 @@ class FewTokenLayer:
     def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
         """The forward from x and w_router [E_total, H]; returns (y, logits)."""
         if logits is None:
-            logits = _empty(self._logits, torch.float32, self.device, stream)
+            logits = _empty(self._logits, torch.float32, self.ws, stream)
         else:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, self.dtype, self.device)
@@ -236,11 +237,11 @@ def int8_quantize(x, q=None, scales=None, stream=None):
         raise ValueError("x: expected a contiguous tensor")
     handle = _on(dev, stream)
     if q is None:
-        q = _empty(shape, torch.int8, dev, stream)
+        q = _empty(shape, torch.int8, x, stream)
     else:
         _expect(q, "q", shape, torch.int8, dev)
     if scales is None:
-        scales = _empty(shape[:-1], torch.float32, dev, stream)
+        scales = _empty(shape[:-1], torch.float32, x, stream)
     else:
         _expect(scales, "scales", shape[:-1], torch.float32, dev)
     K = shape[-1]
@@ -252,7 +253,8 @@ def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bflo
     """y [M, N] of 8-bit rows x [M, K] and weights w [N, K], or w [G, N, K] with offsets [G + 1] int32: rows
     offsets[g] .. offsets[g+1]-1 are multiplied by w[g]. A y that is given sets the dtype, and its rows
     outside the groups are left as they were (a y made here holds anything there)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (2 if offsets is None else 3):
+    if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor)
+            or w.dim() != (2 if offsets is None else 3)):
         raise ValueError("expected x [M, K] and w [N, K], or w [G, N, K] with offsets")
     dev, (M, K) = x.device, x.shape
     handle = _on(dev, stream)
@@ -269,7 +271,7 @@ def int8_matmul(x, x_scales, w, w_scales, offsets=None, y=None, dtype=torch.bflo
         _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
     if y is None:
         t = _int8_type(dtype)
-        y = _empty((M, N), dtype, dev, stream)
+        y = _empty((M, N), dtype, x, stream)
     else:
         t = _int8_type(y.dtype)
         _expect(y, "y", (M, N), y.dtype, dev)
@@ -293,11 +295,11 @@ class Int8Layer:
     def _run(self, x, w_router, logits, w_gate, w_up, w_down, y, stream):
         dev = self.device
         handle = _on(dev, stream)
+        _expect(x, "x", self._x, torch.bfloat16, dev)
         if y is None:
-            y = _empty(self._x, torch.bfloat16, dev, stream)
+            y = _empty(self._x, torch.bfloat16, x, stream)
         else:
             _expect(y, "y", self._x, torch.bfloat16, dev)
-        _expect(x, "x", self._x, torch.bfloat16, dev)
         for name, (w, s), shape in (("w_gate", w_gate, self._w_in), ("w_up", w_up, self._w_in),
                                     ("w_down", w_down, self._w_out)):
             _expect(w, name, shape, torch.int8, dev)
@@ -314,7 +316,7 @@ class Int8Layer:
     def forward_router(self, x, w_router, w_gate, w_up, w_down, y=None, logits=None, stream=None):
         """The forward from x and w_router [E_total, H] bf16; returns (y, logits)."""
         if logits is None:
-            logits = _empty(self._logits, torch.float32, self.device, stream)
+            logits = _empty(self._logits, torch.float32, self.ws, stream)
         else:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, torch.bfloat16, self.device)
