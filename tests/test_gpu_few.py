@@ -157,19 +157,20 @@ def test_ties_and_lowest_values():
 
 @pytest.mark.parametrize("T", [5, 40])
 def test_masked_logits(T):
-    """Experts masked by minus infinity: fewer left than slots give weights of zero, none left gives NaN in that
-    token's y alone, as in moe_fwd."""
+    """Experts masked by minus infinity: fewer left than slots give weights of zero, none left, or a NaN, gives NaN
+    in that token's y alone, as in moe_fwd."""
     print("case few masked", T, flush=True)
     k = Case(T=T, H=256, F=128, E=6, k=3)
     lg = k.lg.clone()
     y0 = k.run().clone()
     lg[1, 2:] = float("-inf")
     lg[3] = float("-inf")
+    lg[4, 3] = float("nan")
     y = k.run(logits=lg).clone()
     full = MoELayer(T, 256, 128, 6, 3).forward(k.x, lg, k.wg, k.wu, k.wd)
     torch.cuda.synchronize()
-    assert torch.isnan(y[3]).all() and torch.isnan(full[3]).all()
-    rest = [t for t in range(T) if t not in (1, 3)]
+    assert torch.isnan(y[3:5]).all() and torch.isnan(full[3:5]).all()
+    rest = [t for t in range(T) if t not in (1, 3, 4)]
     assert torch.equal(y[rest], y0[rest])
     two = oracle.forward(k.L["x"][1:2], k.L["logits"][1:2, :2], k.L["wg"][:2], k.L["wu"][:2], k.L["wd"][:2], 2)[0]
     assert oracle.rel_frobenius(y[1:2].float().cpu().numpy(), two) <= 2 * TOL["bf16"]

@@ -92,11 +92,11 @@ def test_quantise_ties_swept():
 
 
 def test_quantise_many_short_rows():
-    """More rows than one dimension of a grid takes (2^32 threads at a wavefront a row)."""
+    """More rows than one dimension of a grid takes (2^32 threads at a wavefront a row), and 2^31 elements."""
     print("case int8 quant rows", flush=True)
     rows = (1 << 26) + 9
-    x = torch.arange(16, device="cuda").to(torch.bfloat16).repeat(rows, 1)
-    x[-3:, 0] = torch.tensor([20.0, 30.0, -40.0], device="cuda")
+    x = torch.arange(32, device="cuda").to(torch.bfloat16).repeat(rows, 1)
+    x[-3:, 0] = torch.tensor([40.0, 50.0, -60.0], device="cuda")
     q, s = int8_quantize(x)
     torch.cuda.synchronize()
     for at in (slice(0, 5), slice((1 << 24) - 2, (1 << 24) + 3), slice(rows - 12, rows)):
@@ -348,7 +348,24 @@ def test_layer_matches_float64(c):
     assert torch.equal(first.view(torch.uint8), y.view(torch.uint8))
 
 
-@pytest.mark.parametrize("c", [c for c in LAYERS if c["T"] <= 64 or c["E"] <= 256][::2], ids=name)
+@pytest.mark.parametrize("H,F", [(2048, 128), (256, 2048)])
+def test_layer_past_32_bits(H, F):
+    """More than 2^31 elements of the pairs' outputs, or of h: the first and last tokens are those of a small call
+    (each token's arithmetic is its own, and the tiles' sums are exact)."""
+    print("case int8 large layer", H, F, flush=True)
+    T, E, k = 140000, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+    lg = torch.randn(T, E, device="cuda", generator=g)
+    w = [int8_quantize(torch.randn(E, a, b, device="cuda", generator=g) / b ** 0.5) for a, b in ((F, H), (F, H), (H, F))]
+    y = Int8Layer(T, H, F, E, k).forward(x, lg, *w)
+    small = Int8Layer(100, H, F, E, k)
+    for a in (0, T // 2, T - 100):
+        assert torch.equal(small.forward(x[a:a + 100], lg[a:a + 100], *w), y[a:a + 100]), a
+
+
+@pytest.mark.parametrize("c", [c for c in LAYERS if c["T"] <= 64 or c["E"] <= 256][::2]
+                         + [dict(T=90, H=256, F=128, E=40, k=12)], ids=name)
 def test_layer_with_the_router(c):
     print("case int8 layer router", c, flush=True)
     k = Case(**c)
@@ -367,6 +384,20 @@ def test_layer_share_without_tokens_is_zero():
         y = k.run()
         torch.cuda.synchronize()
         assert torch.count_nonzero(y) == 0 and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("T", [5, 90])
+def test_layer_masked_logits(T):
+    print("case int8 layer masked", T, flush=True)
+    k = Case(T=T, H=256, F=128, E=6, k=3)
+    y0 = k.run().clone()
+    k.lg[1, 2:] = float("-inf")                         # two experts left for three slots
+    k.lg[3] = float("-inf")
+    k.lg[4, 3] = float("nan")
+    y = k.run()
+    torch.cuda.synchronize()
+    rest = [t for t in range(T) if t not in (1, 3, 4)]
+    assert torch.isnan(y[3:5]).all() and torch.isfinite(y[1]).all() and torch.equal(y[rest], y0[rest])
 
 
 def test_layer_nan_token_stays_alone():
@@ -427,7 +458,7 @@ def test_new_outputs_on_another_stream():
         torch.cuda._sleep(20_000_000)
         [t.fill_(5) for t in old]
         del old                                         # freed while the current stream has yet to write them
-        for stream in (side, side.cuda_stream):
+        for stream in (side, side.cuda_stream, side):
             got = int8_quantize(x, stream=stream)
             z = int8_matmul(*got, *got, dtype=torch.float32, stream=stream)
         torch.cuda.synchronize()
