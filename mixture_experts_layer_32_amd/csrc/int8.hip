@@ -3,9 +3,9 @@
 // k_int8_quant       one wavefront per row. Rows of up to 4096 elements are held in registers between
 //                    the maximum and the conversion, longer ones are read twice (the second time from
 //                    L2). Bound by HBM: 2 (4) bytes read and 1 written per bf16 (fp32) element. 65536 x 512
-//                    bf16 20.6 us (4.9 TB/s, a copy's rate), 131072 x 768 fp32 88 us (5.7 TB/s), 65536 x 768
-//                    bf16 37 us (a quarter of its lanes idle). Two or four short rows a wave: 26 us for 512
-//                    columns, 39 us for 768; several rows a wave in a loop and non-temporal loads: slower too.
+//                    bf16 20.3 us (5.0 TB/s, a copy's rate), 131072 x 768 fp32 88 us (5.7 TB/s), 65536 x 768
+//                    bf16 33 us (4.5 TB/s). Two or four short rows a wave: 26 us for 512 columns; several rows a
+//                    wave in a loop and non-temporal loads: slower too.
 // k_int8_rows        y = diag(s) (q p^T) diag(t) for M <= 64: a workgroup takes 16 output channels of one
 //                    group, its waves split K, so that the weight is read once with every load of a
 //                    workgroup in flight at the same time. Bound by reading the weight, and below some MB of it
@@ -30,9 +30,23 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   }
 }
 
-// NV: 512-element pieces of a row held in registers (0: rows of any length, read twice). nrows: the row
+template <class T, int EL>
+__device__ __forceinline__ void load_el(const T* p, float (&v)[EL]) {
+  if constexpr (EL == 8) {
+    load8(p, v);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+  } else {
+    const uint4 a = ld16(p);
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+  }
+}
+
+// NV: pieces of a row, EL elements a lane, held in registers (0: rows of any length, read twice). nrows: the row
 // count on the device, where the host does not know it (null: rows).
-template <class T, int NV>
+template <class T, int NV, int EL>
 __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int64_t rows, int cols,
                                                     const int* __restrict__ nrows, uint8_t* __restrict__ q,
                                                     float* __restrict__ scales) {
@@ -45,28 +59,31 @@ __global__ __launch_bounds__(256) void k_int8_quant(const T* __restrict__ x, int
   uint8_t* out = q + (size_t)r * cols;
   unsigned m = 0u;
   if constexpr (NV > 0) {
-    float v[NV][8];
+    float v[NV][EL];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = 512 * i + 8 * lane;
+      const int c = EL * (64 * i + lane);
       if (c < cols) {
-        load8(row + c, v[i]);
+        load_el<T, EL>(row + c, v[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        for (int j = 0; j < EL; ++j) v[i][j] = 0.f;
       }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[i][j]));
+      for (int j = 0; j < EL; ++j) m = max(m, mag_bits(v[i][j]));
     const Q8Row R(wave_max_u32(m));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = 512 * i + 8 * lane;
-      unsigned o[2];
+      const int c = EL * (64 * i + lane);
+      unsigned o[EL / 4];
       q8_pack<F32>(v[i], R, o);
-      if (c < cols) *reinterpret_cast<uint2*>(out + c) = make_uint2(o[0], o[1]);
+      if (c < cols) {
+        if constexpr (EL == 8) *reinterpret_cast<uint2*>(out + c) = make_uint2(o[0], o[1]);
+        else *reinterpret_cast<unsigned*>(out + c) = o[0];
+      }
     }
     if (lane == 0) scales[r] = R.scale;
   } else {
@@ -94,11 +111,16 @@ void launch_quant_t(const void* x, int64_t rows, int cols, const int* nrows, uin
   // a dimension of a grid holds less than 2^32 threads: 2^22 workgroups, then more rows of them
   const int64_t b = (rows + 3) / 4;
   const dim3 g((unsigned)std::min<int64_t>(b, 1 << 22), (unsigned)((b + (1 << 22) - 1) >> 22));
-  if (cols <= 512) k_int8_quant<T, 1><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
-  else if (cols <= 1024) k_int8_quant<T, 2><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
-  else if (cols <= 2048) k_int8_quant<T, 4><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
-  else if (cols <= 4096) k_int8_quant<T, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
-  else k_int8_quant<T, 0><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  // pieces of 256 or 512 elements, so that few of the lanes are idle: 65536 x 768 bf16 33 us, 36 in pieces of 512;
+  // 262144 x 256 58 and 68; 32768 x 1536 31 in three pieces of 512, 34 in the registers of four
+  if (cols <= 256) k_int8_quant<T, 1, 4><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 512) k_int8_quant<T, 1, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 768) k_int8_quant<T, 3, 4><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 1024) k_int8_quant<T, 2, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 1536) k_int8_quant<T, 3, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 2048) k_int8_quant<T, 4, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else if (cols <= 4096) k_int8_quant<T, 8, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
+  else k_int8_quant<T, 0, 8><<<g, 256, 0, s>>>(p, rows, cols, nrows, q, scales);
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -45,7 +45,7 @@ def check_quant(x, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 528), (1000, 512), (77, 1040), (5, 2048), (9, 4096), (2, 4112),
+@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 528), (1000, 512), (6, 256), (5, 768), (13, 1008), (77, 1040), (3, 1536), (5, 2048), (9, 4096), (2, 4112),
                                        (1, 131072), (4099, 48)])
 def test_quantise_bit_exact(rows, cols, dt):
     print("case int8 quant", rows, cols, dt, flush=True)
