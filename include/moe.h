@@ -285,8 +285,8 @@ moe_status moe_int8_matmul(const int8_t* x, const float* x_scales, const int8_t*
  * (x, y and w_router; MOE_ERR_UNSUPPORTED_MODE otherwise). Weights and scales as moe_int8_quantize
  * gives them for each matrix along its last axis: w_gate, w_up [E_local, F, H] with s_gate, s_up
  * [E_local, F], w_down [E_local, H, F] with s_down [E_local, H].
- * Up to 64 tokens run on the kernels of moe_fwd_few (y summed in fp32), more on the grouped products
- * (each pair's output rounded to bf16 before the combine, as in moe_fwd).
+ * Up to 64 tokens run on the kernels of moe_fwd_few, more on the grouped products; either way the
+ * pairs' outputs are fp32 and y, their sum, is rounded once.
  * logits and w_router as in moe_fwd_few, but with w_router, more than 64 tokens need E_total <= 256
  * (MOE_ERR_UNSUPPORTED_SHAPE: moe_router_fwd, then the call without). desc.recompute has no meaning here.
  * 16-byte alignment of every tensor, 4-byte of logits and scales, 256-byte of ws

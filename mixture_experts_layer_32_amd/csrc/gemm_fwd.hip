@@ -120,9 +120,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(FwdParams p) {
 // 16 bytes: 2048 bf16) of tpw consecutive tokens (combine_tpw), 4 wavefronts per block (the parts of
 // a token in neighbouring wavefronts); the slots' pair positions reach every lane through readlane.
 // (One wavefront per whole token left the last of its ~3 rounds of waves per CU mostly empty.)
-template <class T>
+template <class T, class D>
 __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ src, const int* __restrict__ pair_pos,
-                                                 T* __restrict__ out, int64_t ntok, int k, int H, int tpw) {
+                                                 D* __restrict__ out, int64_t ntok, int k, int H, int tpw) {
   constexpr int VEC = Elem<T>::VEC;
   const int lane = threadIdx.x & 63;
   const int nch = H / VEC, nparts = (nch + 127) / 128;
@@ -152,14 +152,14 @@ hipError_t launch_forward_gemms(const FwdParams& p, int grid, hipStream_t s, boo
   return hipSuccess;
 }
 
-template <class T>
+template <class T, class D>
 hipError_t launch_combine(const void* src, const int* pair_pos, void* out, int64_t T_, int k, int H, int tpw,
                           hipStream_t s) {
   prof_mark_begin("combine", s);
   const int64_t nparts = (H / Elem<T>::VEC + 127) / 128;
   const int64_t waves = (T_ + tpw - 1) / tpw * nparts;
-  k_combine<T><<<(unsigned)((waves + 3) / 4), 256, 0, s>>>(static_cast<const T*>(src), pair_pos,
-                                                           static_cast<T*>(out), T_, k, H, tpw);
+  k_combine<T, D><<<(unsigned)((waves + 3) / 4), 256, 0, s>>>(static_cast<const T*>(src), pair_pos,
+                                                              static_cast<D*>(out), T_, k, H, tpw);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   prof_mark_end(s);
@@ -226,6 +226,7 @@ hipError_t launch_router_bwd_f32(const RouterParams& p, hipStream_t s) {
 
 template hipError_t launch_forward_gemms<float>(const FwdParams&, int, hipStream_t, bool);
 template hipError_t launch_combine<float>(const void*, const int*, void*, int64_t, int, int, int, hipStream_t);
+template hipError_t launch_combine<float, bf16>(const void*, const int*, void*, int64_t, int, int, int, hipStream_t);
 template hipError_t launch_combine<bf16>(const void*, const int*, void*, int64_t, int, int, int, hipStream_t);
 
 }  // namespace moe

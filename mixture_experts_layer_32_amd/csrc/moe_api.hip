@@ -1142,10 +1142,10 @@ Int8Layout int8_layout(moe_desc d) {
   L.scratch = take(L.route.o);   // the forward workspace up to its first activation
   L.xq = take((size_t)d.T * H);
   L.xs = take((size_t)d.T * 4);
-  L.h = take(n * F * 4);
+  L.h = take(n * std::max(F, H) * 4);
+  L.o = L.h;   // the pairs' outputs, fp32, take the place of h once its rows are quantised
   L.hq = take(n * F);
   L.hs = take(n * 4);
-  L.o = take(n * H * 2);
   L.total = off;
   return L;
 }
@@ -1249,12 +1249,13 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
   dp.N = d->H;
   dp.K = d->F;
   dp.G = d->E_local;
+  dp.f32 = true;   // summed by the combine before y's one rounding
   if ((e = launch_int8_quant(h, true, L.route.rows, d->F, rp.offsets + d->E_local,
                              reinterpret_cast<uint8_t*>(w + L.hq), reinterpret_cast<float*>(w + L.hs), "int8_quant_h",
                              s)) != hipSuccess)
     return hip_fail(e, "int8 quantise launch");
   if ((e = launch_int8_matmul(dp, persistent_grid(1), "int8_down", s)) != hipSuccess) return hip_fail(e, "down launch");
-  if ((e = launch_combine<bf16>(w + L.o, rp.pair_pos, y, d->T, d->topk, d->H,
+  if ((e = launch_combine<float, bf16>(w + L.o, rp.pair_pos, y, d->T, d->topk, d->H,
                                 combine_tpw(d->topk, d->E_local, d->E_total), s)) != hipSuccess)
     return hip_fail(e, "combine launch");
   return MOE_OK;

@@ -272,10 +272,11 @@ __host__ __device__ constexpr int combine_tpw(int k, int E_local, int E_total) {
 // lane takes two chunks, so 16 slot rows are in flight per lane. The loop is uniform over the wave,
 // with every lane active at the readlane (a value computed under a narrower exec mask is undefined in
 // the lanes outside it, and the slots' lanes can lie past a short row's last chunk): lanes past the
-// row's end load zeros and store nothing.
-template <class T, int VEC>
+// row's end load zeros and store nothing. A chunk is 16 bytes of the source; the output is of its type, or bf16
+// from fp32 sources (8 bytes a chunk).
+template <class T, int VEC, class D>
 __device__ __forceinline__ void combine_row_part(const T* __restrict__ src, int ppv, int slot0, int k, int H, int nch,
-                                                 int part, int nparts, int lane, T* __restrict__ dst) {
+                                                 int part, int nparts, int lane, D* __restrict__ dst) {
   for (int cb = 128 * part; cb < nch; cb += 128 * nparts) {
     const int c0 = cb + lane;
     float acc[2][VEC];
@@ -305,10 +306,14 @@ __device__ __forceinline__ void combine_row_part(const T* __restrict__ src, int 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 res;
-      T* r = reinterpret_cast<T*>(&res);
+      D* r = reinterpret_cast<D*>(&res);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) r[v] = cvt_out<T>(acc[h][v]);
-      if (c0 + 64 * h < nch) st16(dst + (size_t)(c0 + 64 * h) * VEC, res);
+      for (int v = 0; v < VEC; ++v) r[v] = cvt_out<D>(acc[h][v]);
+      D* at = dst + (size_t)(c0 + 64 * h) * VEC;
+      if (c0 + 64 * h < nch) {
+        if constexpr (VEC * sizeof(D) == 16) st16(at, res);
+        else *reinterpret_cast<uint2*>(at) = make_uint2(res.x, res.y);
+      }
     }
   }
 }

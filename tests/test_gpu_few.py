@@ -15,6 +15,7 @@ import oracle
 from mixture_experts_layer_32_amd import inputs
 from mixture_experts_layer_32_amd.layer import FewTokenLayer, MoELayer
 from gpu_util import to_dev
+from rounding import BAR, excess
 
 pytestmark = pytest.mark.gpu
 
@@ -100,6 +101,18 @@ def test_few_matches_the_oracle(c):
     k.run()
     torch.cuda.synchronize()
     assert torch.equal(first.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("c", [c for c in CASES if c.get("mode") != "fp32"], ids=name)
+def test_few_is_rounded_once(c):
+    """h reaches the down product with both of its parts: y is off by half a bf16 step and fp32's accuracy."""
+    print("case few accuracy", c, flush=True)
+    k = Case(**c)
+    y = k.run()
+    torch.cuda.synchronize()
+    off = excess(y.float().cpu().numpy(), k.ref())
+    print("largest", float(off.max()), flush=True)
+    assert (off <= BAR).all(), int(np.argmax(off))
 
 
 @pytest.mark.parametrize("c", [c for i, c in enumerate(CASES) if i % 2 == 0], ids=name)

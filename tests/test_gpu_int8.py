@@ -16,6 +16,7 @@ import oracle
 from mixture_experts_layer_32_amd import inputs
 from mixture_experts_layer_32_amd.layer import FewTokenLayer, Int8Layer, int8_matmul, int8_quantize
 from gpu_util import to_dev
+from rounding import BAR, excess
 
 pytestmark = pytest.mark.gpu
 
@@ -346,6 +347,27 @@ def test_layer_matches_float64(c):
     k.run()
     torch.cuda.synchronize()
     assert torch.equal(first.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("c", [
+    dict(T=33, H=512, F=256, E=12, k=6),
+    dict(T=65, H=256, F=128, E=4, k=2),
+    dict(T=100, H=512, F=256, E=64, k=6, zipf_s=2.5),
+    dict(T=300, H=256, F=128, E=300, k=20),
+    dict(T=333, H=1024, F=640, E=16, k=4, E_local=4, e0=8),
+    dict(T=2100, H=256, F=1024, E=8, k=4),              # the 256 x 256 engine, gate/up and down
+], ids=name)
+def test_layer_is_rounded_once(c):
+    """Every token's y is off by half a bf16 step and fp32's accuracy, on both sides of 64 tokens. A byte of h within
+    its fp32 error (2^-21 of a value of 20 steps on average) of a tie may go the other way: 2e-5 of the up to 4096
+    bytes of a token, so fewer than one token in ten, are off by more."""
+    print("case int8 layer accuracy", c, flush=True)
+    k = Case(**c)
+    y = k.run()
+    torch.cuda.synchronize()
+    off = excess(y.float().cpu().numpy(), k.ref())
+    print("tokens past the bar", float((off > BAR).mean()), "largest", float(off.max()), flush=True)
+    assert (off <= BAR).mean() >= 0.9
 
 
 @pytest.mark.parametrize("H,F", [(2048, 128), (256, 2048)])
