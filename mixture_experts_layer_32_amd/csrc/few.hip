@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
       a *= xs * g[i];
       b *= xs * u[i];
     }
-    h[i] = wt * (a / (1.0f + expf(-a)) * b);
+    h[i] = weighted_swiglu(wt, a, b);
   }
   const size_t at = (size_t)pos * p.F + f0;
   if constexpr (sizeof(T) == 2) {

@@ -76,6 +76,11 @@ __device__ __forceinline__ void q8_pack(const float (&x)[N], const Q8Row& r, uns
   }
 }
 
+// w silu(a) b of the few-token kernels and of the 8-bit layer for any number of tokens: expf and a division, so that
+// a token's h has the same bits in either (with the hardware's approximate exponential and reciprocal in one of
+// them, bytes of h near a tie differed)
+__device__ __forceinline__ float weighted_swiglu(float w, float a, float b) { return w * (a / (1.0f + expf(-a)) * b); }
+
 // largest of v over the wave (values as unsigned), in every lane
 __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
   v = max(v, dpp_mov<kDppXor1>(v));

@@ -370,6 +370,32 @@ def test_layer_is_rounded_once(c):
     assert (off <= BAR).mean() >= 0.9
 
 
+def test_one_formula_on_both_sides_of_64_tokens():
+    """A token's h has the same bytes in a call of 64 tokens and in one of 96. Gate values of about -30, where an
+    approximate exponential is off by 30 times 2^-24, and rows of h of one magnitude, most of whose bytes are large: 16384
+    bytes a token, of which such an error moves one in 4e4. A moved byte shifts the token's whole row; without one the rows
+    differ in the order of fp32 sums, about 1e-6 of a row's rms, which changes the rounding of one output in 10^3."""
+    print("case int8 one formula", flush=True)
+    T, H, F, E, k = 96, 1024, 2048, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(12)
+
+    def randn(*s):
+        return torch.randn(*s, device="cuda", generator=g)
+
+    x = (1 + 0.05 * randn(T, H)).bfloat16()
+    wg = -30.0 / H + 0.3 * randn(E, F, H) / H ** 0.5
+    wu = 3.0 / H + 0.3 * randn(E, F, H) / H ** 0.5
+    w = [int8_quantize(v) for v in (wg, wu, randn(E, H, F) / F ** 0.5)]
+    lg = 0.1 * randn(T, E)
+    few = Int8Layer(64, H, F, E, k).forward(x[:64], lg[:64], *w)
+    many = Int8Layer(T, H, F, E, k).forward(x, lg, *w)[:64]
+    torch.cuda.synchronize()
+    differ = (few != many).float().mean(1)
+    print("most differing outputs of a token", float(differ.max()), "tokens", int((differ > 0.02).sum()), flush=True)
+    assert torch.isfinite(few).all() and (few != 0).any(1).all()
+    assert float(differ.max()) <= 0.02
+
+
 @pytest.mark.parametrize("H,F", [(2048, 128), (256, 2048)])
 def test_layer_past_32_bits(H, F):
     """More than 2^31 elements of the pairs' outputs, or of h: the first and last tokens are those of a small call
