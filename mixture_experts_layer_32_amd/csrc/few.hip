@@ -30,7 +30,7 @@
 //   k_few_down       9                32 (5.4 TB/s)     117 (6.1 TB/s)
 // About 5 us of the one-token k_few_gateup are its launch and the choice of experts, which it must wait for.
 //
-// h is kept in fp32's accuracy: as fp32, or in bf16 mode as the pair hi = bf16(h), lo = bf16(h - hi),
+// h is kept as fp32, or in bf16 mode to 2^-18 of each value as the pair hi = bf16(h), lo = bf16(h - hi),
 // whose two products cost matrix time that a read-bound kernel does not miss.
 #include <math.h>
 
@@ -363,10 +363,16 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
   }
   const size_t at = (size_t)pos * p.F + f0;
   if constexpr (sizeof(T) == 2) {
-    float lo[4];
+    // The high part is at most bf16's largest value: an h between that and fp32's would round to an infinity, and
+    // the low part of an infinite h would be a NaN. An infinite h has an infinite low part instead, a NaN a NaN.
+    constexpr float kTop = 0x1.fep127f;
+    float hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = h[i] - (float)(bf16)h[i];
-    eng::st8(static_cast<bf16*>(p.h) + at, eng::pack4(h[0], h[1], h[2], h[3]));
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = fminf(fmaxf(h[i], -kTop), kTop);
+      lo[i] = h[i] - (float)(bf16)hi[i];
+    }
+    eng::st8(static_cast<bf16*>(p.h) + at, eng::pack4(hi[0], hi[1], hi[2], hi[3]));
     eng::st8(static_cast<bf16*>(p.hlo) + at, eng::pack4(lo[0], lo[1], lo[2], lo[3]));
   } else {
     *reinterpret_cast<float4*>(static_cast<float*>(p.h) + at) = make_float4(h[0], h[1], h[2], h[3]);

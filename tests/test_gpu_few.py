@@ -202,6 +202,35 @@ def test_nan_token_stays_alone():
     assert torch.equal(y0[rest], y1[rest])
 
 
+@pytest.mark.parametrize("T,H", [(1, 256), (6, 256), (12, 2048), (12, 4096), (40, 256)])
+def test_h_at_the_top_of_fp32(T, H):
+    """h beyond bf16's largest value but not fp32's gives a finite y, an infinite h infinities, as the formula has it:
+    one expert, h = (x_0 w_gate)(x_0 w_up) since the sigmoid is 1, y the sum of F equal terms."""
+    print("case few large h", T, H, flush=True)
+    F, g = 128, 181.0 / 128
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    if T > 1:
+        x[T - 1, 0] = 4.0                               # h past fp32's range
+        x[T - 2, 0] = float("inf")
+        x[T - 3, 0] = float("nan")
+        x[T - 4, 0] = 0.0
+    wg, wu = (torch.zeros(1, F, H, dtype=torch.bfloat16) for _ in range(2))
+    wg[0, :, 0], wu[0, :, 0] = g * 2.0 ** 64, g * 2.0 ** 63     # h = 1.9996 * 2^127
+    wd = torch.full((1, H, F), 2.0 ** -20, dtype=torch.bfloat16)
+    wd[0, 1::2] *= -1
+    y = FewTokenLayer(T, H, F, 1, 1).forward(x.cuda(), torch.zeros(T, 1, device="cuda"), wg.cuda(), wu.cuda(), wd.cuda())
+    torch.cuda.synchronize()
+    y = y.float().cpu().numpy().astype(np.float64)
+    x0 = x[:, :1].double().numpy()
+    h = (x0 * g * 2.0 ** 64) * (x0 * g * 2.0 ** 63)
+    ref = np.where(h > np.finfo(np.float32).max, np.inf, h) * F * wd[0, :, 0].double().numpy()
+    fin = np.isfinite(ref).all(1)
+    assert fin.sum() == T - (3 if T > 1 else 0)
+    assert np.array_equal(y[~fin], ref[~fin], equal_nan=True)
+    assert np.allclose(y[fin], ref[fin], rtol=2.0 ** -8, atol=0)    # one rounding and 2^-17
+
+
 def test_prompt_then_tokens():
     """A prompt through the training forward, then its tokens again a few at a time: the same layer, each
     output rounded (moe_fwd also rounds w h and the experts' outputs to bf16: 3 roundings of 2^-8)."""
