@@ -109,41 +109,6 @@ __device__ __forceinline__ int block_sum(int v) {
 // ------------------------------------------------------------------------------------------------
 // routing of the few tokens inside a workgroup
 
-// The k best experts of a token by one wave (E <= 64 PER): lane j < k ends with the j-th expert and its
-// logit. A round takes the largest of the order-preserving 32-bit keys over the wave (DPP), and of the
-// lanes that hold it the lowest expert (ballots, experts 0..63 first).
-template <int PER>
-__device__ __forceinline__ void wave_topk(const float* row, int E, int k, int lane, int& my_e, float& my_v) {
-  unsigned key[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = e < E ? max((unsigned)(topk_key(row[e], 0) >> 32), 1u) : 0u;   // 0: no expert
-  }
-#pragma unroll 1
-  for (int j = 0; j < k; ++j) {
-    unsigned m = key[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
-    m = wave_max_u32(m);
-    int e = -1;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (e < 0) {
-        const unsigned long long at = __ballot(key[i] == m);
-        if (at) {
-          const int l = __ffsll(at) - 1;
-          e = 64 * i + l;
-          key[i] = lane == l ? 0u : key[i];
-        }
-      }
-    if (lane == j) {
-      my_e = e;
-      my_v = key_value((unsigned long long)m << 32);
-    }
-  }
-}
-
 // Experts with pairs, in classes by their number of tokens: more than 16, 9-16 (both "heavy"), 5-8, 3-4, 1-2.
 constexpr int kClasses = 5;
 constexpr int kClassBits = 12, kClassMask = (1 << kClassBits) - 1;   // of a count of experts by class, up to 512; five in 64 bits

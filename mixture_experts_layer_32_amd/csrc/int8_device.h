@@ -81,15 +81,4 @@ __device__ __forceinline__ void q8_pack(const float (&x)[N], const Q8Row& r, uns
 // them, bytes of h near a tie differed)
 __device__ __forceinline__ float weighted_swiglu(float w, float a, float b) { return w * (a / (1.0f + expf(-a)) * b); }
 
-// largest of v over the wave (values as unsigned), in every lane
-__device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
-  v = max(v, dpp_mov<kDppXor1>(v));
-  v = max(v, dpp_mov<kDppXor2>(v));
-  v = max(v, dpp_mov<kDppHalfMirror>(v));
-  v = max(v, dpp_mov<kDppMirror>(v));
-  const unsigned a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-  const unsigned c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-  return max(max(a, b), max(c, d));
-}
-
 }  // namespace moe

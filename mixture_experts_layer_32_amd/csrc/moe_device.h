@@ -353,6 +353,17 @@ __device__ __forceinline__ float group_max8(float m) {
   return fmaxf(m, dpp_mov<kDppHalfMirror>(m));
 }
 
+// largest of v over the wave (values as unsigned), in every lane
+__device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
+  v = max(v, dpp_mov<kDppXor1>(v));
+  v = max(v, dpp_mov<kDppXor2>(v));
+  v = max(v, dpp_mov<kDppHalfMirror>(v));
+  v = max(v, dpp_mov<kDppMirror>(v));
+  const unsigned a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const unsigned c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  return max(max(a, b), max(c, d));
+}
+
 // sigma(z) = 1 / (1 + e^-z), with the hardware reciprocal (v_rcp_f32, about 1 ulp) instead of an
 // IEEE division: the division's scale/Newton/fixup sequence was about ten instructions per element
 // in the SwiGLU and dSwiGLU epilogues, whose VALU work the matrix cores wait on. For large -z the

@@ -12,7 +12,7 @@
 //   k_route_topk     k <= 8: 64 tokens per block, 8 lanes per token; each lane sorts its eighth of
 //                    the experts 8 at a time by sorting networks on 64-bit (logit, index) keys into
 //                    a top-8 list, three shuffle steps merge the lists (route_device.h).
-//   k_route_topk_wave  k > 8: one wavefront per token, k rounds of a wave-wide argmax.
+//   k_route_topk_wave  k > 8: one wavefront per token, k rounds of a wave-wide maximum of the keys.
 //                    Both write, per block and local expert, a 64-bit mask of the tokens that chose it.
 //   k_route_colscan  one block per local expert: exclusive scan of the per-block counts.
 //   k_route_offsets  one block: expert offsets, M-tile tables and counts, and the offsets of the
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * LPT) void k_route_topk(RouteParams p) {
   }
 }
 
-// k > 8: one wavefront per token, k rounds of a wave-wide (value desc, index asc) argmax.
+// k > 8: one wavefront per token (wave_topk).
 template <int PER_LANE>
 __global__ __launch_bounds__(256) void k_route_topk_wave(RouteParams p) {
   __shared__ unsigned long long mask[kMaxExperts];
@@ -85,42 +85,10 @@ __global__ __launch_bounds__(256) void k_route_topk_wave(RouteParams p) {
     const int64_t t = t_base + tl;
     if (t >= p.T) break;
     const float* row = p.logits + t * p.E;
-    float v[PER_LANE];
-#pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
-      const int e = lane + 64 * i;
-      v[i] = e < p.E ? row[e] : -INFINITY;
-    }
-    unsigned taken = 0;
-    float top = 0.f, my_v = 0.f;
     int my_e = -1;
-    for (int j = 0; j < p.k; ++j) {
-      float bv = -INFINITY;
-      int be = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < PER_LANE; ++i) {
-        const int e = lane + 64 * i;
-        if (e < p.E && !((taken >> i) & 1u) && better(v[i], e, bv, be)) {
-          bv = v[i];
-          be = e;
-        }
-      }
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) {
-        const float ov = __shfl_xor(bv, off);
-        const int oe = __shfl_xor(be, off);
-        if (better(ov, oe, bv, be)) {
-          bv = ov;
-          be = oe;
-        }
-      }
-      if ((be & 63) == lane) taken |= 1u << (be >> 6);
-      if (lane == j) {
-        my_v = bv;
-        my_e = be;
-      }
-      if (j == 0) top = bv;
-    }
+    float my_v = 0.f;
+    wave_topk<PER_LANE>(row, p.E, p.k, lane, my_e, my_v);
+    const float top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_v), 0));
     const float z = lane < p.k ? expf(my_v - top) : 0.f;
     float s = z;
 #pragma unroll

@@ -11,16 +11,13 @@
 
 namespace moe {
 
-__device__ __forceinline__ bool better(float av, int ae, float bv, int be) {
-  return av > bv || (av == bv && ae < be);
-}
-
 // Order-preserving 64-bit key of (logit v, expert e): a larger key is a better candidate (larger logit,
 // then lower index). The high word maps the fp32 bits monotonically to unsigned order, with -0 taken
-// as +0 so that the two zeros tie as equal logits do; the low word is ~e. Finite logits only.
+// as +0 so that the two zeros tie as equal logits do; the low word is ~e. A NaN, of either sign, ranks above +infinity:
+// it is chosen, and makes the token's weights NaN.
 __device__ __forceinline__ unsigned long long topk_key(float v, int e) {
   unsigned u = __float_as_uint(v);
-  u = u == 0x80000000u ? 0u : u;
+  u = v != v ? 0x7fffffffu : u == 0x80000000u ? 0u : u;
   const unsigned o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   return ((unsigned long long)o << 32) | (unsigned)~e;
 }
@@ -98,6 +95,41 @@ __device__ __forceinline__ void select_top8(int E, int q, Get get, float (&tv)[8
   for (int j = 0; j < 8; ++j) {
     tv[j] = key_value(t[j]);
     ti[j] = key_expert(t[j]);
+  }
+}
+
+// The k best experts of a token by one wave (E <= 64 PER, every lane active): lane j < k ends with the j-th
+// expert and its logit. A round takes the largest of the order-preserving 32-bit keys over the wave (DPP), and of the
+// lanes that hold it the lowest expert (ballots, experts 0..63 first).
+template <int PER>
+__device__ __forceinline__ void wave_topk(const float* row, int E, int k, int lane, int& my_e, float& my_v) {
+  unsigned key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < E ? (unsigned)(topk_key(row[e], 0) >> 32) : 0u;   // 0: no expert (of no logit)
+  }
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    unsigned m = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    m = wave_max_u32(m);
+    int e = -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e < 0) {
+        const unsigned long long at = __ballot(key[i] == m);
+        if (at) {
+          const int l = __ffsll(at) - 1;
+          e = 64 * i + l;
+          key[i] = lane == l ? 0u : key[i];
+        }
+      }
+    if (lane == j) {
+      my_e = e;
+      my_v = key_value((unsigned long long)m << 32);
+    }
   }
 }
 

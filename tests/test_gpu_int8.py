@@ -460,6 +460,28 @@ def test_layer_nan_token_stays_alone():
         assert torch.isnan(y1[[7, 11]]).all() and torch.equal(y0[rest], y1[rest])
 
 
+@pytest.mark.parametrize("router", [False, True])
+def test_layer_nan_token_with_more_than_eight_slots(router):
+    """Logits that are NaN choose experts whose weights are NaN: the token's y is NaN, never zeros."""
+    print("case int8 layer nan top-12", router, flush=True)
+    for T in (20, 90):
+        k = Case(T=T, H=256, F=128, E=40, k=12)
+
+        def run():
+            return k.layer.forward_router(k.x, k.wr, *k.w, k.y)[0].clone() if router else k.run().clone()
+
+        y0 = run()
+        if router:
+            k.x[7, 3], k.x[11, 0] = float("nan"), float("inf")
+        else:
+            k.lg[7] = float("nan")
+            k.lg[11, 5] = float("nan")
+        y1 = run()
+        torch.cuda.synchronize()
+        rest = [t for t in range(T) if t not in (7, 11)]
+        assert torch.isnan(y1[[7, 11]]).all() and torch.equal(y0[rest], y1[rest]), T
+
+
 def test_prompt_then_tokens_with_one_set_of_weights():
     """A server's path: weights quantised once, a prompt through the grouped products, its rows again as few
     tokens, and the composition of the public calls (quantise, grouped product by the routing's offsets)."""

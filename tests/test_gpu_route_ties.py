@@ -90,3 +90,30 @@ def test_routing_ties_bit_exact(T, E, k, el, e0):
     assert np.max(np.abs(got["weight"][eq] - 1.0 / k)) <= 1e-7
     # on all-equal rows the chosen experts are 0..k-1 in order
     assert np.array_equal(got["idx"][eq], np.broadcast_to(np.arange(k), (int(eq.sum()), k)))
+
+
+@pytest.mark.parametrize("E,k", [(128, 8), (40, 12), (128, 16), (200, 32), (512, 12)])
+def test_nan_logits_choose_real_experts(E, k):
+    """A NaN among a token's logits: k different experts all the same, with weights of NaN, and every pair in the
+    permutation; the other tokens are routed as without it."""
+    print(f"case route NaN E={E} k={k}", flush=True)
+    T = 150
+    lg = np.random.default_rng(E + k).standard_normal((T, E)).astype(np.float32)
+    want = oracle.route(lg, k)
+    bad = [3, 64, 77, 90, 149]
+    lg[3] = np.nan
+    lg[64, 5] = np.nan
+    lg[77, ::2] = np.nan
+    lg[90, 2] = np.copysign(np.float32(np.nan), -1)       # a NaN with its sign set
+    lg[149, 1:] = np.nan
+    layer = MoELayer(T, 256, 128, E, k)
+    layer.route(torch.from_numpy(lg).to("cuda"))
+    torch.cuda.synchronize()
+    r = {n: t.numpy() for n, t in layer.routing().items()}
+    rest = [t for t in range(T) if t not in bad]
+    assert np.array_equal(r["idx"][rest], want["idx"][rest])
+    assert np.isfinite(r["weight"][rest]).all() and np.isnan(r["weight"][bad]).all()
+    s = np.sort(r["idx"][bad], 1)
+    assert s.min() >= 0 and s.max() < E and (np.diff(s, axis=1) > 0).all()
+    assert np.array_equal(np.sort(r["perm"]), np.arange(T * k))
+    assert r["offsets"][-1] == T * k and np.array_equal(np.bincount(r["idx"].reshape(-1), minlength=E), r["counts"])
