@@ -52,6 +52,17 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _workspace(nbytes, device):
+    """Scratch memory that a layer's calls may use on any stream. torch may give memory that was freed on the current
+    stream with work queued that still writes it, and a call on another stream would not be behind that work: it is
+    waited for here, once. (Not while the stream is being captured, where nothing runs: such a layer's calls belong on
+    the captured stream, or behind it.)"""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+    return ws
+
+
 def _device(device):
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
@@ -69,9 +80,8 @@ class MoELayer:
         self.dtype = torch.float32 if mode == "fp32" else torch.bfloat16
         self.device = _device(device)
         self.fwd_ws_bytes, self.bwd_ws_bytes, self.saved_bytes = binding.query_sizes(self.desc)
-        u8 = dict(dtype=torch.uint8, device=self.device)
-        self.ws = torch.empty(max(self.fwd_ws_bytes, self.bwd_ws_bytes), **u8)
-        self.saved = torch.empty(self.saved_bytes, **u8)
+        self.ws = _workspace(max(self.fwd_ws_bytes, self.bwd_ws_bytes), self.device)
+        self.saved = _workspace(self.saved_bytes, self.device)
 
     @property
     def shape(self):
@@ -133,7 +143,7 @@ class MoELayer:
     def _router_ws(self):
         if getattr(self, "router_ws", None) is None:
             f, b = binding.query_router_sizes(self.desc)
-            self.router_ws = torch.empty(max(f, b, 256), dtype=torch.uint8, device=self.device)
+            self.router_ws = _workspace(max(f, b, 256), self.device)
         return self.router_ws
 
     def router_forward(self, x, w_router, logits=None, stream=None):
@@ -184,7 +194,7 @@ class FewTokenLayer:
         self.mode = mode
         self.dtype = torch.float32 if mode == "fp32" else torch.bfloat16
         self.device = _device(device)
-        self.ws = torch.empty(binding.query_few_sizes(d), dtype=torch.uint8, device=self.device)
+        self.ws = _workspace(binding.query_few_sizes(d), self.device)
         self._x, self._logits, self._wr = (d.T, d.H), (d.T, d.E_total), (d.E_total, d.H)
         self._w_in, self._w_out = (d.E_local, d.F, d.H), (d.E_local, d.H, d.F)
 
@@ -288,7 +298,7 @@ class Int8Layer:
     def __init__(self, T, H, F, E_total, topk, E_local=None, expert_offset=0, device="cuda"):
         self.desc = d = binding.Desc.make(T, H, F, E_total, topk, "bf16", E_local, expert_offset)
         self.device = _device(device)
-        self.ws = torch.empty(binding.query_int8_sizes(d), dtype=torch.uint8, device=self.device)
+        self.ws = _workspace(binding.query_int8_sizes(d), self.device)
         self._x, self._logits, self._wr = (d.T, d.H), (d.T, d.E_total), (d.E_total, d.H)
         self._w_in, self._w_out = (d.E_local, d.F, d.H), (d.E_local, d.H, d.F)
 

@@ -13,7 +13,7 @@ import torch
 
 import oracle
 from mixture_experts_layer_32_amd import inputs
-from mixture_experts_layer_32_amd.layer import FewTokenLayer, MoELayer
+from mixture_experts_layer_32_amd.layer import FewTokenLayer, Int8Layer, MoELayer
 from gpu_util import to_dev
 from rounding import BAR, excess
 
@@ -249,6 +249,49 @@ def test_prompt_then_tokens():
     ref = oracle.forward(L["x"], L["logits"], L["wg"], L["wu"], L["wd"], k)[0]
     assert oracle.rel_frobenius(got, ref) <= TOL["bf16"]
     assert oracle.rel_frobenius(got, y.float().cpu().numpy()) <= 4 * 2.0 ** -8
+
+
+def test_a_workspace_made_behind_queued_work():
+    """A workspace in memory that the stream of its making still writes is not used before it is written: by the
+    time the constructor returns, calls on any stream may use it."""
+    print("case few workspace", flush=True)
+    k = Case(T=20, H=4096, F=256, E=8, k=2)
+    want = k.run().clone()
+    args = (20, 4096, 256, 8, 2)
+    side = torch.cuda.Stream()
+    for make in (FewTokenLayer, Int8Layer, MoELayer):
+        size = make(*args).ws.numel()
+        torch.cuda.synchronize()
+        old = torch.empty(size, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(50_000_000)
+        old.fill_(0xFF)
+        written = torch.cuda.Event()
+        written.record()
+        at = old.data_ptr()
+        del old                                         # freed while the current stream has yet to write it
+        layer = make(*args)
+        assert written.query(), make.__name__
+        assert layer.ws.data_ptr() == at                # the case that this is about
+        if make is FewTokenLayer:
+            y = layer.forward(k.x, k.lg, k.wg, k.wu, k.wd, stream=side)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+
+
+def test_a_layer_made_in_a_captured_graph():
+    print("case few layer in a graph", flush=True)
+    k = Case(T=9, H=512, F=256, E=16, k=4)
+    want = k.run().clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer = FewTokenLayer(9, 512, 256, 16, 4)
+        y = layer.forward(k.x, k.lg, k.wg, k.wu, k.wd)
+    for _ in range(3):
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
 
 
 def test_a_new_output_on_another_stream():
