@@ -47,7 +47,8 @@ def _empty(shape, dtype, like, stream):
         # the cheapest of torch's calls for it: 0.9 us against 1.4 of torch.empty
         return torch.empty_like(like, dtype=dtype) if like.shape == shape else like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
+        # (of handle 0, the null stream's, ExternalStream would make a new stream)
+        stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 

@@ -535,6 +535,35 @@ def test_new_outputs_on_another_stream():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(z, y)
 
 
+def stream_of(t):
+    """The handle of the stream from whose memory t was made."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("no segment")
+
+
+def test_new_outputs_come_from_the_given_streams_memory():
+    """A stream given as an object or as a handle, the null stream's handle 0 among them."""
+    print("case int8 output streams", flush=True)
+    x = torch.randn(48, 256, device="cuda")
+    q, s = int8_quantize(x)
+    k, few = Case(T=5, H=256, F=128, E=8, k=2), FewTokenLayer(5, 256, 128, 8, 2)
+    w = [to_dev(k.L[n], torch.bfloat16) for n in ("wg", "wu", "wd")]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for current in (torch.cuda.default_stream(), side):
+        for given in (0, torch.cuda.default_stream(), side.cuda_stream, side, None):
+            want = given if isinstance(given, int) else (given or current).cuda_stream
+            with torch.cuda.stream(current):
+                new = [*int8_quantize(x, stream=given), int8_matmul(q, s, q, s, stream=given),
+                       k.layer.forward(k.x, k.lg, *k.w, stream=given),
+                       *k.layer.forward_router(k.x, k.wr, *k.w, stream=given),
+                       few.forward(k.x, k.lg, *w, stream=given), *few.forward_router(k.x, k.wr, *w, stream=given)]
+            torch.cuda.synchronize()
+            assert [stream_of(t) for t in new] == [want] * len(new), (current, given)
+
+
 @pytest.mark.parametrize("T,router", [(9, False), (9, True), (40, False), (130, False), (130, True)])
 def test_layer_graph_replays(T, router):
     print("case int8 graph", T, router, flush=True)
