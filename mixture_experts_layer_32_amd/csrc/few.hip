@@ -324,7 +324,8 @@ __device__ __forceinline__ void store_h(const FewParams& p, int pos, int t, floa
       a *= xs * g[i];
       b *= xs * u[i];
     }
-    h[i] = weighted_swiglu(wt, a, b);
+    if constexpr (sizeof(T) == 1) h[i] = weighted_swiglu8(wt, a, b);
+    else h[i] = wt * (a / (1.0f + expf(-a)) * b);
   }
   const size_t at = (size_t)pos * p.F + f0;
   if constexpr (sizeof(T) == 2) {

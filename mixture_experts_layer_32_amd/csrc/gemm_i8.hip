@@ -238,7 +238,7 @@ __device__ __forceinline__ void epilogue(const I8Params& p, const i32x16 (&acc)[
           } else {
             const int us = NJ == 1 ? __shfl_xor(acc[i][0][q], 16) : acc[i][NJ == 1 ? 0 : NJ / 2 + v][q];
             const float ga = (float)acc[i][v][q] * (s[b] * g[v]), up = (float)us * (s[b] * u[v]);
-            o[v] = weighted_swiglu(w[b], ga, up);
+            o[v] = weighted_swiglu8(w[b], ga, up);
           }
         }
         if constexpr (WIDE) {   // aux 2: non-temporal
