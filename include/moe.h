@@ -232,9 +232,9 @@ moe_status moe_router_bwd(const moe_desc* d, const void* x, const void* w_router
 
 /* The whole layer for a few tokens (1 <= T <= 64), forward only: the step of a decoder, where the time
  * goes into reading the chosen experts' weights once. The same y as moe_fwd (same routing, ties and
- * expert share; the sums run in another order, and h = w silu(a) b keeps fp32's accuracy up to the
- * down product, where moe_fwd rounds it to bf16), without `saved`, in two to four
- * kernels:
+ * expert share; the sums run in another order, and in bf16 mode h = w silu(a) b is kept to 2^-18 of each
+ * value up to the down product, where moe_fwd rounds it to bf16), without `saved`, in two kernels and up to three
+ * more: the router's, above 16 tokens the choice of experts, above 8 or 16 the down products of experts of more than 8:
  *   w_router = NULL  logits [T, E_total] is an input, as in moe_fwd
  *   w_router given   [E_total, H], elem: logits = x w_router^T first (one more kernel); logits is an output
  * A token none of whose experts is in the share gets y = 0. Modes FP32 and BF16

@@ -17,11 +17,11 @@
 //                 waves take (expert, 4 or 8 rows of F) units, each on its own, and write h = w silu(a) b into
 //                 the workspace. Bound by the read of the gate and up rows.
 //   k_few_down    a workgroup owns 4 NQ rows of H for every expert: its waves share the (expert, F) axis,
-//                 each keeping its own sum per token, and the sums are added in a fixed order. No
-//                 partial sums in memory, no atomics on sums: repeated calls give the same bits. Bound by the
-//                 read of the down rows.
+//                 each keeping its own sum per token, and the sums are added in a fixed order, without
+//                 atomics: repeated calls give the same bits. Bound by the read of the down rows.
 // Experts of more than 8 tokens ("heavy") take 16 x 16 MFMA tiles with their tokens' rows in LDS, so that
-// their weights too are read once: in k_few_gateup and, mostly, in k_few_heavy ahead of k_few_down (heavy_ahead).
+// their weights too are read once: in k_few_gateup and, mostly, in k_few_heavy ahead of k_few_down (heavy_ahead), which
+// leaves the heavy experts' products, [pairs, H] in fp32, in memory for k_few_down to add. The others' stay in LDS.
 //
 // Measured, one launch, median us (2048 x 768 and 4096 x 1536, 128 experts, top-8, bf16; read rate of the weights):
 //                    1 token 2048     8 tokens 2048     64 skewed tokens 4096
@@ -30,8 +30,9 @@
 //   k_few_down       9                32 (5.4 TB/s)     117 (6.1 TB/s)
 // About 5 us of the one-token k_few_gateup are its launch and the choice of experts, which it must wait for.
 //
-// h is kept as fp32, or in bf16 mode to 2^-18 of each value as the pair hi = bf16(h), lo = bf16(h - hi),
-// whose two products cost matrix time that a read-bound kernel does not miss.
+// h is kept as fp32, or in bf16 mode to 2^-18 of each value as the pair hi = bf16(h), lo = bf16(h - hi), whose two
+// products cost matrix time that a read-bound kernel does not miss. y is off by 2.5e-6 of its rms for it, as much as fp32 sums
+// of 4096 terms in a row are; with hi alone by 1.7e-3, as much as by y's own rounding.
 #include <math.h>
 
 #include <algorithm>
@@ -881,7 +882,8 @@ __global__ __launch_bounds__(kDW * 64, 4) void k_few_down(FewParams p) {
   }
 }
 
-// the down products of the heavy experts, into oh: 64 tokens on 8 experts, 4096 x 1536, 36 us (101 MB of weights)
+// the down products of the heavy experts, into oh: 64 tokens on 8 experts, 4096 x 1536, 36 us (101 MB of weights).
+// Its 128 registers, for two workgroups a CU, leave 4 values of the bf16 form and one of the 8-bit form in scratch.
 template <class T>
 __global__ __launch_bounds__(512, 4) void k_few_heavy(FewParams p) {
   __shared__ __attribute__((aligned(16))) char smem[heavy_lds(4, sizeof(T) == 2 ? 2 : 1)];
@@ -1030,8 +1032,9 @@ hipError_t launch_layer(const FewParams& p, hipStream_t s) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
     prof_mark_end(s);
   }
-  // as many rows per workgroup (each read of h serves them all) as leave every CU one. Half as many: 64 tokens of 128
-  // experts, 4096 x 1536 281 -> 370 us, 2048 x 768 102 -> 145; one token 23 -> 25 and 11.5 -> 15.
+  // as many rows per workgroup (each read of h serves them all) as leave each of 256 CUs one at H = 2048 and 4096, the
+  // widths measured; between them the last round of workgroups is part empty. Half as many: 64 tokens of 128 experts,
+  // 4096 x 1536 281 -> 370 us, 2048 x 768 102 -> 145; one token 23 -> 25 and 11.5 -> 15.
   if (p.H >= kDown4) return launch_down<T, 4, FLY>(p, s);
   return p.H >= 2048 ? launch_down<T, 2, FLY>(p, s) : launch_down<T, 1, FLY>(p, s);
 }

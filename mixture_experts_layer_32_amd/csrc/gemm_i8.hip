@@ -10,8 +10,9 @@
 //             2 x 4 blocks of 32 x 32 (128 accumulators). A ring of two 64 KB stages; a K-tile is four
 //             MFMA steps of 32 elements, each step's fragments (6 reads of 1 KB per wave) read while the
 //             previous step's 8 MFMAs run. A tile of up to 128 rows runs half of them.
-//             16384 x 4096 x 2048 in 128-140 us, 2.0-2.1 Pop/s, the matrix cores busy half of the cycles at 1.95 GHz;
-//             the products of 65536 pairs with K = 768 in 172-185 us, 1.15 Pop/s. Bound by the main loop (2.4 Pop/s
+//             16384 x 4096 x 2048 in 128-146 us by card and run (149 and 154 in the median of two traces), 1.8-2.1 Pop/s,
+//             the matrix cores busy half of the cycles at 1.95 GHz; the products of 65536 pairs with K = 768 in 172-187 us,
+//             1.15 Pop/s. Bound by the main loop (2.4 Pop/s
 //             alone) and the stores, which run at the write rate and which nothing overlaps: without them 114 and
 //             138 us, without the loads 120 and 154. Tried against that: the next tile's first K-tiles ahead of the
 //             stores (no gain); two workgroups of 4 waves a CU on 128 x 256 tiles (148 and 208 us: half as many
@@ -189,6 +190,7 @@ __device__ __forceinline__ void tile_operands(const I8Params& p, int g, int r0, 
 // Epilogue of a tile: rows r0 .. end-1 (block i of the wave: rows AST i + 32 wm of the tile, element 4 a + b of
 // lane l its row 8 a + 4 (l / 32) + b), channels from n0. sx, wt: the tile rows' scales and routing weights,
 // sw: the channels' scales (kGateUp: half of them gate, then as many up), all in LDS.
+// Without WIDE the outputs are stored one by one, as any N and any address allow.
 // WIDE (N a multiple of 8, y 16-byte aligned): vector stores through a buffer whose range ends behind the
 // tile's last row, so that the hardware drops the rows past it, and channels past N at an offset outside. Every
 // lane issues every store: no branch between them, and their number is known.
@@ -464,6 +466,9 @@ int64_t tiles(const I8Params& p, int64_t rows, int bm, int bn) {
 // 256 x 256 tiles once the expected rows make enough to fill three quarters of the CUs, else 128 x 128 ones if
 // they do, else 64 x 64. 1117 x 777 x 1104 in 9 groups: 55 us on 256 x 256, 10 us on 64 x 64. The products of
 // 1333 tokens on 16 of 128 experts (2048 x 768): 28 and 14 us on 256 x 256, 18 and 12 us on 128 x 128.
+// 256 x 256 tiles need the vector stores (`wide`); other N and addresses stay on the small tiles, which store any. 16384 x
+// 2048 by 4104 and by 4100 channels, bf16: 156 and 236 us (4104 into an odd address 232), fp32 172 and 279; 65536 x 768 by 2048
+// and by 2044: 123 and 249, fp32 154 and 294; 4096 rows of 2048 channels: 32 and 31 us.
 template <Out OUT>
 void launch_i8(const I8Params& p, int grid, hipStream_t s) {
   constexpr int half = OUT == kGateUp ? 2 : 1;

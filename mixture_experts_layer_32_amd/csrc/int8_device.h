@@ -76,12 +76,12 @@ __device__ __forceinline__ void q8_pack(const float (&x)[N], const Q8Row& r, uns
   }
 }
 
-// w silu(a) b of the 8-bit layer, for few tokens and many alike, so that a token's h has the same bits in either (with
-// two accuracies, bytes of h near a tie differed). silu(a) = a / (1 + e^-a) with e^-a = 2^t e^c: t = -a log2 e as rounded
-// (by up to 2^-18 at the ends, which alone would cost e^-a 40 units in the last place), c = -a - t ln 2 what the rounding left
-// out, e^c = 1 + c. The hardware's power of two and reciprocal are good to one unit, the whole to 1.5 to 3. Below a = -88, where the power would
-// leave fp32, 0. The gate/up product of 131072 pairs of 768 values takes 454 us with the plain power and reciprocal,
-// 492 so, and 522 with expf and a division.
+// w silu(a) b of the 8-bit layer, for few tokens and many alike, so that a token's h has the same bits in either
+// (with two accuracies, bytes of h near a tie differed). silu(a) = a / (1 + e^-a) with e^-a = 2^t e^c: t = -a log2 e as
+// rounded (by up to 2^-18 at the ends, which alone would cost e^-a 30 units in the last place), c = -a - t ln 2 what
+// the rounding left out, e^c = 1 + c. The hardware's power of two and reciprocal are good to one unit, the whole to
+// 1.5 to 3. Below a = -88, where the power would leave fp32, 0. The gate/up product of 131072 pairs of 768 values takes
+// 454 us with the plain power and reciprocal, 492 so, and 522 with expf and a division.
 __device__ __forceinline__ float weighted_swiglu8(float w, float a, float b) {
   constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465430e-9f;
   const float z = __builtin_amdgcn_fmed3f(-a, -104.0f, 88.0f);

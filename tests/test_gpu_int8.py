@@ -4,7 +4,8 @@ The quantiser and the product are compared bit for bit with their definitions in
 is compared with the same steps in float64. Its bars, relative Frobenius: y is rounded to bf16 once, by at
 most 2^-8 of each value (up to 64 tokens), or each pair's output and y are (more tokens: 2 * 2^-8); h's
 fp32 error (about 2^-22 of a value of up to 127 steps) moves about one in 10^4 of its bytes by one step of
-1/127 of the row's largest, less than 1e-3 in all.
+1/127 of the row's largest, less than 1e-3 in all. These bars leave room for a rounding of each pair's output that the
+layer does not make; test_layer_is_rounded_once holds every token to one rounding.
 """
 import threading
 
