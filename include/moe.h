@@ -255,7 +255,8 @@ moe_status moe_fwd_few(const moe_desc* d, const void* x, const void* w_router, f
  *   q_i = the whole number nearest to the real quotient 127 v_i / D, ties to even (|q_i| <= 127).
  * A row of zeros has s = 2^-126. A row that holds a NaN or an infinity has s = NaN and q = 0, so that
  * whatever is computed from it is NaN. */
-typedef enum { MOE_TYPE_FP32 = 0, MOE_TYPE_BF16 = 1 } moe_type;
+/* Element types. INT8 is taken by moe_dispatch alone. */
+typedef enum { MOE_TYPE_FP32 = 0, MOE_TYPE_BF16 = 1, MOE_TYPE_INT8 = 2 } moe_type;
 
 /* Quantises the rows of in [rows, cols] (row-major, `type`) into q [rows, cols] and scales [rows]:
  * tokens along their features, or a weight [N, K] (or [E, N, K] as E*N rows) along its contraction
@@ -296,6 +297,111 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
                         const int8_t* w_gate, const float* s_gate, const int8_t* w_up, const float* s_up,
                         const int8_t* w_down, const float* s_down, void* y, void* ws, size_t ws_bytes,
                         void* stream);
+
+/* The layer taken apart: the (token, slot) pairs sorted by expert, the tokens' rows brought into that order
+ * ("A Magia da Fusão": dispatch) and back (combine), with their gradients, for programs that have experts or a
+ * router of their own, or run the grouped products below and above by themselves.
+ *
+ * Pair q = t*topk + j is slot j of token t. pair_pos[q] is the row at which the pair stands among the pairs sorted
+ * by expert, -1 where it has none; moe_sort_pairs makes it, and `saved` holds it after moe_route (moe_saved_layout).
+ * In these calls a position outside 0..nrows-1 counts as -1, and no position may appear twice.
+ *
+ * moe_sort_pairs sorts any choice of experts (of any router): idx[pairs] names each pair's expert. Pairs of the
+ * experts [expert_offset, expert_offset + E_local) are sorted stably by (expert, pair number); all others (-1 for
+ * a dropped pair, other ranks' experts) get no position. Outputs, all overwritten:
+ *   offsets  [E_local + 1]  first position of each expert's pairs; offsets[E_local] = P, their number
+ *   perm     [pairs]        the pair at each position, -1 from position P on
+ *   pair_pos [pairs]        the position of each pair, or -1
+ * The order is moe_route's. A token may name an expert twice. E_local <= 512, pairs < 2^31. Every pointer needs
+ * 4-byte alignment, ws 256 (its size, 0 for few pairs, is moe_query_sort_sizes's; its contents need not be
+ * preserved, and calls that share one must be ordered by the caller; null where the size is 0). */
+moe_status moe_query_sort_sizes(int64_t pairs, int E_local, size_t* ws);
+moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int expert_offset, int32_t* offsets,
+                          int32_t* perm, int32_t* pair_pos, void* ws, size_t ws_bytes, void* stream);
+
+/* rows[pair_pos[t, j]] = x[t] for every pair that has a position: x [T, H], rows [nrows, H], both of `type`. Rows
+ * that no pair stands at are left as they were. With moe_int8_quantize's bytes (MOE_TYPE_INT8) and scales
+ * (MOE_TYPE_FP32, H = 1) it gives the operands of a grouped moe_int8_matmul. Its gradient is moe_combine without
+ * weights, on the gradient of rows.
+ * Here and below: any H >= 1, 1 <= topk <= 32, T*topk < 2^31, T*H, nrows*H < 2^40 (MOE_ERR_UNSUPPORTED_SHAPE); pointers aligned
+ * to their elements. Rows of a multiple of 16 bytes behind 16-byte aligned pointers run fastest. */
+moe_status moe_dispatch(const void* x, int type, int64_t T, int topk, int64_t H, const int32_t* pair_pos, void* rows,
+                        int64_t nrows, void* stream);
+
+/* y[t] = sum over the slots j with a position of weight[t, j] * rows[pair_pos[t, j]], products and sum in fp32 in
+ * slot order, rounded once: rows [nrows, H] of rows_type, y [T, H] of type (FP32 or BF16 each), weight [T, topk] fp32, or
+ * null for 1. A token without any position gets 0; rows at no pair's position are not read. */
+moe_status moe_combine(const void* rows, int rows_type, int64_t nrows, const int32_t* pair_pos, const float* weight,
+                       int64_t T, int topk, int64_t H, void* y, int type, void* stream);
+
+/* The gradients of <dy, y> of moe_combine with weights (without weights the gradient of rows is moe_dispatch's of dy,
+ * of the same types):
+ *   drows[pair_pos[t, j]] = weight[t, j] * dy[t]           [nrows, H] rows_type; rows at no position left as they were
+ *   dweight[t, j]         = <dy[t], rows[pair_pos[t, j]]>  [T, topk] fp32; 0 without a position
+ * and with dlogits (else null, and idx is not read), for weights that are a softmax over the chosen experts' logits, as
+ * moe_route's:
+ *   dlogits[t, idx[t, j]] = weight[t, j] * (dweight[t, j] - sum_i weight[t, i] dweight[t, i])
+ * [T, E_total] fp32, 0 elsewhere; slots of one token that name the same expert add up, an idx outside
+ * 0..E_total-1 gets none. E_total <= 512. In an expert share dweight and dlogits are its linear contribution, as moe_bwd's.
+ * Sums in fp32 in a fixed order. */
+moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_type, int64_t nrows,
+                           const int32_t* pair_pos, const float* weight, const int32_t* idx, int64_t T, int topk,
+                           int64_t H, int E_total, void* drows, float* dweight, float* dlogits, void* stream);
+
+/* Products with 4-bit weights that have a scale for each group of inputs, for serving: bf16 rows against weights of
+ * half a byte.
+ *
+ * A weight [N, K] is held as whole numbers q of -8..7 and one bf16 scale for each `group` (32, 64 or 128) consecutive
+ * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory the numbers lie in tiles of 16 channels by
+ * 128 inputs, 1024 bytes each, in the order in which a wavefront takes them, and a weight [N, K] is
+ * ceil(N/16) rows of ceil(K/128) tiles, the weights of [G, N, K] one after the other (padding: q = 0, s = 0). The
+ * scales of a tile are [16 channels][128 / group]. With c = n % 16, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] + 8 is the four bits from bit
+ * 16 (j % 2) + 4 (j / 2) of the 32-bit word (16 h + c) * 4 + i of its tile. */
+moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* q_bytes, size_t* scale_bytes);
+
+/* Quantises a weight in [G, N, K] (row-major, `type`) for each group of inputs: D = the group's largest |v|,
+ * s = D / 7 in fp32, at least 2^-126, rounded to bf16, q = the whole number nearest to the real quotient v / s, ties to even, kept within -7..7.
+ * A group that holds a NaN or an infinity has s = NaN and q = 0. K a multiple of group, <= 131072; N <= 2^20; G <= 512;
+ * G*N*K < 2^40. in, q and scales need 16-byte alignment. */
+moe_status moe_int4_quantize(const void* in, int type, int G, int64_t N, int64_t K, int group, uint8_t* q,
+                             void* scales, void* stream);
+/* Lays out a weight that is quantised already: values [G, N, K], one signed byte each (beyond -8..7: the nearer of
+ * the two), in_scales [G, N, K / group] bf16. Limits and alignment as above. */
+moe_status moe_int4_pack(const int8_t* values, const void* in_scales, int G, int64_t N, int64_t K, int group,
+                         uint8_t* q, void* scales, void* stream);
+
+/* y[m, n] = sum over the groups of s[g, n, group] * (sum over the group's inputs of x[m, k] q[g, n, k]): x [M, K] bf16, y
+ * [M, N] of `type`, rounded once; products exact, sums in fp32. offsets, groups of rows, and the rows of y outside of
+ * them as in moe_int8_matmul. A NaN or an infinity in a row of x reaches that row of y alone (as NaN, where it meets other
+ * values). M <= 2^31 - 512, M*N < 2^40, the rest as above. x and q need 16-byte alignment, scales 8-byte,
+ * offsets 4-byte, y its type's. */
+moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, int64_t M, int64_t N, int64_t K,
+                           int group, int G, const int32_t* offsets, void* y, int type, void* stream);
+
+/* The norm over many tensors together, and their scaling: what a training step does with the gradients that
+ * moe_bwd and moe_router_bwd leave.
+ *   norm = sqrt(sum over all tensors and elements g^2)             squares and sums in 64 bits, fp32 at the end
+ *   c    = min(1, max_norm / (norm + 1e-6))                        in fp32; NaN if norm is NaN
+ *   out  = c * g                                                   each element rounded once
+ * The descriptions are read on the host during the call: count of them (0: the norm is 0), each a device pointer
+ * (aligned to its elements), a number of elements (0: data may be null) and a type (FP32 or BF16). Together less than
+ * 2^40 elements. out = null scales in place, and writes nothing where c = 1; otherwise out[i] has tensors[i]'s size, its type may
+ * be the other one, and everything is written. Tensors may not overlap, but out[i] may be tensors[i].
+ * moe_grad_norm writes norm [1] fp32; moe_grad_clip scales by a norm given (other ranks' gradients may have
+ * joined it); moe_clip_grad_norm does both in fewer launches. ws: 256-byte aligned, of moe_query_norm_sizes's size;
+ * contents need not be preserved, and calls that share one must be ordered by the caller. max_norm >= 0.
+ * A launch takes some hundred tensors; more take more launches. */
+typedef struct {
+  void* data;
+  int64_t n;
+  int32_t type;   /* moe_type */
+} moe_tensor;
+moe_status moe_query_norm_sizes(const moe_tensor* tensors, int count, size_t* ws);
+moe_status moe_grad_norm(const moe_tensor* tensors, int count, float* norm, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int count, const float* norm,
+                         float max_norm, void* stream);
+moe_status moe_clip_grad_norm(const moe_tensor* tensors, const moe_tensor* out, int count, float max_norm,
+                              float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* Byte offsets of the routing results inside `saved`.
  *   idx       int32 [T*k]      chosen experts, slot order (logit desc, index asc)

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(PKG, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe.h")
 
 MODES = {"fp32": 0, "bf16": 1, "mxfp8": 2, "fp8_bwd": 3, "fp8": 4}
-TYPES = {"fp32": 0, "bf16": 1}
+TYPES = {"fp32": 0, "bf16": 1, "int8": 2}
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
           3: "MOE_ERR_UNSUPPORTED_MODE", 4: "MOE_ERR_WORKSPACE_TOO_SMALL", 5: "MOE_ERR_HIP"}
 
@@ -36,6 +36,11 @@ class Desc(ctypes.Structure):
 class SavedOffsets(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("idx", "weight", "counts", "offsets", "perm", "pair_pos", "qoff", "qcols",
                                                "hwt", "hwt_scales", "wdt", "wdt_scales", "wgut", "wgut_scales")]
+
+
+class Tensor(ctypes.Structure):
+    """moe_tensor: one of the tensors of a gradient norm."""
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
 class MoEError(RuntimeError):
@@ -88,12 +93,30 @@ def lib():
         L.moe_int8_matmul.argtypes = [_P, _P, _P, _P, i64, i64, i64, ctypes.c_int, _P, _P, ctypes.c_int, _P]
         L.moe_query_int8_sizes.argtypes = [_D, ctypes.POINTER(ctypes.c_size_t)]
         L.moe_fwd_int8.argtypes = [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        size, ci = ctypes.POINTER(ctypes.c_size_t), ctypes.c_int
+        L.moe_query_sort_sizes.argtypes = [i64, ci, size]
+        L.moe_sort_pairs.argtypes = [_P, i64, ci, ci, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.moe_dispatch.argtypes = [_P, ci, i64, ci, i64, _P, _P, i64, _P]
+        L.moe_combine.argtypes = [_P, ci, i64, _P, _P, i64, ci, i64, _P, ci, _P]
+        L.moe_combine_bwd.argtypes = [_P, ci, _P, ci, i64, _P, _P, _P, i64, ci, i64, ci, _P, _P, _P, _P]
+        L.moe_query_int4_sizes.argtypes = [ci, i64, i64, ci, size, size]
+        L.moe_int4_quantize.argtypes = [_P, ci, ci, i64, i64, ci, _P, _P, _P]
+        L.moe_int4_pack.argtypes = [_P, _P, ci, i64, i64, ci, _P, _P, _P]
+        L.moe_int4_matmul.argtypes = [_P, _P, _P, i64, i64, i64, ci, ci, _P, _P, ci, _P]
+        tensors = ctypes.POINTER(Tensor)
+        L.moe_query_norm_sizes.argtypes = [tensors, ci, size]
+        L.moe_grad_norm.argtypes = [tensors, ci, _P, _P, ctypes.c_size_t, _P]
+        L.moe_grad_clip.argtypes = [tensors, tensors, ci, _P, ctypes.c_float, _P]
+        L.moe_clip_grad_norm.argtypes = [tensors, tensors, ci, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]
         L.moe_profile_enable.argtypes = [ctypes.c_int]
         L.moe_profile_kernel.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                          ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double)]
         for n in ("moe_query_sizes", "moe_route", "moe_route_static", "moe_fwd", "moe_fwd_router", "moe_bwd", "moe_saved_layout", "moe_mx_quantize",
                   "moe_fp8_block_quantize", "moe_query_few_sizes", "moe_fwd_few", "moe_int8_quantize",
                   "moe_int8_matmul", "moe_query_int8_sizes", "moe_fwd_int8",
+                  "moe_query_sort_sizes", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_bwd",
+                  "moe_query_int4_sizes", "moe_int4_quantize", "moe_int4_pack", "moe_int4_matmul",
+                  "moe_query_norm_sizes", "moe_grad_norm", "moe_grad_clip", "moe_clip_grad_norm",
                   "moe_query_router_sizes", "moe_router_fwd", "moe_router_bwd", "moe_profile_enable",
                   "moe_profile_disable", "moe_profile_collect", "moe_profile_kernel"):
             getattr(L, n).restype = st
@@ -212,6 +235,69 @@ def moe_fwd_int8(desc, x, w_router, logits, w_gate, s_gate, w_up, s_up, w_down, 
     _check(lib().moe_fwd_int8(ctypes.byref(desc), ptr(x), ptr(w_router), ptr(logits), ptr(w_gate), ptr(s_gate),
                               ptr(w_up), ptr(s_up), ptr(w_down), ptr(s_down), ptr(y), ptr(ws), ws_bytes,
                               _stream(stream)))
+
+
+def query_sort_sizes(pairs, E_local):
+    n = ctypes.c_size_t()
+    _check(lib().moe_query_sort_sizes(pairs, E_local, ctypes.byref(n)))
+    return n.value
+
+
+def moe_sort_pairs(idx, pairs, E_local, expert_offset, offsets, perm, pair_pos, ws, ws_bytes, stream=None):
+    _check(lib().moe_sort_pairs(ptr(idx), pairs, E_local, expert_offset, ptr(offsets), ptr(perm), ptr(pair_pos), ptr(ws),
+                                ws_bytes, _stream(stream)))
+
+
+def moe_dispatch(x, type, T, topk, H, pair_pos, rows, nrows, stream=None):
+    _check(lib().moe_dispatch(ptr(x), type, T, topk, H, ptr(pair_pos), ptr(rows), nrows, _stream(stream)))
+
+
+def moe_combine(rows, rows_type, nrows, pair_pos, weight, T, topk, H, y, type, stream=None):
+    _check(lib().moe_combine(ptr(rows), rows_type, nrows, ptr(pair_pos), ptr(weight), T, topk, H, ptr(y), type,
+                             _stream(stream)))
+
+
+def moe_combine_bwd(dy, type, rows, rows_type, nrows, pair_pos, weight, idx, T, topk, H, E_total, drows, dweight,
+                    dlogits, stream=None):
+    _check(lib().moe_combine_bwd(ptr(dy), type, ptr(rows), rows_type, nrows, ptr(pair_pos), ptr(weight), ptr(idx), T,
+                                 topk, H, E_total, ptr(drows), ptr(dweight), ptr(dlogits), _stream(stream)))
+
+
+def query_int4_sizes(G, N, K, group):
+    q, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_query_int4_sizes(G, N, K, group, ctypes.byref(q), ctypes.byref(s)))
+    return q.value, s.value
+
+
+def moe_int4_quantize(x, type, G, N, K, group, q, scales, stream=None):
+    _check(lib().moe_int4_quantize(ptr(x), type, G, N, K, group, ptr(q), ptr(scales), _stream(stream)))
+
+
+def moe_int4_pack(values, in_scales, G, N, K, group, q, scales, stream=None):
+    _check(lib().moe_int4_pack(ptr(values), ptr(in_scales), G, N, K, group, ptr(q), ptr(scales), _stream(stream)))
+
+
+def moe_int4_matmul(x, q, scales, M, N, K, group, G, offsets, y, type, stream=None):
+    _check(lib().moe_int4_matmul(ptr(x), ptr(q), ptr(scales), M, N, K, group, G, ptr(offsets), ptr(y), type,
+                                 _stream(stream)))
+
+
+def query_norm_sizes(tensors, count):
+    n = ctypes.c_size_t()
+    _check(lib().moe_query_norm_sizes(tensors, count, ctypes.byref(n)))
+    return n.value
+
+
+def moe_grad_norm(tensors, count, norm, ws, ws_bytes, stream=None):
+    _check(lib().moe_grad_norm(tensors, count, ptr(norm), ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grad_clip(tensors, out, count, norm, max_norm, stream=None):
+    _check(lib().moe_grad_clip(tensors, out, count, ptr(norm), max_norm, _stream(stream)))
+
+
+def moe_clip_grad_norm(tensors, out, count, max_norm, norm, ws, ws_bytes, stream=None):
+    _check(lib().moe_clip_grad_norm(tensors, out, count, max_norm, ptr(norm), ptr(ws), ws_bytes, _stream(stream)))
 
 
 def moe_mx_quantize(x, rows, cols, axis, q, scales, stream=None):

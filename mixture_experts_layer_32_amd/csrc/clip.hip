@@ -1,0 +1,264 @@
+// The norm over many tensors together, and their scaling: what a training step does with the weight gradients that
+// the backward passes leave.
+//
+//   k_norm    each workgroup takes a contiguous run of the tensors' chunks and leaves one partial sum of squares.
+//             Squares and sums in 64 bits: no range is lost, and the order (fixed by the sizes alone) hardly shows.
+//   k_root    norm = sqrt(sum of the partial sums).
+//   k_scale   out = c g, c = min(1, max_norm / (norm + 1e-6)); with the norm given, or from the partial sums, which
+//             every workgroup then adds up for itself (one launch less).
+// The tensors' addresses and sizes travel in the launch's arguments, kTable (kPair with outputs) tensors a launch.
+#include <algorithm>
+
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kChunk = 8192;    // elements
+constexpr int kTable = 160;     // 160 * 20 bytes: within the 4 KiB of a launch's arguments
+constexpr int kPair = 120;
+
+struct NormTable {
+  const void* src[kTable];
+  int64_t n[kTable];
+  int first[kTable + 1];        // first chunk of each tensor, then their number
+  unsigned f32[kTable / 32];
+  int count;
+};
+struct ScaleTable {
+  const void* src[kPair];
+  void* dst[kPair];
+  int64_t n[kPair];
+  int first[kPair + 1];
+  unsigned f32[(kPair + 31) / 32], d32[(kPair + 31) / 32];
+  int count;
+};
+static_assert(sizeof(NormTable) <= 3800 && sizeof(ScaleTable) <= 3800, "launch arguments");
+
+// the tensor that chunk c lies in
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table& a, int c) {
+  int lo = 0, hi = a.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ bool bit(const unsigned* w, int i) { return (w[i >> 5] >> (i & 31)) & 1; }
+
+// elements ahead of the first 16-byte boundary
+template <class T>
+__device__ __forceinline__ int head16(const T* p, int m) {
+  return min(m, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
+}
+template <class T>
+__device__ __forceinline__ void add_sq(uint4 v, double& s) {
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+    const double d = (double)(float)e[i];
+    s = fma(d, d, s);
+  }
+}
+
+// sum of squares of p[0 .. m), this thread's share
+template <class T>
+__device__ __forceinline__ void sq_chunk(const T* p, int m, double& s) {
+  constexpr int V = 16 / sizeof(T);
+  const int tid = threadIdx.x, h = head16(p, m), nv = (m - h) / V;
+  if (tid < h) {
+    const double d = (double)(float)p[tid];
+    s = fma(d, d, s);
+  }
+  const uint4* v = reinterpret_cast<const uint4*>(p + h);
+#pragma unroll 4
+  for (int i = tid; i < nv; i += 256) add_sq<T>(v[i], s);
+  const int t = h + nv * V + tid;
+  if (t < m) {
+    const double d = (double)(float)p[t];
+    s = fma(d, d, s);
+  }
+}
+
+// the workgroup's sum, in every thread, in a fixed order
+__device__ __forceinline__ double block_sum(double s, double* lds) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__global__ __launch_bounds__(256) void k_norm(NormTable a, double* part) {
+  __shared__ double lds[4];
+  const int C = a.first[a.count];
+  const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
+  double s = 0.0;
+  int i = tensor_of(a, c0);
+  for (int c = c0; c < c1; ++c) {
+    while (c >= a.first[i + 1]) ++i;
+    const int64_t at = (int64_t)(c - a.first[i]) * kChunk;
+    const int m = (int)min((int64_t)kChunk, a.n[i] - at);
+    if (bit(a.f32, i)) sq_chunk(static_cast<const float*>(a.src[i]) + at, m, s);
+    else sq_chunk(static_cast<const bf16*>(a.src[i]) + at, m, s);
+  }
+  s = block_sum(s, lds);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// sqrt of the partial sums' sum in fp32, in every thread
+__device__ __forceinline__ float root(const double* part, int64_t parts, double* lds) {
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < parts; i += 256) s += part[i];
+  return (float)sqrt(block_sum(s, lds));
+}
+
+__global__ __launch_bounds__(256) void k_root(const double* part, int64_t parts, float* norm) {
+  __shared__ double lds[4];
+  const float r = root(part, parts, lds);
+  if (threadIdx.x == 0) *norm = r;
+}
+
+template <class S, class D>
+__device__ __forceinline__ void scale_chunk(const S* p, D* o, int m, float c) {
+  constexpr int V = 16 / (sizeof(S) < sizeof(D) ? sizeof(S) : sizeof(D));   // whole 16-byte pieces of both
+  const int tid = threadIdx.x;
+  int h = head16(p, m);
+  const bool vec = (reinterpret_cast<uintptr_t>(o + h) & 15) == 0;
+  const int nv = vec ? (m - h) / V : 0;
+  if (!vec) h = 0;
+  if (tid < h) o[tid] = (D)(c * (float)p[tid]);
+#pragma unroll 2
+  for (int i = tid; i < nv; i += 256) {
+    alignas(16) S v[V];
+    alignas(16) D w[V];
+#pragma unroll
+    for (int b = 0; b < V * (int)sizeof(S) / 16; ++b)
+      reinterpret_cast<uint4*>(v)[b] = ld16(reinterpret_cast<const char*>(p + h + (size_t)i * V) + 16 * b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = (D)(c * (float)v[e]);
+#pragma unroll
+    for (int b = 0; b < V * (int)sizeof(D) / 16; ++b)
+      st16(reinterpret_cast<char*>(o + h + (size_t)i * V) + 16 * b, reinterpret_cast<uint4*>(w)[b]);
+  }
+  for (int t = h + nv * V + tid; t < m; t += 256) o[t] = (D)(c * (float)p[t]);
+}
+
+__global__ __launch_bounds__(256) void k_scale(ScaleTable a, float max_norm, const float* norm_in, const double* part,
+                                               int64_t parts, float* norm_out) {
+  __shared__ double lds[4];
+  float norm;
+  if (norm_in) {
+    norm = *norm_in;
+  } else {
+    norm = root(part, parts, lds);
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  }
+  float c = max_norm / (norm + 1e-6f);
+  c = c > 1.f ? 1.f : c;                       // NaN stays
+  const int C = a.first[a.count];
+  const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
+  if (c0 >= c1) return;
+  int i = tensor_of(a, c0);
+  for (int b = c0; b < c1; ++b) {
+    while (b >= a.first[i + 1]) ++i;
+    if (c == 1.f && a.src[i] == a.dst[i] && bit(a.f32, i) == bit(a.d32, i)) continue;   // in place: nothing changes
+    const int64_t at = (int64_t)(b - a.first[i]) * kChunk;
+    const int m = (int)min((int64_t)kChunk, a.n[i] - at);
+    const float* pf = static_cast<const float*>(a.src[i]) + at;
+    const bf16* pb = static_cast<const bf16*>(a.src[i]) + at;
+    float* of = static_cast<float*>(a.dst[i]) + at;
+    bf16* ob = static_cast<bf16*>(a.dst[i]) + at;
+    if (bit(a.f32, i)) {
+      if (bit(a.d32, i)) scale_chunk(pf, of, m, c);
+      else scale_chunk(pf, ob, m, c);
+    } else {
+      if (bit(a.d32, i)) scale_chunk(pb, of, m, c);
+      else scale_chunk(pb, ob, m, c);
+    }
+  }
+}
+
+int chunks(int64_t n) { return (int)((n + kChunk - 1) / kChunk); }
+int parts_of(int C) { return std::min(C, kNormParts); }
+
+// The next tensors from `from` on, at most MAX and as many as hold fewer than 2^31 chunks together; empty ones are
+// passed over. Returns where to go on.
+template <class Table, int MAX>
+int fill(Table& a, const moe_tensor* t, const moe_tensor* out, int count, int from) {
+  a.count = 0;
+  a.first[0] = 0;
+  int i = from;
+  for (; i < count && a.count < MAX; ++i) {
+    if (t[i].n == 0) continue;
+    const int k = a.count++;
+    if (k % 32 == 0) a.f32[k / 32] = 0;
+    a.src[k] = t[i].data;
+    a.n[k] = t[i].n;
+    a.first[k + 1] = a.first[k] + chunks(t[i].n);
+    if (t[i].type == MOE_TYPE_FP32) a.f32[k / 32] |= 1u << (k % 32);
+    if constexpr (MAX == kPair) {
+      const moe_tensor& o = out ? out[i] : t[i];
+      if (k % 32 == 0) a.d32[k / 32] = 0;
+      a.dst[k] = o.data;
+      if (o.type == MOE_TYPE_FP32) a.d32[k / 32] |= 1u << (k % 32);
+    }
+  }
+  return i;
+}
+
+}  // namespace
+
+int64_t norm_parts(const moe_tensor* t, int count) {
+  int64_t parts = 0;
+  NormTable a;
+  for (int i = 0; i < count;) {
+    i = fill<NormTable, kTable>(a, t, nullptr, count, i);
+    parts += parts_of(a.first[a.count]);
+  }
+  return parts;
+}
+
+hipError_t launch_grad_norm(const moe_tensor* t, int count, double* part, float* norm, hipStream_t s) {
+  hipError_t err;
+  int64_t parts = 0;
+  NormTable a;
+  for (int i = 0; i < count;) {
+    i = fill<NormTable, kTable>(a, t, nullptr, count, i);
+    const int grid = parts_of(a.first[a.count]);
+    if (grid == 0) continue;
+    prof_mark_begin("grad_norm", s);
+    k_norm<<<grid, 256, 0, s>>>(a, part + parts);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+    parts += grid;
+  }
+  if (!norm) return hipSuccess;
+  prof_mark_begin("grad_root", s);
+  k_root<<<1, 256, 0, s>>>(part, parts, norm);
+  if ((err = hipGetLastError()) == hipSuccess) prof_mark_end(s);
+  return err;
+}
+
+hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int count, float max_norm, const float* norm_in,
+                            const double* part, int64_t parts, float* norm_out, hipStream_t s) {
+  hipError_t err;
+  ScaleTable a;
+  for (int i = 0; i < count;) {
+    i = fill<ScaleTable, kPair>(a, t, out, count, i);
+    const int grid = parts_of(a.first[a.count]);
+    if (grid == 0) continue;
+    prof_mark_begin("grad_clip", s);
+    k_scale<<<grid, 256, 0, s>>>(a, max_norm, norm_in, part, parts, norm_out);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+    norm_out = nullptr;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

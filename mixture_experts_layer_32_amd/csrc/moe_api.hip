@@ -1261,6 +1261,347 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------------------------------------
+// Pairs sorted by expert and back
+
+namespace {
+struct SortLayout {
+  int nblk;
+  size_t cnt, prefix, total_off, total;
+};
+SortLayout sort_layout(int64_t pairs, int El) {
+  SortLayout L{};
+  if (pairs <= kSortSmall) return L;
+  L.nblk = (int)((pairs + kSortPairs - 1) / kSortPairs);
+  const size_t cells = (size_t)L.nblk * (El + 1) * 4;
+  L.prefix = align256(cells);
+  L.total_off = L.prefix + align256(cells);
+  L.total = L.total_off + align256((size_t)(El + 1) * 4);
+  return L;
+}
+
+moe_status sort_checks(int64_t pairs, int E_local) {
+  if (pairs < 1 || E_local < 1) return fail(MOE_ERR_INVALID_ARG, "pairs and E_local must be positive");
+  if (E_local > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E_local must be <= 512");
+  if (pairs > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "pairs must be < 2^31");
+  return MOE_OK;
+}
+
+size_t elem_size(int type) { return type == MOE_TYPE_FP32 ? 4 : type == MOE_TYPE_BF16 ? 2 : 1; }
+
+// the sizes that moe_dispatch, moe_combine and moe_combine_bwd share
+moe_status pairs_checks(int64_t T, int topk, int64_t H, int64_t nrows) {
+  if (T < 1 || topk < 1 || H < 1 || nrows < 1) return fail(MOE_ERR_INVALID_ARG, "T, topk, H and nrows must be positive");
+  if (topk > kMaxTopk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "topk must be <= 32");
+  if (T > INT32_MAX / topk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*topk must be < 2^31");
+  constexpr int64_t most = int64_t(1) << 40;
+  if (H >= most / T || H >= most / nrows) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*H and nrows*H must be < 2^40");
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_query_sort_sizes(int64_t pairs, int E_local, size_t* ws) {
+  g_last_error.clear();
+  moe_status st = sort_checks(pairs, E_local);
+  if (st != MOE_OK) return st;
+  if (ws) *ws = sort_layout(pairs, E_local).total;
+  return MOE_OK;
+}
+
+moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int expert_offset, int32_t* offsets,
+                          int32_t* perm, int32_t* pair_pos, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status st = sort_checks(pairs, E_local);
+  if (st != MOE_OK) return st;
+  if (expert_offset < 0) return fail(MOE_ERR_INVALID_ARG, "expert_offset must be >= 0");
+  if ((st = check_ptrs({{idx, "idx"}, {offsets, "offsets"}, {perm, "perm"}, {pair_pos, "pair_pos"}}, 4)) != MOE_OK)
+    return st;
+  const SortLayout L = sort_layout(pairs, E_local);
+  if (L.total > 0 && (st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
+  if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "sort workspace too small");
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  char* w = static_cast<char*>(ws);
+  SortParams p{};
+  p.idx = idx;
+  p.offsets = offsets;
+  p.perm = perm;
+  p.pair_pos = pair_pos;
+  p.pairs = pairs;
+  p.El = E_local;
+  p.e0 = expert_offset;
+  p.nblk = L.nblk;
+  if (L.total > 0) {
+    p.cnt = reinterpret_cast<int*>(w);
+    p.prefix = reinterpret_cast<int*>(w + L.prefix);
+    p.total = reinterpret_cast<int*>(w + L.total_off);
+  }
+  const hipError_t e = launch_sort_pairs(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "sort launch");
+  return MOE_OK;
+}
+
+moe_status moe_dispatch(const void* x, int type, int64_t T, int topk, int64_t H, const int32_t* pair_pos, void* rows,
+                        int64_t nrows, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if (type != MOE_TYPE_INT8 && (st = check_type(type)) != MOE_OK) return st;
+  if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
+  if ((st = check_ptrs({{x, "x"}, {rows, "rows"}}, elem_size(type))) != MOE_OK) return st;
+  if ((st = check_ptrs({{pair_pos, "pair_pos"}}, 4)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  PairsParams p{};
+  p.x = x;
+  p.pair_pos = pair_pos;
+  p.out = rows;
+  p.T = T;
+  p.H = H;
+  p.nrows = nrows;
+  p.k = topk;
+  const hipError_t e = launch_dispatch(p, (int)elem_size(type), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "dispatch launch");
+  return MOE_OK;
+}
+
+moe_status moe_combine(const void* rows, int rows_type, int64_t nrows, const int32_t* pair_pos, const float* weight,
+                       int64_t T, int topk, int64_t H, void* y, int type, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(rows_type)) != MOE_OK || (st = check_type(type)) != MOE_OK) return st;
+  if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
+  if ((st = check_ptrs({{rows, "rows"}}, elem_size(rows_type))) != MOE_OK) return st;
+  if ((st = check_ptrs({{y, "y"}}, elem_size(type))) != MOE_OK) return st;
+  if ((st = check_ptrs({{pair_pos, "pair_pos"}}, 4)) != MOE_OK) return st;
+  if (weight && (st = check_ptrs({{weight, "weight"}}, 4)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  PairsParams p{};
+  p.x = rows;
+  p.pair_pos = pair_pos;
+  p.weight = weight;
+  p.out = y;
+  p.T = T;
+  p.H = H;
+  p.nrows = nrows;
+  p.k = topk;
+  p.x32 = type == MOE_TYPE_FP32;
+  p.r32 = rows_type == MOE_TYPE_FP32;
+  const hipError_t e = launch_pairs_combine(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "combine launch");
+  return MOE_OK;
+}
+
+moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_type, int64_t nrows,
+                           const int32_t* pair_pos, const float* weight, const int32_t* idx, int64_t T, int topk,
+                           int64_t H, int E_total, void* drows, float* dweight, float* dlogits, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(rows_type)) != MOE_OK || (st = check_type(type)) != MOE_OK) return st;
+  if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
+  if ((st = check_ptrs({{dy, "dy"}}, elem_size(type))) != MOE_OK) return st;
+  if ((st = check_ptrs({{rows, "rows"}, {drows, "drows"}}, elem_size(rows_type))) != MOE_OK) return st;
+  if ((st = check_ptrs({{pair_pos, "pair_pos"}, {weight, "weight"}, {dweight, "dweight"}}, 4)) != MOE_OK) return st;
+  if (dlogits) {
+    if (E_total < 1) return fail(MOE_ERR_INVALID_ARG, "E_total must be positive");
+    if (E_total > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E_total must be <= 512");
+    if ((st = check_ptrs({{dlogits, "dlogits"}, {idx, "idx"}}, 4)) != MOE_OK) return st;
+  }
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  PairsParams p{};
+  p.x = dy;
+  p.rows = rows;
+  p.pair_pos = pair_pos;
+  p.idx = idx;
+  p.weight = weight;
+  p.out = drows;
+  p.dweight = dweight;
+  p.dlogits = dlogits;
+  p.T = T;
+  p.H = H;
+  p.nrows = nrows;
+  p.k = topk;
+  p.E = E_total;
+  p.x32 = type == MOE_TYPE_FP32;
+  p.r32 = rows_type == MOE_TYPE_FP32;
+  const hipError_t e = launch_pairs_combine_bwd(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "combine gradient launch");
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Products with 4-bit weights
+
+namespace {
+moe_status int4_checks(int G, int64_t N, int64_t K, int group) {
+  if (G < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "N, K and G must be positive");
+  if (group != 32 && group != 64 && group != 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "group must be 32, 64 or 128");
+  if (K % group != 0) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be a multiple of group");
+  if (K > kInt8MaxK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K must be <= 131072");
+  if (G > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "G must be <= 512");
+  if (N > (1 << 20) || (int64_t)G * N * K >= (int64_t(1) << 40))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "N must be <= 2^20 and G*N*K < 2^40");
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* q_bytes, size_t* scale_bytes) {
+  g_last_error.clear();
+  moe_status st = int4_checks(G, N, K, group);
+  if (st != MOE_OK) return st;
+  const size_t tiles = (size_t)G * ((N + 15) / 16) * ((K + 127) / 128);
+  if (q_bytes) *q_bytes = tiles * 1024;
+  if (scale_bytes) *scale_bytes = tiles * 16 * (128 / group) * 2;
+  return MOE_OK;
+}
+
+moe_status moe_int4_quantize(const void* in, int type, int G, int64_t N, int64_t K, int group, uint8_t* q,
+                             void* scales, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(type)) != MOE_OK) return st;
+  if ((st = int4_checks(G, N, K, group)) != MOE_OK) return st;
+  if ((st = check_ptrs({{in, "in"}, {q, "q"}, {scales, "scales"}}, 16)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const hipError_t e = launch_int4_pack(in, type == MOE_TYPE_FP32, nullptr, G, (int)N, (int)K, group, q, scales,
+                                        static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int4 quantise launch");
+  return MOE_OK;
+}
+
+moe_status moe_int4_pack(const int8_t* values, const void* in_scales, int G, int64_t N, int64_t K, int group,
+                         uint8_t* q, void* scales, void* stream) {
+  g_last_error.clear();
+  moe_status st = int4_checks(G, N, K, group);
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs({{values, "values"}, {q, "q"}, {scales, "scales"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{in_scales, "in_scales"}}, 2)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const hipError_t e = launch_int4_pack(values, false, in_scales, G, (int)N, (int)K, group, q, scales,
+                                        static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int4 layout launch");
+  return MOE_OK;
+}
+
+moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, int64_t M, int64_t N, int64_t K,
+                           int group, int G, const int32_t* offsets, void* y, int type, void* stream) {
+  g_last_error.clear();
+  moe_status st;
+  if ((st = check_type(type)) != MOE_OK) return st;
+  if (M < 1) return fail(MOE_ERR_INVALID_ARG, "M must be positive");
+  if ((st = int4_checks(G, N, K, group)) != MOE_OK) return st;
+  if (!offsets && G != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is null with more than one group");
+  if (M > INT32_MAX - 511 || M * N >= (int64_t(1) << 40))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be <= 2^31 - 512 and M*N < 2^40");
+  if ((st = check_ptrs({{x, "x"}, {q, "q"}}, 16)) != MOE_OK) return st;
+  if ((st = check_ptrs({{scales, "scales"}}, 8)) != MOE_OK) return st;
+  if (offsets && (st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;
+  if ((st = check_ptrs({{y, "y"}}, elem_size(type))) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  I4Params p{};
+  p.x = x;
+  p.q = q;
+  p.s = scales;
+  p.offsets = offsets;
+  p.y = y;
+  p.M = M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.G = G;
+  p.group = group;
+  p.f32 = type == MOE_TYPE_FP32;
+  const hipError_t e = launch_int4_matmul(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int4 product launch");
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradient norm and clipping
+
+namespace {
+moe_status tensors_checks(const moe_tensor* t, int count, const char* name) {
+  if (count < 0) return fail(MOE_ERR_INVALID_ARG, "count must be >= 0");
+  if (count > 0 && !t) return fail(MOE_ERR_INVALID_ARG, std::string(name) + " is null");
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    moe_status st;
+    const std::string which = std::string(name) + "[" + std::to_string(i) + "]";
+    if (t[i].type != MOE_TYPE_FP32 && t[i].type != MOE_TYPE_BF16) return fail(MOE_ERR_UNSUPPORTED_MODE, which + ": unknown type");
+    if (t[i].n < 0) return fail(MOE_ERR_INVALID_ARG, which + ": negative size");
+    if (t[i].n == 0) continue;
+    if ((st = check_ptrs({{t[i].data, which.c_str()}}, elem_size(t[i].type))) != MOE_OK) return st;
+    if (t[i].n >= (int64_t(1) << 40) || (total += t[i].n) >= (int64_t(1) << 40))
+      return fail(MOE_ERR_UNSUPPORTED_SHAPE, "the tensors must hold less than 2^40 elements");
+  }
+  return MOE_OK;
+}
+moe_status out_checks(const moe_tensor* t, const moe_tensor* out, int count) {
+  if (!out) return MOE_OK;
+  moe_status st = tensors_checks(out, count, "out");
+  for (int i = 0; st == MOE_OK && i < count; ++i) {
+    if (out[i].n != t[i].n)
+      st = fail(MOE_ERR_INVALID_ARG, "out[" + std::to_string(i) + "] has another size than its tensor");
+    else if (out[i].data == t[i].data && out[i].type != t[i].type && t[i].n > 0)
+      st = fail(MOE_ERR_INVALID_ARG, "out[" + std::to_string(i) + "] is its tensor's memory in another type");
+  }
+  return st;
+}
+size_t norm_bytes(const moe_tensor* t, int count) { return align256((size_t)norm_parts(t, count) * 8); }
+}  // namespace
+
+moe_status moe_query_norm_sizes(const moe_tensor* tensors, int count, size_t* ws) {
+  g_last_error.clear();
+  moe_status st = tensors_checks(tensors, count, "tensors");
+  if (st != MOE_OK) return st;
+  if (ws) *ws = norm_bytes(tensors, count);
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(const moe_tensor* tensors, int count, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status st = tensors_checks(tensors, count, "tensors");
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs({{norm, "norm"}}, 4)) != MOE_OK) return st;
+  const size_t need = norm_bytes(tensors, count);
+  if (need > 0 && (st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "norm workspace too small");
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const hipError_t e = launch_grad_norm(tensors, count, static_cast<double*>(ws), norm, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "norm launch");
+  return MOE_OK;
+}
+
+moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int count, const float* norm,
+                         float max_norm, void* stream) {
+  g_last_error.clear();
+  moe_status st = tensors_checks(tensors, count, "tensors");
+  if (st != MOE_OK || (st = out_checks(tensors, out, count)) != MOE_OK) return st;
+  if (!(max_norm >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if ((st = check_ptrs({{norm, "norm"}}, 4)) != MOE_OK) return st;
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  const hipError_t e = launch_grad_clip(tensors, out, count, max_norm, norm, nullptr, 0, nullptr,
+                                        static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "clip launch");
+  return MOE_OK;
+}
+
+moe_status moe_clip_grad_norm(const moe_tensor* tensors, const moe_tensor* out, int count, float max_norm,
+                              float* norm, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status st = tensors_checks(tensors, count, "tensors");
+  if (st != MOE_OK || (st = out_checks(tensors, out, count)) != MOE_OK) return st;
+  if (!(max_norm >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if ((st = check_ptrs({{norm, "norm"}}, 4)) != MOE_OK) return st;
+  const int64_t parts = norm_parts(tensors, count);
+  if (parts > 0 && (st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
+  if (ws_bytes < align256((size_t)parts * 8)) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "norm workspace too small");
+  if ((st = check_stream(stream)) != MOE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  // without a single element no scaling follows that would write the norm
+  hipError_t e = launch_grad_norm(tensors, count, part, parts == 0 ? norm : nullptr, s);
+  if (e == hipSuccess && parts > 0) e = launch_grad_clip(tensors, out, count, max_norm, nullptr, part, parts, norm, s);
+  if (e != hipSuccess) return hip_fail(e, "clip launch");
+  return MOE_OK;
+}
+
 moe_status moe_mx_quantize(const void* in, int64_t rows, int64_t cols, int axis, uint8_t* q, uint8_t* scales,
                            void* stream) {
   g_last_error.clear();

@@ -243,6 +243,58 @@ bool int8_rows_fit(const I8Params& p);                                          
 hipError_t launch_int8_rows(const I8Params& p, hipStream_t s);                                    // M <= 64
 hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hipStream_t s);      // any M
 
+// Pairs sorted by expert and back: pairs.hip.
+struct SortParams {
+  const int* idx;
+  int *offsets, *perm, *pair_pos;
+  int *cnt, *prefix, *total;   // workspace: [nblk][El + 1], [nblk][El + 1], [El + 1]
+  int64_t pairs;
+  int El, e0, nblk;
+};
+constexpr int kSortPairs = 2048;         // pairs of a workgroup
+constexpr int kSortSmall = 4096;         // up to here one workgroup sorts them all, without a workspace
+hipError_t launch_sort_pairs(const SortParams& p, hipStream_t s);
+struct PairsParams {
+  const void* x;         // dispatch: x; combine: rows; gradients: dy
+  const void* rows;      // gradients: rows
+  const int* pair_pos;
+  const int* idx;
+  const float* weight;
+  void* out;             // rows, y or drows
+  float *dweight, *dlogits;
+  int64_t T, H, nrows;
+  int k, E;
+  bool x32, r32;         // fp32: x or y or dy; rows (else bf16)
+};
+hipError_t launch_dispatch(const PairsParams& p, int elem, hipStream_t s);
+hipError_t launch_pairs_combine(const PairsParams& p, hipStream_t s);
+hipError_t launch_pairs_combine_bwd(const PairsParams& p, hipStream_t s);
+
+// Products with 4-bit weights: int4.hip.
+struct I4Params {
+  const void* x;         // [M, K] bf16
+  const uint8_t* q;      // tiles
+  const void* s;         // bf16
+  const int* offsets;    // [G + 1] or null
+  void* y;
+  int64_t M;
+  int N, K, G, group;
+  bool f32;
+};
+hipError_t launch_int4_matmul(const I4Params& p, hipStream_t s);
+// in: fp32 or bf16 to quantise, or (scales given) signed bytes to lay out
+hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G, int N, int K, int group, uint8_t* q,
+                            void* out_scales, hipStream_t s);
+
+// Gradient norm and clipping: clip.hip.
+constexpr int kNormParts = 2048;         // partial sums of a launch at most
+int64_t norm_parts(const moe_tensor* t, int count);   // partial sums of the norm of these tensors
+// norm partial sums into part; then, with norm, their root there
+hipError_t launch_grad_norm(const moe_tensor* t, int count, double* part, float* norm, hipStream_t s);
+// scales t into out (null: in place) by norm_in, or by the root of parts partial sums, which it writes to norm_out
+hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int count, float max_norm, const float* norm_in,
+                            const double* part, int64_t parts, float* norm_out, hipStream_t s);
+
 hipError_t launch_forward_gemms_mx(const FwdParams& p, int grid, hipStream_t s, bool recompute = false);
 hipError_t launch_backward_gemms_mx(const BwdParams& p, int grid, hipStream_t s);
 hipError_t launch_quant_rows(const void* in, uint8_t* q, uint8_t* sc, int64_t n, const char* name, hipStream_t s,

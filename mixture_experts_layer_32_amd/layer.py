@@ -2,8 +2,9 @@
 
 MoELayer holds the workspace and saved buffers for one layer shape, and calls moe_fwd/moe_bwd (and
 the router projection's moe_router_fwd/moe_router_bwd) through the binding. For serving, FewTokenLayer
-(up to 64 tokens), Int8Layer (8-bit weights, any number of tokens), int8_quantize and int8_matmul. No
-arithmetic happens here.
+(up to 64 tokens), Int8Layer (8-bit weights, any number of tokens), int8_quantize and int8_matmul, and
+int4_quantize, int4_pack and int4_matmul. For programs that take the layer apart, sort_pairs, dispatch, combine and
+combine_backward; for training steps, GradNorm. No arithmetic happens here.
 """
 from __future__ import annotations
 
@@ -166,6 +167,23 @@ class MoELayer:
         ws = self._router_ws()
         binding.moe_router_bwd(d, x, w_router, dlogits, dx, dw_router, ws, ws.numel(), stream)
         return dw_router
+
+    def pairs(self):
+        """Routing results in `saved` as tensors on the device, as sort_pairs, dispatch and combine name them: idx,
+        weight and pair_pos [T, topk], offsets [E_local + 1], perm [T * topk] (the first offsets[-1] count). They are
+        views of `saved`, which the layer's next forward or route overwrites."""
+        d = self.desc
+        off = binding.saved_layout(d)
+
+        def view(name, shape, dt):
+            n = 4
+            for v in shape:
+                n *= v
+            return self.saved[off[name]:off[name] + n].view(dt).view(shape)
+        tk = (d.T, d.topk)
+        return dict(idx=view("idx", tk, torch.int32), weight=view("weight", tk, torch.float32),
+                    offsets=view("offsets", (d.E_local + 1,), torch.int32),
+                    perm=view("perm", (d.T * d.topk,), torch.int32), pair_pos=view("pair_pos", tk, torch.int32))
 
     def routing(self):
         """Routing results from `saved` as CPU tensors: idx, weight, counts, offsets, perm, pair_pos."""
@@ -332,3 +350,244 @@ class Int8Layer:
             _expect(logits, "logits", self._logits, torch.float32, self.device)
         _expect(w_router, "w_router", self._wr, torch.bfloat16, self.device)
         return self._run(x, w_router, logits, w_gate, w_up, w_down, y, stream), logits
+
+
+def _matrix(t, name, types):
+    """Raises ValueError unless t is a contiguous matrix of one of these dtypes; its type number otherwise."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a tensor of two dimensions")
+    n = types.get(t.dtype)
+    if n is None:
+        raise ValueError(f"{name}: expected one of {[str(d) for d in types]}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return n
+
+
+_DISPATCH_TYPES = {**_INT8_TYPES, torch.int8: binding.TYPES["int8"]}
+
+
+def sort_pairs(idx, E_local, expert_offset=0, stream=None):
+    """The (token, slot) pairs sorted by expert: idx [T, topk] int32 names each pair's expert (of any router; -1 or
+    another rank's: no position). Returns offsets [E_local + 1], perm [T * topk] and pair_pos [T, topk], int32: the
+    first position of each expert's pairs, the pair at each position (-1 behind the last), and each pair's position
+    (-1: none)."""
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2:
+        raise ValueError("idx: expected a tensor of two dimensions")
+    shape, dev, n = idx.shape, idx.device, idx.numel()
+    handle = _on(dev, stream)
+    _expect(idx, "idx", shape, torch.int32, dev)
+    ws_bytes = binding.query_sort_sizes(n, E_local)
+    offsets = _empty((E_local + 1,), torch.int32, idx, stream)
+    perm = _empty((n,), torch.int32, idx, stream)
+    pair_pos = _empty(shape, torch.int32, idx, stream)
+    ws = _empty((ws_bytes,), torch.uint8, idx, stream) if ws_bytes else None
+    binding.moe_sort_pairs(idx, n, E_local, expert_offset, offsets, perm, pair_pos, ws, ws_bytes, handle)
+    return offsets, perm, pair_pos
+
+
+def dispatch(x, pair_pos, rows=None, stream=None):
+    """rows[pair_pos[t, j]] = x[t] for x [T, H] (bf16, fp32 or int8) and pair_pos [T, topk] int32. rows [n, H] is
+    [T * topk, H] unless it is given; rows that no pair stands at are left as they were (rows made here hold anything
+    there). The gradient with respect to x is combine(drows, pair_pos)."""
+    t = _matrix(x, "x", _DISPATCH_TYPES)
+    dev, (T, H) = x.device, x.shape
+    handle = _on(dev, stream)
+    k = pair_pos.shape[-1] if isinstance(pair_pos, torch.Tensor) and pair_pos.dim() == 2 else 0
+    _expect(pair_pos, "pair_pos", (T, k), torch.int32, dev)
+    if rows is None:
+        rows = _empty((T * k, H), x.dtype, x, stream)
+    else:
+        _matrix(rows, "rows", _DISPATCH_TYPES)
+        _expect(rows, "rows", (rows.shape[0], H), x.dtype, dev)
+    binding.moe_dispatch(x, t, T, k, H, pair_pos, rows, rows.shape[0], handle)
+    return rows
+
+
+def combine(rows, pair_pos, weight=None, y=None, dtype=None, stream=None):
+    """y[t] = sum over the slots j with a position of weight[t, j] rows[pair_pos[t, j]] (weight None: 1), in fp32 and
+    rounded once: rows [n, H] (bf16 or fp32), pair_pos [T, topk] int32, weight [T, topk] fp32, y [T, H] of dtype
+    (rows' own if None)."""
+    rt = _matrix(rows, "rows", _INT8_TYPES)
+    dev, (n, H) = rows.device, rows.shape
+    handle = _on(dev, stream)
+    if not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
+        raise ValueError("pair_pos: expected a tensor of two dimensions")
+    T, k = pair_pos.shape
+    _expect(pair_pos, "pair_pos", (T, k), torch.int32, dev)
+    if weight is not None:
+        _expect(weight, "weight", (T, k), torch.float32, dev)
+    if y is None:
+        t = rt if dtype is None else _int8_type(dtype)
+        y = _empty((T, H), rows.dtype if dtype is None else dtype, rows, stream)
+    else:
+        t = _matrix(y, "y", _INT8_TYPES)
+        _expect(y, "y", (T, H), y.dtype if dtype is None else dtype, dev)
+    binding.moe_combine(rows, rt, n, pair_pos, weight, T, k, H, y, t, handle)
+    return y
+
+
+def combine_backward(dy, rows, weight, pair_pos, idx=None, E_total=None, drows=None, stream=None):
+    """The gradients of combine(rows, pair_pos, weight) for dy [T, H]: (drows, dweight), and with the pairs' experts idx
+    [T, topk] int32 and E_total also dlogits [T, E_total] fp32, for weights that are a softmax over the chosen experts'
+    logits. drows [n, H] is of rows' type; its rows that no pair stands at are left as they were."""
+    rt, t = _matrix(rows, "rows", _INT8_TYPES), _matrix(dy, "dy", _INT8_TYPES)
+    dev, (n, H), T = rows.device, rows.shape, dy.shape[0]
+    handle = _on(dev, stream)
+    k = pair_pos.shape[-1] if isinstance(pair_pos, torch.Tensor) and pair_pos.dim() == 2 else 0
+    _expect(pair_pos, "pair_pos", (T, k), torch.int32, dev)
+    _expect(dy, "dy", (T, H), dy.dtype, dev)
+    _expect(weight, "weight", (T, k), torch.float32, dev)
+    if (idx is None) != (E_total is None):
+        raise ValueError("expected both idx and E_total, or neither")
+    if idx is not None:
+        _expect(idx, "idx", (T, k), torch.int32, dev)
+    if drows is None:
+        drows = _empty((n, H), rows.dtype, rows, stream)
+    else:
+        _expect(drows, "drows", (n, H), rows.dtype, dev)
+    dweight = _empty((T, k), torch.float32, weight, stream)
+    dlogits = _empty((T, E_total), torch.float32, rows, stream) if idx is not None else None
+    binding.moe_combine_bwd(dy, t, rows, rt, n, pair_pos, weight, idx, T, k, H, E_total or 0, drows, dweight, dlogits,
+                            handle)
+    return (drows, dweight) if idx is None else (drows, dweight, dlogits)
+
+
+def _int4_out(shape, group, like, stream):
+    """New tiles and scales of a weight [.., N, K] in 4 bits."""
+    *lead, N, K = shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: expected 32, 64 or 128, got {group}")
+    tiles = (*lead, -(-N // 16), -(-K // 128))
+    return (_empty((*tiles, 1024), torch.uint8, like, stream),
+            _empty((*tiles, 16, 128 // group), torch.bfloat16, like, stream))
+
+
+def _int4_shape(w, name):
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected [N, K] or [G, N, K]")
+    if not w.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return 1 if w.dim() == 2 else w.shape[0], w.shape[-2], w.shape[-1]
+
+
+def int4_quantize(w, group=128, stream=None):
+    """A weight w [N, K] or [G, N, K] (bf16 or fp32) in 4 bits with a bf16 scale for each `group` (32, 64 or 128) inputs:
+    the (tiles, scales) pair that int4_matmul takes."""
+    G, N, K = _int4_shape(w, "w")
+    t, handle = _int8_type(w.dtype), _on(w.device, stream)
+    q, s = _int4_out(w.shape, group, w, stream)
+    binding.moe_int4_quantize(w, t, G, N, K, group, q, s, handle)
+    return q, s
+
+
+def int4_pack(values, scales, stream=None):
+    """The (tiles, scales) pair of a weight that is quantised already: values [N, K] or [G, N, K] int8, whole numbers of
+    -8..7, and scales [.., N, K / group] bf16."""
+    G, N, K = _int4_shape(values, "values")
+    dev = values.device
+    handle = _on(dev, stream)
+    _expect(values, "values", values.shape, torch.int8, dev)
+    n = scales.shape[-1] if isinstance(scales, torch.Tensor) and scales.dim() else 0
+    _expect(scales, "scales", (*values.shape[:-1], n), torch.bfloat16, dev)
+    group = K // n if n and K % n == 0 else 0
+    q, s = _int4_out(values.shape, group, values, stream)
+    binding.moe_int4_pack(values, scales, G, N, K, group, q, s, handle)
+    return q, s
+
+
+def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16, stream=None):
+    """y [M, N] of bf16 rows x [M, K] and a weight in 4 bits, (q, scales) of int4_quantize or int4_pack on [N, K], or
+    on [G, N, K] with offsets [G + 1] int32: rows offsets[g] .. offsets[g+1]-1 are multiplied by weight g. N is
+    needed where it is no multiple of 16 (and y is not given). A y that is given sets the dtype, and its rows outside
+    the groups are left as they were (a y made here holds anything there)."""
+    if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(q, torch.Tensor)
+            or q.dim() != (3 if offsets is None else 4) or not isinstance(scales, torch.Tensor)
+            or scales.dim() != q.dim() + 1):
+        raise ValueError("expected x [M, K] and (q, scales) of a weight [N, K], or of [G, N, K] with offsets")
+    dev, (M, K) = x.device, x.shape
+    handle = _on(dev, stream)
+    _expect(x, "x", (M, K), torch.bfloat16, dev)
+    G, Nt, ng = 1 if offsets is None else q.shape[0], q.shape[-3], scales.shape[-1]
+    if ng not in (1, 2, 4):
+        raise ValueError(f"scales: expected 1, 2 or 4 for each 128 inputs, got {ng}")
+    tiles = (*q.shape[:-2], -(-K // 128))
+    _expect(q, "q", (*tiles, 1024), torch.uint8, dev)
+    _expect(scales, "scales", (*tiles, 16, ng), torch.bfloat16, dev)
+    if offsets is not None:
+        _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
+    if N is None:
+        N = y.shape[-1] if isinstance(y, torch.Tensor) and y.dim() else 16 * Nt
+    if -(-N // 16) != Nt:
+        raise ValueError(f"N: {N} channels do not fill {Nt} tiles of 16")
+    if y is None:
+        t = _int8_type(dtype)
+        y = _empty((M, N), dtype, x, stream)
+    else:
+        t = _int8_type(y.dtype)
+        _expect(y, "y", (M, N), y.dtype, dev)
+    binding.moe_int4_matmul(x, q, scales, M, N, K, 128 // ng, G, offsets, y, t, handle)
+    return y
+
+
+class GradNorm:
+    """The norm over many gradients together, and their scaling so that it stays within a bound: holds the list of
+    tensors and the workspace, for gradients that stay in place from step to step. Calls of one object share the
+    workspace: order them, or give concurrent streams an object each, and keep an object until its calls have run."""
+
+    def __init__(self, grads, out=None):
+        """grads: contiguous bf16 and fp32 tensors on the current GPU, which may not overlap. out: where the scaled
+        gradients go (the same sizes, either type), or None for in place."""
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        if not self.grads:
+            raise ValueError("grads: expected at least one tensor")
+        if self.out is not None and len(self.out) != len(self.grads):
+            raise ValueError(f"out: expected {len(self.grads)} tensors, got {len(self.out)}")
+        self.device = self.grads[0].device if isinstance(self.grads[0], torch.Tensor) else torch.device("cpu")
+        self._in = self._table(self.grads, "grads")
+        self._out = None if self.out is None else self._table(self.out, "out")
+        spans = []
+        for i, g in enumerate(self.grads):
+            o = g if self.out is None else self.out[i]
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{i}]: expected {g.numel()} elements, got {o.numel()}")
+            spans.append((g.data_ptr(), g.numel() * g.element_size(), f"grads[{i}]"))
+            if o.data_ptr() != g.data_ptr() or o.dtype != g.dtype:
+                spans.append((o.data_ptr(), o.numel() * o.element_size(), f"out[{i}]"))
+        spans = sorted(s for s in spans if s[1])
+        for (a, n, name), (b, _, other) in zip(spans, spans[1:]):
+            if b < a + n:
+                raise ValueError(f"{name} and {other} overlap")
+        self.ws = _workspace(max(256, binding.query_norm_sizes(self._in, len(self.grads))), self.device)
+
+    def _table(self, tensors, name):
+        table = (binding.Tensor * len(tensors))()
+        for i, t in enumerate(tensors):
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"{name}[{i}]: expected a torch.Tensor, got {type(t).__name__}")
+            _expect(t, f"{name}[{i}]", t.shape, t.dtype, self.device)
+            table[i] = binding.Tensor(t.data_ptr(), t.numel(), _int8_type(t.dtype))
+        return table
+
+    def norm(self, stream=None):
+        """The norm, an fp32 tensor without dimensions on the device."""
+        handle = _on(self.device, stream)
+        norm = _empty((), torch.float32, self.ws, stream)
+        binding.moe_grad_norm(self._in, len(self.grads), norm, self.ws, self.ws.numel(), handle)
+        return norm
+
+    def clip(self, max_norm, norm=None, stream=None):
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)) and returns the norm: their own, or the one given (an
+        fp32 tensor of one element, such as a norm over all ranks' gradients)."""
+        handle = _on(self.device, stream)
+        n = len(self.grads)
+        if norm is None:
+            norm = _empty((), torch.float32, self.ws, stream)
+            binding.moe_clip_grad_norm(self._in, self._out, n, max_norm, norm, self.ws, self.ws.numel(), handle)
+            return norm
+        if not isinstance(norm, torch.Tensor) or norm.numel() != 1:
+            raise ValueError("norm: expected a tensor of one element")
+        _expect(norm, "norm", norm.shape, torch.float32, self.device)
+        binding.moe_grad_clip(self._in, self._out, n, norm, max_norm, handle)
+        return norm
