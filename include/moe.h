@@ -355,8 +355,11 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
  * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory the numbers lie in tiles of 16 channels by
  * 128 inputs, 1024 bytes each, in the order in which a wavefront takes them, and a weight [N, K] is
  * ceil(N/16) rows of ceil(K/128) tiles, the weights of [G, N, K] one after the other (padding: q = 0, s = 0). The
- * scales of a tile are [16 channels][128 / group]. With c = n % 16, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] + 8 is the four bits from bit
- * 16 (j % 2) + 4 (j / 2) of the 32-bit word (16 h + c) * 4 + i of its tile. */
+ * scales of a tile are [16 channels][128 / group].
+ * With c = n % 16, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] lies in the 32-bit word
+ * (16 h + c) * 4 + i of its tile, as m = q (q >= 0) or -q - 1 (q < 0) and a sign bit that is 1 for q < 0: for
+ * j < 4, m in the three bits from bit 8 j and the sign in bit 8 j + 7; for j >= 4, m from bit 8 (j - 4) + 4 and the
+ * sign in bit (8 (j - 4) + 11) % 32. */
 moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* q_bytes, size_t* scale_bytes);
 
 /* Quantises a weight in [G, N, K] (row-major, `type`) for each group of inputs: D = the group's largest |v|,
@@ -373,8 +376,8 @@ moe_status moe_int4_pack(const int8_t* values, const void* in_scales, int G, int
 /* y[m, n] = sum over the groups of s[g, n, group] * (sum over the group's inputs of x[m, k] q[g, n, k]): x [M, K] bf16, y
  * [M, N] of `type`, rounded once; products exact, sums in fp32. offsets, groups of rows, and the rows of y outside of
  * them as in moe_int8_matmul. A NaN or an infinity in a row of x reaches that row of y alone (as NaN, where it meets other
- * values). M <= 2^31 - 512, M*N < 2^40, the rest as above. x and q need 16-byte alignment, scales 8-byte,
- * offsets 4-byte, y its type's. */
+ * values). M <= 2^31 - 512, M*N < 2^40, the rest as above. x, q and scales need 16-byte alignment, offsets 4-byte, y
+ * its type's (8-byte, fp32 16-byte, and N % 4 = 0 write faster). */
 moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, int64_t M, int64_t N, int64_t K,
                            int group, int G, const int32_t* offsets, void* y, int type, void* stream);
 

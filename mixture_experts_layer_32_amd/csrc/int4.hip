@@ -3,12 +3,18 @@
 //   k_int4_pack   a weight's tiles, from fp32 or bf16 (quantised here) or from whole numbers and scales.
 //   k_int4_rows   y = sum over groups of s (x q^T): a workgroup takes 16 output channels, its waves split K, and the
 //                 weight is read once for up to 64 rows.
-// A number q of a weight is held as u = q + 8 in four bits. Put into the upper bits of a bf16's significand they give
-// 16 + u exactly with a shift and one and-or for two numbers, and x q = x (16 + u) - 24 x: the matrix instruction that
-// multiplies with 16 + u starts from the sum that another one makes with the constant -24.
+//   k_int4_tile   the same for many rows: tiles in LDS, the weight's numbers unpacked once for a workgroup.
+// A number q of a weight is held in four bits, a sign bit and m = q or -q - 1. Two masks give four numbers each as
+// bytes, whose low bits are m; with the sign added to them they are q in sign and magnitude, and such a byte below 16 is
+// q 2^-9 in e4m3, which v_cvt_scalef32_pk_bf16_fp8 (two a cycle and lane, the rate of a plain instruction) turns into
+// q in bf16. So the matrix instruction's products x q are exact, and its fp32 sums of a group are multiplied with the scale.
+// (16 + u with u = q + 8 takes a shift and one and-or for two numbers, half as much, but then 24 times the group's sum of x has to
+// be subtracted, another matrix instruction and three bits of the sum.)
 #include <algorithm>
+#include <type_traits>
 
 #include "engine.h"
+#include "group_tiles.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -16,13 +22,22 @@ namespace {
 
 constexpr int kTileN = 16, kTileK = 128, kTileBytes4 = 1024;
 
-// Two numbers of each of the four words that a lane holds of a tile, 16 + u in bf16: element 2d in the low half,
-// 2d + 1 in the high one.
+// The numbers 2d and 2d + 1 of a word in bf16, d = 0..3.
 __device__ __forceinline__ uint4 unpack16(unsigned w) {
-  return make_uint4(((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                    ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u);
+  unsigned a = w & 0x87878787u, b = __builtin_amdgcn_alignbit(w, w, 4) & 0x87878787u;
+  a += (a >> 7) & 0x01010101u;
+  b += (b >> 7) & 0x01010101u;
+  const auto two = [](unsigned v, auto half) {
+    return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, decltype(half)::value));
+  };
+  return make_uint4(two(a, std::false_type{}), two(a, std::true_type{}), two(b, std::false_type{}),
+                    two(b, std::true_type{}));
 }
-constexpr unsigned kMinus24 = 0xC1C0C1C0u;   // bf16 -24 twice
+// the word's bits for its number j
+__device__ __forceinline__ unsigned pack4(int q, int j) {
+  const unsigned sign = q < 0, m = (unsigned)(q < 0 ? -q - 1 : q);
+  return j < 4 ? m << (8 * j) | sign << (8 * j + 7) : m << (8 * (j - 4) + 4) | sign << ((8 * (j - 4) + 11) & 31);
+}
 
 __device__ __forceinline__ float bf16_bits(unsigned short b) { return __uint_as_float((unsigned)b << 16); }
 
@@ -103,7 +118,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
       }
       w[i] = 0u;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[i] |= (unsigned)((int)v[i][j] + 8) << (16 * (j & 1) + 4 * (j >> 1));
+      for (int j = 0; j < 8; ++j) w[i] |= pack4((int)v[i][j], j);
       if (h == 0 && i == i0) sout[(tile * kTileN + c) * ng + i / per] = sb;
     }
     st16(q + tile * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
@@ -125,7 +140,7 @@ __device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g,
   const bf16* px[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) px[i] = static_cast<const bf16*>(p.x) + (r0 + min(16 * i + c, cnt - 1)) * p.K + 8 * h;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u), m24 = make_uint4(kMinus24, kMinus24, kMinus24, kMinus24);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   f32x4 acc[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -147,7 +162,6 @@ __device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g,
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
           const uint4 xv = k < p.K ? ld16(px[i] + k) : zero;
-          mma16<bf16>(part[i], xv, m24);
           mma16<bf16>(part[i], xv, wv);
         }
       }
@@ -196,14 +210,230 @@ __global__ __launch_bounds__(kRW4 * 64) void k_int4_rows(I4Params p) {
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// k_int4_tile: WM x WN waves of MI x NJ blocks of 16 x 16, K in stages of 64 inputs, two of them in LDS as rows of 128
+// bytes. x comes there by direct loads; the weight's numbers through registers, unpacked once for the workgroup. A
+// stage's sums (PER = 1: its halves') start from zero and are added to the accumulators times their scales.
+constexpr int kRowB = 128;   // bytes of a row in a stage
+
+// The 16-byte chunk c of row r lies in slot c ^ swz(r). Rows of x: 16 consecutive rows at one chunk, which a fragment
+// read takes, stand in distinct banks; rows of weights: also rows 16 a + b for a < 4 and four consecutive b, which an
+// unpacking wave writes.
+__device__ __forceinline__ int swz_x(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int swz_w(int r) { return ((r >> 1) ^ (r >> 4 << 1)) & 7; }
+
+// eng::gl2lds from a uniform address and a lane's offset
+__device__ __forceinline__ void gl2lds_at(const void* base, unsigned off, char* lds) {
+  const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
+}
+
+template <int MI, int NJ, int WM, int WN, int PER>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
+  constexpr int NW = WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN, OPA = BM * kRowB, ST = OPA + BN * kRowB;
+  constexpr int LA = BM / (8 * NW), TB = BN / (16 * NW), NS = 4 / PER;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * ST];
+  __shared__ Groups groups;
+  const int lane = threadIdx.x & 63, w = eng::wave_id(), wm = w / WN, wn = w % WN, c = lane & 15, h = lane >> 4;
+  const int Nt = (p.N + kTileN - 1) / kTileN, Kt = (p.K + kTileK - 1) / kTileK, nst = (p.K + 63) / 64;
+  const bool half = p.K % 64 != 0;             // the last stage has 32 inputs
+  const int ntn = (p.N + BN - 1) / BN;
+  const bool wide = p.N % NJ == 0 && reinterpret_cast<uintptr_t>(p.y) % (NJ * (p.f32 ? 4 : 2)) == 0;
+  // the lane's fragment reads: chunk 4 s + h of row c of a block
+  int ao[2], bo[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    ao[s] = (16 * MI * wm + c) * kRowB + ((4 * s + h) ^ swz_x(c)) * 16;
+    bo[s] = OPA + (16 * NJ * wn + c) * kRowB + ((4 * s + h) ^ swz_w(16 * NJ * wn + c)) * 16;
+  }
+  const int mtiles = group_tiles<BM>(p, groups);
+  const XcdRange xr = xcd_range(mtiles * ntn);
+  for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
+    const int mt = tile / ntn, n0 = (tile - mt * ntn) * BN;
+    int g, r0, end;
+    find_tile<BM>(p, groups, mt, g, r0, end);
+    const char* xb = reinterpret_cast<const char*>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K);
+    unsigned xo[LA];                           // at most 256 rows of 131072 inputs: 32 bits
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+      const int r = (w * LA + j) * 8 + lane / 8;
+      xo[j] = 2u * min(r, end - 1 - r0) * (unsigned)p.K + 16 * ((lane & 7) ^ swz_x(r));
+    }
+    // Inputs beyond K (half a stage, or a tile's second one) have zero weights; read for them are others of the same row.
+    auto issue = [&](int st) {
+      const int in = min(st, nst - 1);
+      const char* at = xb + (size_t)in * kRowB;
+      const unsigned back = half && in + 1 == nst ? 64u : 0u;
+      char* to = smem + (st & 1) * ST + w * LA * 1024;
+#pragma unroll
+      for (int j = 0; j < LA; ++j)
+        gl2lds_at(at, xo[j] - (back & (((lane & 7) ^ swz_x((w * LA + j) * 8 + lane / 8)) << 4)), to + j * 1024);
+    };
+    // weights: this wave unpacks the TB tiles of 16 channels from w TB on. A wave's column block j holds the channels
+    // NJ c + j of its 16 NJ, so that a lane's blocks are neighbours in y: row 16 j + c of its rows of LDS.
+    const uint8_t* qb[TB];
+    int wo[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      const int t = w * TB + b, n = 16 * t + c, m = n % (16 * NJ), r = n - m + 16 * (m % NJ) + m / NJ;
+      qb[b] = p.q + ((size_t)g * Nt + min(n0 / kTileN + t, Nt - 1)) * Kt * kTileBytes4;
+      wo[b] = OPA + r * kRowB + (h ^ swz_w(r)) * 16;   // step 1: 4 chunks further, the same but for bit 6
+    }
+    const int n1 = n0 + 16 * NJ * wn + NJ * c;   // the lane's first channel
+    const uint16_t* ps = static_cast<const uint16_t*>(p.s) +
+                         (((size_t)g * Nt + min(n1 / kTileN, Nt - 1)) * Kt * kTileN + n1 % kTileN) * NS;
+    struct alignas(NJ * NS * 2 < 16 ? NJ * NS * 2 : 16) Scales {   // two a word
+      unsigned w[NJ * NS / 2];
+      __device__ __forceinline__ float operator[](int i) const {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      }
+    };
+    uint4 q[TB];
+    Scales sc, sn;
+    auto load_q = [&](int kb) {
+#pragma unroll
+      for (int b = 0; b < TB; ++b) q[b] = ld16(qb[b] + (size_t)kb * kTileBytes4 + 16 * lane);
+    };
+    auto unpack = [&](int o, int b, int s) {   // step s of an even (o = 0) or odd stage of tile b into LDS
+      const unsigned lo = s ? q[b].y : q[b].x, hi = s ? q[b].w : q[b].z;
+      st16(smem + o * ST + (wo[b] ^ (64 * s)), unpack16(o ? hi : lo));
+    };
+    f32x4 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load_q(0);
+    sn = *reinterpret_cast<const Scales*>(ps);
+    eng::block_sync();   // every wave is done reading the previous tile's stages
+    issue(0);
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      unpack(0, b, 0);
+      unpack(0, b, 1);
+    }
+    auto stage = [&](int st, auto odd) {
+      constexpr int O = decltype(odd)::value;
+      const char* cur = smem + O * ST;
+      eng::wait_vm<0>();
+      // what the compiler loaded itself has come too: said here, so that it does not wait for it behind the loads below
+#pragma unroll
+      for (int b = 0; b < TB; ++b) asm volatile("" : "+v"(q[b].x), "+v"(q[b].y), "+v"(q[b].z), "+v"(q[b].w));
+#pragma unroll
+      for (int b = 0; b < (int)(sizeof(Scales) + 3) / 4; ++b) asm volatile("" : "+v"(sn.w[b]));
+      eng::block_sync();
+      issue(st + 1);
+      uint4 fb[2][NJ], fa[2][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        fa[0][s] = ld16(cur + ao[s]);
+        int b = bo[s];
+        asm volatile("" : "+v"(b));            // the blocks' addresses are made here rather than kept in registers
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) fb[s][j] = ld16(cur + (b ^ ((2 * j & 7) * 16)) + j * 16 * kRowB);
+      }
+      float f[NJ];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (i + 1 < MI)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) fa[(i + 1) & 1][s] = ld16(cur + ao[s] + (i + 1) * 16 * kRowB);
+        // the other buffer's weights in the first half, then the next tile's numbers
+        constexpr int PP = (4 * TB + MI - 1) / MI;
+#pragma unroll
+        for (int b = PP * i; b < PP * (i + 1) && b < 2 * TB; ++b) unpack(1 - O, b >> 1, b & 1);
+        if (O == 0 && i == MI / 2) {
+          const int next = min(st / 2 + 1, Kt - 1);   // (behind the last tile: read once more, and not used)
+          load_q(next);
+          sn = *reinterpret_cast<const Scales*>(ps + (size_t)next * kTileN * NS);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; s += PER == 1 ? 1 : 2) {
+          f32x4 part[NJ];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            mma16<bf16>(part[j], fa[i & 1][s], fb[s][j]);
+          }
+          if constexpr (PER > 1)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) mma16<bf16>(part[j], fa[i & 1][1], fb[1][j]);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            f[j] = sc[j * NS + (PER == 1 ? 2 * O + s : PER == 2 ? O : 0)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(f[j], part[j][e], acc[i][j][e]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int kb = 0; kb < Kt; ++kb) {
+      sc = sn;
+      stage(2 * kb, std::integral_constant<int, 0>{});
+      stage(2 * kb + 1, std::integral_constant<int, 1>{});
+    }
+    eng::wait_vm<0>();
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 16 * (MI * wm + i) + 4 * h + e;
+        if (r >= end) continue;
+        const size_t at = (size_t)r * p.N + n1;
+        if (wide) {
+          if (n1 >= p.N) continue;
+          if (p.f32) {
+            float* o = static_cast<float*>(p.y) + at;
+            if constexpr (NJ == 4) *reinterpret_cast<f32x4*>(o) = f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]};
+            else *reinterpret_cast<float2*>(o) = make_float2(acc[i][0][e], acc[i][1][e]);
+          } else {
+            alignas(8) bf16 v[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) v[j] = (bf16)acc[i][j][e];
+            bf16* o = static_cast<bf16*>(p.y) + at;
+            if constexpr (NJ == 4) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(v);
+            else *reinterpret_cast<unsigned*>(o) = *reinterpret_cast<const unsigned*>(v);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            if (n1 + j >= p.N) continue;
+            if (p.f32) static_cast<float*>(p.y)[at + j] = acc[i][j][e];
+            else static_cast<bf16*>(p.y)[at + j] = (bf16)acc[i][j][e];
+          }
+        }
+      }
+  }
+}
+
+// Tiles of bm rows by bn columns for the rows in as many groups as the product may have.
+int64_t tiles4(const I4Params& p, int bm, int bn) {
+  const int64_t m = p.M / bm + (p.offsets ? std::min<int64_t>(p.G, p.M) : 1);
+  return std::min<int64_t>(m, p.M) * ((p.N + bn - 1) / bn);
+}
+
+template <int PER>
+void launch4(const I4Params& p, int grid, hipStream_t s) {
+  if (p.M <= 64 || p.M <= 16 * p.G) {
+    k_int4_rows<PER><<<dim3((p.N + kTileN - 1) / kTileN, p.G, (unsigned)std::min<int64_t>((p.M + 63) / 64, 256)), kRW4 * 64, 0, s>>>(p);
+  } else if (4 * tiles4(p, 256, 256) >= 3 * grid) {
+    k_int4_tile<8, 4, 2, 4, PER><<<grid, 512, 0, s>>>(p);
+  } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
+    k_int4_tile<4, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
+  } else {
+    k_int4_tile<2, 2, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_int4_matmul(const I4Params& p, hipStream_t s) {
-  prof_mark_begin("int4_rows", s);
-  const dim3 grid((p.N + kTileN - 1) / kTileN, p.G, (unsigned)std::min<int64_t>((p.M + 63) / 64, 256));
-  if (p.group == 32) k_int4_rows<1><<<grid, kRW4 * 64, 0, s>>>(p);
-  else if (p.group == 64) k_int4_rows<2><<<grid, kRW4 * 64, 0, s>>>(p);
-  else k_int4_rows<4><<<grid, kRW4 * 64, 0, s>>>(p);
+  prof_mark_begin("int4_matmul", s);
+  const int grid = persistent_grid(1);
+  if (p.group == 32) launch4<1>(p, grid, s);
+  else if (p.group == 64) launch4<2>(p, grid, s);
+  else launch4<4>(p, grid, s);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;

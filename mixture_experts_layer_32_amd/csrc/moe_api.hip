@@ -1490,8 +1490,7 @@ moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, 
   if (!offsets && G != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is null with more than one group");
   if (M > INT32_MAX - 511 || M * N >= (int64_t(1) << 40))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be <= 2^31 - 512 and M*N < 2^40");
-  if ((st = check_ptrs({{x, "x"}, {q, "q"}}, 16)) != MOE_OK) return st;
-  if ((st = check_ptrs({{scales, "scales"}}, 8)) != MOE_OK) return st;
+  if ((st = check_ptrs({{x, "x"}, {q, "q"}, {scales, "scales"}}, 16)) != MOE_OK) return st;
   if (offsets && (st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;
   if ((st = check_ptrs({{y, "y"}}, elem_size(type))) != MOE_OK) return st;
   if ((st = check_stream(stream)) != MOE_OK) return st;

@@ -127,7 +127,7 @@ def test_int4_arguments():
     refused(SHAPE, lambda: matmul(M=1 << 30, N=1 << 10))
     refused(MODE, lambda: matmul(type=2))
     refused(ARG, lambda: matmul(G=2, offsets=None), "offsets is null")
-    for t, a in (("x", 16), ("q", 16), ("scales", 8), ("y", 2)):
+    for t, a in (("x", 16), ("q", 16), ("scales", 16), ("y", 2)):
         refused(ARG, lambda: matmul(**{t: None}), f"{t} is null")
         refused(ARG, lambda: matmul(**{t: FAKE + a // 2}), f"{t} is not {a}-byte aligned")
     refused(ARG, lambda: matmul(type=0, y=FAKE + 2), "y is not 4-byte aligned")

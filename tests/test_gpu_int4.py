@@ -22,8 +22,9 @@ def unpack(q, s, N, K):
     c, i, h, j = n % 16, k % 128 // 32, k % 32 // 8, k % 8
     words = q.contiguous().view(torch.int32).long() & 0xffffffff              # [.., Nt, Kt, 256]
     w = words[..., n // 16, k // 128, (16 * h + c) * 4 + i]
-    v = (w >> (16 * (j % 2) + 4 * (j // 2))) & 15
-    return v - 8, s[..., n // 16, k // 128, c, (k % 128) // group]
+    m = (w >> torch.where(j < 4, 8 * j, 8 * (j - 4) + 4)) & 7
+    sign = (w >> torch.where(j < 4, 8 * j + 7, (8 * (j - 4) + 11) % 32)) & 1
+    return torch.where(sign == 1, -m - 1, m), s[..., n // 16, k // 128, c, (k % 128) // group]
 
 
 def quantised(w, group):
@@ -98,11 +99,11 @@ def offsets_of(M, G, g, skew=1.0, lead=0, tail=0):
 
 
 def bound(x, v, s, group):
-    """What fp32 sums may be off by: in a group each input adds x (16 + u) and -24 x, up to 55 |x|, in at most 2 `group`
-    additions; the groups' sums are then added in K / group fused steps and 16 across the waves."""
+    """What fp32 sums may be off by: in a group each input adds up to 8 |x|, in at most `group` additions; the groups'
+    sums are then added in K / group fused steps (K / 64 of half groups at most), and 16 across the waves."""
     K = x.shape[-1]
     size = x.double().abs() @ s.double().abs().repeat_interleave(group, -1).transpose(-1, -2)
-    return (2 * group + K / group + 16) * U * 55 * size
+    return (group + K / min(group, 64) + 16) * U * 8 * size
 
 
 # (M, N, K): one row to several tiles of rows, odd everything, one group of inputs, long rows
@@ -187,7 +188,7 @@ def test_values_that_are_not_finite(M):
 
 
 def test_large_and_small_values():
-    """Rows near bf16's largest and smallest values: 55 |x| of a group still lies within fp32."""
+    """Rows near bf16's largest and smallest values, whose sums still lie within fp32."""
     g = gen(8)
     v, s = rand_weight((32, 128), 32, g, exact=True)
     x = torch.randint(-4, 5, (3, 128), generator=g, device=DEV).float()
