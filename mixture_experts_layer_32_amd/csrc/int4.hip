@@ -21,6 +21,14 @@ namespace moe {
 namespace {
 
 constexpr int kTileN = 16, kTileK = 128, kTileBytes4 = 1024;
+// Four tiles share 64 channels: tile t's column c is channel 4 c + t of them, so that a wavefront that takes all four
+// holds four neighbouring channels in a lane.
+__host__ __device__ constexpr int tile_rows(int N) { return (N + 63) / 64 * 4; }
+__device__ __forceinline__ int channel4(int nt, int c) { return nt / 4 * 64 + 4 * c + nt % 4; }
+// the first scale of channel n in a tile column kb of ng scales each
+__device__ __forceinline__ int64_t scale_at(int64_t weight_tiles, int Kt, int kb, int n, int ng) {
+  return (weight_tiles / 4 * Kt + (int64_t)(n / 64) * Kt + kb) * 64 * ng + n % 64 * ng;
+}
 
 // The numbers 2d and 2d + 1 of a word in bf16, d = 0..3.
 __device__ __forceinline__ uint4 unpack16(unsigned w) {
@@ -48,13 +56,13 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
                                                    int N, int K, int group, uint8_t* __restrict__ q,
                                                    uint16_t* __restrict__ sout) {
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
-  const int Nt = (N + kTileN - 1) / kTileN, Kt = (K + kTileK - 1) / kTileK;
+  const int Nt = tile_rows(N), Kt = (K + kTileK - 1) / kTileK;
   const int per = group / 32, ng = 4 / per;     // steps of 32 inputs in a group, groups of a tile
   for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += (int64_t)gridDim.x * 4) {
     const int64_t nt = tile / Kt;               // over the weights
     const int kb = (int)(tile - nt * Kt);
     const int64_t g = nt / Nt;
-    const int n = (int)(nt - g * Nt) * kTileN + c;
+    const int n = channel4((int)(nt - g * Nt), c);
     const int64_t row = g * N + n;
     float v[4][8];
     unsigned m[4];
@@ -119,7 +127,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
       w[i] = 0u;
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[i] |= pack4((int)v[i][j], j);
-      if (h == 0 && i == i0) sout[(tile * kTileN + c) * ng + i / per] = sb;
+      if (h == 0 && i == i0) sout[scale_at(g * Nt, Kt, kb, n, ng) + i / per] = sb;
     }
     st16(q + tile * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
   }
@@ -133,10 +141,9 @@ template <int NG, int PER>
 __device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g, int nt, int64_t r0, int cnt) {
   constexpr int NS = 4 / PER;   // scales of a tile and channel
   const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), c = lane & 15, h = lane >> 4;
-  const int Nt = (p.N + kTileN - 1) / kTileN, Kt = (p.K + kTileK - 1) / kTileK;
-  const int64_t tile0 = ((int64_t)g * Nt + nt) * Kt;
-  const uint8_t* pq = p.q + tile0 * kTileBytes4 + 16 * lane;
-  const uint16_t* ps = static_cast<const uint16_t*>(p.s) + (tile0 * kTileN + c) * NS;
+  const int Nt = tile_rows(p.N), Kt = (p.K + kTileK - 1) / kTileK;
+  const uint8_t* pq = p.q + ((int64_t)g * Nt + nt) * Kt * kTileBytes4 + 16 * lane;
+  const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(nt, c), NS);
   const bf16* px[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) px[i] = static_cast<const bf16*>(p.x) + (r0 + min(16 * i + c, cnt - 1)) * p.K + 8 * h;
@@ -149,7 +156,7 @@ __device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g,
     const unsigned qw[4] = {q.x, q.y, q.z, q.w};
     uint16_t s[NS];
 #pragma unroll
-    for (int a = 0; a < NS; ++a) s[a] = ps[(size_t)kb * kTileN * NS + a];
+    for (int a = 0; a < NS; ++a) s[a] = ps[(size_t)kb * 64 * NS + a];
 #pragma unroll
     for (int a = 0; a < NS; ++a) {
       f32x4 part[NG];
@@ -178,7 +185,7 @@ __device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g,
     red[w * 64 + lane] = acc[i];
     __syncthreads();
     if (tid < 256) {
-      const int f = tid & 15, r = tid >> 4, n = nt * kTileN + f;
+      const int f = tid & 15, r = tid >> 4, n = channel4(nt, f);
       const float* rs = reinterpret_cast<const float*>(red) + ((r >> 2) * 16 + f) * 4 + (r & 3);
       float sum = 0.f;
 #pragma unroll
@@ -211,16 +218,15 @@ __global__ __launch_bounds__(kRW4 * 64) void k_int4_rows(I4Params p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_int4_tile: WM x WN waves of MI x NJ blocks of 16 x 16, K in stages of 64 inputs, two of them in LDS as rows of 128
-// bytes. x comes there by direct loads; the weight's numbers through registers, unpacked once for the workgroup. A
-// stage's sums (PER = 1: its halves') start from zero and are added to the accumulators times their scales.
+// k_int4_tile: WM x WN waves of MI x NJ blocks of 16 x 16, K in stages of 64 inputs. x comes into LDS by direct loads,
+// two stages of it in rows of 128 bytes; each wave unpacks its own channels' numbers into fragments, those of the next
+// stage behind the last products of this one. A stage's sums (PER = 1: its halves') start from zero and are added to the
+// accumulators times their scales, a row block later than they are made, so that the matrix cores have work meanwhile.
 constexpr int kRowB = 128;   // bytes of a row in a stage
 
-// The 16-byte chunk c of row r lies in slot c ^ swz(r). Rows of x: 16 consecutive rows at one chunk, which a fragment
-// read takes, stand in distinct banks; rows of weights: also rows 16 a + b for a < 4 and four consecutive b, which an
-// unpacking wave writes.
+// The 16-byte chunk c of row r lies in slot c ^ swz_x(r): 16 consecutive rows at one chunk, which a fragment read
+// takes, stand in distinct banks.
 __device__ __forceinline__ int swz_x(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int swz_w(int r) { return ((r >> 1) ^ (r >> 4 << 1)) & 7; }
 
 // eng::gl2lds from a uniform address and a lane's offset
 __device__ __forceinline__ void gl2lds_at(const void* base, unsigned off, char* lds) {
@@ -228,24 +234,30 @@ __device__ __forceinline__ void gl2lds_at(const void* base, unsigned off, char* 
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
 
+// a load from a uniform address and a lane's offset
+template <class T>
+__device__ __forceinline__ T ld_at(const void* base, unsigned off) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((unsigned)(a >> 32)) << 32 |
+                     (unsigned)__builtin_amdgcn_readfirstlane((unsigned)a);
+  return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(u) + off);
+}
+
 template <int MI, int NJ, int WM, int WN, int PER>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
-  constexpr int NW = WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN, OPA = BM * kRowB, ST = OPA + BN * kRowB;
-  constexpr int LA = BM / (8 * NW), TB = BN / (16 * NW), NS = 4 / PER;
+  constexpr int NW = WM * WN, BM = 16 * MI * WM, BN = 16 * NJ * WN, ST = BM * kRowB;
+  constexpr int LA = BM / (8 * NW), NS = 4 / PER;
   __shared__ __attribute__((aligned(1024))) char smem[2 * ST];
   __shared__ Groups groups;
   const int lane = threadIdx.x & 63, w = eng::wave_id(), wm = w / WN, wn = w % WN, c = lane & 15, h = lane >> 4;
-  const int Nt = (p.N + kTileN - 1) / kTileN, Kt = (p.K + kTileK - 1) / kTileK, nst = (p.K + 63) / 64;
+  const int Nt = tile_rows(p.N), Kt = (p.K + kTileK - 1) / kTileK, nst = (p.K + 63) / 64;
   const bool half = p.K % 64 != 0;             // the last stage has 32 inputs
   const int ntn = (p.N + BN - 1) / BN;
   const bool wide = p.N % NJ == 0 && reinterpret_cast<uintptr_t>(p.y) % (NJ * (p.f32 ? 4 : 2)) == 0;
   // the lane's fragment reads: chunk 4 s + h of row c of a block
-  int ao[2], bo[2];
+  const char* ao[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    ao[s] = (16 * MI * wm + c) * kRowB + ((4 * s + h) ^ swz_x(c)) * 16;
-    bo[s] = OPA + (16 * NJ * wn + c) * kRowB + ((4 * s + h) ^ swz_w(16 * NJ * wn + c)) * 16;
-  }
+  for (int s = 0; s < 2; ++s) ao[s] = smem + (16 * MI * wm + c) * kRowB + ((4 * s + h) ^ swz_x(c)) * 16;
   const int mtiles = group_tiles<BM>(p, groups);
   const XcdRange xr = xcd_range(mtiles * ntn);
   for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
@@ -253,123 +265,104 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     int g, r0, end;
     find_tile<BM>(p, groups, mt, g, r0, end);
     const char* xb = reinterpret_cast<const char*>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K);
-    unsigned xo[LA];                           // at most 256 rows of 131072 inputs: 32 bits
-#pragma unroll
-    for (int j = 0; j < LA; ++j) {
-      const int r = (w * LA + j) * 8 + lane / 8;
-      xo[j] = 2u * min(r, end - 1 - r0) * (unsigned)p.K + 16 * ((lane & 7) ^ swz_x(r));
-    }
+    // This lane moves chunk (lane % 8) ^ swz_x(r) of rows r = (w LA + j) 8 + lane / 8; of an even LA that is the same
+    // chunk for all even j, and the one 4 further for the odd ones. (At most 256 rows of 131072 inputs: 32 bits.)
+    const unsigned K2 = 2u * (unsigned)p.K, x0 = K2 * (w * LA * 8 + lane / 8), xlast = K2 * (end - 1 - r0);
+    const unsigned ch = ((lane & 7) ^ swz_x(w * LA * 8 + lane / 8)) * 16;
+    static_assert(LA % 2 == 0, "");
     // Inputs beyond K (half a stage, or a tile's second one) have zero weights; read for them are others of the same row.
     auto issue = [&](int st) {
       const int in = min(st, nst - 1);
       const char* at = xb + (size_t)in * kRowB;
-      const unsigned back = half && in + 1 == nst ? 64u : 0u;
+      const unsigned in4 = half && in + 1 == nst ? 63u : 127u;
       char* to = smem + (st & 1) * ST + w * LA * 1024;
+      unsigned x = x0, even = ch & in4, odd = (ch ^ 64u) & in4;
+      asm volatile("" : "+v"(x), "+v"(even), "+v"(odd));   // the offsets are made here rather than kept in registers
 #pragma unroll
       for (int j = 0; j < LA; ++j)
-        gl2lds_at(at, xo[j] - (back & (((lane & 7) ^ swz_x((w * LA + j) * 8 + lane / 8)) << 4)), to + j * 1024);
+        gl2lds_at(at, min(x + 8 * j * K2, xlast) + (j & 1 ? odd : even), to + j * 1024);
     };
-    // weights: this wave unpacks the TB tiles of 16 channels from w TB on. A wave's column block j holds the channels
-    // NJ c + j of its 16 NJ, so that a lane's blocks are neighbours in y: row 16 j + c of its rows of LDS.
-    const uint8_t* qb[TB];
-    int wo[TB];
-#pragma unroll
-    for (int b = 0; b < TB; ++b) {
-      const int t = w * TB + b, n = 16 * t + c, m = n % (16 * NJ), r = n - m + 16 * (m % NJ) + m / NJ;
-      qb[b] = p.q + ((size_t)g * Nt + min(n0 / kTileN + t, Nt - 1)) * Kt * kTileBytes4;
-      wo[b] = OPA + r * kRowB + (h ^ swz_w(r)) * 16;   // step 1: 4 chunks further, the same but for bit 6
-    }
-    const int n1 = n0 + 16 * NJ * wn + NJ * c;   // the lane's first channel
-    const uint16_t* ps = static_cast<const uint16_t*>(p.s) +
-                         (((size_t)g * Nt + min(n1 / kTileN, Nt - 1)) * Kt * kTileN + n1 % kTileN) * NS;
+    const int nt = n0 / kTileN + NJ * wn, n1 = channel4(nt, c);   // the lane's channels: NJ from n1 on
+    const int ntc = min(nt, Nt - NJ);          // (a wave whose channels lie behind the last works on others, for nothing)
+    const uint8_t* qb = p.q + ((size_t)g * Nt + ntc) * Kt * kTileBytes4;
+    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(ntc, 0), NS);
     struct alignas(NJ * NS * 2 < 16 ? NJ * NS * 2 : 16) Scales {   // two a word
       unsigned w[NJ * NS / 2];
       __device__ __forceinline__ float operator[](int i) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
       }
     };
-    uint4 q[TB];
+    uint4 q[NJ], fb[2][NJ];
     Scales sc, sn;
-    auto load_q = [&](int kb) {
+    auto load = [&](int kb) {                  // (behind the last tile: read once more, and not used)
+      const size_t k = min(kb, Kt - 1);
 #pragma unroll
-      for (int b = 0; b < TB; ++b) q[b] = ld16(qb[b] + (size_t)kb * kTileBytes4 + 16 * lane);
-    };
-    auto unpack = [&](int o, int b, int s) {   // step s of an even (o = 0) or odd stage of tile b into LDS
-      const unsigned lo = s ? q[b].y : q[b].x, hi = s ? q[b].w : q[b].z;
-      st16(smem + o * ST + (wo[b] ^ (64 * s)), unpack16(o ? hi : lo));
+      for (int j = 0; j < NJ; ++j) q[j] = ld_at<uint4>(qb + ((size_t)j * Kt + k) * kTileBytes4, 16 * lane);
+      sn = ld_at<Scales>(ps + k * 64 * NS, 4 * c * NS * 2);
     };
     f32x4 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_q(0);
-    sn = *reinterpret_cast<const Scales*>(ps);
     eng::block_sync();   // every wave is done reading the previous tile's stages
     issue(0);
+    load(0);
 #pragma unroll
-    for (int b = 0; b < TB; ++b) {
-      unpack(0, b, 0);
-      unpack(0, b, 1);
+    for (int j = 0; j < NJ; ++j) {
+      fb[0][j] = unpack16(q[j].x);
+      fb[1][j] = unpack16(q[j].y);
     }
     auto stage = [&](int st, auto odd) {
       constexpr int O = decltype(odd)::value;
-      const char* cur = smem + O * ST;
       eng::wait_vm<0>();
-      // what the compiler loaded itself has come too: said here, so that it does not wait for it behind the loads below
+      if (O == 0) {
+        // the scales have come too: said here, so that the compiler does not wait for them behind the loads below
 #pragma unroll
-      for (int b = 0; b < TB; ++b) asm volatile("" : "+v"(q[b].x), "+v"(q[b].y), "+v"(q[b].z), "+v"(q[b].w));
-#pragma unroll
-      for (int b = 0; b < (int)(sizeof(Scales) + 3) / 4; ++b) asm volatile("" : "+v"(sn.w[b]));
+        for (int b = 0; b < NJ * NS / 2; ++b) asm volatile("" : "+v"(sn.w[b]));
+        sc = sn;
+      }
       eng::block_sync();
       issue(st + 1);
-      uint4 fb[2][NJ], fa[2][2];
+      if (O == 1) load(st / 2 + 1);
+      uint4 fa[2][2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        fa[0][s] = ld16(cur + ao[s]);
-        int b = bo[s];
-        asm volatile("" : "+v"(b));            // the blocks' addresses are made here rather than kept in registers
+      for (int s = 0; s < 2; ++s) fa[0][s] = ld16(ao[s] + O * ST);
+      constexpr int H = PER == 1 ? 2 : 1;      // sums of a stage and row block
+      f32x4 part[2][NJ];
+      auto add = [&](int u) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[s][j] = ld16(cur + (b ^ ((2 * j & 7) * 16)) + j * 16 * kRowB);
-      }
-      float f[NJ];
+        for (int j = 0; j < NJ; ++j) {
+          const float f = sc[j * NS + (PER == 1 ? 2 * O + u % H : PER == 2 ? O : 0)];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        if (i + 1 < MI)
-#pragma unroll
-          for (int s = 0; s < 2; ++s) fa[(i + 1) & 1][s] = ld16(cur + ao[s] + (i + 1) * 16 * kRowB);
-        // the other buffer's weights in the first half, then the next tile's numbers
-        constexpr int PP = (4 * TB + MI - 1) / MI;
-#pragma unroll
-        for (int b = PP * i; b < PP * (i + 1) && b < 2 * TB; ++b) unpack(1 - O, b >> 1, b & 1);
-        if (O == 0 && i == MI / 2) {
-          const int next = min(st / 2 + 1, Kt - 1);   // (behind the last tile: read once more, and not used)
-          load_q(next);
-          sn = *reinterpret_cast<const Scales*>(ps + (size_t)next * kTileN * NS);
+          for (int e = 0; e < 4; ++e) acc[u / H][j][e] = fmaf(f, part[u & 1][j][e], acc[u / H][j][e]);
         }
+      };
 #pragma unroll
-        for (int s = 0; s < 2; s += PER == 1 ? 1 : 2) {
-          f32x4 part[NJ];
+      for (int u = 0; u < MI * H; ++u) {
+        const int i = u / H;
+        if (u % H == 0 && i + 1 < MI)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) fa[(i + 1) & 1][s] = ld16(ao[s] + O * ST + (i + 1) * 16 * kRowB);
+#pragma unroll
+        for (int s = u % H; s < 2; s += H)
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            mma16<bf16>(part[j], fa[i & 1][s], fb[s][j]);
+            f32x4& t = part[u & 1][j];
+            if (s == u % H) t = f32x4{0.f, 0.f, 0.f, 0.f};
+            mma16<bf16>(t, fa[i & 1][s], fb[s][j]);
           }
-          if constexpr (PER > 1)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) mma16<bf16>(part[j], fa[i & 1][1], fb[1][j]);
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            f[j] = sc[j * NS + (PER == 1 ? 2 * O + s : PER == 2 ? O : 0)];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(f[j], part[j][e], acc[i][j][e]);
-          }
-        }
+        if (u > 0) add(u - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        fb[0][j] = unpack16(O ? q[j].x : q[j].z);
+        fb[1][j] = unpack16(O ? q[j].y : q[j].w);
+      }
+      add(MI * H - 1);
     };
     for (int kb = 0; kb < Kt; ++kb) {
-      sc = sn;
       stage(2 * kb, std::integral_constant<int, 0>{});
       stage(2 * kb + 1, std::integral_constant<int, 1>{});
     }
@@ -416,9 +409,9 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
   if (p.M <= 64 || p.M <= 16 * p.G) {
-    k_int4_rows<PER><<<dim3((p.N + kTileN - 1) / kTileN, p.G, (unsigned)std::min<int64_t>((p.M + 63) / 64, 256)), kRW4 * 64, 0, s>>>(p);
-  } else if (4 * tiles4(p, 256, 256) >= 3 * grid) {
-    k_int4_tile<8, 4, 2, 4, PER><<<grid, 512, 0, s>>>(p);
+    k_int4_rows<PER><<<dim3(tile_rows(p.N), p.G, (unsigned)std::min<int64_t>((p.M + 63) / 64, 256)), kRW4 * 64, 0, s>>>(p);
+  } else if (4 * tiles4(p, 256, 128) >= 6 * grid) {
+    k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
     k_int4_tile<4, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else {
@@ -442,7 +435,7 @@ hipError_t launch_int4_matmul(const I4Params& p, hipStream_t s) {
 hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G, int N, int K, int group, uint8_t* q,
                             void* out_scales, hipStream_t s) {
   prof_mark_begin("int4_pack", s);
-  const int64_t tiles = (int64_t)G * ((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
+  const int64_t tiles = (int64_t)G * tile_rows(N) * ((K + kTileK - 1) / kTileK);
   const unsigned grid = (unsigned)std::min<int64_t>((tiles + 3) / 4, 1 << 22);
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);

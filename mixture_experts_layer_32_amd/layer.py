@@ -458,9 +458,9 @@ def _int4_out(shape, group, like, stream):
     *lead, N, K = shape
     if group not in (32, 64, 128):
         raise ValueError(f"group: expected 32, 64 or 128, got {group}")
-    tiles = (*lead, -(-N // 16), -(-K // 128))
-    return (_empty((*tiles, 1024), torch.uint8, like, stream),
-            _empty((*tiles, 16, 128 // group), torch.bfloat16, like, stream))
+    rows, cols = -(-N // 64), -(-K // 128)
+    return (_empty((*lead, rows, 4, cols, 1024), torch.uint8, like, stream),
+            _empty((*lead, rows, cols, 64, 128 // group), torch.bfloat16, like, stream))
 
 
 def _int4_shape(w, name):
@@ -499,27 +499,26 @@ def int4_pack(values, scales, stream=None):
 def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16, stream=None):
     """y [M, N] of bf16 rows x [M, K] and a weight in 4 bits, (q, scales) of int4_quantize or int4_pack on [N, K], or
     on [G, N, K] with offsets [G + 1] int32: rows offsets[g] .. offsets[g+1]-1 are multiplied by weight g. N is
-    needed where it is no multiple of 16 (and y is not given). A y that is given sets the dtype, and its rows outside
+    needed where it is no multiple of 64 (and y is not given). A y that is given sets the dtype, and its rows outside
     the groups are left as they were (a y made here holds anything there)."""
     if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(q, torch.Tensor)
-            or q.dim() != (3 if offsets is None else 4) or not isinstance(scales, torch.Tensor)
-            or scales.dim() != q.dim() + 1):
+            or q.dim() != (4 if offsets is None else 5) or not isinstance(scales, torch.Tensor)
+            or scales.dim() != q.dim()):
         raise ValueError("expected x [M, K] and (q, scales) of a weight [N, K], or of [G, N, K] with offsets")
     dev, (M, K) = x.device, x.shape
     handle = _on(dev, stream)
     _expect(x, "x", (M, K), torch.bfloat16, dev)
-    G, Nt, ng = 1 if offsets is None else q.shape[0], q.shape[-3], scales.shape[-1]
+    G, rows, cols, ng = 1 if offsets is None else q.shape[0], q.shape[-4], -(-K // 128), scales.shape[-1]
     if ng not in (1, 2, 4):
         raise ValueError(f"scales: expected 1, 2 or 4 for each 128 inputs, got {ng}")
-    tiles = (*q.shape[:-2], -(-K // 128))
-    _expect(q, "q", (*tiles, 1024), torch.uint8, dev)
-    _expect(scales, "scales", (*tiles, 16, ng), torch.bfloat16, dev)
+    _expect(q, "q", (*q.shape[:-3], 4, cols, 1024), torch.uint8, dev)
+    _expect(scales, "scales", (*q.shape[:-3], cols, 64, ng), torch.bfloat16, dev)
     if offsets is not None:
         _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
     if N is None:
-        N = y.shape[-1] if isinstance(y, torch.Tensor) and y.dim() else 16 * Nt
-    if -(-N // 16) != Nt:
-        raise ValueError(f"N: {N} channels do not fill {Nt} tiles of 16")
+        N = y.shape[-1] if isinstance(y, torch.Tensor) and y.dim() else 64 * rows
+    if -(-N // 64) != rows:
+        raise ValueError(f"N: {N} channels are not {rows} times 64, or up to 63 less")
     if y is None:
         t = _int8_type(dtype)
         y = _empty((M, N), dtype, x, stream)

@@ -19,12 +19,12 @@ def unpack(q, s, N, K):
     """(values, scales) [.., N, K] that the tiles hold, by the layout that the header gives."""
     group = 128 // s.shape[-1]
     n, k = torch.arange(N, device=DEV)[:, None], torch.arange(K, device=DEV)[None]
-    c, i, h, j = n % 16, k % 128 // 32, k % 32 // 8, k % 8
-    words = q.contiguous().view(torch.int32).long() & 0xffffffff              # [.., Nt, Kt, 256]
-    w = words[..., n // 16, k // 128, (16 * h + c) * 4 + i]
+    c, i, h, j = n % 64 // 4, k % 128 // 32, k % 32 // 8, k % 8
+    words = q.contiguous().view(torch.int32).long() & 0xffffffff              # [.., N / 64, 4, K / 128, 256]
+    w = words[..., n // 64, n % 4, k // 128, (16 * h + c) * 4 + i]
     m = (w >> torch.where(j < 4, 8 * j, 8 * (j - 4) + 4)) & 7
     sign = (w >> torch.where(j < 4, 8 * j + 7, (8 * (j - 4) + 11) % 32)) & 1
-    return torch.where(sign == 1, -m - 1, m), s[..., n // 16, k // 128, c, (k % 128) // group]
+    return torch.where(sign == 1, -m - 1, m), s[..., n // 64, k // 128, n % 64, (k % 128) // group]
 
 
 def quantised(w, group):
@@ -67,7 +67,7 @@ def test_quantize_values_that_are_not_finite_and_padding():
     w[2, :32] = 1e-42
     w[2, 32:] = 3e38
     q, s = int4_quantize(w, 32)
-    v, sc = unpack(q, s, 16, 128)
+    v, sc = unpack(q, s, 64, 128)
     assert bool(sc[0, :32].isnan().all()) and bool((v[0, :32] == 0).all()) and bool(sc[1, 32:64].isnan().all())
     want_v, want_s = quantised(w, 32)
     assert torch.equal(v[:3, :64], want_v)
@@ -161,8 +161,9 @@ def test_offsets_outside_the_rows():
     v, s = rand_weight((4, 32, 64), 32, g, exact=True)
     x = torch.randint(-4, 5, (100, 64), generator=g, device=DEV).to(torch.bfloat16)
     w = int4_pack(v, s)
-    good = int4_matmul(x, *w, offsets=torch.tensor([0, 0, 90, 100, 100], dtype=torch.int32, device=DEV))
-    assert torch.equal(int4_matmul(x, *w, offsets=torch.tensor([-70, -5, 90, 1000, 2 ** 31 - 1], dtype=torch.int32, device=DEV)), good)
+    good = int4_matmul(x, *w, N=32, offsets=torch.tensor([0, 0, 90, 100, 100], dtype=torch.int32, device=DEV))
+    far = torch.tensor([-70, -5, 90, 1000, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    assert torch.equal(int4_matmul(x, *w, N=32, offsets=far), good)
     y = torch.full((100, 32), 2.0, device=DEV)
     int4_matmul(x, *w, offsets=torch.tensor([100, 100, 100, 100, 100], dtype=torch.int32, device=DEV), y=y)
     assert bool((y == 2).all())
@@ -179,10 +180,10 @@ def test_values_that_are_not_finite(M):
     bad[M // 2] = True
     if M > 2:
         x[M - 1, 3], bad[M - 1] = float("inf"), True
-    y = int4_matmul(x, *int4_pack(v, s), dtype=torch.float32)
+    y = int4_matmul(x, *int4_pack(v, s), N=48, dtype=torch.float32)
     assert torch.equal(y[~bad], want[~bad]) and not bool(torch.isfinite(y[bad]).any())
     s[5, 1] = float("nan")                         # a group's scale: its channel alone
-    y = int4_matmul(x, *int4_pack(v, s), dtype=torch.float32)
+    y = int4_matmul(x, *int4_pack(v, s), N=48, dtype=torch.float32)
     keep = torch.arange(48, device=DEV) != 5
     assert bool(y[:, 5].isnan().all()) and torch.equal(y[~bad][:, keep], want[~bad][:, keep])
 
@@ -193,7 +194,7 @@ def test_large_and_small_values():
     v, s = rand_weight((32, 128), 32, g, exact=True)
     x = torch.randint(-4, 5, (3, 128), generator=g, device=DEV).float()
     x = (x * torch.tensor([[2.0 ** 110], [2.0 ** -110], [1.0]], device=DEV)).to(torch.bfloat16)
-    assert torch.equal(int4_matmul(x, *int4_pack(v, s), dtype=torch.float32), (x.double() @ real(v, s, 32).T).float())
+    assert torch.equal(int4_matmul(x, *int4_pack(v, s), N=32, dtype=torch.float32), (x.double() @ real(v, s, 32).T).float())
 
 
 def test_more_than_two_to_the_31_numbers():
@@ -239,7 +240,7 @@ def test_captured_and_replayed(M):
         y.zero_()
         torch.cuda.synchronize()
         graph.replay()
-        assert torch.equal(y, int4_matmul(x, *w, offsets=off, dtype=torch.float32))
+        assert torch.equal(y, int4_matmul(x, *w, N=80, offsets=off, dtype=torch.float32))
 
 
 @pytest.mark.parametrize("kind", ["object", "handle", "null"])
@@ -247,11 +248,11 @@ def test_on_a_given_stream(kind):
     g = gen(4)
     v, s = rand_weight((96, 256), 64, g)
     x = torch.randn(40, 256, generator=g, device=DEV).to(torch.bfloat16)
-    want = int4_matmul(x, *int4_pack(v, s))
+    want = int4_matmul(x, *int4_pack(v, s), N=96)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     h = {"object": side, "handle": side.cuda_stream, "null": 0}[kind]
-    y = int4_matmul(x, *int4_pack(v, s, stream=h), stream=h)
+    y = int4_matmul(x, *int4_pack(v, s, stream=h), N=96, stream=h)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
 
@@ -276,10 +277,10 @@ def test_wrong_tensors_are_refused():
     x = torch.zeros((4, 128), dtype=torch.bfloat16, device=DEV)
     off = torch.zeros(2, dtype=torch.int32, device=DEV)
     for call in (lambda: int4_matmul(x.float(), q, sc), lambda: int4_matmul(x[0], q, sc), lambda: int4_matmul(x[:, ::2], q, sc),
-                 lambda: int4_matmul(x, q[:, :, :512], sc), lambda: int4_matmul(x, q, sc[..., :1]),
+                 lambda: int4_matmul(x, q[..., :512], sc), lambda: int4_matmul(x, q, sc[..., :1]),
                  lambda: int4_matmul(x, q, sc.float()), lambda: int4_matmul(x, q, sc, offsets=off),
                  lambda: int4_matmul(x, q[None], sc[None], offsets=off.long()), lambda: int4_matmul(x, q[None], sc[None]),
-                 lambda: int4_matmul(x, q, sc, N=16), lambda: int4_matmul(x, q, sc, N=33),
+                 lambda: int4_matmul(x, q, sc, N=0), lambda: int4_matmul(x, q, sc, N=65),
                  lambda: int4_matmul(x, q, sc, dtype=torch.float16),
                  lambda: int4_matmul(x, q, sc, y=torch.zeros((5, 32), device=DEV)),
                  lambda: int4_matmul(torch.zeros((4, 256), dtype=torch.bfloat16, device=DEV), q, sc),
