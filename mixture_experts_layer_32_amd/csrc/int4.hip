@@ -134,87 +134,182 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
 }
 
 // ------------------------------------------------------------------------------------------------
-constexpr int kRW4 = 8;   // waves of k_int4_rows
+// k_int4_rows: a task is up to 16 rows of a group and 8 / wk tiles of 16 channels; wk of the workgroup's 8 waves share a
+// tile and split K, each in units of kUnit tile columns. Workgroups take tasks round-robin, first those of up to 4 rows
+// (FEW), then the others. Behind a column's products its numbers are replaced by the same column's of the next unit, of this
+// task or the next, so that some are in flight all the time; no load stands in a branch, where the compiler could not
+// count those in flight. Of up to 4 rows x is loaded a unit ahead too: as the matrix instruction's 16 rows would be mostly
+// empty, they are 4 rows of the unit's 4 columns, and of a column's products the quarter of the lanes counts that holds
+// its rows. More rows are loaded at the start of their unit.
+constexpr int kRW4 = 8, kRows4 = 16, kFew4 = 4, kUnit = 4;
 
-// 16 channels from n0 of group g times its rows r0 .. r0 + cnt (up to 16 NG of them). PER: steps of 32 inputs a group.
-template <int NG, int PER>
-__device__ __forceinline__ void rows4_task(const I4Params& p, f32x4* red, int g, int nt, int64_t r0, int cnt) {
+// A load of 2 to 32 bytes from a uniform address and a lane's offset. Made in the global address space: a flat load would
+// wait for LDS as well, and for all loads before it.
+template <class T>
+__device__ __forceinline__ T ld_at(const void* base, unsigned off) {
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((unsigned)(a >> 32)) << 32 |
+                     (unsigned)__builtin_amdgcn_readfirstlane((unsigned)a);
+  typedef const __attribute__((address_space(1))) char* global;
+  const global at = (global)u + off;
+#define MOE_LD(V) __builtin_bit_cast(T, *(const __attribute__((address_space(1))) V*)at)
+  if constexpr (sizeof(T) == 2) return MOE_LD(uint16_t);
+  else if constexpr (sizeof(T) == 4) return MOE_LD(unsigned);
+  else if constexpr (sizeof(T) == 8) return MOE_LD(u32x2);
+  else if constexpr (sizeof(T) == 16) return MOE_LD(u32x4);
+  else {
+    struct Two { u32x4 a, b; };
+    const Two t = {*(const __attribute__((address_space(1))) u32x4*)at, *(const __attribute__((address_space(1))) u32x4*)(at + 16)};
+    return __builtin_bit_cast(T, t);
+  }
+#undef MOE_LD
+}
+
+// find_tile with two LDS round trips instead of one for each halving
+template <int BM>
+__device__ __forceinline__ void find_tile64(const I4Params& p, const Groups& s, int mt, int lane, int& g, int& r0, int& end) {
+  if (!p.offsets) return find_tile<BM>(p, s, mt, g, r0, end);
+  const int per = (p.G + 63) / 64;
+  const int a = __popcll(__ballot(s.tile0[min(lane * per, p.G)] <= mt && lane * per < p.G)) - 1;   // tile0[0] = 0
+  const int b = a * per + min(lane, per - 1);
+  const unsigned long long m = __ballot(lane < per && b < p.G && s.tile0[min(b, p.G)] <= mt);
+  g = __builtin_amdgcn_readfirstlane(a * per + __popcll(m) - 1);
+  r0 = __builtin_amdgcn_readfirstlane(s.row0[g] + (mt - s.tile0[g]) * BM);
+  end = __builtin_amdgcn_readfirstlane(max(s.row0[g + 1], s.row0[g]));
+}
+
+template <int PER, bool FEW>
+__device__ __forceinline__ void rows4_tasks(const I4Params& p, const Groups& groups, f32x4 (&red)[2][kRW4 * 64], int tasks,
+                                            int ntn, int wk, int& parity) {
   constexpr int NS = 4 / PER;   // scales of a tile and channel
+  struct alignas(2 * NS) Scales { uint16_t v[NS]; };
   const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), c = lane & 15, h = lane >> 4;
+  const int kw = w % wk, tw = w / wk, wt = kRW4 / wk;
   const int Nt = tile_rows(p.N), Kt = (p.K + kTileK - 1) / kTileK;
-  const uint8_t* pq = p.q + ((int64_t)g * Nt + nt) * Kt * kTileBytes4 + 16 * lane;
-  const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(nt, c), NS);
-  const bf16* px[NG];
+  const int k0 = kw * Kt / wk, k1 = (kw + 1) * Kt / wk;   // the wave's tile columns
+  // the unit that is loaded next: task `task`, from column kb on
+  int task = (int)blockIdx.x - (int)gridDim.x, kb = k0, g = 0, r0 = 0, cnt = 0, nt = 0;
+  auto find = [&] {   // the next task of up to 4 rows, or of more
+    do {
+      task += gridDim.x;
+      if (task >= tasks) return;
+      const int mt = task / ntn;
+      int end;
+      find_tile64<kRows4>(p, groups, mt, lane, g, r0, end);
+      cnt = min(end - r0, kRows4);
+      nt = min((task - mt * ntn) * wt + tw, Nt - 1);      // (behind the last tile: that one again, not stored)
+    } while ((cnt <= kFew4) != FEW);
+  };
+  uint4 q[kUnit], x[FEW ? 1 : 2][4], xn[4];
+  Scales sc[kUnit];
+  const uint8_t* pq;
+  const uint16_t* ps;
+  auto at = [&] {
+    pq = p.q + ((size_t)g * Nt + nt) * Kt * kTileBytes4;
+    ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(nt, 0), NS);
+  };
+  auto load = [&](int b) {   // (behind the wave's last column: that one again, which is not added)
+    const int k = max(min(kb + b, k1 - 1), 0);
+    q[b] = ld_at<uint4>(pq + (size_t)k * kTileBytes4, 16 * lane);
+    sc[b] = ld_at<Scales>(ps + (size_t)k * 64 * NS, 8 * c * NS);
+  };
+  auto rows = [&](int r0) { return static_cast<const bf16*>(p.x) + (size_t)r0 * p.K; };
+  // inputs beyond K have zero weights: others of the row are read
+  auto load_few = [&] {
+    const bf16* row = rows(r0);
+    const unsigned off = min(c & 3, cnt - 1) * (unsigned)p.K * 2 + 16 * h;
+    const int k = max(min(kb + (c >> 2), k1 - 1), 0) * kTileK;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) px[i] = static_cast<const bf16*>(p.x) + (r0 + min(16 * i + c, cnt - 1)) * p.K + 8 * h;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  f32x4 acc[NG];
+    for (int st = 0; st < 4; ++st) xn[st] = ld_at<uint4>(row, off + 2 * min(k + 32 * st, p.K - 32));
+  };
+  find();
+  if (task >= tasks) return;
+  at();
+  if (FEW) load_few();
 #pragma unroll
-  for (int i = 0; i < NG; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb = w * Kt / kRW4; kb < (w + 1) * Kt / kRW4; ++kb) {
-    const uint4 q = ld16(pq + (size_t)kb * kTileBytes4);
-    const unsigned qw[4] = {q.x, q.y, q.z, q.w};
-    uint16_t s[NS];
+  for (int b = 0; b < kUnit; ++b) load(b);
+  while (task < tasks) {
+    const int mr0 = r0, mcnt = cnt, n0 = task % ntn * wt;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int mkb = k0;;) {
+      const int n = k1 - mkb;   // columns from this unit on
+      const bf16* row = rows(mr0);
+      const unsigned off = min(c, mcnt - 1) * (unsigned)p.K * 2 + 16 * h;
+      auto load_x = [&](int b0) {   // columns b0 and b0 + 1
 #pragma unroll
-    for (int a = 0; a < NS; ++a) s[a] = ps[(size_t)kb * 64 * NS + a];
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int a = 0; a < NS; ++a) {
-      f32x4 part[NG];
+          for (int st = 0; st < 4; ++st)
+            x[FEW ? 0 : b][st] = ld_at<uint4>(row + min((mkb + b0 + b) * kTileK + 32 * st, p.K - 32), off);
+      };
+      if (FEW) {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) part[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int st = 0; st < 4; ++st) x[0][st] = xn[st];
+      } else {
+        load_x(0);
+      }
+      kb += kUnit;
+      if (kb >= k1) {
+        kb = k0;
+        find();
+        if (task < tasks) at();
+      }
+      if (FEW) load_few();
 #pragma unroll
-      for (int b = 0; b < PER; ++b) {
-        const int st = a * PER + b, k = kb * kTileK + 32 * st;
-        const uint4 wv = unpack16(qw[st]);
+      for (int b = 0; b < kUnit; ++b) {
+        const unsigned qw[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          const uint4 xv = k < p.K ? ld16(px[i] + k) : zero;
-          mma16<bf16>(part[i], xv, wv);
+        for (int a = 0; a < NS; ++a) {
+          f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[FEW ? 0 : b & 1][st], unpack16(qw[st]));
+          const float sf = bf16_bits(sc[b].v[a]);
+          if (FEW ? h == b && b < n : b < n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(sf, part[e], acc[e]);
+        }
+        // (more rows: those of the third and fourth column come ahead of the next unit's numbers)
+        if (!FEW && b == 1) load_x(2);
+        if (FEW || b > 1) load(b);
+        if (!FEW && b == 1) {
+          load(0);
+          load(1);
         }
       }
-      const float sf = bf16_bits(s[a]);
-#pragma unroll
-      for (int i = 0; i < NG; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(sf, part[i][e], acc[i][e]);
+      mkb += kUnit;
+      if (mkb >= k1) break;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    if (16 * i >= cnt) break;
-    red[w * 64 + lane] = acc[i];
+    // the waves' sums: row r of tile t is component r % 4 of lanes 16 (r / 4) + f of waves wk t .., of few rows the sum of
+    // the four quarters
+    f32x4* to = red[parity];
+    parity ^= 1;
+    to[w * 64 + lane] = acc;
     __syncthreads();
-    if (tid < 256) {
-      const int f = tid & 15, r = tid >> 4, n = channel4(nt, f);
-      const float* rs = reinterpret_cast<const float*>(red) + ((r >> 2) * 16 + f) * 4 + (r & 3);
+    for (int o = tid; o < wt * (FEW ? 64 : 256); o += kRW4 * 64) {
+      const int f = o & 15, r = FEW ? (o >> 4) & 3 : (o >> 4) & 15, t = FEW ? o >> 6 : o >> 8, ch = channel4(n0 + t, f);
+      if (r >= mcnt || n0 + t >= Nt || ch >= p.N) continue;
+      const float* rs = reinterpret_cast<const float*>(to + wk * t * 64 + (r >> 2) * 16 + f) + (r & 3);
       float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < kRW4; ++v) sum += rs[v * 256];
-      if (16 * i + r < cnt && n < p.N) {
-        const size_t at = (size_t)(r0 + 16 * i + r) * p.N + n;
-        if (p.f32) static_cast<float*>(p.y)[at] = sum;
-        else static_cast<bf16*>(p.y)[at] = (bf16)sum;
-      }
+      for (int v = 0; v < wk; ++v)
+        sum += FEW ? (rs[v * 256] + rs[v * 256 + 64]) + (rs[v * 256 + 128] + rs[v * 256 + 192]) : rs[v * 256];
+      const size_t to_y = (size_t)(mr0 + r) * p.N + ch;
+      if (p.f32) static_cast<float*>(p.y)[to_y] = sum;
+      else static_cast<bf16*>(p.y)[to_y] = (bf16)sum;
     }
-    __syncthreads();
   }
 }
 
 template <int PER>
-__global__ __launch_bounds__(kRW4 * 64) void k_int4_rows(I4Params p) {
-  __shared__ f32x4 red[kRW4 * 64];
-  const int g = blockIdx.y, nt = blockIdx.x;
-  int64_t r0 = 0, r1 = p.M;
-  if (p.offsets) {
-    r0 = min(max((int64_t)p.offsets[g], (int64_t)0), p.M);
-    r1 = min(max((int64_t)p.offsets[g + 1], r0), p.M);
-  }
-  for (int64_t r = r0 + 64 * (int64_t)blockIdx.z; r < r1; r += 64 * (int64_t)gridDim.z) {
-    const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)64, r1 - r));
-    if (cnt <= 16) rows4_task<1, PER>(p, red, g, nt, r, cnt);
-    else if (cnt <= 32) rows4_task<2, PER>(p, red, g, nt, r, cnt);
-    else rows4_task<4, PER>(p, red, g, nt, r, cnt);
-  }
+__global__ __launch_bounds__(kRW4 * 64, 4) void k_int4_rows(I4Params p, int wk) {
+  __shared__ f32x4 red[2][kRW4 * 64];
+  __shared__ Groups groups;
+  const int wt = kRW4 / wk, ntn = (tile_rows(p.N) + wt - 1) / wt;
+  const int tasks = group_tiles<kRows4>(p, groups) * ntn;
+  int parity = 0;
+  rows4_tasks<PER, true>(p, groups, red, tasks, ntn, wk, parity);
+  rows4_tasks<PER, false>(p, groups, red, tasks, ntn, wk, parity);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -232,15 +327,6 @@ __device__ __forceinline__ int swz_x(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ void gl2lds_at(const void* base, unsigned off, char* lds) {
   const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
-}
-
-// a load from a uniform address and a lane's offset
-template <class T>
-__device__ __forceinline__ T ld_at(const void* base, unsigned off) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((unsigned)(a >> 32)) << 32 |
-                     (unsigned)__builtin_amdgcn_readfirstlane((unsigned)a);
-  return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(u) + off);
 }
 
 template <int MI, int NJ, int WM, int WN, int PER>
@@ -409,7 +495,13 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
   if (p.M <= 64 || p.M <= 16 * p.G) {
-    k_int4_rows<PER><<<dim3(tile_rows(p.N), p.G, (unsigned)std::min<int64_t>((p.M + 63) / 64, 256)), kRW4 * 64, 0, s>>>(p);
+    // fewer waves a tile where their columns would make less than a unit, as long as every CU keeps two workgroups
+    const int64_t tiles = std::min<int64_t>(p.M, p.G) * tile_rows(p.N);
+    const int Kt = (p.K + kTileK - 1) / kTileK;
+    int wk = kRW4;
+    while (wk > 1 && Kt < kUnit * wk && tiles * wk / kRW4 >= 4 * grid) wk /= 2;
+    const int64_t tasks = (p.M / kRows4 + std::min<int64_t>(p.M, p.G)) * ((tile_rows(p.N) * wk + kRW4 - 1) / kRW4);
+    k_int4_rows<PER><<<(unsigned)std::min<int64_t>(tasks, 2 * grid), kRW4 * 64, 0, s>>>(p, wk);
   } else if (4 * tiles4(p, 256, 128) >= 6 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
