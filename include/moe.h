@@ -352,14 +352,13 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
  * half a byte.
  *
  * A weight [N, K] is held as whole numbers q of -8..7 and one bf16 scale for each `group` (32, 64 or 128) consecutive
- * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory the numbers lie in tiles of 16 channels by
- * 128 inputs, 1024 bytes each, in the order in which a wavefront takes them: q is [ceil(N/64)][4][ceil(K/128)][1024]
- * bytes, and tile t of the four holds the channels n with n % 4 = t. The scales are
- * [ceil(N/64)][ceil(K/128)][64][128 / group]. The weights of [G, N, K] follow one another; padding has q = 0, s = 0.
+ * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory 64 channels follow one another, and the weights
+ * of [G, N, K] likewise; 64 channels hold four tiles a 128 inputs, [4][ceil(K/128)][1024] bytes in the order in which a
+ * wavefront takes them, tile t holding the channels n with n % 4 = t, and then 16 bytes, a 32-bit word that is 0 if no
+ * number is -8, and zeros or anything. Their scales are [ceil(K/128)][64][128 / group]. Padding has q = 0, s = 0.
  * With c = n % 64 / 4, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] lies in the 32-bit word
- * (16 h + c) * 4 + i of its tile, as m = q (q >= 0) or -q - 1 (q < 0) and a sign bit that is 1 for q < 0: for
- * j < 4, m in the three bits from bit 8 j and the sign in bit 8 j + 7; for j >= 4, m from bit 8 (j - 4) + 4 and the
- * sign in bit (8 (j - 4) + 11) % 32. */
+ * (16 h + c) * 4 + i of its tile as a sign (1: q < 0) and m = |q| % 8: for j < 4, m in the three bits from bit 8 j and the
+ * sign in bit 8 j + 7; for j >= 4, m from bit 8 (j - 4) + 4 and the sign in bit (8 (j - 4) + 11) % 32. */
 moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* q_bytes, size_t* scale_bytes);
 
 /* Quantises a weight in [G, N, K] (row-major, `type`) for each group of inputs: D = the group's largest |v|,

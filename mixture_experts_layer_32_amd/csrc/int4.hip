@@ -4,12 +4,11 @@
 //   k_int4_rows   y = sum over groups of s (x q^T): a workgroup takes 16 output channels, its waves split K, and the
 //                 weight is read once for up to 64 rows.
 //   k_int4_tile   the same for many rows: tiles in LDS, the weight's numbers unpacked once for a workgroup.
-// A number q of a weight is held in four bits, a sign bit and m = q or -q - 1. Two masks give four numbers each as
-// bytes, whose low bits are m; with the sign added to them they are q in sign and magnitude, and such a byte below 16 is
-// q 2^-9 in e4m3, which v_cvt_scalef32_pk_bf16_fp8 (two a cycle and lane, the rate of a plain instruction) turns into
-// q in bf16. So the matrix instruction's products x q are exact, and its fp32 sums of a group are multiplied with the scale.
-// (16 + u with u = q + 8 takes a shift and one and-or for two numbers, half as much, but then 24 times the group's sum of x has to
-// be subtracted, another matrix instruction and three bits of the sum.)
+// A number q of a weight is held in four bits, a sign and m = |q| (sign 1 and m = 0: -8). Two masks give four numbers
+// each as bytes, a sign bit and the low three; such a byte is q 2^-9 in e4m3, and v_cvt_scalef32_pk_bf16_fp8 (two numbers
+// an instruction, at the rate of a plain one) makes q in bf16 of it: 7 instructions for 8 numbers. -8, which a symmetric
+// quantiser does not make, takes 12 more; 64 channels that hold none say so in a word of theirs. The matrix instruction's products x q
+// are exact, and its fp32 sums of a group are multiplied with the scale.
 #include <algorithm>
 #include <type_traits>
 
@@ -20,50 +19,80 @@
 namespace moe {
 namespace {
 
-constexpr int kTileN = 16, kTileK = 128, kTileBytes4 = 1024;
+constexpr int kTileN = 16, kTileK = 128, kTileBytes4 = 1024, kFlagBytes = 16;
 // Four tiles share 64 channels: tile t's column c is channel 4 c + t of them, so that a wavefront that takes all four
 // holds four neighbouring channels in a lane.
-__host__ __device__ constexpr int tile_rows(int N) { return (N + 63) / 64 * 4; }
+__host__ __device__ constexpr int rows64(int N) { return (N + 63) / 64; }
 __device__ __forceinline__ int channel4(int nt, int c) { return nt / 4 * 64 + 4 * c + nt % 4; }
-// the first scale of channel n in a tile column kb of ng scales each
-__device__ __forceinline__ int64_t scale_at(int64_t weight_tiles, int Kt, int kb, int n, int ng) {
-  return (weight_tiles / 4 * Kt + (int64_t)(n / 64) * Kt + kb) * 64 * ng + n % 64 * ng;
+// 64 channels (row64 over all weights): their tiles, and behind them the word that says whether one holds a -8
+__device__ __forceinline__ size_t row_bytes(int Kt) { return (size_t)4 * Kt * kTileBytes4 + kFlagBytes; }
+__device__ __forceinline__ const uint8_t* tile_at(const uint8_t* q, int64_t row64, int t, int Kt) {
+  return q + row64 * row_bytes(Kt) + (size_t)t * Kt * kTileBytes4;
+}
+__device__ __forceinline__ int holds_8(const uint8_t* q, int64_t row64, int Kt) {
+  return eng::ld_uniform(reinterpret_cast<const int*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4), 0);
+}
+// the first scale of channel n of 64 in tile column kb, of ng each
+__device__ __forceinline__ size_t scale_at(int64_t row64, int Kt, int kb, int n, int ng) {
+  return ((size_t)(row64 * Kt + kb) * 64 + n) * ng;
 }
 
-// The numbers 2d and 2d + 1 of a word in bf16, d = 0..3.
-__device__ __forceinline__ uint4 unpack16(unsigned w) {
-  unsigned a = w & 0x87878787u, b = __builtin_amdgcn_alignbit(w, w, 4) & 0x87878787u;
-  a += (a >> 7) & 0x01010101u;
-  b += (b >> 7) & 0x01010101u;
+// The numbers of a word as bytes: sign and magnitude.
+struct Bytes8 { unsigned a, b; };   // numbers 0..3 and 4..7
+__device__ __forceinline__ Bytes8 bytes8(unsigned w) {
+  return {w & 0x87878787u, __builtin_amdgcn_alignbit(w, w, 4) & 0x87878787u};
+}
+__device__ __forceinline__ unsigned with_8(unsigned t) {   // sign 1 and magnitude 0 become -8
+  const unsigned some = (t & 0x07070707u) + 0x07070707u;   // bit 3: a magnitude other than 0
+  return t | ((t >> 4) & ~some & 0x08080808u);
+}
+// The numbers 2d and 2d + 1 in bf16, d = 0..3.
+__device__ __forceinline__ uint4 numbers8(Bytes8 v) {
   const auto two = [](unsigned v, auto half) {
     return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, decltype(half)::value));
   };
-  return make_uint4(two(a, std::false_type{}), two(a, std::true_type{}), two(b, std::false_type{}),
-                    two(b, std::true_type{}));
+  return make_uint4(two(v.a, std::false_type{}), two(v.a, std::true_type{}), two(v.b, std::false_type{}),
+                    two(v.b, std::true_type{}));
+}
+// A condition that the compiler does not know to be the same all the time: it would make two loops of one.
+__device__ __forceinline__ bool here(int b) {
+  int v = __builtin_amdgcn_readfirstlane(b);
+  asm volatile("" : "+s"(v));
+  return v != 0;
+}
+// The four words of a tile column that a lane holds, as fragments.
+__device__ __forceinline__ void unpack4(uint4 q, int eights, uint4 (&f)[4]) {
+  Bytes8 v[4] = {bytes8(q.x), bytes8(q.y), bytes8(q.z), bytes8(q.w)};
+  if (here(eights))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = {with_8(v[i].a), with_8(v[i].b)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = numbers8(v[i]);
 }
 // the word's bits for its number j
 __device__ __forceinline__ unsigned pack4(int q, int j) {
-  const unsigned sign = q < 0, m = (unsigned)(q < 0 ? -q - 1 : q);
+  const unsigned sign = q < 0, m = (unsigned)(q < 0 ? -q : q) & 7u;
   return j < 4 ? m << (8 * j) | sign << (8 * j + 7) : m << (8 * (j - 4) + 4) | sign << ((8 * (j - 4) + 11) & 31);
 }
 
 __device__ __forceinline__ float bf16_bits(unsigned short b) { return __uint_as_float((unsigned)b << 16); }
 
-// KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. One wavefront per tile; lane 16 h + c takes channel c and
-// inputs 32 i + 8 h + j, i < 4, j < 8.
+// KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, its wave t their tile t, a
+// tile column at a time; lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
 template <int KIND>
-__global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, const uint16_t* __restrict__ sin, int64_t tiles,
+__global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, const uint16_t* __restrict__ sin, int64_t rows,
                                                    int N, int K, int group, uint8_t* __restrict__ q,
                                                    uint16_t* __restrict__ sout) {
-  const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
-  const int Nt = tile_rows(N), Kt = (K + kTileK - 1) / kTileK;
+  const int t = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
+  const int Kt = (K + kTileK - 1) / kTileK;
   const int per = group / 32, ng = 4 / per;     // steps of 32 inputs in a group, groups of a tile
-  for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += (int64_t)gridDim.x * 4) {
-    const int64_t nt = tile / Kt;               // over the weights
-    const int kb = (int)(tile - nt * Kt);
-    const int64_t g = nt / Nt;
-    const int n = channel4((int)(nt - g * Nt), c);
-    const int64_t row = g * N + n;
+  const int64_t row64 = blockIdx.x;             // over the weights
+  const int64_t g = row64 / rows64(N);
+  const int n = (int)(row64 - g * rows64(N)) * 64 + 4 * c + t;
+  const int64_t row = g * N + n;
+  unsigned* flag = reinterpret_cast<unsigned*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4);
+  bool eights = false;
+  for (int kb = 0; kb < Kt; ++kb) {
     float v[4][8];
     unsigned m[4];
 #pragma unroll
@@ -126,22 +155,28 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
       }
       w[i] = 0u;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[i] |= pack4((int)v[i][j], j);
-      if (h == 0 && i == i0) sout[scale_at(g * Nt, Kt, kb, n, ng) + i / per] = sb;
+      for (int j = 0; j < 8; ++j) {
+        w[i] |= pack4((int)v[i][j], j);
+        if constexpr (KIND == 2) eights |= v[i][j] == -8.f;
+      }
+      if (h == 0 && i == i0) sout[scale_at(row64, Kt, kb, 4 * c + t, ng) + i / per] = sb;
     }
-    st16(q + tile * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
+    st16(q + row64 * row_bytes(Kt) + ((size_t)t * Kt + kb) * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
   }
+  const int any = __syncthreads_or(eights);
+  if (threadIdx.x < kFlagBytes / 4) flag[threadIdx.x] = any != 0;
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_int4_rows: a task is up to 16 rows of a group and 8 / wk tiles of 16 channels; wk of the workgroup's 8 waves share a
-// tile and split K, each in units of kUnit tile columns. Workgroups take tasks round-robin, first those of up to 4 rows
-// (FEW), then the others. Behind a column's products its numbers are replaced by the same column's of the next unit, of this
-// task or the next, so that some are in flight all the time; no load stands in a branch, where the compiler could not
-// count those in flight. Of up to 4 rows x is loaded a unit ahead too: as the matrix instruction's 16 rows would be mostly
-// empty, they are 4 rows of the unit's 4 columns, and of a column's products the quarter of the lanes counts that holds
-// its rows. More rows are loaded at the start of their unit.
-constexpr int kRW4 = 8, kRows4 = 16, kFew4 = 4, kUnit = 4;
+// k_int4_rows: persistent workgroups take tasks round-robin, first those of up to 4 rows of a group, then those of up to 16.
+// wk of the workgroup's NW waves share a task's channels and split K, and their sums meet in LDS. Behind a tile's products its
+// numbers are replaced by the next ones needed, of this task or the next, so that some are in flight all the time; no load
+// stands in a branch, where the compiler could not count those in flight.
+//   up to 4 rows   a wave takes one tile of 16 channels, in units of kUnit tile columns. As the matrix instruction's 16
+//                  rows would be mostly empty, they are 4 rows of the unit's 4 columns, and of a column's products the
+//                  quarter of the lanes counts that holds its rows.
+//   up to 16 rows  a wave takes TL tiles, a column at a time, so that a row's fragments serve TL products.
+constexpr int kRows4 = 16, kFew4 = 4, kUnit = 4;
 
 // A load of 2 to 32 bytes from a uniform address and a lane's offset. Made in the global address space: a flat load would
 // wait for LDS as well, and for all loads before it.
@@ -180,18 +215,48 @@ __device__ __forceinline__ void find_tile64(const I4Params& p, const Groups& s, 
   end = __builtin_amdgcn_readfirstlane(max(s.row0[g + 1], s.row0[g]));
 }
 
-template <int PER, bool FEW>
-__device__ __forceinline__ void rows4_tasks(const I4Params& p, const Groups& groups, f32x4 (&red)[2][kRW4 * 64], int tasks,
-                                            int ntn, int wk, int& parity) {
+// Where the waves of a task are: those of the workgroup, wk to a task.
+template <int NW>
+struct Waves {
+  int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4, wk, kw, tw, wt;
+  __device__ __forceinline__ explicit Waves(int wk) : wk(wk) {
+    const int w = eng::wave_id();
+    kw = w % wk;
+    tw = w / wk;
+    wt = NW / wk;
+  }
+};
+
+// The sums of the task's wk waves in LDS for each of TL tiles, as stored by lanes 16 h + c: rows 4 h .. 4 h + 3 of
+// channel c (FEW: rows 0 .. 3, a quarter of the sum). They are added and stored to y from row r0 on, cnt rows, and channels
+// of the tiles from nt on.
+template <int NW, int TL, bool FEW>
+__device__ __forceinline__ void store_sums(const I4Params& p, const f32x4* red, int wk, int64_t r0, int cnt, int nt, int ntiles) {
+  constexpr int ROWS = FEW ? 4 : 16;
+  for (int o = threadIdx.x; o < NW / wk * TL * 16 * ROWS; o += NW * 64) {
+    const int f = o & 15, r = (o >> 4) % ROWS, t = o / (16 * ROWS), n = channel4(nt + t, f);
+    if (r >= cnt || nt + t >= ntiles || n >= p.N) continue;
+    // wave (t / TL) wk + v holds tile t % TL
+    const float* rs = reinterpret_cast<const float*>(red + ((t / TL * wk) * TL + t % TL) * 64 + (r >> 2) * 16 + f) + (r & 3);
+    float sum = 0.f;
+    for (int v = 0; v < wk; ++v, rs += TL * 256) sum += FEW ? (rs[0] + rs[64]) + (rs[128] + rs[192]) : rs[0];
+    const size_t at = (size_t)(r0 + r) * p.N + n;
+    if (p.f32) static_cast<float*>(p.y)[at] = sum;
+    else static_cast<bf16*>(p.y)[at] = (bf16)sum;
+  }
+}
+
+template <int PER, int NW>
+__device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk, int& parity) {
   constexpr int NS = 4 / PER;   // scales of a tile and channel
   struct alignas(2 * NS) Scales { uint16_t v[NS]; };
-  const int tid = threadIdx.x, lane = tid & 63, w = eng::wave_id(), c = lane & 15, h = lane >> 4;
-  const int kw = w % wk, tw = w / wk, wt = kRW4 / wk;
-  const int Nt = tile_rows(p.N), Kt = (p.K + kTileK - 1) / kTileK;
-  const int k0 = kw * Kt / wk, k1 = (kw + 1) * Kt / wk;   // the wave's tile columns
+  const Waves<NW> W(wk);
+  const int lane = W.lane, c = W.c, h = W.h;
+  const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, ntn = (Nt + W.wt - 1) / W.wt, tasks = mtiles * ntn;
+  const int k0 = W.kw * Kt / wk, k1 = (W.kw + 1) * Kt / wk;   // the wave's tile columns
   // the unit that is loaded next: task `task`, from column kb on
   int task = (int)blockIdx.x - (int)gridDim.x, kb = k0, g = 0, r0 = 0, cnt = 0, nt = 0;
-  auto find = [&] {   // the next task of up to 4 rows, or of more
+  auto find = [&] {
     do {
       task += gridDim.x;
       if (task >= tasks) return;
@@ -199,117 +264,177 @@ __device__ __forceinline__ void rows4_tasks(const I4Params& p, const Groups& gro
       int end;
       find_tile64<kRows4>(p, groups, mt, lane, g, r0, end);
       cnt = min(end - r0, kRows4);
-      nt = min((task - mt * ntn) * wt + tw, Nt - 1);      // (behind the last tile: that one again, not stored)
-    } while ((cnt <= kFew4) != FEW);
+      nt = min((task - mt * ntn) * W.wt + W.tw, Nt - 1);      // (behind the last tile: that one again, not stored)
+    } while (cnt > kFew4);
   };
-  uint4 q[kUnit], x[FEW ? 1 : 2][4], xn[4];
+  uint4 q[kUnit], x[4], xn[4];
   Scales sc[kUnit];
   const uint8_t* pq;
   const uint16_t* ps;
+  int eights, eights_next;
   auto at = [&] {
-    pq = p.q + ((size_t)g * Nt + nt) * Kt * kTileBytes4;
-    ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(nt, 0), NS);
+    const int64_t row64 = (int64_t)g * (Nt / 4) + nt / 4;
+    pq = tile_at(p.q, row64, nt % 4, Kt);
+    ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
+    eights_next = holds_8(p.q, row64, Kt);
   };
   auto load = [&](int b) {   // (behind the wave's last column: that one again, which is not added)
     const int k = max(min(kb + b, k1 - 1), 0);
     q[b] = ld_at<uint4>(pq + (size_t)k * kTileBytes4, 16 * lane);
     sc[b] = ld_at<Scales>(ps + (size_t)k * 64 * NS, 8 * c * NS);
   };
-  auto rows = [&](int r0) { return static_cast<const bf16*>(p.x) + (size_t)r0 * p.K; };
-  // inputs beyond K have zero weights: others of the row are read
-  auto load_few = [&] {
-    const bf16* row = rows(r0);
+  auto load_x = [&] {   // inputs beyond K have zero weights: others of the row are read
     const unsigned off = min(c & 3, cnt - 1) * (unsigned)p.K * 2 + 16 * h;
     const int k = max(min(kb + (c >> 2), k1 - 1), 0) * kTileK;
 #pragma unroll
-    for (int st = 0; st < 4; ++st) xn[st] = ld_at<uint4>(row, off + 2 * min(k + 32 * st, p.K - 32));
+    for (int st = 0; st < 4; ++st)
+      xn[st] = ld_at<uint4>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K, off + 2 * min(k + 32 * st, p.K - 32));
   };
   find();
   if (task >= tasks) return;
   at();
-  if (FEW) load_few();
+  load_x();
 #pragma unroll
   for (int b = 0; b < kUnit; ++b) load(b);
   while (task < tasks) {
-    const int mr0 = r0, mcnt = cnt, n0 = task % ntn * wt;
+    const int mr0 = r0, mcnt = cnt, n0 = task % ntn * W.wt;
+    eights = eights_next;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int mkb = k0;;) {
       const int n = k1 - mkb;   // columns from this unit on
-      const bf16* row = rows(mr0);
-      const unsigned off = min(c, mcnt - 1) * (unsigned)p.K * 2 + 16 * h;
-      auto load_x = [&](int b0) {   // columns b0 and b0 + 1
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int st = 0; st < 4; ++st)
-            x[FEW ? 0 : b][st] = ld_at<uint4>(row + min((mkb + b0 + b) * kTileK + 32 * st, p.K - 32), off);
-      };
-      if (FEW) {
-#pragma unroll
-        for (int st = 0; st < 4; ++st) x[0][st] = xn[st];
-      } else {
-        load_x(0);
-      }
+      for (int st = 0; st < 4; ++st) x[st] = xn[st];
       kb += kUnit;
       if (kb >= k1) {
         kb = k0;
         find();
         if (task < tasks) at();
       }
-      if (FEW) load_few();
+      load_x();
 #pragma unroll
       for (int b = 0; b < kUnit; ++b) {
-        const unsigned qw[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
+        uint4 f[4];
+        unpack4(q[b], eights, f);
 #pragma unroll
         for (int a = 0; a < NS; ++a) {
           f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[FEW ? 0 : b & 1][st], unpack16(qw[st]));
+          for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[st], f[st]);
           const float sf = bf16_bits(sc[b].v[a]);
-          if (FEW ? h == b && b < n : b < n)
+          if (h == b && b < n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = fmaf(sf, part[e], acc[e]);
         }
-        // (more rows: those of the third and fourth column come ahead of the next unit's numbers)
-        if (!FEW && b == 1) load_x(2);
-        if (FEW || b > 1) load(b);
-        if (!FEW && b == 1) {
-          load(0);
-          load(1);
-        }
+        load(b);
       }
       mkb += kUnit;
       if (mkb >= k1) break;
     }
-    // the waves' sums: row r of tile t is component r % 4 of lanes 16 (r / 4) + f of waves wk t .., of few rows the sum of
-    // the four quarters
-    f32x4* to = red[parity];
+    f32x4* to = red + parity * NW * 64;
     parity ^= 1;
-    to[w * 64 + lane] = acc;
+    to[threadIdx.x] = acc;
     __syncthreads();
-    for (int o = tid; o < wt * (FEW ? 64 : 256); o += kRW4 * 64) {
-      const int f = o & 15, r = FEW ? (o >> 4) & 3 : (o >> 4) & 15, t = FEW ? o >> 6 : o >> 8, ch = channel4(n0 + t, f);
-      if (r >= mcnt || n0 + t >= Nt || ch >= p.N) continue;
-      const float* rs = reinterpret_cast<const float*>(to + wk * t * 64 + (r >> 2) * 16 + f) + (r & 3);
-      float sum = 0.f;
-      for (int v = 0; v < wk; ++v)
-        sum += FEW ? (rs[v * 256] + rs[v * 256 + 64]) + (rs[v * 256 + 128] + rs[v * 256 + 192]) : rs[v * 256];
-      const size_t to_y = (size_t)(mr0 + r) * p.N + ch;
-      if (p.f32) static_cast<float*>(p.y)[to_y] = sum;
-      else static_cast<bf16*>(p.y)[to_y] = (bf16)sum;
-    }
+    store_sums<NW, 1, true>(p, to, wk, mr0, mcnt, n0, Nt);
   }
 }
 
-template <int PER>
-__global__ __launch_bounds__(kRW4 * 64, 4) void k_int4_rows(I4Params p, int wk) {
-  __shared__ f32x4 red[2][kRW4 * 64];
+template <int PER, int NW, int TL>
+__device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk) {
+  constexpr int NS = 4 / PER;
+  struct alignas(TL * NS * 2 < 16 ? TL * NS * 2 : 16) Scales { uint16_t v[TL * NS]; };
+  const Waves<NW> W(wk);
+  const int lane = W.lane, c = W.c, h = W.h;
+  const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, per = W.wt * TL, ntn = (Nt + per - 1) / per,
+            tasks = mtiles * ntn;
+  const int k0 = W.kw * Kt / wk, k1 = (W.kw + 1) * Kt / wk;
+  int task = (int)blockIdx.x - (int)gridDim.x, kb = k0, g = 0, r0 = 0, cnt = 0, nt = 0;
+  auto find = [&] {
+    do {
+      task += gridDim.x;
+      if (task >= tasks) return;
+      const int mt = task / ntn;
+      int end;
+      find_tile64<kRows4>(p, groups, mt, lane, g, r0, end);
+      cnt = min(end - r0, kRows4);
+      nt = min((task - mt * ntn) * per + W.tw * TL, Nt - TL);
+    } while (cnt <= kFew4);
+  };
+  uint4 q[TL], x[4], xn[4];
+  Scales sc, sn;
+  const uint8_t* pq;
+  const uint16_t* ps;
+  int eights, eights_next;
+  auto at = [&] {
+    const int64_t row64 = (int64_t)g * (Nt / 4) + nt / 4;
+    pq = tile_at(p.q, row64, nt % 4, Kt);
+    ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
+    eights_next = holds_8(p.q, row64, Kt);
+  };
+  auto column = [&] { return max(min(kb, k1 - 1), 0); };
+  auto load = [&](int t) { q[t] = ld_at<uint4>(pq + ((size_t)t * Kt + column()) * kTileBytes4, 16 * lane); };
+  auto load_x = [&] {
+    const bf16* row = static_cast<const bf16*>(p.x) + (size_t)r0 * p.K;
+    const unsigned off = min(c, cnt - 1) * (unsigned)p.K * 2 + 16 * h;
+#pragma unroll
+    for (int st = 0; st < 4; ++st) xn[st] = ld_at<uint4>(row + min(column() * kTileK + 32 * st, p.K - 32), off);
+    sn = ld_at<Scales>(ps + (size_t)column() * 64 * NS, 8 * c * NS);
+  };
+  find();
+  if (task >= tasks) return;
+  at();
+  load_x();
+#pragma unroll
+  for (int t = 0; t < TL; ++t) load(t);
+  while (task < tasks) {
+    const int mr0 = r0, mcnt = cnt, n0 = task % ntn * per;
+    eights = eights_next;
+    f32x4 acc[TL];
+#pragma unroll
+    for (int t = 0; t < TL; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int mkb = k0;;) {
+      const bool in = mkb < k1;   // (a wave without columns adds nothing)
+#pragma unroll
+      for (int st = 0; st < 4; ++st) x[st] = xn[st];
+      sc = sn;
+      if (++kb >= k1) {
+        kb = k0;
+        find();
+        if (task < tasks) at();
+      }
+      load_x();
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        uint4 f[4];
+        unpack4(q[t], eights, f);
+#pragma unroll
+        for (int a = 0; a < NS; ++a) {
+          f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[st], f[st]);
+          const float sf = in ? bf16_bits(sc.v[t * NS + a]) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(sf, part[e], acc[t][e]);
+        }
+        load(t);
+      }
+      if (++mkb >= k1) break;
+    }
+    __syncthreads();   // the previous task's sums are read
+#pragma unroll
+    for (int t = 0; t < TL; ++t) red[(eng::wave_id() * TL + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    store_sums<NW, TL, false>(p, red, wk, mr0, mcnt, n0, Nt);
+  }
+}
+
+template <int PER, int NW, int TL>
+__global__ __launch_bounds__(NW * 64, 4) void k_int4_rows(I4Params p, int wk) {
+  __shared__ f32x4 red[(TL > 2 ? TL : 2) * NW * 64];
   __shared__ Groups groups;
-  const int wt = kRW4 / wk, ntn = (tile_rows(p.N) + wt - 1) / wt;
-  const int tasks = group_tiles<kRows4>(p, groups) * ntn;
+  const int mtiles = group_tiles<kRows4>(p, groups);
   int parity = 0;
-  rows4_tasks<PER, true>(p, groups, red, tasks, ntn, wk, parity);
-  rows4_tasks<PER, false>(p, groups, red, tasks, ntn, wk, parity);
+  tasks_few<PER, NW>(p, groups, red, mtiles, wk, parity);
+  tasks_more<PER, NW, TL>(p, groups, red, mtiles, wk);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -336,7 +461,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
   __shared__ __attribute__((aligned(1024))) char smem[2 * ST];
   __shared__ Groups groups;
   const int lane = threadIdx.x & 63, w = eng::wave_id(), wm = w / WN, wn = w % WN, c = lane & 15, h = lane >> 4;
-  const int Nt = tile_rows(p.N), Kt = (p.K + kTileK - 1) / kTileK, nst = (p.K + 63) / 64;
+  const int R64 = rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, nst = (p.K + 63) / 64;
   const bool half = p.K % 64 != 0;             // the last stage has 32 inputs
   const int ntn = (p.N + BN - 1) / BN;
   const bool wide = p.N % NJ == 0 && reinterpret_cast<uintptr_t>(p.y) % (NJ * (p.f32 ? 4 : 2)) == 0;
@@ -369,9 +494,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
         gl2lds_at(at, min(x + 8 * j * K2, xlast) + (j & 1 ? odd : even), to + j * 1024);
     };
     const int nt = n0 / kTileN + NJ * wn, n1 = channel4(nt, c);   // the lane's channels: NJ from n1 on
-    const int ntc = min(nt, Nt - NJ);          // (a wave whose channels lie behind the last works on others, for nothing)
-    const uint8_t* qb = p.q + ((size_t)g * Nt + ntc) * Kt * kTileBytes4;
-    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at((int64_t)g * Nt, Kt, 0, channel4(ntc, 0), NS);
+    // (a wave whose channels lie behind the last works on others, for nothing)
+    const int64_t row64 = (int64_t)g * R64 + min(nt / 4, R64 - 1);
+    const uint8_t* qb = tile_at(p.q, row64, nt % 4, Kt);
+    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
+    const int eights = holds_8(p.q, row64, Kt);
     struct alignas(NJ * NS * 2 < 16 ? NJ * NS * 2 : 16) Scales {   // two a word
       unsigned w[NJ * NS / 2];
       __device__ __forceinline__ float operator[](int i) const {
@@ -394,11 +521,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     eng::block_sync();   // every wave is done reading the previous tile's stages
     issue(0);
     load(0);
+    auto columns = [&](auto with8) {           // all of K, for weights with -8 among them or not
+    auto word = [&](unsigned w) {
+      const Bytes8 v = bytes8(w);
+      if constexpr (decltype(with8)::value) return numbers8({with_8(v.a), with_8(v.b)});
+      else return numbers8(v);
+    };
+    auto unpack = [&](bool odd) {              // the stage's words of q
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      fb[0][j] = unpack16(q[j].x);
-      fb[1][j] = unpack16(q[j].y);
-    }
+      for (int j = 0; j < NJ; ++j) {
+        fb[0][j] = word(odd ? q[j].z : q[j].x);
+        fb[1][j] = word(odd ? q[j].w : q[j].y);
+      }
+    };
+    unpack(false);
     auto stage = [&](int st, auto odd) {
       constexpr int O = decltype(odd)::value;
       eng::wait_vm<0>();
@@ -441,17 +577,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
         if (u > 0) add(u - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        fb[0][j] = unpack16(O ? q[j].x : q[j].z);
-        fb[1][j] = unpack16(O ? q[j].y : q[j].w);
-      }
+      unpack(!O);
       add(MI * H - 1);
     };
     for (int kb = 0; kb < Kt; ++kb) {
       stage(2 * kb, std::integral_constant<int, 0>{});
       stage(2 * kb + 1, std::integral_constant<int, 1>{});
     }
+    };
+    if (eights) columns(std::true_type{});
+    else columns(std::false_type{});
     eng::wait_vm<0>();
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -495,13 +630,19 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
   if (p.M <= 64 || p.M <= 16 * p.G) {
-    // fewer waves a tile where their columns would make less than a unit, as long as every CU keeps two workgroups
-    const int64_t tiles = std::min<int64_t>(p.M, p.G) * tile_rows(p.N);
+    const int64_t mt = p.offsets ? p.M / kRows4 + std::min<int64_t>(p.M, p.G) : (p.M + kRows4 - 1) / kRows4;
+    const int64_t work = mt * rows64(p.N);      // of 64 channels
     const int Kt = (p.K + kTileK - 1) / kTileK;
-    int wk = kRW4;
-    while (wk > 1 && Kt < kUnit * wk && tiles * wk / kRW4 >= 4 * grid) wk /= 2;
-    const int64_t tasks = (p.M / kRows4 + std::min<int64_t>(p.M, p.G)) * ((tile_rows(p.N) * wk + kRW4 - 1) / kRW4);
-    k_int4_rows<PER><<<(unsigned)std::min<int64_t>(tasks, 2 * grid), kRW4 * 64, 0, s>>>(p, wk);
+    auto go = [&](auto kernel, int NW, int TL, int wgs) {
+      // fewer waves a task where their columns would make less than a unit, as long as every CU keeps its workgroups
+      int wk = NW;
+      while (wk > 1 && Kt < kUnit * wk && 4 * work * wk / NW >= 2 * wgs * grid) wk /= 2;
+      const int64_t tasks = (4 * work * wk + NW - 1) / NW;
+      kernel<<<(unsigned)std::min<int64_t>(tasks, wgs * grid), NW * 64, 0, s>>>(p, wk);
+    };
+    if (4 * work < 2 * grid) go(k_int4_rows<PER, 8, 1>, 8, 1, 2);
+    else if (work < 2 * grid) go(k_int4_rows<PER, 4, 1>, 4, 1, 4);
+    else go(k_int4_rows<PER, 4, 4>, 4, 4, 4);
   } else if (4 * tiles4(p, 256, 128) >= 6 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
@@ -527,8 +668,8 @@ hipError_t launch_int4_matmul(const I4Params& p, hipStream_t s) {
 hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G, int N, int K, int group, uint8_t* q,
                             void* out_scales, hipStream_t s) {
   prof_mark_begin("int4_pack", s);
-  const int64_t tiles = (int64_t)G * tile_rows(N) * ((K + kTileK - 1) / kTileK);
-  const unsigned grid = (unsigned)std::min<int64_t>((tiles + 3) / 4, 1 << 22);
+  const int64_t tiles = (int64_t)G * rows64(N);   // at most 2^23 workgroups
+  const unsigned grid = (unsigned)tiles;
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);
   if (scales) k_int4_pack<2><<<grid, 256, 0, s>>>(in, si, tiles, N, K, group, q, so);

@@ -1446,9 +1446,9 @@ moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* 
   g_last_error.clear();
   moe_status st = int4_checks(G, N, K, group);
   if (st != MOE_OK) return st;
-  const size_t tiles = (size_t)G * ((N + 63) / 64) * ((K + 127) / 128);   // of 64 channels
-  if (q_bytes) *q_bytes = tiles * 4096;
-  if (scale_bytes) *scale_bytes = tiles * 64 * (128 / group) * 2;
+  const size_t rows = (size_t)G * ((N + 63) / 64), cols = (size_t)(K + 127) / 128;   // of 64 channels, 128 inputs
+  if (q_bytes) *q_bytes = rows * (cols * 4096 + 16);
+  if (scale_bytes) *scale_bytes = rows * cols * 64 * (128 / group) * 2;
   return MOE_OK;
 }
 

@@ -459,7 +459,7 @@ def _int4_out(shape, group, like, stream):
     if group not in (32, 64, 128):
         raise ValueError(f"group: expected 32, 64 or 128, got {group}")
     rows, cols = -(-N // 64), -(-K // 128)
-    return (_empty((*lead, rows, 4, cols, 1024), torch.uint8, like, stream),
+    return (_empty((*lead, rows, 4096 * cols + 16), torch.uint8, like, stream),
             _empty((*lead, rows, cols, 64, 128 // group), torch.bfloat16, like, stream))
 
 
@@ -502,17 +502,17 @@ def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16
     needed where it is no multiple of 64 (and y is not given). A y that is given sets the dtype, and its rows outside
     the groups are left as they were (a y made here holds anything there)."""
     if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(q, torch.Tensor)
-            or q.dim() != (4 if offsets is None else 5) or not isinstance(scales, torch.Tensor)
-            or scales.dim() != q.dim()):
+            or q.dim() != (2 if offsets is None else 3) or not isinstance(scales, torch.Tensor)
+            or scales.dim() != q.dim() + 2):
         raise ValueError("expected x [M, K] and (q, scales) of a weight [N, K], or of [G, N, K] with offsets")
     dev, (M, K) = x.device, x.shape
     handle = _on(dev, stream)
     _expect(x, "x", (M, K), torch.bfloat16, dev)
-    G, rows, cols, ng = 1 if offsets is None else q.shape[0], q.shape[-4], -(-K // 128), scales.shape[-1]
+    G, rows, cols, ng = 1 if offsets is None else q.shape[0], q.shape[-2], -(-K // 128), scales.shape[-1]
     if ng not in (1, 2, 4):
         raise ValueError(f"scales: expected 1, 2 or 4 for each 128 inputs, got {ng}")
-    _expect(q, "q", (*q.shape[:-3], 4, cols, 1024), torch.uint8, dev)
-    _expect(scales, "scales", (*q.shape[:-3], cols, 64, ng), torch.bfloat16, dev)
+    _expect(q, "q", (*q.shape[:-1], 4096 * cols + 16), torch.uint8, dev)
+    _expect(scales, "scales", (*q.shape[:-1], cols, 64, ng), torch.bfloat16, dev)
     if offsets is not None:
         _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
     if N is None:

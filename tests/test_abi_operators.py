@@ -121,7 +121,7 @@ def test_int4_sizes(kw, code):
 
 
 def test_int4_arguments():
-    assert b.query_int4_sizes(3, 65, 160, 32) == (3 * 2 * 2 * 4096, 3 * 2 * 2 * 64 * 4 * 2)
+    assert b.query_int4_sizes(3, 65, 160, 32) == (3 * 2 * (2 * 4096 + 16), 3 * 2 * 2 * 64 * 4 * 2)
     refused(ARG, lambda: matmul(M=0))
     refused(SHAPE, lambda: matmul(M=1 << 31))
     refused(SHAPE, lambda: matmul(M=1 << 30, N=1 << 10))
@@ -183,7 +183,7 @@ def test_tensors_off_the_gpu_are_refused():
     calls = [lambda: layer.sort_pairs(i, 8), lambda: layer.dispatch(x, i), lambda: layer.combine(x, i),
              lambda: layer.combine_backward(x, x, torch.zeros(4, 2), i), lambda: layer.int4_quantize(x),
              lambda: layer.int4_pack(torch.zeros((4, 32), dtype=torch.int8), torch.zeros((4, 1), dtype=torch.bfloat16)),
-             lambda: layer.int4_matmul(x, torch.zeros((1, 4, 1, 1024), dtype=torch.uint8),
+             lambda: layer.int4_matmul(x, torch.zeros((1, 4112), dtype=torch.uint8),
                                        torch.zeros((1, 1, 64, 1), dtype=torch.bfloat16)),
              lambda: layer.GradNorm([x]).norm()]
     for c in calls:

@@ -20,11 +20,16 @@ def unpack(q, s, N, K):
     group = 128 // s.shape[-1]
     n, k = torch.arange(N, device=DEV)[:, None], torch.arange(K, device=DEV)[None]
     c, i, h, j = n % 64 // 4, k % 128 // 32, k % 32 // 8, k % 8
-    words = q.contiguous().view(torch.int32).long() & 0xffffffff              # [.., N / 64, 4, K / 128, 256]
+    flags = q[..., -16:].contiguous().view(torch.int32)[..., 0]              # [.., N / 64]
+    words = q[..., :-16].contiguous().view(torch.int32).long() & 0xffffffff
+    words = words.unflatten(-1, (4, -1, 256))                                # [.., N / 64, 4, K / 128, 256]
     w = words[..., n // 64, n % 4, k // 128, (16 * h + c) * 4 + i]
     m = (w >> torch.where(j < 4, 8 * j, 8 * (j - 4) + 4)) & 7
     sign = (w >> torch.where(j < 4, 8 * j + 7, (8 * (j - 4) + 11) % 32)) & 1
-    return torch.where(sign == 1, -m - 1, m), s[..., n // 64, k // 128, n % 64, (k % 128) // group]
+    v = torch.where(sign == 1, torch.where(m == 0, -8, -m), m)
+    for r in range(flags.shape[-1]):                                         # a word says whether 64 channels hold a -8
+        assert torch.equal(flags[..., r] != 0, (v[..., 64 * r:64 * r + 64, :] == -8).flatten(-2).any(-1))
+    return v, s[..., n // 64, k // 128, n % 64, (k % 128) // group]
 
 
 def quantised(w, group):
@@ -277,7 +282,7 @@ def test_wrong_tensors_are_refused():
     x = torch.zeros((4, 128), dtype=torch.bfloat16, device=DEV)
     off = torch.zeros(2, dtype=torch.int32, device=DEV)
     for call in (lambda: int4_matmul(x.float(), q, sc), lambda: int4_matmul(x[0], q, sc), lambda: int4_matmul(x[:, ::2], q, sc),
-                 lambda: int4_matmul(x, q[..., :512], sc), lambda: int4_matmul(x, q, sc[..., :1]),
+                 lambda: int4_matmul(x, q[..., :4096], sc), lambda: int4_matmul(x, q, sc[..., :1]),
                  lambda: int4_matmul(x, q, sc.float()), lambda: int4_matmul(x, q, sc, offsets=off),
                  lambda: int4_matmul(x, q[None], sc[None], offsets=off.long()), lambda: int4_matmul(x, q[None], sc[None]),
                  lambda: int4_matmul(x, q, sc, N=0), lambda: int4_matmul(x, q, sc, N=65),
