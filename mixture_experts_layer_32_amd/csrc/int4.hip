@@ -77,6 +77,20 @@ __device__ __forceinline__ unsigned pack4(int q, int j) {
 
 __device__ __forceinline__ float bf16_bits(unsigned short b) { return __uint_as_float((unsigned)b << 16); }
 
+// N bf16 scales, two a word: taken apart where they are used, so that they do not fill a register each meanwhile.
+template <int N>
+struct alignas(N * 2 < 16 ? N * 2 : 16) Scales4 {
+  unsigned w[N / 2];
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+};
+template <>
+struct Scales4<1> {
+  uint16_t v;
+  __device__ __forceinline__ float operator[](int) const { return bf16_bits(v); }
+};
+
 // KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, its wave t their tile t, a
 // tile column at a time; lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
 template <int KIND>
@@ -168,14 +182,16 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_int4_rows: persistent workgroups take tasks round-robin, first those of up to 4 rows of a group, then those of up to 16.
-// wk of the workgroup's NW waves share a task's channels and split K, and their sums meet in LDS. Behind a tile's products its
-// numbers are replaced by the next ones needed, of this task or the next, so that some are in flight all the time; no load
-// stands in a branch, where the compiler could not count those in flight.
-//   up to 4 rows   a wave takes one tile of 16 channels, in units of kUnit tile columns. As the matrix instruction's 16
-//                  rows would be mostly empty, they are 4 rows of the unit's 4 columns, and of a column's products the
-//                  quarter of the lanes counts that holds its rows.
-//   up to 16 rows  a wave takes TL tiles, a column at a time, so that a row's fragments serve TL products.
+// k_int4_rows: persistent workgroups take tasks round-robin, each up to 16 rows of a group. wk of the workgroup's NW waves
+// share a task's channels and split K, and their sums meet in LDS. Behind a tile's products its numbers are replaced by the
+// next ones needed, of this task or the next, so that some are in flight all the time; no load stands in a branch, where the
+// compiler could not count those in flight.
+//   tasks_more  a wave takes TL tiles of 16 channels, a tile column at a time, so that a row's fragments serve TL products.
+//   tasks_few   up to 4 rows where there are few tasks (TL = 1), in units of kUnit columns, which are all in flight at
+//               once. As the matrix instruction's 16 rows would be mostly empty, they are 4 rows of the unit's 4 columns, and
+//               of a column's products the quarter of the lanes counts that holds its rows. One row of 1536 x 4096
+//               5.1 us, 6.0 a column at a time; with TL = 4 the other form is as fast or faster (2 rows of 307200 x 4096
+//               117 us, 142 here).
 constexpr int kRows4 = 16, kFew4 = 4, kUnit = 4;
 
 // A load of 2 to 32 bytes from a uniform address and a lane's offset. Made in the global address space: a flat load would
@@ -247,9 +263,9 @@ __device__ __forceinline__ void store_sums(const I4Params& p, const f32x4* red, 
 }
 
 template <int PER, int NW>
-__device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk, int& parity) {
+__device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk) {
   constexpr int NS = 4 / PER;   // scales of a tile and channel
-  struct alignas(2 * NS) Scales { uint16_t v[NS]; };
+  using Scales = Scales4<NS>;
   const Waves<NW> W(wk);
   const int lane = W.lane, c = W.c, h = W.h;
   const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, ntn = (Nt + W.wt - 1) / W.wt, tasks = mtiles * ntn;
@@ -296,6 +312,7 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
   load_x();
 #pragma unroll
   for (int b = 0; b < kUnit; ++b) load(b);
+  int parity = 0;
   while (task < tasks) {
     const int mr0 = r0, mcnt = cnt, n0 = task % ntn * W.wt;
     eights = eights_next;
@@ -320,12 +337,13 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
           f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[st], f[st]);
-          const float sf = bf16_bits(sc[b].v[a]);
+          const float sf = sc[b][a];
           if (h == b && b < n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = fmaf(sf, part[e], acc[e]);
         }
         load(b);
+        __builtin_amdgcn_sched_barrier(0);   // (columns worked on at the same time take more registers than there are)
       }
       mkb += kUnit;
       if (mkb >= k1) break;
@@ -341,7 +359,7 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
 template <int PER, int NW, int TL>
 __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk) {
   constexpr int NS = 4 / PER;
-  struct alignas(TL * NS * 2 < 16 ? TL * NS * 2 : 16) Scales { uint16_t v[TL * NS]; };
+  using Scales = Scales4<TL * NS>;
   const Waves<NW> W(wk);
   const int lane = W.lane, c = W.c, h = W.h;
   const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, per = W.wt * TL, ntn = (Nt + per - 1) / per,
@@ -357,7 +375,7 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
       find_tile64<kRows4>(p, groups, mt, lane, g, r0, end);
       cnt = min(end - r0, kRows4);
       nt = min((task - mt * ntn) * per + W.tw * TL, Nt - TL);
-    } while (cnt <= kFew4);
+    } while (TL == 1 && cnt <= kFew4);
   };
   uint4 q[TL], x[4], xn[4];
   Scales sc, sn;
@@ -411,11 +429,12 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
           f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int st = a * PER; st < (a + 1) * PER; ++st) mma16<bf16>(part, x[st], f[st]);
-          const float sf = in ? bf16_bits(sc.v[t * NS + a]) : 0.f;
+          const float sf = in ? sc[t * NS + a] : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(sf, part[e], acc[t][e]);
         }
         load(t);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (++mkb >= k1) break;
     }
@@ -427,13 +446,14 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
   }
 }
 
+// workgroups of 4 waves a CU: with four scales a tile column the registers serve three
+constexpr int rows_wgs(int PER) { return PER == 1 ? 3 : 4; }
 template <int PER, int NW, int TL>
-__global__ __launch_bounds__(NW * 64, 4) void k_int4_rows(I4Params p, int wk) {
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : rows_wgs(PER)) void k_int4_rows(I4Params p, int wk) {
   __shared__ f32x4 red[(TL > 2 ? TL : 2) * NW * 64];
   __shared__ Groups groups;
   const int mtiles = group_tiles<kRows4>(p, groups);
-  int parity = 0;
-  tasks_few<PER, NW>(p, groups, red, mtiles, wk, parity);
+  if constexpr (TL == 1) tasks_few<PER, NW>(p, groups, red, mtiles, wk);
   tasks_more<PER, NW, TL>(p, groups, red, mtiles, wk);
 }
 
@@ -499,12 +519,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     const uint8_t* qb = tile_at(p.q, row64, nt % 4, Kt);
     const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
     const int eights = holds_8(p.q, row64, Kt);
-    struct alignas(NJ * NS * 2 < 16 ? NJ * NS * 2 : 16) Scales {   // two a word
-      unsigned w[NJ * NS / 2];
-      __device__ __forceinline__ float operator[](int i) const {
-        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-      }
-    };
+    using Scales = Scales4<NJ * NS>;
     uint4 q[NJ], fb[2][NJ];
     Scales sc, sn;
     auto load = [&](int kb) {                  // (behind the last tile: read once more, and not used)
@@ -640,9 +655,9 @@ void launch4(const I4Params& p, int grid, hipStream_t s) {
       const int64_t tasks = (4 * work * wk + NW - 1) / NW;
       kernel<<<(unsigned)std::min<int64_t>(tasks, wgs * grid), NW * 64, 0, s>>>(p, wk);
     };
-    if (4 * work < 2 * grid) go(k_int4_rows<PER, 8, 1>, 8, 1, 2);
-    else if (work < 2 * grid) go(k_int4_rows<PER, 4, 1>, 4, 1, 4);
-    else go(k_int4_rows<PER, 4, 4>, 4, 4, 4);
+    if (4 * work < 2 * grid) go(k_int4_rows<PER, 8, 1>, 8, 1, 1);
+    else if (work < 2 * grid) go(k_int4_rows<PER, 4, 1>, 4, 1, rows_wgs(PER));
+    else go(k_int4_rows<PER, 4, 4>, 4, 4, rows_wgs(PER));
   } else if (4 * tiles4(p, 256, 128) >= 6 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
