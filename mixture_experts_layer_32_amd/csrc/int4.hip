@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_int4_rows: persistent workgroups take tasks round-robin, each up to 16 rows of a group. wk of the workgroup's NW waves
+// k_int4_rows: persistent workgroups take tasks round-robin, each up to 16 rows of a group. wk of the workgroup's waves
 // share a task's channels and split K, and their sums meet in LDS. Behind a tile's products its numbers are replaced by the
 // next ones needed, of this task or the next, so that some are in flight all the time; no load stands in a branch, where the
 // compiler could not count those in flight.
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
 //               of a column's products the quarter of the lanes counts that holds its rows. One row of 1536 x 4096
 //               5.1 us, 6.0 a column at a time; with TL = 4 the other form is as fast or faster (2 rows of 307200 x 4096
 //               117 us, 142 here).
-constexpr int kRows4 = 16, kFew4 = 4, kUnit = 4;
+constexpr int kRows4 = 16, kFew4 = 4, kUnit = 4, kRowWaves = 4;
 
 // A load of 2 to 32 bytes from a uniform address and a lane's offset. Made in the global address space: a flat load would
 // wait for LDS as well, and for all loads before it.
@@ -232,24 +232,23 @@ __device__ __forceinline__ void find_tile64(const I4Params& p, const Groups& s, 
 }
 
 // Where the waves of a task are: those of the workgroup, wk to a task.
-template <int NW>
 struct Waves {
   int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4, wk, kw, tw, wt;
   __device__ __forceinline__ explicit Waves(int wk) : wk(wk) {
     const int w = eng::wave_id();
     kw = w % wk;
     tw = w / wk;
-    wt = NW / wk;
+    wt = kRowWaves / wk;
   }
 };
 
 // The sums of the task's wk waves in LDS for each of TL tiles, as stored by lanes 16 h + c: rows 4 h .. 4 h + 3 of
 // channel c (FEW: rows 0 .. 3, a quarter of the sum). They are added and stored to y from row r0 on, cnt rows, and channels
 // of the tiles from nt on.
-template <int NW, int TL, bool FEW>
+template <int TL, bool FEW>
 __device__ __forceinline__ void store_sums(const I4Params& p, const f32x4* red, int wk, int64_t r0, int cnt, int nt, int ntiles) {
   constexpr int ROWS = FEW ? 4 : 16;
-  for (int o = threadIdx.x; o < NW / wk * TL * 16 * ROWS; o += NW * 64) {
+  for (int o = threadIdx.x; o < kRowWaves / wk * TL * 16 * ROWS; o += kRowWaves * 64) {
     const int f = o & 15, r = (o >> 4) % ROWS, t = o / (16 * ROWS), n = channel4(nt + t, f);
     if (r >= cnt || nt + t >= ntiles || n >= p.N) continue;
     // wave (t / TL) wk + v holds tile t % TL
@@ -262,11 +261,11 @@ __device__ __forceinline__ void store_sums(const I4Params& p, const f32x4* red, 
   }
 }
 
-template <int PER, int NW>
+template <int PER>
 __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk) {
   constexpr int NS = 4 / PER;   // scales of a tile and channel
   using Scales = Scales4<NS>;
-  const Waves<NW> W(wk);
+  const Waves W(wk);
   const int lane = W.lane, c = W.c, h = W.h;
   const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, ntn = (Nt + W.wt - 1) / W.wt, tasks = mtiles * ntn;
   const int k0 = W.kw * Kt / wk, k1 = (W.kw + 1) * Kt / wk;   // the wave's tile columns
@@ -348,19 +347,19 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
       mkb += kUnit;
       if (mkb >= k1) break;
     }
-    f32x4* to = red + parity * NW * 64;
+    f32x4* to = red + parity * kRowWaves * 64;
     parity ^= 1;
     to[threadIdx.x] = acc;
     __syncthreads();
-    store_sums<NW, 1, true>(p, to, wk, mr0, mcnt, n0, Nt);
+    store_sums<1, true>(p, to, wk, mr0, mcnt, n0, Nt);
   }
 }
 
-template <int PER, int NW, int TL>
+template <int PER, int TL>
 __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& groups, f32x4* red, int mtiles, int wk) {
   constexpr int NS = 4 / PER;
   using Scales = Scales4<TL * NS>;
-  const Waves<NW> W(wk);
+  const Waves W(wk);
   const int lane = W.lane, c = W.c, h = W.h;
   const int Nt = 4 * rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK, per = W.wt * TL, ntn = (Nt + per - 1) / per,
             tasks = mtiles * ntn;
@@ -442,19 +441,19 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
 #pragma unroll
     for (int t = 0; t < TL; ++t) red[(eng::wave_id() * TL + t) * 64 + lane] = acc[t];
     __syncthreads();
-    store_sums<NW, TL, false>(p, red, wk, mr0, mcnt, n0, Nt);
+    store_sums<TL, false>(p, red, wk, mr0, mcnt, n0, Nt);
   }
 }
 
-// workgroups of 4 waves a CU: with four scales a tile column the registers serve three
+// workgroups a CU: with four scales a tile column the registers serve three
 constexpr int rows_wgs(int PER) { return PER == 1 ? 3 : 4; }
-template <int PER, int NW, int TL>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : rows_wgs(PER)) void k_int4_rows(I4Params p, int wk) {
-  __shared__ f32x4 red[(TL > 2 ? TL : 2) * NW * 64];
+template <int PER, int TL>
+__global__ __launch_bounds__(kRowWaves * 64, rows_wgs(PER)) void k_int4_rows(I4Params p, int wk) {
+  __shared__ f32x4 red[(TL > 2 ? TL : 2) * kRowWaves * 64];
   __shared__ Groups groups;
   const int mtiles = group_tiles<kRows4>(p, groups);
-  if constexpr (TL == 1) tasks_few<PER, NW>(p, groups, red, mtiles, wk);
-  tasks_more<PER, NW, TL>(p, groups, red, mtiles, wk);
+  if constexpr (TL == 1) tasks_few<PER>(p, groups, red, mtiles, wk);
+  tasks_more<PER, TL>(p, groups, red, mtiles, wk);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -642,25 +641,32 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
   return std::min<int64_t>(m, p.M) * ((p.N + bn - 1) / bn);
 }
 
+// The kernel by the rows of a group that has any, as far as the host knows, and by how much work there is.
+// Rows kernel, us, against the best tiles: 2048 rows in 64 groups of 1536 x 4096 76 and 104, 4096 rows 150 and 109; 128 rows of
+// 4096 x 4096 16 and 21, 256 rows 28 and 30, 512 rows 50 and 35. TL = 4 against 1: one row of 4096 x 4096 9.3 and 5.0,
+// of 32768 x 4096 14 and 17; 16 rows of 4096 x 4096 9.5 and 7.9, 32 rows 9.7 and 12.4.
+// Tiles of 256 x 128, 128 x 128 and 64 x 64, us: 16384 rows of 2048 x 768 in 64 groups 63, 69, 138; 8192 rows of 1536 x 4096 in 64
+// groups 224, 135, 285, 4096 rows 198, 111, 109; 1024 rows of 4096 x 4096 73, 49, 67, 512 rows 70, 44, 35.
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
-  if (p.M <= 64 || p.M <= 16 * p.G) {
-    const int64_t mt = p.offsets ? p.M / kRows4 + std::min<int64_t>(p.M, p.G) : (p.M + kRows4 - 1) / kRows4;
-    const int64_t work = mt * rows64(p.N);      // of 64 channels
-    const int Kt = (p.K + kTileK - 1) / kTileK;
-    auto go = [&](auto kernel, int NW, int TL, int wgs) {
+  const int64_t groups = std::min<int64_t>(p.M, p.G);
+  const int64_t mt = p.offsets ? p.M / kRows4 + groups : (p.M + kRows4 - 1) / kRows4;
+  const int64_t work = mt * rows64(p.N);        // 16 rows by 64 channels
+  const int Kt = (p.K + kTileK - 1) / kTileK;
+  if (p.M <= 32 * groups || work <= 2 * grid) {
+    auto go = [&](auto kernel, int TL) {
       // fewer waves a task where their columns would make less than a unit, as long as every CU keeps its workgroups
-      int wk = NW;
-      while (wk > 1 && Kt < kUnit * wk && 4 * work * wk / NW >= 2 * wgs * grid) wk /= 2;
-      const int64_t tasks = (4 * work * wk + NW - 1) / NW;
-      kernel<<<(unsigned)std::min<int64_t>(tasks, wgs * grid), NW * 64, 0, s>>>(p, wk);
+      const int64_t wgs = rows_wgs(PER) * grid;
+      int wk = kRowWaves;
+      while (wk > 1 && Kt < kUnit * wk && 4 * work * wk / kRowWaves >= 2 * wgs) wk /= 2;
+      const int64_t tasks = (4 * work * wk / TL + kRowWaves - 1) / kRowWaves;
+      kernel<<<(unsigned)std::min(tasks, wgs), kRowWaves * 64, 0, s>>>(p, wk);
     };
-    if (4 * work < 2 * grid) go(k_int4_rows<PER, 8, 1>, 8, 1, 1);
-    else if (work < 2 * grid) go(k_int4_rows<PER, 4, 1>, 4, 1, rows_wgs(PER));
-    else go(k_int4_rows<PER, 4, 4>, 4, 4, rows_wgs(PER));
-  } else if (4 * tiles4(p, 256, 128) >= 6 * grid) {
+    if (work <= (p.M <= kFew4 * groups ? grid : 3 * grid / 8)) go(k_int4_rows<PER, 1>, 1);
+    else go(k_int4_rows<PER, 4>, 4);
+  } else if (p.M >= 192 * groups && 4 * tiles4(p, 256, 128) >= 6 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
-  } else if (4 * tiles4(p, 128, 128) >= 3 * grid) {
+  } else if (p.M >= 72 * groups && 4 * tiles4(p, 128, 128) >= 3 * grid) {
     k_int4_tile<4, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
   } else {
     k_int4_tile<2, 2, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
