@@ -139,13 +139,13 @@ def ptr(t):
 
 
 def _stream(stream):
+    if type(stream) is int:
+        return stream
     if stream is None:
         import torch
         # the current stream's handle without the Stream object, whose making takes 2.7 us a call
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    if isinstance(stream, int):
-        return stream
-    return stream.cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def version():

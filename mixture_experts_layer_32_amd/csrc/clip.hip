@@ -6,8 +6,9 @@
 //   k_root    norm = sqrt(sum of the partial sums).
 //   k_scale   out = c g, c = min(1, max_norm / (norm + 1e-6)); with the norm given, or from the partial sums, which
 //             every workgroup then adds up for itself (one launch less).
-// The tensors' addresses and sizes travel in the launch's arguments, kTable (kPair with outputs) tensors a launch.
+// The tensors' addresses and sizes travel in the launch's arguments, kTable (with outputs kPair) tensors a launch.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -16,29 +17,31 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 8192;    // elements
-constexpr int kTable = 160;     // 160 * 20 bytes: within the 4 KiB of a launch's arguments
-constexpr int kPair = 120;
+constexpr int kTable = 184;     // 184 * 20 bytes: within the 4 KiB of a launch's arguments
+constexpr int kPair = 128;
 
-struct NormTable {
-  const void* src[kTable];
-  int64_t n[kTable];
-  int first[kTable + 1];        // first chunk of each tensor, then their number
-  unsigned f32[kTable / 32];
+struct Table {                  // the norm's tensors, and those scaled in place
+  static constexpr int MAX = kTable;
+  const void* src[MAX];
+  int64_t n[MAX];
+  int first[MAX + 1];           // first chunk of each tensor, then their number
+  unsigned f32[(MAX + 31) / 32];
   int count;
 };
-struct ScaleTable {
-  const void* src[kPair];
-  void* dst[kPair];
-  int64_t n[kPair];
-  int first[kPair + 1];
-  unsigned f32[(kPair + 31) / 32], d32[(kPair + 31) / 32];
+struct PairTable {              // tensors and outputs
+  static constexpr int MAX = kPair;
+  const void* src[MAX];
+  void* dst[MAX];
+  int64_t n[MAX];
+  int first[MAX + 1];
+  unsigned f32[(MAX + 31) / 32], d32[(MAX + 31) / 32];
   int count;
 };
-static_assert(sizeof(NormTable) <= 3800 && sizeof(ScaleTable) <= 3800, "launch arguments");
+static_assert(sizeof(Table) <= 3900 && sizeof(PairTable) <= 3900, "launch arguments");
 
 // the tensor that chunk c lies in
-template <class Table>
-__device__ __forceinline__ int tensor_of(const Table& a, int c) {
+template <class T>
+__device__ __forceinline__ int tensor_of(const T& a, int c) {
   int lo = 0, hi = a.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -93,7 +96,7 @@ __device__ __forceinline__ double block_sum(double s, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-__global__ __launch_bounds__(256) void k_norm(NormTable a, double* part) {
+__global__ __launch_bounds__(256) void k_norm(Table a, double* part) {
   __shared__ double lds[4];
   const int C = a.first[a.count];
   const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
@@ -148,8 +151,10 @@ __device__ __forceinline__ void scale_chunk(const S* p, D* o, int m, float c) {
   for (int t = h + nv * V + tid; t < m; t += 256) o[t] = (D)(c * (float)p[t]);
 }
 
-__global__ __launch_bounds__(256) void k_scale(ScaleTable a, float max_norm, const float* norm_in, const double* part,
-                                               int64_t parts, float* norm_out) {
+template <class T>
+__global__ __launch_bounds__(256) void k_scale(T a, float max_norm, const float* norm_in, const double* part, int64_t parts,
+                                               float* norm_out) {
+  constexpr bool PAIRS = std::is_same_v<T, PairTable>;
   __shared__ double lds[4];
   float norm;
   if (norm_in) {
@@ -160,25 +165,31 @@ __global__ __launch_bounds__(256) void k_scale(ScaleTable a, float max_norm, con
   }
   float c = max_norm / (norm + 1e-6f);
   c = c > 1.f ? 1.f : c;                       // NaN stays
+  if (!PAIRS && c == 1.f) return;              // in place: nothing changes
   const int C = a.first[a.count];
   const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
-  if (c0 >= c1) return;
   int i = tensor_of(a, c0);
   for (int b = c0; b < c1; ++b) {
     while (b >= a.first[i + 1]) ++i;
-    if (c == 1.f && a.src[i] == a.dst[i] && bit(a.f32, i) == bit(a.d32, i)) continue;   // in place: nothing changes
+    const void* dst = a.src[i];
+    bool f32 = bit(a.f32, i), d32 = f32;
+    if constexpr (PAIRS) {
+      dst = a.dst[i];
+      d32 = bit(a.d32, i);
+      if (c == 1.f && dst == a.src[i]) continue;
+    }
     const int64_t at = (int64_t)(b - a.first[i]) * kChunk;
     const int m = (int)min((int64_t)kChunk, a.n[i] - at);
     const float* pf = static_cast<const float*>(a.src[i]) + at;
     const bf16* pb = static_cast<const bf16*>(a.src[i]) + at;
-    float* of = static_cast<float*>(a.dst[i]) + at;
-    bf16* ob = static_cast<bf16*>(a.dst[i]) + at;
-    if (bit(a.f32, i)) {
-      if (bit(a.d32, i)) scale_chunk(pf, of, m, c);
-      else scale_chunk(pf, ob, m, c);
+    float* of = static_cast<float*>(const_cast<void*>(dst)) + at;
+    bf16* ob = static_cast<bf16*>(const_cast<void*>(dst)) + at;
+    if (f32) {
+      if (d32) scale_chunk(pf, of, m, c);
+      else if constexpr (PAIRS) scale_chunk(pf, ob, m, c);
     } else {
-      if (bit(a.d32, i)) scale_chunk(pb, of, m, c);
-      else scale_chunk(pb, ob, m, c);
+      if (!d32) scale_chunk(pb, ob, m, c);
+      else if constexpr (PAIRS) scale_chunk(pb, of, m, c);
     }
   }
 }
@@ -188,12 +199,12 @@ int parts_of(int C) { return std::min(C, kNormParts); }
 
 // The next tensors from `from` on, at most MAX and as many as hold fewer than 2^31 chunks together; empty ones are
 // passed over. Returns where to go on.
-template <class Table, int MAX>
-int fill(Table& a, const moe_tensor* t, const moe_tensor* out, int count, int from) {
+template <class T>
+int fill(T& a, const moe_tensor* t, const moe_tensor* out, int count, int from) {
   a.count = 0;
   a.first[0] = 0;
   int i = from;
-  for (; i < count && a.count < MAX; ++i) {
+  for (; i < count && a.count < T::MAX; ++i) {
     if (t[i].n == 0) continue;
     const int k = a.count++;
     if (k % 32 == 0) a.f32[k / 32] = 0;
@@ -201,24 +212,44 @@ int fill(Table& a, const moe_tensor* t, const moe_tensor* out, int count, int fr
     a.n[k] = t[i].n;
     a.first[k + 1] = a.first[k] + chunks(t[i].n);
     if (t[i].type == MOE_TYPE_FP32) a.f32[k / 32] |= 1u << (k % 32);
-    if constexpr (MAX == kPair) {
-      const moe_tensor& o = out ? out[i] : t[i];
+    if constexpr (std::is_same_v<T, PairTable>) {
       if (k % 32 == 0) a.d32[k / 32] = 0;
-      a.dst[k] = o.data;
-      if (o.type == MOE_TYPE_FP32) a.d32[k / 32] |= 1u << (k % 32);
+      a.dst[k] = out[i].data;
+      if (out[i].type == MOE_TYPE_FP32) a.d32[k / 32] |= 1u << (k % 32);
     }
   }
   return i;
 }
 
+template <class T>
+hipError_t scale_all(const moe_tensor* t, const moe_tensor* out, int count, float max_norm, const float* norm_in,
+                     const double* part, int64_t parts, float* norm_out, hipStream_t s) {
+  hipError_t err;
+  T a;
+  for (int i = 0; i < count;) {
+    i = fill(a, t, out, count, i);
+    const int grid = parts_of(a.first[a.count]);
+    if (grid == 0) continue;
+    prof_mark_begin("grad_clip", s);
+    k_scale<T><<<grid, 256, 0, s>>>(a, max_norm, norm_in, part, parts, norm_out);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+    norm_out = nullptr;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
-int64_t norm_parts(const moe_tensor* t, int count) {
+int64_t norm_parts(const moe_tensor* t, int count) {   // as launch_grad_norm cuts them
   int64_t parts = 0;
-  NormTable a;
   for (int i = 0; i < count;) {
-    i = fill<NormTable, kTable>(a, t, nullptr, count, i);
-    parts += parts_of(a.first[a.count]);
+    int chunk = 0;
+    for (int k = 0; i < count && k < Table::MAX; ++i) {
+      chunk += chunks(t[i].n);
+      k += t[i].n > 0;
+    }
+    parts += parts_of(chunk);
   }
   return parts;
 }
@@ -226,9 +257,9 @@ int64_t norm_parts(const moe_tensor* t, int count) {
 hipError_t launch_grad_norm(const moe_tensor* t, int count, double* part, float* norm, hipStream_t s) {
   hipError_t err;
   int64_t parts = 0;
-  NormTable a;
+  Table a;
   for (int i = 0; i < count;) {
-    i = fill<NormTable, kTable>(a, t, nullptr, count, i);
+    i = fill(a, t, nullptr, count, i);
     const int grid = parts_of(a.first[a.count]);
     if (grid == 0) continue;
     prof_mark_begin("grad_norm", s);
@@ -246,19 +277,8 @@ hipError_t launch_grad_norm(const moe_tensor* t, int count, double* part, float*
 
 hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int count, float max_norm, const float* norm_in,
                             const double* part, int64_t parts, float* norm_out, hipStream_t s) {
-  hipError_t err;
-  ScaleTable a;
-  for (int i = 0; i < count;) {
-    i = fill<ScaleTable, kPair>(a, t, out, count, i);
-    const int grid = parts_of(a.first[a.count]);
-    if (grid == 0) continue;
-    prof_mark_begin("grad_clip", s);
-    k_scale<<<grid, 256, 0, s>>>(a, max_norm, norm_in, part, parts, norm_out);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-    prof_mark_end(s);
-    norm_out = nullptr;
-  }
-  return hipSuccess;
+  return out ? scale_all<PairTable>(t, out, count, max_norm, norm_in, part, parts, norm_out, s)
+             : scale_all<Table>(t, nullptr, count, max_norm, norm_in, part, parts, norm_out, s);
 }
 
 }  // namespace moe

@@ -1520,12 +1520,12 @@ moe_status tensors_checks(const moe_tensor* t, int count, const char* name) {
   if (count > 0 && !t) return fail(MOE_ERR_INVALID_ARG, std::string(name) + " is null");
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
-    moe_status st;
-    const std::string which = std::string(name) + "[" + std::to_string(i) + "]";
-    if (t[i].type != MOE_TYPE_FP32 && t[i].type != MOE_TYPE_BF16) return fail(MOE_ERR_UNSUPPORTED_MODE, which + ": unknown type");
-    if (t[i].n < 0) return fail(MOE_ERR_INVALID_ARG, which + ": negative size");
+    // (names only for errors: hundreds of strings would take longer than the launches)
+    auto which = [&] { return std::string(name) + "[" + std::to_string(i) + "]"; };
+    if (t[i].type != MOE_TYPE_FP32 && t[i].type != MOE_TYPE_BF16) return fail(MOE_ERR_UNSUPPORTED_MODE, which() + ": unknown type");
+    if (t[i].n < 0) return fail(MOE_ERR_INVALID_ARG, which() + ": negative size");
     if (t[i].n == 0) continue;
-    if ((st = check_ptrs({{t[i].data, which.c_str()}}, elem_size(t[i].type))) != MOE_OK) return st;
+    if (!t[i].data || !aligned(t[i].data, elem_size(t[i].type))) return check_ptrs({{t[i].data, which().c_str()}}, elem_size(t[i].type));
     if (t[i].n >= (int64_t(1) << 40) || (total += t[i].n) >= (int64_t(1) << 40))
       return fail(MOE_ERR_UNSUPPORTED_SHAPE, "the tensors must hold less than 2^40 elements");
   }
