@@ -17,6 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kChunk = 8192;    // elements
+constexpr int kScaleBlocks = 1024;
 constexpr int kTable = 184;     // 184 * 20 bytes: within the 4 KiB of a launch's arguments
 constexpr int kPair = 128;
 
@@ -78,7 +79,7 @@ __device__ __forceinline__ void sq_chunk(const T* p, int m, double& s) {
   }
   const uint4* v = reinterpret_cast<const uint4*>(p + h);
 #pragma unroll 4
-  for (int i = tid; i < nv; i += 256) add_sq<T>(v[i], s);
+  for (int i = tid; i < nv; i += 256) add_sq<T>(ld16_nt(v + i), s);
   const int t = h + nv * V + tid;
   if (t < m) {
     const double d = (double)(float)p[t];
@@ -135,18 +136,23 @@ __device__ __forceinline__ void scale_chunk(const S* p, D* o, int m, float c) {
   const int nv = vec ? (m - h) / V : 0;
   if (!vec) h = 0;
   if (tid < h) o[tid] = (D)(c * (float)p[tid]);
-#pragma unroll 2
-  for (int i = tid; i < nv; i += 256) {
-    alignas(16) S v[V];
-    alignas(16) D w[V];
+  constexpr int U = 4, LB = V * (int)sizeof(S) / 16, SB = V * (int)sizeof(D) / 16;
+  for (int i0 = tid; i0 < nv; i0 += U * 256) {
+    uint4 v[U][LB];
 #pragma unroll
-    for (int b = 0; b < V * (int)sizeof(S) / 16; ++b)
-      reinterpret_cast<uint4*>(v)[b] = ld16(reinterpret_cast<const char*>(p + h + (size_t)i * V) + 16 * b);
+    for (int u = 0; u < U; ++u)
+      if (i0 + 256 * u < nv)
 #pragma unroll
-    for (int e = 0; e < V; ++e) w[e] = (D)(c * (float)v[e]);
+        for (int b = 0; b < LB; ++b) v[u][b] = ld16_nt(reinterpret_cast<const uint4*>(p + h) + (i0 + 256 * u) * LB + b);
 #pragma unroll
-    for (int b = 0; b < V * (int)sizeof(D) / 16; ++b)
-      st16(reinterpret_cast<char*>(o + h + (size_t)i * V) + 16 * b, reinterpret_cast<uint4*>(w)[b]);
+    for (int u = 0; u < U; ++u)
+      if (i0 + 256 * u < nv) {
+        uint4 w[SB];
+#pragma unroll
+        for (int e = 0; e < V; ++e) reinterpret_cast<D*>(w)[e] = (D)(c * (float)reinterpret_cast<const S*>(v[u])[e]);
+#pragma unroll
+        for (int b = 0; b < SB; ++b) st16_nt(reinterpret_cast<uint4*>(o + h) + (i0 + 256 * u) * SB + b, w[b]);
+      }
   }
   for (int t = h + nv * V + tid; t < m; t += 256) o[t] = (D)(c * (float)p[t]);
 }
@@ -168,9 +174,9 @@ __global__ __launch_bounds__(256) void k_scale(T a, float max_norm, const float*
   if (!PAIRS && c == 1.f) return;              // in place: nothing changes
   const int C = a.first[a.count];
   const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
-  int i = tensor_of(a, c0);
-  for (int b = c0; b < c1; ++b) {
-    while (b >= a.first[i + 1]) ++i;
+  int i = tensor_of(a, C - 1 - (int)blockIdx.x);
+  for (int b = C - 1 - (int)blockIdx.x; b >= 0; b -= gridDim.x) {
+    while (b < a.first[i]) --i;
     const void* dst = a.src[i];
     bool f32 = bit(a.f32, i), d32 = f32;
     if constexpr (PAIRS) {
@@ -231,7 +237,7 @@ hipError_t scale_all(const moe_tensor* t, const moe_tensor* out, int count, floa
     const int grid = parts_of(a.first[a.count]);
     if (grid == 0) continue;
     prof_mark_begin("grad_clip", s);
-    k_scale<T><<<grid, 256, 0, s>>>(a, max_norm, norm_in, part, parts, norm_out);
+    k_scale<T><<<std::min(grid, kScaleBlocks), 256, 0, s>>>(a, max_norm, norm_in, part, parts, norm_out);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     prof_mark_end(s);
     norm_out = nullptr;
