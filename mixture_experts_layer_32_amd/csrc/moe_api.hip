@@ -1274,6 +1274,8 @@ SortLayout sort_layout(int64_t pairs, int El) {
   if (pairs <= kSortSmall) return L;
   L.nblk = (int)((pairs + kSortPairs - 1) / kSortPairs);
   const size_t cells = (size_t)L.nblk * (El + 1) * 4;
+  L.total = align256(cells);
+  if (L.nblk <= kSortBlocks) return L;
   L.prefix = align256(cells);
   L.total_off = L.prefix + align256(cells);
   L.total = L.total_off + align256((size_t)(El + 1) * 4);
@@ -1332,8 +1334,8 @@ moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int ex
   p.nblk = L.nblk;
   if (L.total > 0) {
     p.cnt = reinterpret_cast<int*>(w);
-    p.prefix = reinterpret_cast<int*>(w + L.prefix);
-    p.total = reinterpret_cast<int*>(w + L.total_off);
+    p.prefix = L.prefix ? reinterpret_cast<int*>(w + L.prefix) : nullptr;
+    p.total = L.prefix ? reinterpret_cast<int*>(w + L.total_off) : nullptr;
   }
   const hipError_t e = launch_sort_pairs(p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "sort launch");

@@ -247,11 +247,12 @@ hipError_t launch_int8_matmul(const I8Params& p, int grid, const char* name, hip
 struct SortParams {
   const int* idx;
   int *offsets, *perm, *pair_pos;
-  int *cnt, *prefix, *total;   // workspace: [nblk][El + 1], [nblk][El + 1], [El + 1]
+  int *cnt, *prefix, *total;   // workspace: [nblk][El + 1], and for many blocks [nblk][El + 1], [El + 1] (else null)
   int64_t pairs;
   int El, e0, nblk;
 };
 constexpr int kSortPairs = 2048;         // pairs of a workgroup
+constexpr int kSortBlocks = 128;         // up to here each workgroup adds up all blocks' counts by itself
 constexpr int kSortSmall = 4096;         // up to here one workgroup sorts them all, without a workspace
 hipError_t launch_sort_pairs(const SortParams& p, hipStream_t s);
 struct PairsParams {

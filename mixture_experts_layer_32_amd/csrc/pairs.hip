@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kSW * 64) void k_sort_small(SortParams p) {
     if (i < rounds) place(p, (w * rounds + i) * 64 + (tid & 63), e[i], cnt[w], tot[p.El]);
 }
 
-constexpr int kCW = 4;    // waves of a block of kSortPairs pairs
+constexpr int kCW = 8;    // waves of a block of kSortPairs pairs
 constexpr int kCP = kSortPairs / (64 * kCW);   // pairs of a lane: kCP w + i of 64 each, all loaded at once
 __device__ __forceinline__ void load_experts(const SortParams& p, int64_t q0, int (&e)[kCP]) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -172,21 +172,51 @@ __global__ __launch_bounds__(256) void k_sort_scan(SortParams p) {
 
 __global__ __launch_bounds__(kCW * 64) void k_sort_place(SortParams p) {
   __shared__ int cnt[kCW][kMaxExperts + 1];
-  __shared__ int tot[kMaxExperts + 1];
+  __shared__ int tot[kMaxExperts + 1], pre[kMaxExperts + 1];
+  __shared__ int2 part[kCW][64];
   __shared__ int lds[kCW];
   const int tid = threadIdx.x, w = tid >> 6, nb = p.El + 1;
   const int64_t q0 = (int64_t)blockIdx.x * kSortPairs;
   int e[kCP];
   load_experts(p, q0, e);
+  if (p.prefix) {
+    for (int i = tid; i < nb; i += kCW * 64) {
+      tot[i] = p.total[i];
+      pre[i] = p.prefix[(size_t)blockIdx.x * nb + i];
+    }
+  } else {
+    // few blocks: their counts added up here, a quarter of the blocks by each wave
+    for (int i0 = 0; i0 < nb; i0 += 64) {
+      const int i = min(i0 + (tid & 63), nb - 1);
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int b = w; b < p.nblk; b += kCW) {
+        const int c = p.cnt[(size_t)b * nb + i];
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
+      }
+      part[w][tid & 63] = make_int2(all, before);
+      __syncthreads();
+      if (tid < 64 && i0 + tid < nb) {
+        int2 s = part[0][tid];
+        for (int v = 1; v < kCW; ++v) {
+          s.x += part[v][tid].x;
+          s.y += part[v][tid].y;
+        }
+        tot[i0 + tid] = s.x;
+        pre[i0 + tid] = s.y;
+      }
+      __syncthreads();
+    }
+  }
   for (int i = tid; i < kCW * nb; i += kCW * 64) cnt[i / nb][i % nb] = 0;
-  for (int i = tid; i < nb; i += kCW * 64) tot[i] = p.total[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kCP; ++i)
     if (e[i] >= 0) atomicAdd(&cnt[w][e[i]], 1);
   scan_bins<kCW * 64>(tot, nb, lds);   // (its barriers stand behind the counts too)
   for (int i = tid; i < nb; i += kCW * 64) {
-    int s = tot[i] + p.prefix[(size_t)blockIdx.x * nb + i];
+    int s = tot[i] + pre[i];
     for (int v = 0; v < kCW; ++v) {
       const int c = cnt[v][i];
       cnt[v][i] = s;
@@ -578,10 +608,12 @@ hipError_t launch_sort_pairs(const SortParams& p, hipStream_t s) {
   k_sort_count<<<p.nblk, kCW * 64, 0, s>>>(p);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   prof_mark_end(s);
-  prof_mark_begin("sort_scan", s);
-  k_sort_scan<<<p.El + 1, 256, 0, s>>>(p);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
-  prof_mark_end(s);
+  if (p.prefix) {
+    prof_mark_begin("sort_scan", s);
+    k_sort_scan<<<p.El + 1, 256, 0, s>>>(p);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    prof_mark_end(s);
+  }
   prof_mark_begin("sort_place", s);
   k_sort_place<<<p.nblk, kCW * 64, 0, s>>>(p);
   if ((err = hipGetLastError()) != hipSuccess) return err;

@@ -48,7 +48,7 @@ def choose(T, k, E, seed, drop=0.0, zipf=0.0):
 @pytest.mark.parametrize("T,k,E,El,e0", [
     (1, 1, 1, 1, 0), (1, 8, 128, 128, 0), (8, 8, 128, 128, 0), (63, 3, 5, 5, 0), (64, 1, 512, 512, 0),
     (511, 8, 64, 64, 0), (512, 8, 128, 16, 16), (513, 8, 128, 128, 0), (4096, 1, 512, 512, 0), (4097, 1, 7, 3, 2),
-    (2731, 3, 100, 100, 0), (1333, 6, 128, 16, 112), (16384, 8, 128, 128, 0), (300, 32, 512, 512, 0),
+    (2731, 3, 100, 100, 0), (1333, 6, 128, 16, 112), (16384, 8, 128, 128, 0), (300, 32, 512, 512, 0), (32768, 8, 40, 40, 0), (32769, 8, 300, 200, 50),
     (70001, 2, 300, 257, 43),
 ])
 def test_sort(T, k, E, El, e0):
