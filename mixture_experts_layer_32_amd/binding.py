@@ -125,17 +125,13 @@ def lib():
 
 
 def _check(status):
-    if status != 0:
+    if status:
         raise MoEError(status, lib().moe_last_error().decode())
 
 
 def ptr(t):
     """Device (or host) address of a tensor, an int address, or None (NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or type(t) is int else t.data_ptr()
 
 
 def _stream(stream):

@@ -18,7 +18,7 @@ from . import binding
 def _expect(t, name, shape, dtype, device):
     """Raises ValueError unless t is a contiguous tensor of this shape and dtype on this device: the
     C ABI receives bare pointers and cannot check any of it."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
@@ -48,10 +48,12 @@ def _empty(shape, dtype, like, stream):
     """A new output for a call on `stream`, on the device of the tensor `like`, from that stream's memory: memory of
     the current stream may still be written by work of its own."""
     if stream is None:
-        # the cheapest of torch's calls for it: 1.1 us against 1.6 of torch.empty
-        if like.dtype == dtype:
-            return torch.empty_like(like) if like.shape == shape else like.new_empty(*shape) if shape else like.new_empty(shape)
-        return torch.empty_like(like, dtype=dtype) if like.shape == shape else like.new_empty(shape, dtype=dtype)
+        # the cheapest of torch's calls for it: 1.1 to 1.3 us against 1.6 of torch.empty
+        if like.shape == shape:
+            return torch.empty_like(like, dtype=dtype)
+        if len(shape) == 2:
+            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         # (of handle 0, the null stream's, ExternalStream would make a new stream)
         stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
@@ -373,7 +375,9 @@ _DISPATCH_TYPES = {**_INT8_TYPES, torch.int8: binding.TYPES["int8"]}
 
 
 @functools.lru_cache(maxsize=256)
-def _sort_bytes(pairs, E_local):
+def _sort_bytes(pairs, E_local, expert_offset):
+    if not -2 ** 31 <= E_local < 2 ** 31 or not -2 ** 31 <= expert_offset < 2 ** 31:
+        raise ValueError("E_local and expert_offset: expected 32-bit numbers")
     return binding.query_sort_sizes(pairs, E_local)
 
 
@@ -387,7 +391,7 @@ def sort_pairs(idx, E_local, expert_offset=0, stream=None):
     shape, dev, n = idx.shape, idx.device, idx.numel()
     handle = _on(dev, stream)
     _expect(idx, "idx", shape, torch.int32, dev)
-    ws_bytes = _sort_bytes(n, E_local)
+    ws_bytes = _sort_bytes(n, E_local, expert_offset)
     # one allocation and three views: 1 us less than three
     offsets, perm, pair_pos = _empty((E_local + 1 + 2 * n,), torch.int32, idx, stream).split_with_sizes((E_local + 1, n, n))
     ws = _empty((ws_bytes,), torch.uint8, idx, stream) if ws_bytes else None
@@ -428,9 +432,10 @@ def combine(rows, pair_pos, weight=None, y=None, dtype=None, stream=None):
         _expect(weight, "weight", shape, torch.float32, dev)
     T, k = shape
     if y is None:
-        if dtype is None:
-            dtype = rows.dtype
-        t = rt if dtype is rows.dtype else _int8_type(dtype)
+        if dtype is None or dtype is rows.dtype:
+            dtype, t = rows.dtype, rt
+        else:
+            t = _int8_type(dtype)
         y = _empty((T, H), dtype, rows, stream)
     else:
         t = _matrix(y, "y", _INT8_TYPES)

@@ -86,8 +86,8 @@ def test_pack_takes_the_nearer_of_the_bounds():
     assert torch.equal(unpack(q, s, 1, 256)[0], v.long().clamp(-8, 7))
 
 
-def rand_weight(shape, group, g, exact=False):
-    v = torch.randint(-8, 8, shape, generator=g, device=DEV).to(torch.int8)
+def rand_weight(shape, group, g, exact=False, low=-8):
+    v = torch.randint(low, 8, shape, generator=g, device=DEV).to(torch.int8)
     s = torch.rand((*shape[:-1], shape[-1] // group), generator=g, device=DEV) + 0.5
     s = torch.exp2((4 * s).floor() - 4) if exact else s / shape[-1] ** 0.5
     return v, s.to(torch.bfloat16)
@@ -114,7 +114,7 @@ def bound(x, v, s, group):
 # (M, N, K): one row to several tiles of rows, odd everything, one group of inputs, long rows
 SHAPES = [(1, 1, 32), (1, 16, 128), (1, 1536, 4096), (2, 33, 96), (7, 777, 1120), (16, 100, 512), (17, 48, 640), (31, 130, 1024),
           (33, 64, 2048), (64, 256, 1024), (65, 40, 320), (128, 128, 128), (200, 300, 544), (257, 513, 1056), (1000, 96, 768),
-          (3, 16, 16384), (700, 1024, 2048)]
+          (3, 16, 16384), (700, 1024, 2048), (40, 4096, 512), (200, 2112, 256), (520, 4160, 192), (2100, 4100, 224), (5000, 2056, 160)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -124,11 +124,13 @@ def test_matmul(M, N, K, group, out):
     K = -(-K // group) * group
     g = gen(M * N + K)
     # whole numbers and scales that are powers of two: every sum is exact in fp32, so that y is exactly rounded
-    v, s = rand_weight((N, K), group, g, exact=True)
     x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
-    want = x.double() @ real(v, s, group).T
-    w = int4_pack(v, s)
-    assert torch.equal(int4_matmul(x, *w, N=N, dtype=out), want.to(out))
+    for low in (-8, -7):                           # with and without the number that takes more steps to unpack
+        v, s = rand_weight((N, K), group, g, exact=True, low=low)
+        if low == -8 and N > 64:
+            v[64:128].clamp_(min=-7)               # one run of 64 channels without it among others
+        want = x.double() @ real(v, s, group).T
+        assert torch.equal(int4_matmul(x, *int4_pack(v, s), N=N, dtype=out), want.to(out))
     # real values
     v, s = rand_weight((N, K), group, g)
     x = (torch.randn(M, K, generator=g, device=DEV) * torch.exp(torch.randn(M, 1, generator=g, device=DEV))).to(torch.bfloat16)
@@ -140,7 +142,8 @@ def test_matmul(M, N, K, group, out):
 # (M, G, N, K, skew, rows ahead of the first group, rows behind the last)
 GROUPS = [(1, 1, 16, 32, 0, 0, 0), (1, 8, 40, 256, 0, 0, 0), (8, 16, 768, 512, 0, 0, 0), (64, 128, 192, 1024, 0, 0, 0), (64, 16, 64, 128, 2, 0, 0),
           (50, 7, 33, 160, 1, 3, 5), (300, 5, 100, 416, 1, 11, 30), (1117, 9, 777, 1120, 2, 0, 0), (2000, 130, 64, 256, 1, 0, 7),
-          (900, 2, 257, 352, 4, 1, 1), (40, 512, 16, 64, 0, 0, 0), (6, 4, 32, 128, 0, 3, 3)]
+          (900, 2, 257, 352, 4, 1, 1), (40, 512, 16, 64, 0, 0, 0), (6, 4, 32, 128, 0, 3, 3),
+          (3000, 20, 513, 256, 0, 2, 1), (9000, 24, 640, 192, 1, 0, 9), (700, 200, 130, 128, 0, 0, 0)]
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -150,6 +153,7 @@ def test_grouped(M, G, N, K, skew, lead, tail, group):
     g = gen(M + G + N)
     off = offsets_of(M, G, g, skew, lead, tail)
     v, s = rand_weight((G, N, K), group, g, exact=True)
+    v[::2].clamp_(min=-7)                          # every other weight without a -8
     x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
     for out in (torch.bfloat16, torch.float32):
         want = torch.full((M, N), 6.0, dtype=out, device=DEV)
