@@ -312,7 +312,7 @@ moe_status moe_fwd_int8(const moe_desc* d, const void* x, const void* w_router, 
  *   offsets  [E_local + 1]  first position of each expert's pairs; offsets[E_local] = P, their number
  *   perm     [pairs]        the pair at each position, -1 from position P on
  *   pair_pos [pairs]        the position of each pair, or -1
- * The order is moe_route's. A token may name an expert twice. E_local <= 512, pairs < 2^31. Every pointer needs
+ * The order is moe_route's. A token may name an expert twice. E_local <= 512, pairs 0 .. 2^31 - 1. Every pointer needs
  * 4-byte alignment, ws 256 (its size, 0 for few pairs, is moe_query_sort_sizes's; its contents need not be
  * preserved, and calls that share one must be ordered by the caller; null where the size is 0). */
 moe_status moe_query_sort_sizes(int64_t pairs, int E_local, size_t* ws);
@@ -323,8 +323,8 @@ moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int ex
  * that no pair stands at are left as they were. With moe_int8_quantize's bytes (MOE_TYPE_INT8) and scales
  * (MOE_TYPE_FP32, H = 1) it gives the operands of a grouped moe_int8_matmul. Its gradient is moe_combine without
  * weights, on the gradient of rows.
- * Here and below: any H >= 1, 1 <= topk <= 32, T*topk < 2^31, T*H, nrows*H < 2^40 (MOE_ERR_UNSUPPORTED_SHAPE); pointers aligned
- * to their elements. Rows of a multiple of 16 bytes behind 16-byte aligned pointers run fastest. */
+ * Here and below: any H >= 1, 1 <= topk <= 32, T*topk < 2^31, T*H, nrows*H < 2^40 (MOE_ERR_UNSUPPORTED_SHAPE); T and
+ * nrows may be 0 (what has no elements may be null); pointers aligned to their elements. Rows of a multiple of 16 bytes behind 16-byte aligned pointers run fastest. */
 moe_status moe_dispatch(const void* x, int type, int64_t T, int topk, int64_t H, const int32_t* pair_pos, void* rows,
                         int64_t nrows, void* stream);
 
@@ -374,8 +374,8 @@ moe_status moe_int4_pack(const int8_t* values, const void* in_scales, int G, int
 
 /* y[m, n] = sum over the groups of s[g, n, group] * (sum over the group's inputs of x[m, k] q[g, n, k]): x [M, K] bf16, y
  * [M, N] of `type`, rounded once; products exact, sums in fp32. offsets, groups of rows, and the rows of y outside of
- * them as in moe_int8_matmul. A NaN or an infinity in a row of x reaches that row of y alone (as NaN, where it meets other
- * values). M <= 2^31 - 512, M*N < 2^40, the rest as above. x, q and scales need 16-byte alignment, offsets 4-byte, y
+ * them as in moe_int8_matmul. A NaN or an infinity in a row of x makes values of that row of y NaN or infinite, and no
+ * other's. 0 <= M <= 2^31 - 512, M*N < 2^40, the rest as above. x, q and scales need 16-byte alignment, offsets 4-byte, y
  * its type's (8-byte, fp32 16-byte, and N % 4 = 0 write faster). */
 moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, int64_t M, int64_t N, int64_t K,
                            int group, int G, const int32_t* offsets, void* y, int type, void* stream);

@@ -1283,7 +1283,7 @@ SortLayout sort_layout(int64_t pairs, int El) {
 }
 
 moe_status sort_checks(int64_t pairs, int E_local) {
-  if (pairs < 1 || E_local < 1) return fail(MOE_ERR_INVALID_ARG, "pairs and E_local must be positive");
+  if (pairs < 0 || E_local < 1) return fail(MOE_ERR_INVALID_ARG, "E_local must be positive and pairs >= 0");
   if (E_local > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E_local must be <= 512");
   if (pairs > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "pairs must be < 2^31");
   return MOE_OK;
@@ -1293,11 +1293,12 @@ size_t elem_size(int type) { return type == MOE_TYPE_FP32 ? 4 : type == MOE_TYPE
 
 // the sizes that moe_dispatch, moe_combine and moe_combine_bwd share
 moe_status pairs_checks(int64_t T, int topk, int64_t H, int64_t nrows) {
-  if (T < 1 || topk < 1 || H < 1 || nrows < 1) return fail(MOE_ERR_INVALID_ARG, "T, topk, H and nrows must be positive");
+  if (topk < 1 || H < 1 || T < 0 || nrows < 0)
+    return fail(MOE_ERR_INVALID_ARG, "topk and H must be positive, T and nrows >= 0");
   if (topk > kMaxTopk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "topk must be <= 32");
   if (T > INT32_MAX / topk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*topk must be < 2^31");
   constexpr int64_t most = int64_t(1) << 40;
-  if (H >= most / T || H >= most / nrows) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*H and nrows*H must be < 2^40");
+  if (H >= most / std::max<int64_t>(T, 1) || H >= most / std::max<int64_t>(nrows, 1)) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*H and nrows*H must be < 2^40");
   return MOE_OK;
 }
 }  // namespace
@@ -1316,8 +1317,8 @@ moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int ex
   moe_status st = sort_checks(pairs, E_local);
   if (st != MOE_OK) return st;
   if (expert_offset < 0) return fail(MOE_ERR_INVALID_ARG, "expert_offset must be >= 0");
-  if ((st = check_ptrs({{idx, "idx"}, {offsets, "offsets"}, {perm, "perm"}, {pair_pos, "pair_pos"}}, 4)) != MOE_OK)
-    return st;
+  if ((st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;
+  if (pairs > 0 && (st = check_ptrs({{idx, "idx"}, {perm, "perm"}, {pair_pos, "pair_pos"}}, 4)) != MOE_OK) return st;
   const SortLayout L = sort_layout(pairs, E_local);
   if (L.total > 0 && (st = check_ptrs({{ws, "ws"}}, 256)) != MOE_OK) return st;
   if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "sort workspace too small");
@@ -1348,6 +1349,7 @@ moe_status moe_dispatch(const void* x, int type, int64_t T, int topk, int64_t H,
   moe_status st;
   if (type != MOE_TYPE_INT8 && (st = check_type(type)) != MOE_OK) return st;
   if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
+  if (T == 0 || nrows == 0) return MOE_OK;   // nothing to write
   if ((st = check_ptrs({{x, "x"}, {rows, "rows"}}, elem_size(type))) != MOE_OK) return st;
   if ((st = check_ptrs({{pair_pos, "pair_pos"}}, 4)) != MOE_OK) return st;
   if ((st = check_stream(stream)) != MOE_OK) return st;
@@ -1370,7 +1372,8 @@ moe_status moe_combine(const void* rows, int rows_type, int64_t nrows, const int
   moe_status st;
   if ((st = check_type(rows_type)) != MOE_OK || (st = check_type(type)) != MOE_OK) return st;
   if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
-  if ((st = check_ptrs({{rows, "rows"}}, elem_size(rows_type))) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (nrows > 0 && (st = check_ptrs({{rows, "rows"}}, elem_size(rows_type))) != MOE_OK) return st;
   if ((st = check_ptrs({{y, "y"}}, elem_size(type))) != MOE_OK) return st;
   if ((st = check_ptrs({{pair_pos, "pair_pos"}}, 4)) != MOE_OK) return st;
   if (weight && (st = check_ptrs({{weight, "weight"}}, 4)) != MOE_OK) return st;
@@ -1398,8 +1401,9 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
   moe_status st;
   if ((st = check_type(rows_type)) != MOE_OK || (st = check_type(type)) != MOE_OK) return st;
   if ((st = pairs_checks(T, topk, H, nrows)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
   if ((st = check_ptrs({{dy, "dy"}}, elem_size(type))) != MOE_OK) return st;
-  if ((st = check_ptrs({{rows, "rows"}, {drows, "drows"}}, elem_size(rows_type))) != MOE_OK) return st;
+  if (nrows > 0 && (st = check_ptrs({{rows, "rows"}, {drows, "drows"}}, elem_size(rows_type))) != MOE_OK) return st;
   if ((st = check_ptrs({{pair_pos, "pair_pos"}, {weight, "weight"}, {dweight, "dweight"}}, 4)) != MOE_OK) return st;
   if (dlogits) {
     if (E_total < 1) return fail(MOE_ERR_INVALID_ARG, "E_total must be positive");
@@ -1487,11 +1491,12 @@ moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, 
   g_last_error.clear();
   moe_status st;
   if ((st = check_type(type)) != MOE_OK) return st;
-  if (M < 1) return fail(MOE_ERR_INVALID_ARG, "M must be positive");
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M must be >= 0");
   if ((st = int4_checks(G, N, K, group)) != MOE_OK) return st;
   if (!offsets && G != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is null with more than one group");
   if (M > INT32_MAX - 511 || M * N >= (int64_t(1) << 40))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "M must be <= 2^31 - 512 and M*N < 2^40");
+  if (M == 0) return MOE_OK;
   if ((st = check_ptrs({{x, "x"}, {q, "q"}, {scales, "scales"}}, 16)) != MOE_OK) return st;
   if (offsets && (st = check_ptrs({{offsets, "offsets"}}, 4)) != MOE_OK) return st;
   if ((st = check_ptrs({{y, "y"}}, elem_size(type))) != MOE_OK) return st;
@@ -1596,9 +1601,12 @@ moe_status moe_clip_grad_norm(const moe_tensor* tensors, const moe_tensor* out, 
   if ((st = check_stream(stream)) != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(ws);
-  // without a single element no scaling follows that would write the norm
-  hipError_t e = launch_grad_norm(tensors, count, part, parts == 0 ? norm : nullptr, s);
-  if (e == hipSuccess && parts > 0) e = launch_grad_clip(tensors, out, count, max_norm, nullptr, part, parts, norm, s);
+  // The scaling's workgroups add the partial sums up by themselves, a launch less, where these are few (of one launch's
+  // tensors, or two's); and without a single element no scaling follows that would write the norm.
+  const bool apart = parts == 0 || parts > 2 * kNormParts;
+  hipError_t e = launch_grad_norm(tensors, count, part, apart ? norm : nullptr, s);
+  if (e == hipSuccess && parts > 0)
+    e = launch_grad_clip(tensors, out, count, max_norm, apart ? norm : nullptr, part, parts, norm, s);
   if (e != hipSuccess) return hip_fail(e, "clip launch");
   return MOE_OK;
 }

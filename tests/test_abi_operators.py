@@ -33,7 +33,7 @@ def sort(pairs=5000, E_local=8, expert_offset=0, **kw):
                      a["ws_bytes"], stream=0)
 
 
-@pytest.mark.parametrize("pairs,E_local,code", [(0, 8, ARG), (-3, 8, ARG), (8, 0, ARG), (8, 513, SHAPE),
+@pytest.mark.parametrize("pairs,E_local,code", [(-1, 8, ARG), (-3, 8, ARG), (8, 0, ARG), (8, 513, SHAPE),
                                                 (1 << 31, 8, SHAPE)])
 def test_sort_sizes(pairs, E_local, code):
     refused(code, lambda: b.query_sort_sizes(pairs, E_local))
@@ -74,7 +74,7 @@ def combine_bwd(rows_type=1, type=1, T=4, topk=2, H=16, nrows=8, E_total=8, **kw
 
 @pytest.mark.parametrize("call", [dispatch, combine, combine_bwd])
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=0), ARG), (dict(topk=0), ARG), (dict(H=0), ARG), (dict(nrows=0), ARG), (dict(topk=33), SHAPE),
+    (dict(T=-1), ARG), (dict(topk=0), ARG), (dict(H=0), ARG), (dict(nrows=-1), ARG), (dict(topk=33), SHAPE),
     (dict(T=1 << 28, topk=8), SHAPE), (dict(T=1 << 62), SHAPE), (dict(H=1 << 40), SHAPE), (dict(H=1 << 62), SHAPE),
     (dict(H=1 << 30, nrows=1 << 10), SHAPE), (dict(type=3), MODE), (dict(type=-1), MODE),
 ])
@@ -101,6 +101,13 @@ def test_pairs_arguments():
     refused(MODE, lambda: combine_bwd(rows_type=2))
 
 
+def test_without_tokens_or_rows_there_is_nothing_to_do():
+    dispatch(T=0, x=None, pair_pos=None)
+    dispatch(nrows=0, rows=None)
+    combine(T=0, y=None, pair_pos=None, weight=None)
+    combine_bwd(T=0, dy=None, pair_pos=None, weight=None, idx=None, dweight=None, dlogits=None)
+
+
 def matmul(M=4, N=16, K=128, group=32, G=1, type=1, **kw):
     a = dict(x=FAKE, q=FAKE, scales=FAKE, offsets=None if G == 1 else FAKE, y=FAKE)
     a.update(kw)
@@ -122,7 +129,8 @@ def test_int4_sizes(kw, code):
 
 def test_int4_arguments():
     assert b.query_int4_sizes(3, 65, 160, 32) == (3 * 2 * (2 * 4096 + 16), 3 * 2 * 2 * 64 * 4 * 2)
-    refused(ARG, lambda: matmul(M=0))
+    refused(ARG, lambda: matmul(M=-1))
+    matmul(M=0, x=None, y=None)                    # no rows: nothing to do
     refused(SHAPE, lambda: matmul(M=1 << 31))
     refused(SHAPE, lambda: matmul(M=1 << 30, N=1 << 10))
     refused(MODE, lambda: matmul(type=2))

@@ -32,7 +32,7 @@ def ref_norm(ts):
 BF, FP = torch.bfloat16, torch.float32
 LISTS = [([1], [BF]), ([7], [FP]), ([0, 5, 0], [FP]), ([8191], [BF]), ([8192], [FP]), ([8193], [BF]), ([100003], [FP]),
          ([3, 17, 4096, 1, 0, 70001, 255, 8192, 33], [BF, FP]), (list(range(1, 330)), [FP, BF, BF]),
-         ([16] * 700, [BF, FP]), ([5000003, 2, 1 << 20], [BF]), ([40000001], [FP, BF])]
+         ([16] * 700, [BF, FP]), ([5000003, 2, 1 << 20], [BF]), ([40000001], [FP, BF]), ([5000000] * 3 + [1000000] * 600, [BF, BF, FP])]
 
 
 @pytest.mark.parametrize("lead", [0, 1, 3])

@@ -298,7 +298,8 @@ def test_wrong_tensors_are_refused():
                  lambda: int4_pack(v, s[:, :0])):
         with pytest.raises(ValueError):
             call()
-    for call in (lambda: int4_matmul(x[:0], q, sc), lambda: int4_matmul(x[:, :96].contiguous(), q, sc),
+    assert int4_matmul(x[:0], q, sc).shape == (0, 64)
+    for call in (lambda: int4_matmul(x[:, :96].contiguous(), q, sc),
                  lambda: int4_quantize(torch.zeros((4, 80), device=DEV), 32)):
         with pytest.raises(b.MoEError):
             call()

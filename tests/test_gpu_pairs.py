@@ -311,6 +311,26 @@ def test_on_a_given_stream(kind):
     assert torch.equal(pos, want_pos) and torch.equal(y, want)
 
 
+def test_without_tokens_or_rows():
+    idx = torch.zeros((0, 3), dtype=torch.int32, device=DEV)
+    offsets, perm, pos = sort_pairs(idx, 5)
+    assert offsets.tolist() == [0] * 6 and perm.numel() == 0 and pos.shape == (0, 3)
+    x, w = torch.zeros((0, 8), device=DEV), torch.zeros((0, 3), device=DEV)
+    rows = dispatch(x, pos)
+    assert rows.shape == (0, 8) and combine(rows, pos, w).shape == (0, 8)
+    out = combine_backward(x, rows, w, pos, idx=idx, E_total=4)
+    assert [tuple(t.shape) for t in out] == [(0, 8), (0, 3), (0, 4)]
+    # tokens, none of whose pairs has a row
+    idx = torch.full((5, 3), 9, dtype=torch.int32, device=DEV)
+    offsets, perm, pos = sort_pairs(idx, 5)
+    assert offsets.tolist() == [0] * 6 and bool((perm == -1).all()) and bool((pos == -1).all())
+    x, w, rows = torch.ones((5, 8), device=DEV), torch.ones((5, 3), device=DEV), torch.zeros((0, 8), device=DEV)
+    dispatch(x, pos, rows=rows)
+    assert torch.equal(combine(rows, pos, w), torch.zeros_like(x))
+    drows, dw, dl = combine_backward(x, rows, w, pos, idx=idx, E_total=10)
+    assert drows.shape == (0, 8) and bool((dw == 0).all()) and bool((dl == 0).all())
+
+
 def test_wrong_tensors_are_refused():
     idx = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
     x = torch.zeros(4, 16, device=DEV)
@@ -327,7 +347,7 @@ def test_wrong_tensors_are_refused():
                  lambda: sort_pairs(idx, 4, 2 ** 32)):
         with pytest.raises(ValueError):
             call()
-    for call in (lambda: sort_pairs(idx[:0], 4), lambda: sort_pairs(idx, 0), lambda: sort_pairs(idx, 4, -1),
+    for call in (lambda: sort_pairs(idx, 0), lambda: sort_pairs(idx, 4, -1),
                  lambda: dispatch(x[:, :0].contiguous(), idx)):
         with pytest.raises(b.MoEError):
             call()
