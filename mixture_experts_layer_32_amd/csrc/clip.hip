@@ -173,7 +173,6 @@ __global__ __launch_bounds__(256) void k_scale(T a, float max_norm, const float*
   c = c > 1.f ? 1.f : c;                       // NaN stays
   if (!PAIRS && c == 1.f) return;              // in place: nothing changes
   const int C = a.first[a.count];
-  const int c0 = (int)((int64_t)C * blockIdx.x / gridDim.x), c1 = (int)((int64_t)C * (blockIdx.x + 1) / gridDim.x);
   int i = tensor_of(a, C - 1 - (int)blockIdx.x);
   for (int b = C - 1 - (int)blockIdx.x; b >= 0; b -= gridDim.x) {
     while (b < a.first[i]) --i;

@@ -496,8 +496,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     find_tile<BM>(p, groups, mt, g, r0, end);
     const char* xb = reinterpret_cast<const char*>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K);
     // This lane moves chunk (lane % 8) ^ swz_x(r) of rows r = (w LA + j) 8 + lane / 8; of an even LA that is the same
-    // chunk for all even j, and the one 4 further for the odd ones. (At most 256 rows of 131072 inputs: 32 bits.)
-    const unsigned K2 = 2u * (unsigned)p.K, x0 = K2 * (w * LA * 8 + lane / 8), xlast = K2 * (end - 1 - r0);
+    // chunk for all even j, and the one 4 further for the odd ones. (At most BM rows of 131072 inputs: 32 bits.)
+    const unsigned K2 = 2u * (unsigned)p.K, x0 = K2 * (w * LA * 8 + lane / 8), xlast = K2 * min(end - 1 - r0, BM - 1);
     const unsigned ch = ((lane & 7) ^ swz_x(w * LA * 8 + lane / 8)) * 16;
     static_assert(LA % 2 == 0, "");
     // Inputs beyond K (half a stage, or a tile's second one) have zero weights; read for them are others of the same row.

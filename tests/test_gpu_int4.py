@@ -231,6 +231,23 @@ def test_more_than_two_to_the_31_numbers():
     assert y.numel() > 2 ** 31 and bool((y[:-1] == 64).all()) and bool((y[-1] == 192).all())
 
 
+def test_rows_that_pass_4_gib():
+    """x of more than 2^32 bytes in one group: rows of the first tiles, of the last and of one between, among zeros."""
+    M, N, K = 2 ** 14 + 3, 64, 2 ** 17
+    g = gen(11)
+    v, s = rand_weight((N, K), 128, g, exact=True)
+    q, sc = int4_pack(v, s)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 2, 3, 63, 64, 255, 8191, M - 4, M - 1], device=DEV)
+    rows = torch.randint(-1, 2, (len(at), K), generator=g, device=DEV).to(torch.bfloat16)
+    x[at] = rows
+    y = int4_matmul(x, q, sc, dtype=torch.float32)
+    # whole quarters below 2^17 * 8 * 2: exact in fp32
+    want = torch.zeros((M, N), device=DEV)
+    want[at] = (rows.double() @ real(v, s, 128).T).float()
+    assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("M", [4, 300])
 def test_captured_and_replayed(M):
     g = gen(M)
