@@ -91,13 +91,15 @@ struct Scales4<1> {
   __device__ __forceinline__ float operator[](int) const { return bf16_bits(v); }
 };
 
-// KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, its wave t their tile t, a
-// tile column at a time; lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
+// KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, a wave one of their tiles, every
+// fourth column of it (in a grid of y workgroups to the channels: every 4 y-th); lane 16 h + c takes inputs 32 i + 8 h + j,
+// i < 4, j < 8. KIND 2 takes y = 1, as the word that says whether there is a -8 is made of all columns.
+constexpr int kPackWaves = 16;
 template <int KIND>
-__global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, const uint16_t* __restrict__ sin, int64_t rows,
+__global__ __launch_bounds__(kPackWaves * 64) void k_int4_pack(const void* __restrict__ in, const uint16_t* __restrict__ sin, int64_t rows,
                                                    int N, int K, int group, uint8_t* __restrict__ q,
                                                    uint16_t* __restrict__ sout) {
-  const int t = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
+  const int t = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int Kt = (K + kTileK - 1) / kTileK;
   const int per = group / 32, ng = 4 / per;     // steps of 32 inputs in a group, groups of a tile
   const int64_t row64 = blockIdx.x;             // over the weights
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
   const int64_t row = g * N + n;
   unsigned* flag = reinterpret_cast<unsigned*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4);
   bool eights = false;
-  for (int kb = 0; kb < Kt; ++kb) {
+  for (int kb = blockIdx.y * (kPackWaves / 4) + (threadIdx.x >> 8); kb < Kt; kb += gridDim.y * (kPackWaves / 4)) {
     float v[4][8];
     unsigned m[4];
 #pragma unroll
@@ -159,12 +161,15 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
           const bf16 s = (bf16)fmaxf(__uint_as_float(mg) / 7.0f, 0x1p-126f);
           sb = __builtin_bit_cast(uint16_t, s);
         }
-        // the quotient in 64 bits, where no rounding can carry it onto or over a tie: numerator and denominator have 24
-        // and 8 significant bits
-        const double s = (double)bf16_bits(sb);
+        // v / s to the nearest whole number, ties to even. v and s have 24 and 8 significant bits, so that a quotient that is
+        // no tie lies 2^-25 or more from one; v times 1 / s, each rounded to 64 bits, is off by 2^-49 at most, and rounded
+        // to a multiple of 2^-32 (by adding a number with such a step) it is a tie where the quotient is one, and only there.
+        const double r = 1.0 / (double)bf16_bits(sb), step = 0x1.8p20;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[i][j] = mg >= 0x7f800000u ? 0.f : (float)fmin(7.0, fmax(-7.0, rint((double)v[i][j] / s)));
+        for (int j = 0; j < 8; ++j) {
+          const double x = fma((double)v[i][j], r, step) - step;
+          v[i][j] = mg >= 0x7f800000u ? 0.f : fminf(7.f, fmaxf(-7.f, (float)rint(x)));
+        }
         if (!ok) sb = 0;
       }
       w[i] = 0u;
@@ -178,7 +183,7 @@ __global__ __launch_bounds__(256) void k_int4_pack(const void* __restrict__ in, 
     st16(q + row64 * row_bytes(Kt) + ((size_t)t * Kt + kb) * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
   }
   const int any = __syncthreads_or(eights);
-  if (threadIdx.x < kFlagBytes / 4) flag[threadIdx.x] = any != 0;
+  if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) flag[threadIdx.x] = any != 0;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -690,12 +695,13 @@ hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G,
                             void* out_scales, hipStream_t s) {
   prof_mark_begin("int4_pack", s);
   const int64_t tiles = (int64_t)G * rows64(N);   // at most 2^23 workgroups
-  const unsigned grid = (unsigned)tiles;
+  const int columns = ((K + kTileK - 1) / kTileK + kPackWaves / 4 - 1) / (kPackWaves / 4), few = 2 * persistent_grid(1);
+  const dim3 grid((unsigned)tiles, scales ? 1u : (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)));
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);
-  if (scales) k_int4_pack<2><<<grid, 256, 0, s>>>(in, si, tiles, N, K, group, q, so);
-  else if (f32) k_int4_pack<1><<<grid, 256, 0, s>>>(in, nullptr, tiles, N, K, group, q, so);
-  else k_int4_pack<0><<<grid, 256, 0, s>>>(in, nullptr, tiles, N, K, group, q, so);
+  if (scales) k_int4_pack<2><<<grid, kPackWaves * 64, 0, s>>>(in, si, tiles, N, K, group, q, so);
+  else if (f32) k_int4_pack<1><<<grid, kPackWaves * 64, 0, s>>>(in, nullptr, tiles, N, K, group, q, so);
+  else k_int4_pack<0><<<grid, kPackWaves * 64, 0, s>>>(in, nullptr, tiles, N, K, group, q, so);
   const hipError_t err = hipGetLastError();
   if (err == hipSuccess) prof_mark_end(s);
   return err;
