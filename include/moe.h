@@ -324,7 +324,8 @@ moe_status moe_sort_pairs(const int32_t* idx, int64_t pairs, int E_local, int ex
  * (MOE_TYPE_FP32, H = 1) it gives the operands of a grouped moe_int8_matmul. Its gradient is moe_combine without
  * weights, on the gradient of rows.
  * Here and below: any H >= 1, 1 <= topk <= 32, T*topk < 2^31, T*H, nrows*H < 2^40 (MOE_ERR_UNSUPPORTED_SHAPE); T and
- * nrows may be 0 (what has no elements may be null); pointers aligned to their elements. Rows of a multiple of 16 bytes behind 16-byte aligned pointers run fastest. */
+ * nrows may be 0 (what has no elements may be null); pointers aligned to their elements. Rows of a multiple of 16 bytes
+ * behind 16-byte aligned pointers run fastest. Inputs and outputs may not overlap. */
 moe_status moe_dispatch(const void* x, int type, int64_t T, int topk, int64_t H, const int32_t* pair_pos, void* rows,
                         int64_t nrows, void* stream);
 
@@ -362,7 +363,8 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
 moe_status moe_query_int4_sizes(int G, int64_t N, int64_t K, int group, size_t* q_bytes, size_t* scale_bytes);
 
 /* Quantises a weight in [G, N, K] (row-major, `type`) for each group of inputs: D = the group's largest |v|,
- * s = D / 7 in fp32, at least 2^-126, rounded to bf16, q = the whole number nearest to the real quotient v / s, ties to even, kept within -7..7.
+ * s = D / 7 in fp32, at least 2^-126, rounded to bf16, q = the whole number nearest to the real quotient v / s, ties to
+ * even, kept within -7..7.
  * A group that holds a NaN or an infinity has s = NaN and q = 0. K a multiple of group, <= 131072; N <= 2^20; G <= 512;
  * G*N*K < 2^40. in, q and scales need 16-byte alignment. */
 moe_status moe_int4_quantize(const void* in, int type, int G, int64_t N, int64_t K, int group, uint8_t* q,
@@ -387,12 +389,13 @@ moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, 
  *   out  = c * g                                                   each element rounded once
  * The descriptions are read on the host during the call: count of them (0: the norm is 0), each a device pointer
  * (aligned to its elements), a number of elements (0: data may be null) and a type (FP32 or BF16). Together less than
- * 2^40 elements. out = null scales in place, and writes nothing where c = 1; otherwise out[i] has tensors[i]'s size, its type may
- * be the other one, and everything is written. Tensors may not overlap, but out[i] may be tensors[i].
+ * 2^40 elements. out = null scales in place, and writes nothing where c = 1; otherwise out[i] has tensors[i]'s size, its
+ * type may be the other one, and everything is written. Tensors may not overlap, but out[i] may be tensors[i].
  * moe_grad_norm writes norm [1] fp32; moe_grad_clip scales by a norm given (other ranks' gradients may have
- * joined it); moe_clip_grad_norm does both in fewer launches. ws: 256-byte aligned, of moe_query_norm_sizes's size;
- * contents need not be preserved, and calls that share one must be ordered by the caller. max_norm >= 0.
- * A launch takes some hundred tensors; more take more launches. */
+ * joined it); moe_clip_grad_norm does both, in a launch less where the tensors are few. ws: 256-byte aligned, of
+ * moe_query_norm_sizes's size; contents need not be preserved, and calls that share one must be ordered by the caller.
+ * max_norm >= 0.
+ * A launch takes 184 tensors (in place) or 128 (with outputs); more take more launches. */
 typedef struct {
   void* data;
   int64_t n;

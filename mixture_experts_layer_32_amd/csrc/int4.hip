@@ -1,14 +1,21 @@
 // Products with 4-bit weights and a scale for each group of inputs.
 //
 //   k_int4_pack   a weight's tiles, from fp32 or bf16 (quantised here) or from whole numbers and scales.
-//   k_int4_rows   y = sum over groups of s (x q^T): a workgroup takes 16 output channels, its waves split K, and the
-//                 weight is read once for up to 64 rows.
-//   k_int4_tile   the same for many rows: tiles in LDS, the weight's numbers unpacked once for a workgroup.
-// A number q of a weight is held in four bits, a sign and m = |q| (sign 1 and m = 0: -8). Two masks give four numbers
-// each as bytes, a sign bit and the low three; such a byte is q 2^-9 in e4m3, and v_cvt_scalef32_pk_bf16_fp8 (two numbers
-// an instruction, at the rate of a plain one) makes q in bf16 of it: 7 instructions for 8 numbers. -8, which a symmetric
-// quantiser does not make, takes 12 more; 64 channels that hold none say so in a word of theirs. The matrix instruction's products x q
-// are exact, and its fp32 sums of a group are multiplied with the scale.
+//   k_int4_rows   y = sum over groups of s (x q^T) for few rows: 16 at a time, the weight straight from memory into
+//                 registers, K split over a workgroup's waves. Bound by reading the weight (6.6 TB/s with 64 rows among 128
+//                 experts of 1536 x 4096, 31 us), and with one weight by the launch (one row of 1536 x 4096 5.1 us).
+//   k_int4_deep   64 x 64 tiles for products of few tiles: all operands come straight into LDS.
+//   k_int4_tile   256 x 128 and 128 x 128 tiles for products of many: x in LDS, the weight unpacked from registers.
+//                 16384 x 4096 x 2048 270 to 300 us (920 to 1020 TFLOP/s, box to box); a bf16 product of this size by the
+//                 library takes 243, and a loop of this many matrix instructions on such numbers, with nothing else, reached
+//                 1120 to 1270 TFLOP/s (1415 on zeros): the clock falls with their load.
+// launch4 says which takes what, with times. A number q of a weight is held in four bits, a sign and m = |q| (sign 1 and
+// m = 0: -8). Two masks give four numbers each as bytes, a sign bit and the low three; such a byte is q 2^-9 in e4m3, and
+// v_cvt_scalef32_pk_bf16_fp8 (two numbers an instruction, at the rate of a plain one) makes q in bf16 of it: 7 instructions
+// for 8 numbers (13 from two's complement with masks and additions). -8, which a symmetric quantiser does not make, takes 12
+// more; 64 channels that hold none say so in a word of theirs. The matrix instruction's products x q are exact, and its
+// fp32 sums of a group are multiplied with the scale. Numbers in bytes 16 + q, with 16 times the sum of x taken off, would
+// save the signs but lose bits where x's sum is large.
 #include <algorithm>
 #include <type_traits>
 
@@ -91,6 +98,7 @@ struct Scales4<1> {
   __device__ __forceinline__ float operator[](int) const { return bf16_bits(v); }
 };
 
+// Once for a weight: 128 x 1536 x 4096 from bf16 576 us (3.5 TB/s), 4096 x 4096 17 us, laid out from bytes 475 and 42.
 // KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, a wave one of their tiles, every
 // fourth column of it (in a grid of y workgroups to the channels: every 4 y-th); lane 16 h + c takes inputs 32 i + 8 h + j,
 // i < 4, j < 8. KIND 2 takes y = 1, as the word that says whether there is a -8 is made of all columns.
@@ -462,10 +470,12 @@ __global__ __launch_bounds__(kRowWaves * 64, rows_wgs(PER)) void k_int4_rows(I4P
 }
 
 // ------------------------------------------------------------------------------------------------
-// k_int4_tile: WM x WN waves of MI x NJ blocks of 16 x 16, K in stages of 64 inputs. x comes into LDS by direct loads,
-// two stages of it in rows of 128 bytes; each wave unpacks its own channels' numbers into fragments, those of the next
-// stage behind the last products of this one. A stage's sums (PER = 1: its halves') start from zero and are added to the
-// accumulators times their scales, a row block later than they are made, so that the matrix cores have work meanwhile.
+// k_int4_tile: WM x WN waves of MI x NJ blocks of 16 x 16, K in stages of 64 inputs, for products whose tiles hide what a
+// stage waits for; a wave's tile as large as its registers allow, as each number is unpacked once for it. Unpacking into LDS,
+// once for the workgroup, took 312 us (16384 x 4096 x 2048) where this took 299. x comes into LDS by direct loads, two stages
+// of it in rows of 128 bytes; each wave unpacks its own channels' numbers into fragments, those of the next stage behind the
+// last products of this one. A stage's sums (PER = 1: its halves') start from zero and are added to the accumulators times
+// their scales, a row block later than they are made, so that the matrix cores have work meanwhile.
 constexpr int kRowB = 128;   // bytes of a row in a stage
 
 // The 16-byte chunk c of row r lies in slot c ^ swz_x(r): 16 consecutive rows at one chunk, which a fragment read
@@ -476,6 +486,39 @@ __device__ __forceinline__ int swz_x(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ void gl2lds_at(const void* base, unsigned off, char* lds) {
   const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
+}
+
+// 4 bytes a lane
+__device__ __forceinline__ void gl2lds4_at(const void* base, unsigned off, char* lds) {
+  const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
+}
+
+// NJ neighbouring channels of a row from n on, at element `at` of y; wide: all at once
+template <int NJ, class F>
+__device__ __forceinline__ void store_channels(const I4Params& p, size_t at, int n, bool wide, const F& v) {
+  if (wide) {
+    if (n >= p.N) return;
+    if (p.f32) {
+      float* o = static_cast<float*>(p.y) + at;
+      if constexpr (NJ == 4) *reinterpret_cast<f32x4*>(o) = f32x4{v(0), v(1), v(2), v(3)};
+      else *reinterpret_cast<float2*>(o) = make_float2(v(0), v(1));
+    } else {
+      alignas(8) bf16 b[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) b[j] = (bf16)v(j);
+      bf16* o = static_cast<bf16*>(p.y) + at;
+      if constexpr (NJ == 4) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(b);
+      else *reinterpret_cast<unsigned*>(o) = *reinterpret_cast<const unsigned*>(b);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (n + j >= p.N) continue;
+      if (p.f32) static_cast<float*>(p.y)[at + j] = v(j);
+      else static_cast<bf16*>(p.y)[at + j] = (bf16)v(j);
+    }
+  }
 }
 
 template <int MI, int NJ, int WM, int WN, int PER>
@@ -613,52 +656,162 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
       for (int e = 0; e < 4; ++e) {
         const int r = r0 + 16 * (MI * wm + i) + 4 * h + e;
         if (r >= end) continue;
-        const size_t at = (size_t)r * p.N + n1;
-        if (wide) {
-          if (n1 >= p.N) continue;
-          if (p.f32) {
-            float* o = static_cast<float*>(p.y) + at;
-            if constexpr (NJ == 4) *reinterpret_cast<f32x4*>(o) = f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]};
-            else *reinterpret_cast<float2*>(o) = make_float2(acc[i][0][e], acc[i][1][e]);
-          } else {
-            alignas(8) bf16 v[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) v[j] = (bf16)acc[i][j][e];
-            bf16* o = static_cast<bf16*>(p.y) + at;
-            if constexpr (NJ == 4) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(v);
-            else *reinterpret_cast<unsigned*>(o) = *reinterpret_cast<const unsigned*>(v);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            if (n1 + j >= p.N) continue;
-            if (p.f32) static_cast<float*>(p.y)[at + j] = acc[i][j][e];
-            else static_cast<bf16*>(p.y)[at + j] = (bf16)acc[i][j][e];
-          }
-        }
+        store_channels<NJ>(p, (size_t)r * p.N + n1, n1, wide, [&](int j) { return acc[i][j][e]; });
       }
   }
 }
 
-// Tiles of bm rows by bn columns for the rows in as many groups as the product may have.
-int64_t tiles4(const I4Params& p, int bm, int bn) {
-  const int64_t m = p.M / bm + (p.offsets ? std::min<int64_t>(p.G, p.M) : 1);
-  return std::min<int64_t>(m, p.M) * ((p.N + bn - 1) / bn);
+// ------------------------------------------------------------------------------------------------
+// k_int4_deep: 64 rows by 64 channels, stages of 128 inputs. x, the words of q and the scales go straight into LDS, so
+// that no load's latency stands between a stage's products; 4 waves of 2 x 2 blocks. KG = 2 groups of them share the inputs of
+// a tile, where there is no more than a tile for a CU, and their sums meet in LDS; with more tiles three workgroups of KG = 1
+// share a CU. 256 rows of 4096 x 4096 17 us (KG = 1 21; in stages of 64 inputs with q and scales in registers 33), 4096
+// rows in 64 groups of 1536 x 4096 99 us (157). Bound by the unpacking and the matrix instructions together, 0.35 us a stage
+// and CU: three stages in LDS, or the next one's fragments in registers ahead of time, or 64 x 128 tiles with fewer bytes for
+// a product all took as long or longer (256 rows 17.5, 18.2 and 24 to 28 us).
+template <int PER, int KG>
+__global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Params p) {
+  constexpr int BM = 64, XB = BM * 2 * kTileK, QB = 4 * kTileBytes4, SB = 1024, ST = XB + QB + SB, NS = 4 / PER, NJ = 2;
+  __shared__ __attribute__((aligned(1024))) char smem[KG * 2 * ST];
+  __shared__ Groups groups;
+  const int lane = threadIdx.x & 63, w = eng::wave_id() % 4, kg = eng::wave_id() / 4, wm = w / 2, wn = w % 2, c = lane & 15,
+            h = lane >> 4;
+  char* own = smem + kg * 2 * ST;   // the group's stages
+  const int R64 = rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK;
+  const bool wide = p.N % NJ == 0 && reinterpret_cast<uintptr_t>(p.y) % (NJ * (p.f32 ? 4 : 2)) == 0;
+  const int mtiles = group_tiles<BM>(p, groups);
+  const XcdRange xr = xcd_range(mtiles * R64);
+  for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
+    const int mt = tile / R64, n64 = tile - mt * R64;
+    int g, r0, end;
+    find_tile<BM>(p, groups, mt, g, r0, end);
+    const char* xb = reinterpret_cast<const char*>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K);
+    // A row's 16 chunks of a stage: chunk b of row r lies in slot b ^ (r % 16). This lane moves rows 16 w + 4 j + lane / 16.
+    const unsigned K2 = 2u * (unsigned)p.K, x0 = K2 * (16 * w + (lane >> 4)), xlast = K2 * min(end - 1 - r0, BM - 1);
+    const unsigned b0 = (lane & 15) ^ (lane >> 4);
+    const int64_t row64 = (int64_t)g * R64 + n64;
+    const uint8_t* qb = tile_at(p.q, row64, w, Kt);
+    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, 0, NS);
+    // Inputs beyond K have zero weights; read for them is another chunk of the same row.
+    auto issue = [&](int st, char* to) {
+      const char* at = xb + (size_t)st * 2 * kTileK;
+      const unsigned last = min(kTileK, p.K - st * kTileK) / 8 - 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        gl2lds_at(at, min(x0 + 4 * j * K2, xlast) + 16 * min(b0 ^ (4 * j), last), to + (4 * w + j) * 1024);
+      gl2lds_at(qb + (size_t)st * kTileBytes4, 16 * lane, to + XB + w * 1024);
+      // 128 NS bytes, over and over
+      gl2lds4_at(ps + (size_t)st * 64 * NS, (4 * lane + 256 * wn) & (128 * NS - 1), to + XB + QB + w * 256);
+    };
+    const int eights = holds_8(p.q, row64, Kt);
+    using Scales = Scales4<NJ * NS>;
+    f32x4 acc[2][NJ];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    eng::block_sync();   // every wave is done reading the previous tile's stages
+    // the group's stages are kg, kg + KG, .. of K, in two places in turn
+    if (kg < Kt) issue(kg, own);
+    auto columns = [&](auto with8) {
+      int place = 0;
+      for (int st = kg; st < Kt + kg; st += KG) {   // (as often in each group)
+        eng::wait_vm<0>();
+        eng::block_sync();
+        const char* at = own + place;
+        place ^= ST;
+        if (st + KG < Kt) issue(st + KG, own + place);
+        if (KG > 1 && st >= Kt) break;
+        uint4 q[NJ], fa[2][4];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) q[j] = ld16(at + XB + (NJ * wn + j) * 1024 + 16 * lane);
+        const Scales sc = *reinterpret_cast<const Scales*>(at + XB + QB + (4 * c + 2 * wn) * NS * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) fa[i][s] = ld16(at + (32 * wm + 16 * i + c) * 256 + 16 * ((4 * s + h) ^ c));
+#pragma unroll
+        for (int a = 0; a < NS; ++a) {
+          f32x4 part[2][NJ];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) part[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = a * PER; s < (a + 1) * PER; ++s)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              Bytes8 v = bytes8(s == 0 ? q[j].x : s == 1 ? q[j].y : s == 2 ? q[j].z : q[j].w);
+              if constexpr (decltype(with8)::value) v = {with_8(v.a), with_8(v.b)};
+              const uint4 f = numbers8(v);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) mma16<bf16>(part[i][j], fa[i][s], f);
+            }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const float sf = sc[j * NS + a];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sf, part[i][j][e], acc[i][j][e]);
+          }
+        }
+      }
+    };
+    if (eights) columns(std::true_type{});
+    else columns(std::false_type{});
+    // of KG = 2 groups, each stores a row block of its waves: the other's sums of it come through LDS
+    static_assert(KG == 1 || KG == 2, "");
+    if constexpr (KG == 2) {
+      eng::block_sync();
+      f32x4* red = reinterpret_cast<f32x4*>(smem) + (w * 2 * 64 + lane) * NJ;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) red[kg * 64 * NJ + j] = kg ? acc[0][j] : acc[1][j];
+      eng::block_sync();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const f32x4 o = red[(1 - kg) * 64 * NJ + j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][j][e] = (kg ? acc[1][j][e] : acc[0][j][e]) + o[e];
+      }
+    }
+    const int n1 = 64 * n64 + 4 * c + 2 * wn;
+#pragma unroll
+    for (int i = 0; i < 2 / KG; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 32 * wm + 16 * (i + kg) + 4 * h + e;
+        if (r >= end) continue;
+        store_channels<NJ>(p, (size_t)r * p.N + n1, n1, wide, [&](int j) { return acc[i][j][e]; });
+      }
+  }
 }
 
-// The kernel by the rows of a group that has any, as far as the host knows, and by how much work there is.
-// Rows kernel, us, against the best tiles: 2048 rows in 64 groups of 1536 x 4096 76 and 104, 4096 rows 150 and 109; 128 rows of
-// 4096 x 4096 16 and 21, 256 rows 28 and 30, 512 rows 50 and 35. TL = 4 against 1: one row of 4096 x 4096 9.3 and 5.0,
-// of 32768 x 4096 14 and 17; 16 rows of 4096 x 4096 9.5 and 7.9, 32 rows 9.7 and 12.4.
-// Tiles of 256 x 128, 128 x 128 and 64 x 64, us: 16384 rows of 2048 x 768 in 64 groups 63, 69, 138; 8192 rows of 1536 x 4096 in 64
-// groups 224, 135, 285, 4096 rows 198, 111, 109; 1024 rows of 4096 x 4096 73, 49, 67, 512 rows 70, 44, 35.
+// Tiles of bm rows by bn columns; for groups, whose sizes the host does not know, as many as evenly spread ones have.
+int64_t tiles4(const I4Params& p, int bm, int bn) {
+  const int64_t groups = std::min<int64_t>(p.G, p.M);
+  const int64_t m = p.offsets ? std::max(groups, p.M / bm + groups / 2) : (p.M + bm - 1) / bm;
+  return m * ((p.N + bn - 1) / bn);
+}
+
+// The kernel by the rows of a group that has any, as far as the host knows, and by how much work there is. In us, R:
+// rows with TL = 4 (1: with TL = 1), D, DD: deep with one and two groups of waves, 128, 256: tiles of 128 x 128 and
+// 256 x 128; W: the work in units of 16 rows by 64 channels, on 256 CUs.
+//   rows of 4096 x 4096      16 (W 64): 1 8.4, R 10.2    64 (256): R 10.7, DD 15.3   128 (512): R 16.6, DD 15.7
+//                            256: DD 17, D 21, 128 42    512: D 27, DD 30, 128 43    1024: D 49, 128 46   2048: D 89, 128 72, 256 79
+//   rows of 1536 x 4096      64 (96): 1 12.8, R 10.1     192 (288): R 15.3, DD 15.8  384 (576): R 21, DD 16   2048: D 38, 128 45, 256 70
+//   rows of 16384 x 2048     512: D 47, 128 40, 256 42   768: D 72, 128 56, 256 64   1024: D 93, 128 79, 256 69
+//   64 groups, 1536 x 4096   of 8 rows: R 43, D 68       16: R 60, D 68              24: R 75, D 69   40: D 68, 128 93   64: D 99, 128 94
+//   128 groups, 768 x 2048   of 8 rows: R 30, D 39       16: R 44, D 39              40: D 39, 128 50 64: D 55, 128 52
+//   16 groups, 768 x 2048    of 4 rows (240): 1 9.4, R 8.1   128: D 16, 128 26
+// One row of 32768 x 4096 (W 512): 1 17, R 14; 16384 rows of 2048 x 768 in 64 groups: 256 63, 128 69.
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
   const int64_t groups = std::min<int64_t>(p.M, p.G);
   const int64_t mt = p.offsets ? p.M / kRows4 + groups : (p.M + kRows4 - 1) / kRows4;
   const int64_t work = mt * rows64(p.N);        // 16 rows by 64 channels
   const int Kt = (p.K + kTileK - 1) / kTileK;
-  if (p.M <= 32 * groups || work <= 2 * grid) {
+  if (p.M <= 14 * groups || 8 * work <= 9 * grid) {
     auto go = [&](auto kernel, int TL) {
       // fewer waves a task where their columns would make less than a unit, as long as every CU keeps its workgroups
       const int64_t wgs = rows_wgs(PER) * grid;
@@ -667,14 +820,16 @@ void launch4(const I4Params& p, int grid, hipStream_t s) {
       const int64_t tasks = (4 * work * wk / TL + kRowWaves - 1) / kRowWaves;
       kernel<<<(unsigned)std::min(tasks, wgs), kRowWaves * 64, 0, s>>>(p, wk);
     };
-    if (work <= (p.M <= kFew4 * groups ? grid : 3 * grid / 8)) go(k_int4_rows<PER, 1>, 1);
+    if (work <= (p.M <= kFew4 * groups ? 3 * grid / 4 : 5 * grid / 16)) go(k_int4_rows<PER, 1>, 1);
     else go(k_int4_rows<PER, 4>, 4);
-  } else if (p.M >= 192 * groups && 4 * tiles4(p, 256, 128) >= 6 * grid) {
+  } else if (p.M >= 192 * groups && 4 * tiles4(p, 256, 128) >= 7 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
-  } else if (p.M >= 72 * groups && 4 * tiles4(p, 128, 128) >= 3 * grid) {
+  } else if (p.M >= 60 * groups && 4 * tiles4(p, 128, 128) >= 5 * grid) {
     k_int4_tile<4, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
+  } else if (tiles4(p, 64, 64) <= grid) {
+    k_int4_deep<PER, 2><<<grid, 512, 0, s>>>(p);
   } else {
-    k_int4_tile<2, 2, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
+    k_int4_deep<PER, 1><<<3 * grid, 256, 0, s>>>(p);
   }
 }
 
