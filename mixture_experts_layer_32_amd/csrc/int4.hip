@@ -98,11 +98,18 @@ struct Scales4<1> {
   __device__ __forceinline__ float operator[](int) const { return bf16_bits(v); }
 };
 
-// Once for a weight: 128 x 1536 x 4096 from bf16 576 us (3.5 TB/s), 4096 x 4096 17 us, laid out from bytes 475 and 42.
+// Once for a weight: 128 x 1536 x 4096 from bf16 576 us (3.5 TB/s), 4096 x 4096 17 us, laid out from bytes 475 and 16.
 // KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, a wave one of their tiles, every
-// fourth column of it (in a grid of y workgroups to the channels: every 4 y-th); lane 16 h + c takes inputs 32 i + 8 h + j,
-// i < 4, j < 8. KIND 2 takes y = 1, as the word that says whether there is a -8 is made of all columns.
+// fourth column of it; with few channels y workgroups share them, and each wave takes every 4 y-th column (values of
+// 4096 x 4096 laid out in 16 us, by one workgroup to the channels in 42). Lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
 constexpr int kPackWaves = 16;
+
+// The words that say whether there is a -8, 0 ahead of y > 1 workgroups that may find one.
+__global__ __launch_bounds__(256) void k_int4_none(uint8_t* q, int64_t n, int Kt) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (r < n) *reinterpret_cast<uint4*>(q + (r + 1) * row_bytes(Kt) - kFlagBytes) = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int KIND>
 __global__ __launch_bounds__(kPackWaves * 64) void k_int4_pack(const void* __restrict__ in, const uint16_t* __restrict__ sin, int64_t rows,
                                                    int N, int K, int group, uint8_t* __restrict__ q,
@@ -191,7 +198,11 @@ __global__ __launch_bounds__(kPackWaves * 64) void k_int4_pack(const void* __res
     st16(q + row64 * row_bytes(Kt) + ((size_t)t * Kt + kb) * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
   }
   const int any = __syncthreads_or(eights);
-  if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) flag[threadIdx.x] = any != 0;
+  if (KIND == 2 && gridDim.y > 1) {
+    if (threadIdx.x == 0 && any) atomicOr(flag, 1u);
+  } else if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) {
+    flag[threadIdx.x] = any != 0;
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -850,8 +861,9 @@ hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G,
                             void* out_scales, hipStream_t s) {
   prof_mark_begin("int4_pack", s);
   const int64_t tiles = (int64_t)G * rows64(N);   // at most 2^23 workgroups
-  const int columns = ((K + kTileK - 1) / kTileK + kPackWaves / 4 - 1) / (kPackWaves / 4), few = 2 * persistent_grid(1);
-  const dim3 grid((unsigned)tiles, scales ? 1u : (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)));
+  const int Kt = (K + kTileK - 1) / kTileK, columns = (Kt + kPackWaves / 4 - 1) / (kPackWaves / 4), few = 2 * persistent_grid(1);
+  const dim3 grid((unsigned)tiles, (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)));
+  if (scales && grid.y > 1) k_int4_none<<<(unsigned)((tiles + 255) / 256), 256, 0, s>>>(q, tiles, Kt);
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);
   if (scales) k_int4_pack<2><<<grid, kPackWaves * 64, 0, s>>>(in, si, tiles, N, K, group, q, so);

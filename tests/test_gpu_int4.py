@@ -86,6 +86,18 @@ def test_pack_takes_the_nearer_of_the_bounds():
     assert torch.equal(unpack(q, s, 1, 256)[0], v.long().clamp(-8, 7))
 
 
+@pytest.mark.parametrize("G,N,K", [(1, 70, 4096), (3, 130, 2080), (600, 64, 256)])
+def test_one_number_of_minus_8_is_found_wherever_it_is(G, N, K):
+    g = gen(K)
+    s = torch.ones((G, N, K // 32), dtype=torch.bfloat16, device=DEV)
+    for at in [(0, 0, 0), (G - 1, N - 1, K - 1), (G // 2, N // 2, K // 2 + 5), (0, N - 1, 600 % K), None]:
+        v = torch.randint(-7, 8, (G, N, K), generator=g, device=DEV).to(torch.int8)
+        if at:
+            v[at] = -8
+        q, sc = int4_pack(v, s)                    # (unpack compares the words with what the numbers are)
+        assert torch.equal(unpack(q, sc, N, K)[0], v.long())
+
+
 def rand_weight(shape, group, g, exact=False, low=-8):
     v = torch.randint(low, 8, shape, generator=g, device=DEV).to(torch.int8)
     s = torch.rand((*shape[:-1], shape[-1] // group), generator=g, device=DEV) + 0.5
