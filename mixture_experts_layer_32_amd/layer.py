@@ -554,7 +554,8 @@ def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16
 class GradNorm:
     """The norm over many gradients together, and their scaling so that it stays within a bound: holds the list of
     tensors and the workspace, for gradients that stay in place from step to step. Calls of one object share the
-    workspace: order them, or give concurrent streams an object each, and keep an object until its calls have run."""
+    workspace: order them, or give concurrent streams an object each, and keep an object until its calls, and the replays of
+    a graph that holds one, have run."""
 
     def __init__(self, grads, out=None):
         """grads: contiguous bf16 and fp32 tensors on the current GPU, which may not overlap. out: where the scaled
