@@ -4,7 +4,7 @@
 //   k_int4_rows   y = sum over groups of s (x q^T) for few rows: 16 at a time, the weight straight from memory into
 //                 registers, K split over a workgroup's waves. Bound by reading the weight (6.6 TB/s with 64 rows among 128
 //                 experts of 1536 x 4096, 31 us), and with one weight by the launch (one row of 1536 x 4096 5.1 us).
-//   k_int4_deep   64 x 64 tiles for products of few tiles: all operands come straight into LDS.
+//   k_int4_deep   64 x 64 and 64 x 128 tiles for products of few: all operands come straight into LDS.
 //   k_int4_tile   256 x 128 and 128 x 128 tiles for products of many: x in LDS, the weight unpacked from registers.
 //                 16384 x 4096 x 2048 270 to 300 us (920 to 1020 TFLOP/s, box to box); a bf16 product of this size by the
 //                 library takes 243, and a loop of this many matrix instructions on such numbers, with nothing else, reached
@@ -676,33 +676,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
 // k_int4_deep: 64 rows by 64 channels, stages of 128 inputs. x, the words of q and the scales go straight into LDS, so
 // that no load's latency stands between a stage's products; 4 waves of 2 x 2 blocks. KG = 2 groups of them share the inputs of
 // a tile, where there is no more than a tile for a CU, and their sums meet in LDS; with more tiles three workgroups of KG = 1
-// share a CU. 256 rows of 4096 x 4096 17 us (KG = 1 21; in stages of 64 inputs with q and scales in registers 33), 4096
-// rows in 64 groups of 1536 x 4096 99 us (157). Bound by the unpacking and the matrix instructions together, 0.35 us a stage
-// and CU: three stages in LDS, or the next one's fragments in registers ahead of time, or 64 x 128 tiles with fewer bytes for
-// a product all took as long or longer (256 rows 17.5, 18.2 and 24 to 28 us).
-template <int PER, int KG>
-__global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Params p) {
-  constexpr int BM = 64, XB = BM * 2 * kTileK, QB = 4 * kTileBytes4, SB = 1024, ST = XB + QB + SB, NS = 4 / PER, NJ = 2;
+// share a CU. WIDE: 64 rows by 128 channels, 4 waves of 4 x 2 blocks side by side, which unpack each number once instead of
+// twice, two workgroups a CU, where there are so many. Bound by the unpacking and the matrix instructions together, 0.35 us
+// a stage of 64 channels and CU (WIDE: 0.29). 256 rows of 4096 x 4096 17 us (KG = 1 21; in stages of 64 inputs with q and
+// scales in registers 33), 4096 rows in 64 groups of 1536 x 4096 82 us (64 channels 99, in registers 157). Three stages in
+// LDS, the next one's fragments in registers ahead of time, or 64 x 128 tiles of 2 x 4 blocks took as long or longer (256
+// rows 17.5, 18.2 and 24 to 28 us).
+template <int PER, int KG, bool WIDE>
+__global__ __launch_bounds__(256 * KG, KG == 2 ? 1 : WIDE ? 2 : 3) void k_int4_deep(I4Params p) {
+  constexpr int BM = 64, XB = BM * 2 * kTileK, NS = 4 / PER, R = WIDE ? 2 : 1, MI = 2 * R, NJ = 2,
+                QB = 4 * R * kTileBytes4, SB = 1024, ST = XB + QB + SB;
   __shared__ __attribute__((aligned(1024))) char smem[KG * 2 * ST];
   __shared__ Groups groups;
-  const int lane = threadIdx.x & 63, w = eng::wave_id() % 4, kg = eng::wave_id() / 4, wm = w / 2, wn = w % 2, c = lane & 15,
-            h = lane >> 4;
+  const int lane = threadIdx.x & 63, w = eng::wave_id() % 4, kg = eng::wave_id() / 4, wn = w % 2, c = lane & 15, h = lane >> 4;
+  const int wm = WIDE ? 0 : w / 2, wr = WIDE ? w / 2 : 0;   // the wave's rows and 64 channels
   char* own = smem + kg * 2 * ST;   // the group's stages
-  const int R64 = rows64(p.N), Kt = (p.K + kTileK - 1) / kTileK;
+  const int R64 = rows64(p.N), ntn = (R64 + R - 1) / R, Kt = (p.K + kTileK - 1) / kTileK;
   const bool wide = p.N % NJ == 0 && reinterpret_cast<uintptr_t>(p.y) % (NJ * (p.f32 ? 4 : 2)) == 0;
   const int mtiles = group_tiles<BM>(p, groups);
-  const XcdRange xr = xcd_range(mtiles * R64);
+  const XcdRange xr = xcd_range(mtiles * ntn);
   for (int tile = xr.first; tile < xr.end; tile += xr.stride) {
-    const int mt = tile / R64, n64 = tile - mt * R64;
+    const int mt = tile / ntn, n64 = (tile - mt * ntn) * R;
     int g, r0, end;
     find_tile<BM>(p, groups, mt, g, r0, end);
     const char* xb = reinterpret_cast<const char*>(static_cast<const bf16*>(p.x) + (size_t)r0 * p.K);
     // A row's 16 chunks of a stage: chunk b of row r lies in slot b ^ (r % 16). This lane moves rows 16 w + 4 j + lane / 16.
     const unsigned K2 = 2u * (unsigned)p.K, x0 = K2 * (16 * w + (lane >> 4)), xlast = K2 * min(end - 1 - r0, BM - 1);
     const unsigned b0 = (lane & 15) ^ (lane >> 4);
-    const int64_t row64 = (int64_t)g * R64 + n64;
-    const uint8_t* qb = tile_at(p.q, row64, w, Kt);
-    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, 0, NS);
+    // 64 channels of the tile (behind the last of all: those again, for nothing)
+    auto row64 = [&](int r) { return (int64_t)g * R64 + min(n64 + r, R64 - 1); };
+    const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64(wr), Kt, 0, 0, NS);
     // Inputs beyond K have zero weights; read for them is another chunk of the same row.
     auto issue = [&](int st, char* to) {
       const char* at = xb + (size_t)st * 2 * kTileK;
@@ -710,15 +713,17 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Param
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         gl2lds_at(at, min(x0 + 4 * j * K2, xlast) + 16 * min(b0 ^ (4 * j), last), to + (4 * w + j) * 1024);
-      gl2lds_at(qb + (size_t)st * kTileBytes4, 16 * lane, to + XB + w * 1024);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        gl2lds_at(tile_at(p.q, row64(r), w, Kt) + (size_t)st * kTileBytes4, 16 * lane, to + XB + (4 * r + w) * 1024);
       // 128 NS bytes, over and over
       gl2lds4_at(ps + (size_t)st * 64 * NS, (4 * lane + 256 * wn) & (128 * NS - 1), to + XB + QB + w * 256);
     };
-    const int eights = holds_8(p.q, row64, Kt);
+    const int eights = holds_8(p.q, row64(wr), Kt);
     using Scales = Scales4<NJ * NS>;
-    f32x4 acc[2][NJ];
+    f32x4 acc[MI][NJ];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     eng::block_sync();   // every wave is done reading the previous tile's stages
@@ -733,19 +738,19 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Param
         place ^= ST;
         if (st + KG < Kt) issue(st + KG, own + place);
         if (KG > 1 && st >= Kt) break;
-        uint4 q[NJ], fa[2][4];
+        uint4 q[NJ], fa[MI][4];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) q[j] = ld16(at + XB + (NJ * wn + j) * 1024 + 16 * lane);
-        const Scales sc = *reinterpret_cast<const Scales*>(at + XB + QB + (4 * c + 2 * wn) * NS * 2);
+        for (int j = 0; j < NJ; ++j) q[j] = ld16(at + XB + (4 * wr + 2 * wn + j) * 1024 + 16 * lane);
+        const Scales sc = *reinterpret_cast<const Scales*>(at + XB + QB + 512 * wr + (4 * c + 2 * wn) * NS * 2);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int s = 0; s < 4; ++s) fa[i][s] = ld16(at + (32 * wm + 16 * i + c) * 256 + 16 * ((4 * s + h) ^ c));
 #pragma unroll
         for (int a = 0; a < NS; ++a) {
-          f32x4 part[2][NJ];
+          f32x4 part[MI][NJ];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) part[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -756,13 +761,13 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Param
               if constexpr (decltype(with8)::value) v = {with_8(v.a), with_8(v.b)};
               const uint4 f = numbers8(v);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) mma16<bf16>(part[i][j], fa[i][s], f);
+              for (int i = 0; i < MI; ++i) mma16<bf16>(part[i][j], fa[i][s], f);
             }
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             const float sf = sc[j * NS + a];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sf, part[i][j][e], acc[i][j][e]);
           }
@@ -772,7 +777,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Param
     if (eights) columns(std::true_type{});
     else columns(std::false_type{});
     // of KG = 2 groups, each stores a row block of its waves: the other's sums of it come through LDS
-    static_assert(KG == 1 || KG == 2, "");
+    static_assert(KG == 1 || (KG == 2 && !WIDE), "");
     if constexpr (KG == 2) {
       eng::block_sync();
       f32x4* red = reinterpret_cast<f32x4*>(smem) + (w * 2 * 64 + lane) * NJ;
@@ -786,9 +791,9 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 3 : 1) void k_int4_deep(I4Param
         for (int e = 0; e < 4; ++e) acc[0][j][e] = (kg ? acc[1][j][e] : acc[0][j][e]) + o[e];
       }
     }
-    const int n1 = 64 * n64 + 4 * c + 2 * wn;
+    const int n1 = 64 * (n64 + wr) + 4 * c + 2 * wn;
 #pragma unroll
-    for (int i = 0; i < 2 / KG; ++i)
+    for (int i = 0; i < MI / KG; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r0 + 32 * wm + 16 * (i + kg) + 4 * h + e;
@@ -806,15 +811,20 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
 }
 
 // The kernel by the rows of a group that has any, as far as the host knows, and by how much work there is. In us, R:
-// rows with TL = 4 (1: with TL = 1), D, DD: deep with one and two groups of waves, 128, 256: tiles of 128 x 128 and
+// rows with TL = 4 (1: with TL = 1), D, DD, DW: deep, with two groups of waves, WIDE, 128, 256: tiles of 128 x 128 and
 // 256 x 128; W: the work in units of 16 rows by 64 channels, on 256 CUs.
 //   rows of 4096 x 4096      16 (W 64): 1 8.4, R 10.2    64 (256): R 10.7, DD 15.3   128 (512): R 16.6, DD 15.7
-//                            256: DD 17, D 21, 128 42    512: D 27, DD 30, 128 43    1024: D 49, 128 46   2048: D 89, 128 72, 256 79
-//   rows of 1536 x 4096      64 (96): 1 12.8, R 10.1     192 (288): R 15.3, DD 15.8  384 (576): R 21, DD 16   2048: D 38, 128 45, 256 70
-//   rows of 16384 x 2048     512: D 47, 128 40, 256 42   768: D 72, 128 56, 256 64   1024: D 93, 128 79, 256 69
-//   64 groups, 1536 x 4096   of 8 rows: R 43, D 68       16: R 60, D 68              24: R 75, D 69   40: D 68, 128 93   64: D 99, 128 94
-//   128 groups, 768 x 2048   of 8 rows: R 30, D 39       16: R 44, D 39              40: D 39, 128 50 64: D 55, 128 52
-//   16 groups, 768 x 2048    of 4 rows (240): 1 9.4, R 8.1   128: D 16, 128 26
+//                            256: DD 17, D 21, 128 42    512: D 27, DD 30, DW 26     1024: D 49, DW 41, 128 46
+//                            1536: DW 57, 128 67         2048: DW 79, 128 72, 256 79
+//   rows of 1536 x 4096      64 (96): 1 12.8, R 10.1     192 (288): R 15.3, DD 15.8  384 (576): R 21, DD 16
+//                            2048: D 37, DW 39, 128 45, 256 70
+//   rows of 16384 x 2048     256: D 25, DW 23, 128 26    512: DW 43, 128 40, 256 42  768: DW 63, 128 57, 256 64
+//                            1024: DW 81, 128 78, 256 69
+//   64 groups, 1536 x 4096   of 8 rows: R 43, DW 60      16: R 60, DW 55   40: D 69, DW 57, 128 93   64: D 101, DW 82, 128 99
+//                            80: DW 104, 128 107         100: DW 109, 128 115
+//   128 groups, 768 x 2048   of 8 rows: R 30, DW 32      16: R 44, DW 32   40: D 39, DW 34, 128 50   64: D 56, DW 49, 128 51
+//                            80: DW 61, 128 52           100: DW 63, 128 54
+//   16 groups, 768 x 2048    of 4 rows (240): 1 9.4, R 8.1   128: D 16, 128 25
 // One row of 32768 x 4096 (W 512): 1 17, R 14; 16384 rows of 2048 x 768 in 64 groups: 256 63, 128 69.
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
@@ -822,7 +832,7 @@ void launch4(const I4Params& p, int grid, hipStream_t s) {
   const int64_t mt = p.offsets ? p.M / kRows4 + groups : (p.M + kRows4 - 1) / kRows4;
   const int64_t work = mt * rows64(p.N);        // 16 rows by 64 channels
   const int Kt = (p.K + kTileK - 1) / kTileK;
-  if (p.M <= 14 * groups || 8 * work <= 9 * grid) {
+  if (p.M <= 12 * groups || 8 * work <= 9 * grid) {
     auto go = [&](auto kernel, int TL) {
       // fewer waves a task where their columns would make less than a unit, as long as every CU keeps its workgroups
       const int64_t wgs = rows_wgs(PER) * grid;
@@ -835,12 +845,14 @@ void launch4(const I4Params& p, int grid, hipStream_t s) {
     else go(k_int4_rows<PER, 4>, 4);
   } else if (p.M >= 192 * groups && 4 * tiles4(p, 256, 128) >= 7 * grid) {
     k_int4_tile<8, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
-  } else if (p.M >= 60 * groups && 4 * tiles4(p, 128, 128) >= 5 * grid) {
+  } else if (p.M >= 72 * groups && tiles4(p, 128, 128) >= 2 * grid) {
     k_int4_tile<4, 4, 2, 2, PER><<<2 * grid, 256, 0, s>>>(p);
+  } else if (tiles4(p, 64, 128) >= 2 * grid) {
+    k_int4_deep<PER, 1, true><<<2 * grid, 256, 0, s>>>(p);
   } else if (tiles4(p, 64, 64) <= grid) {
-    k_int4_deep<PER, 2><<<grid, 512, 0, s>>>(p);
+    k_int4_deep<PER, 2, false><<<grid, 512, 0, s>>>(p);
   } else {
-    k_int4_deep<PER, 1><<<3 * grid, 256, 0, s>>>(p);
+    k_int4_deep<PER, 1, false><<<3 * grid, 256, 0, s>>>(p);
   }
 }
 

@@ -127,7 +127,8 @@ def bound(x, v, s, group):
 SHAPES = [(1, 1, 32), (1, 16, 128), (1, 1536, 4096), (2, 33, 96), (7, 777, 1120), (16, 100, 512), (17, 48, 640), (31, 130, 1024),
           (33, 64, 2048), (64, 256, 1024), (65, 40, 320), (128, 128, 128), (200, 300, 544), (257, 513, 1056), (1000, 96, 768),
           (3, 16, 16384), (700, 1024, 2048), (40, 4096, 512), (200, 2112, 256), (520, 4160, 192), (2100, 4100, 224), (5000, 2056, 160),
-          (300, 1300, 96), (330, 1500, 384), (9000, 1801, 96), (8500, 2048, 160)]
+          (300, 1300, 96), (330, 1500, 384), (9000, 1801, 96), (8500, 2048, 160),
+          (1000, 4100, 160), (1000, 4101, 352)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -157,7 +158,8 @@ GROUPS = [(1, 1, 16, 32, 0, 0, 0), (1, 8, 40, 256, 0, 0, 0), (8, 16, 768, 512, 0
           (50, 7, 33, 160, 1, 3, 5), (300, 5, 100, 416, 1, 11, 30), (1117, 9, 777, 1120, 2, 0, 0), (2000, 130, 64, 256, 1, 0, 7),
           (900, 2, 257, 352, 4, 1, 1), (40, 512, 16, 64, 0, 0, 0), (6, 4, 32, 128, 0, 3, 3),
           (3000, 20, 513, 256, 0, 2, 1), (9000, 24, 640, 192, 1, 0, 9), (700, 200, 130, 128, 0, 0, 0),
-          (14000, 20, 1100, 160, 0.5, 3, 5), (800, 12, 900, 640, 0, 0, 4)]
+          (14000, 20, 1100, 160, 0.5, 3, 5), (800, 12, 900, 640, 0, 0, 4),
+          (3000, 100, 900, 416, 0.5, 2, 3), (9000, 24, 1100, 96, 1, 0, 9)]
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
