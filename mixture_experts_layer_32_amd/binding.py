@@ -131,7 +131,7 @@ def _check(status):
 
 def ptr(t):
     """Device (or host) address of a tensor, an int address, or None (NULL)."""
-    return t if t is None or type(t) is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream):

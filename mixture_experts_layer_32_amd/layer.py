@@ -459,6 +459,8 @@ def combine_backward(dy, rows, weight, pair_pos, idx=None, E_total=None, drows=N
         raise ValueError("expected both idx and E_total, or neither")
     if idx is not None:
         _expect(idx, "idx", (T, k), torch.int32, dev)
+        if not 0 < E_total < 2 ** 31:
+            raise ValueError(f"E_total: expected a positive 32-bit number, got {E_total}")
     if drows is None:
         drows = _empty((n, H), rows.dtype, rows, stream)
     else:

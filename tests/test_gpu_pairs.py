@@ -344,7 +344,9 @@ def test_wrong_tensors_are_refused():
                  lambda: combine_backward(x, x, w, idx, idx=idx), lambda: combine_backward(x, x, w, idx, E_total=4),
                  lambda: combine_backward(x[:3], x, w, idx), lambda: combine_backward(x, x, None, idx),
                  lambda: combine_backward(x, x, w, idx, drows=x[:3]), lambda: sort_pairs(idx, 2 ** 32 + 4),
-                 lambda: sort_pairs(idx, 4, 2 ** 32)):
+                 lambda: sort_pairs(idx, 4, 2 ** 32),
+                 lambda: combine_backward(x, x, w, idx, idx=idx, E_total=2 ** 32 + 128),
+                 lambda: combine_backward(x, x, w, idx, idx=idx, E_total=0)):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: sort_pairs(idx, 0), lambda: sort_pairs(idx, 4, -1),
