@@ -247,6 +247,30 @@ def test_more_than_two_to_the_31_numbers():
     assert y.numel() > 2 ** 31 and bool((y[:-1] == 64).all()) and bool((y[-1] == 192).all())
 
 
+def test_weights_of_2_to_the_22_runs_of_64_channels():
+    """More of them than a launch takes workgroups of 1024 threads along one dimension."""
+    G, N, K = 256, 1 << 20, 32
+    g = gen(12)
+    assert G * N // 64 == 1 << 22
+    v = torch.randint(-7, 8, (G, N, K), generator=g, device=DEV, dtype=torch.int8)
+    at = [0, 127, 128, 255]                        # groups on both sides of the first 2^21 runs, and the last
+    for e in at:
+        v[e, 5::640, 7] = -8
+    s = torch.ones((G, N, 1), dtype=torch.bfloat16, device=DEV)
+    q, sc = int4_pack(v, s)
+    x = torch.randint(-4, 5, (G, K), generator=g, device=DEV).to(torch.bfloat16)
+    y = int4_matmul(x, q, sc, offsets=torch.arange(G + 1, dtype=torch.int32, device=DEV), dtype=torch.float32)
+    for e in range(G):
+        assert torch.equal(y[e], v[e].float() @ x[e].float())        # whole numbers below 2^24: exact
+    del q, sc, y, s
+    w = v.to(torch.bfloat16)
+    del v
+    q, sc = int4_quantize(w, 32)
+    for e in at:
+        one_q, one_s = int4_quantize(w[e], 32)
+        assert torch.equal(q[e], one_q) and torch.equal(sc[e], one_s)
+
+
 def test_rows_that_pass_4_gib():
     """x of more than 2^32 bytes in one group: rows of the first tiles, of the last and of one between, among zeros."""
     M, N, K = 2 ** 14 + 3, 64, 2 ** 17
