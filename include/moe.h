@@ -355,8 +355,8 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
  * A weight [N, K] is held as whole numbers q of -8..7 and one bf16 scale for each `group` (32, 64 or 128) consecutive
  * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory 64 channels follow one another, and the weights
  * of [G, N, K] likewise; 64 channels hold four tiles a 128 inputs, [4][ceil(K/128)][1024] bytes in the order in which a
- * wavefront takes them, tile t holding the channels n with n % 4 = t, and then 16 bytes, a 32-bit word that is 0 if no
- * number is -8, and zeros or anything. Their scales are [ceil(K/128)][64][128 / group]. Padding has q = 0, s = 0.
+ * wavefront takes them, tile t holding the channels n with n % 4 = t, and then 16 bytes: a 32-bit word that is 0 if no
+ * number is -8, one that is 0x4b000000 + K or (not telling) any with other high bits, and anything. Their scales are [ceil(K/128)][64][128 / group]. Padding has q = 0, s = 0.
  * With c = n % 64 / 4, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] lies in the 32-bit word
  * (16 h + c) * 4 + i of its tile as a sign (1: q < 0) and m = |q| % 8: for j < 4, m in the three bits from bit 8 j and the
  * sign in bit 8 j + 7; for j >= 4, m from bit 8 (j - 4) + 4 and the sign in bit (8 (j - 4) + 11) % 32. */
@@ -376,7 +376,8 @@ moe_status moe_int4_pack(const int8_t* values, const void* in_scales, int G, int
 
 /* y[m, n] = sum over the groups of s[g, n, group] * (sum over the group's inputs of x[m, k] q[g, n, k]): x [M, K] bf16, y
  * [M, N] of `type`, rounded once; products exact, sums in fp32. offsets, groups of rows, and the rows of y outside of
- * them as in moe_int8_matmul. A NaN or an infinity in a row of x makes values of that row of y NaN or infinite, and no
+ * them as in moe_int8_matmul. With another K of the same ceil(K/128) than the weight was laid out for, which no check on
+ * the host can see, y is NaN. A NaN or an infinity in a row of x makes values of that row of y NaN or infinite, and no
  * other's. 0 <= M <= 2^31 - 512, M*N < 2^40, the rest as above. x, q and scales need 16-byte alignment, offsets 4-byte, y
  * its type's (8-byte, fp32 16-byte, and N % 4 = 0 write faster). */
 moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, int64_t M, int64_t N, int64_t K,

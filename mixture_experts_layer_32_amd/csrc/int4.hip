@@ -31,13 +31,27 @@ constexpr int kTileN = 16, kTileK = 128, kTileBytes4 = 1024, kFlagBytes = 16;
 // holds four neighbouring channels in a lane.
 __host__ __device__ constexpr int rows64(int N) { return (N + 63) / 64; }
 __device__ __forceinline__ int channel4(int nt, int c) { return nt / 4 * 64 + 4 * c + nt % 4; }
-// 64 channels (row64 over all weights): their tiles, and behind them the word that says whether one holds a -8
+// 64 channels (row64 over all weights): their tiles, and behind them a word that says whether one holds a -8 and one
+// that says K, of which the tiles themselves know no more than ceil(K / 128)
 __device__ __forceinline__ size_t row_bytes(int Kt) { return (size_t)4 * Kt * kTileBytes4 + kFlagBytes; }
 __device__ __forceinline__ const uint8_t* tile_at(const uint8_t* q, int64_t row64, int t, int Kt) {
   return q + row64 * row_bytes(Kt) + (size_t)t * Kt * kTileBytes4;
 }
 __device__ __forceinline__ int holds_8(const uint8_t* q, int64_t row64, int Kt) {
   return eng::ld_uniform(reinterpret_cast<const int*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4), 0);
+}
+constexpr unsigned kSaysK = 0x4b000000u;   // ahead of K in that word; without it K is not said
+__device__ __forceinline__ unsigned says_K(const uint8_t* q, int64_t row64, int Kt) {
+  return (unsigned)eng::ld_uniform(reinterpret_cast<const int*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4), 1);
+}
+// x has another number of inputs than the weight was laid out for: y is NaN then. (Compared behind the products, so that
+// nothing waits for the word ahead of them.)
+__device__ __forceinline__ bool other_K(unsigned says, int K) {
+  return (says & 0xff000000u) == kSaysK && says != (kSaysK | (unsigned)K);
+}
+__device__ __forceinline__ f32x4 nan4() {
+  const float v = __builtin_nanf("");
+  return f32x4{v, v, v, v};
 }
 // the first scale of channel n of 64 in tile column kb, of ng each
 __device__ __forceinline__ size_t scale_at(int64_t row64, int Kt, int kb, int n, int ng) {
@@ -105,10 +119,11 @@ struct Scales4<1> {
 constexpr int kPackWaves = 16;
 constexpr int kPackGrid = 1 << 21;   // workgroups along the channels at most, the rest in their loops
 
-// The words that say whether there is a -8, 0 ahead of y > 1 workgroups that may find one.
-__global__ __launch_bounds__(256) void k_int4_none(uint8_t* q, int64_t n, int Kt) {
+// The words behind the channels, that of -8 still 0, ahead of y > 1 workgroups that may find one.
+__global__ __launch_bounds__(256) void k_int4_none(uint8_t* q, int64_t n, int K) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (r < n) *reinterpret_cast<uint4*>(q + (r + 1) * row_bytes(Kt) - kFlagBytes) = make_uint4(0u, 0u, 0u, 0u);
+  const int Kt = (K + kTileK - 1) / kTileK;
+  if (r < n) *reinterpret_cast<uint4*>(q + (r + 1) * row_bytes(Kt) - kFlagBytes) = make_uint4(0u, kSaysK | (unsigned)K, 0u, 0u);
 }
 
 template <int KIND>
@@ -202,7 +217,7 @@ __global__ __launch_bounds__(kPackWaves * 64) void k_int4_pack(const void* __res
     if (KIND == 2 && gridDim.y > 1) {
       if (threadIdx.x == 0 && any) atomicOr(flag, 1u);
     } else if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) {
-      flag[threadIdx.x] = any != 0;
+      flag[threadIdx.x] = threadIdx.x == 0 ? any != 0 : threadIdx.x == 1 ? kSaysK | (unsigned)K : 0u;
     }
   }
 }
@@ -313,11 +328,13 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
   const uint8_t* pq;
   const uint16_t* ps;
   int eights, eights_next;
+  unsigned says, says_next;
   auto at = [&] {
     const int64_t row64 = (int64_t)g * (Nt / 4) + nt / 4;
     pq = tile_at(p.q, row64, nt % 4, Kt);
     ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
     eights_next = holds_8(p.q, row64, Kt);
+    says_next = says_K(p.q, row64, Kt);
   };
   auto load = [&](int b) {   // (behind the wave's last column: that one again, which is not added)
     const int k = max(min(kb + b, k1 - 1), 0);
@@ -341,6 +358,7 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
   while (task < tasks) {
     const int mr0 = r0, mcnt = cnt, n0 = task % ntn * W.wt;
     eights = eights_next;
+    says = says_next;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int mkb = k0;;) {
       const int n = k1 - mkb;   // columns from this unit on
@@ -373,6 +391,7 @@ __device__ __forceinline__ void tasks_few(const I4Params& p, const Groups& group
       mkb += kUnit;
       if (mkb >= k1) break;
     }
+    if (other_K(says, p.K)) acc = nan4();
     f32x4* to = red + parity * kRowWaves * 64;
     parity ^= 1;
     to[threadIdx.x] = acc;
@@ -407,11 +426,13 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
   const uint8_t* pq;
   const uint16_t* ps;
   int eights, eights_next;
+  unsigned says, says_next;
   auto at = [&] {
     const int64_t row64 = (int64_t)g * (Nt / 4) + nt / 4;
     pq = tile_at(p.q, row64, nt % 4, Kt);
     ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
     eights_next = holds_8(p.q, row64, Kt);
+    says_next = says_K(p.q, row64, Kt);
   };
   auto column = [&] { return max(min(kb, k1 - 1), 0); };
   auto load = [&](int t) { q[t] = ld_at<uint4>(pq + ((size_t)t * Kt + column()) * kTileBytes4, 16 * lane); };
@@ -431,6 +452,7 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
   while (task < tasks) {
     const int mr0 = r0, mcnt = cnt, n0 = task % ntn * per;
     eights = eights_next;
+    says = says_next;
     f32x4 acc[TL];
 #pragma unroll
     for (int t = 0; t < TL; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -463,6 +485,10 @@ __device__ __forceinline__ void tasks_more(const I4Params& p, const Groups& grou
       }
       if (++mkb >= k1) break;
     }
+    if (other_K(says, p.K))
+#pragma unroll
+      for (int t = 0; t < TL; ++t)
+        acc[t] = nan4();
     __syncthreads();   // the previous task's sums are read
 #pragma unroll
     for (int t = 0; t < TL; ++t) red[(eng::wave_id() * TL + t) * 64 + lane] = acc[t];
@@ -579,6 +605,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     const uint8_t* qb = tile_at(p.q, row64, nt % 4, Kt);
     const uint16_t* ps = static_cast<const uint16_t*>(p.s) + scale_at(row64, Kt, 0, nt % 4, NS);
     const int eights = holds_8(p.q, row64, Kt);
+    const unsigned says = says_K(p.q, row64, Kt);
     using Scales = Scales4<NJ * NS>;
     uint4 q[NJ], fb[2][NJ];
     Scales sc, sn;
@@ -662,6 +689,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
     };
     if (eights) columns(std::true_type{});
     else columns(std::false_type{});
+    if (other_K(says, p.K))
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = nan4();
     eng::wait_vm<0>();
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -722,6 +754,7 @@ __global__ __launch_bounds__(256 * KG, KG == 2 ? 1 : WIDE ? 2 : 3) void k_int4_d
       gl2lds4_at(ps + (size_t)st * 64 * NS, (4 * lane + 256 * wn) & (128 * NS - 1), to + XB + QB + w * 256);
     };
     const int eights = holds_8(p.q, row64(wr), Kt);
+    const unsigned says = says_K(p.q, row64(wr), Kt);
     using Scales = Scales4<NJ * NS>;
     f32x4 acc[MI][NJ];
 #pragma unroll
@@ -778,6 +811,11 @@ __global__ __launch_bounds__(256 * KG, KG == 2 ? 1 : WIDE ? 2 : 3) void k_int4_d
     };
     if (eights) columns(std::true_type{});
     else columns(std::false_type{});
+    if (other_K(says, p.K))
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = nan4();
     // of KG = 2 groups, each stores a row block of its waves: the other's sums of it come through LDS
     static_assert(KG == 1 || (KG == 2 && !WIDE), "");
     if constexpr (KG == 2) {
@@ -879,7 +917,7 @@ hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G,
   // (a dimension of a grid holds less than 2^32 threads)
   const dim3 grid((unsigned)std::min<int64_t>(tiles, kPackGrid),
                   (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)));
-  if (scales && grid.y > 1) k_int4_none<<<(unsigned)((tiles + 255) / 256), 256, 0, s>>>(q, tiles, Kt);
+  if (scales && grid.y > 1) k_int4_none<<<(unsigned)((tiles + 255) / 256), 256, 0, s>>>(q, tiles, K);
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);
   if (scales) k_int4_pack<2><<<grid, kPackWaves * 64, 0, s>>>(in, si, tiles, N, K, group, q, so);

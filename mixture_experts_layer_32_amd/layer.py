@@ -518,7 +518,8 @@ def int4_pack(values, scales, stream=None):
 def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16, stream=None):
     """y [M, N] of bf16 rows x [M, K] and a weight in 4 bits, (q, scales) of int4_quantize or int4_pack on [N, K], or
     on [G, N, K] with offsets [G + 1] int32: rows offsets[g] .. offsets[g+1]-1 are multiplied by weight g. N is
-    needed where it is no multiple of 64 (and y is not given). A y that is given sets the dtype, and its rows outside
+    needed where it is no multiple of 64 (and y is not given). The weight's K is checked here to whole 128 inputs; y is
+    NaN where x has another K than the weight within them. A y that is given sets the dtype, and its rows outside
     the groups are left as they were (a y made here holds anything there)."""
     if (not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(q, torch.Tensor)
             or q.dim() != (2 if offsets is None else 3) or not isinstance(scales, torch.Tensor)

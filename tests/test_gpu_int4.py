@@ -336,6 +336,51 @@ def test_odd_addresses_of_y():
             assert bool((buf[:1] == 4).all()) and bool((buf[1 + M * 50:] == 4).all())
 
 
+# shapes for each of the kernels that the library chooses from (on 256 CUs): few rows by 1 and by 4 tiles a wave (5 and
+# more rows by one tile the other form of the first), 64 x 64 tiles with two groups of waves and with one, 64 x 128,
+# 128 x 128 and 256 x 128 tiles
+KERNELS = [pytest.param(3, 100, id="rows1_few"), pytest.param(60, 100, id="rows1"), pytest.param(12, 20000, id="rows4"),
+           pytest.param(330, 1500, id="deep2"), pytest.param(520, 2080, id="deep1"), pytest.param(2100, 2080, id="wide"),
+           pytest.param(2100, 4100, id="tile128"), pytest.param(8500, 2048, id="tile256")]
+
+
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_another_width_than_the_weights_is_seen(M, N):
+    """K within the same 128 inputs cannot be told from the tensors' shapes; the tiles say it, and y is NaN."""
+    g = gen(M)
+    v, s = rand_weight((N, 256), 32, g, exact=True)
+    x = torch.randint(-4, 5, (M, 256), generator=g, device=DEV).to(torch.bfloat16)
+    whole, less = int4_pack(v, s), int4_pack(v[:, :224].contiguous(), s[:, :7].contiguous())
+    narrow = x[:, :224].contiguous()
+    for out in (torch.bfloat16, torch.float32):
+        assert bool(int4_matmul(narrow, *whole, N=N, dtype=out).isnan().all())
+        assert bool(int4_matmul(x, *less, N=N, dtype=out).isnan().all())
+        assert torch.equal(int4_matmul(narrow, *less, N=N, dtype=out), (narrow.double() @ real(v[:, :224], s[:, :7], 32).T).to(out))
+    quantised = int4_quantize(real(v, s, 32).float()[:, :224].contiguous(), 32)
+    assert bool(int4_matmul(x, *quantised, N=N).isnan().all())
+    assert bool(torch.isfinite(int4_matmul(narrow, *quantised, N=N)).all())
+    for words in ((1, 1, 1), (0, 0, 0), (-1, -1, -1)):                # tiles whose words do not tell K
+        q = whole[0].clone()
+        q[:, -12:].view(torch.int32)[:] = torch.tensor(words, dtype=torch.int32, device=DEV)
+        assert torch.equal(int4_matmul(x, q, whole[1], N=N), int4_matmul(x, *whole, N=N))
+
+
+@pytest.mark.parametrize("M,G,N", [(40, 9, 70), (700, 9, 1000), (1000, 9, 1300), (3000, 100, 900), (3000, 20, 2080), (9000, 5, 2048)])
+def test_another_width_in_one_group(M, G, N):
+    g = gen(G)
+    v, s = rand_weight((G, N, 128), 32, g, exact=True)
+    q, sc = int4_pack(v, s)
+    q[2] = int4_pack(v[2, :, :96].contiguous(), s[2, :, :3].contiguous())[0]
+    x = torch.randint(-4, 5, (M, 128), generator=g, device=DEV).to(torch.bfloat16)
+    off = offsets_of(M, G, g, 0)
+    y = int4_matmul(x, q, sc, offsets=off, N=N, dtype=torch.float32)
+    for e, (a, z) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        if e == 2:
+            assert z > a and bool(y[a:z].isnan().all())
+        else:
+            assert torch.equal(y[a:z], (x[a:z].double() @ real(v[e], s[e], 32).T).float())
+
+
 def test_wrong_tensors_are_refused():
     g = gen(1)
     v, s = rand_weight((32, 128), 64, g)
