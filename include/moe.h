@@ -343,7 +343,8 @@ moe_status moe_combine(const void* rows, int rows_type, int64_t nrows, const int
  * moe_route's:
  *   dlogits[t, idx[t, j]] = weight[t, j] * (dweight[t, j] - sum_i weight[t, i] dweight[t, i])
  * [T, E_total] fp32, 0 elsewhere; slots of one token that name the same expert add up, an idx outside
- * 0..E_total-1 gets none. E_total <= 512. In an expert share dweight and dlogits are its linear contribution, as moe_bwd's.
+ * 0..E_total-1 gets none. E_total <= 512. The sum is over the slots with a position: what another slot's weight is, NaN or
+ * infinite too, reaches its own dlogit alone. In an expert share dweight and dlogits are its linear contribution, as moe_bwd's.
  * Sums in fp32 in a fixed order. */
 moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_type, int64_t nrows,
                            const int32_t* pair_pos, const float* weight, const int32_t* idx, int64_t T, int topk,

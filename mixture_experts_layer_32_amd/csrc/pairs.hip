@@ -530,7 +530,7 @@ __global__ __launch_bounds__(256) void k_pairs_combine_bwd(PairsParams p) {
     if (lane < p.k) p.dweight[t * p.k + lane] = dw;
     if (!p.dlogits) continue;
     const int ex = lane < p.k ? p.idx[t * p.k + lane] : -1;
-    const float prod = wl * dw;
+    const float prod = pos >= 0 ? wl * dw : 0.f;   // (the weight of a slot without a position may be anything)
     float mean = 0.f;
     for (int j = 0; j < p.k; ++j) mean += lane_value(prod, j);
     const float dl = wl * (dw - mean);

@@ -207,6 +207,27 @@ def test_masked_rows_are_neither_read_nor_written():
     assert bool(torch.isinf(y[1]).all()) and bool(torch.isfinite(y[[0, 2]]).all())
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H", [40, 1024, 5000])
+def test_weights_of_masked_slots_reach_nothing_else(H, value):
+    """A slot without a position adds nothing to y; its weight reaches no gradient but its own logit's."""
+    idx = torch.tensor([[0, -1, 2], [3, 1, 4], [-1, -1, -1]], dtype=torch.int32, device=DEV)
+    pos = torch.tensor([[0, -1, 3], [2, 1, -1], [-1, -1, -1]], dtype=torch.int32, device=DEV)
+    g = gen(H)
+    rows, dy = torch.randn(4, H, generator=g).to(DEV), torch.randn(3, H, generator=g).to(DEV)
+    w = torch.rand(3, 3, generator=g).to(DEV)
+    bad = torch.where(pos < 0, value, w)
+
+    def gradients(weight):
+        return combine_backward(dy, rows, weight, pos, idx=idx, E_total=6, drows=torch.zeros_like(rows))
+    assert torch.equal(combine(rows, pos, bad), combine(rows, pos, w))
+    (drows, dw, dl), (want_rows, want_dw, want_dl) = gradients(bad), gradients(w)
+    assert torch.equal(drows, want_rows) and torch.equal(dw, want_dw)
+    own = torch.zeros(3, 6, dtype=torch.bool, device=DEV)
+    own[1, 4] = True                               # the masked slot with an expert: weight (0 - sum)
+    assert torch.equal(dl[~own], want_dl[~own]) and not bool(torch.isfinite(dl[own]).any())
+
+
 def test_gradients_against_differences():
     """Of rows and weights, in which y is linear, the differences are exact but for rounding; of the logits, through the
     softmax over the chosen experts, central differences in 64 bits."""
