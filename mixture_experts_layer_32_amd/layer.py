@@ -556,9 +556,11 @@ def int4_matmul(x, q, scales, offsets=None, N=None, y=None, dtype=torch.bfloat16
 
 class GradNorm:
     """The norm over many gradients together, and their scaling so that it stays within a bound: holds the list of
-    tensors and the workspace, for gradients that stay in place from step to step. Calls of one object share the
-    workspace: order them, or give concurrent streams an object each, and keep an object until its calls, and the replays of
-    a graph that holds one, have run."""
+    tensors, their addresses and the workspace, for gradients that stay in place from step to step. Gradients that are new
+    tensors at each step need a new object each (1.5 to 3 us of host time a tensor), or buffers that they are copied to. A
+    tensor whose storage was resized, or which has been given another one, is refused at the next call (of tensors that
+    share a storage, the first is looked at). Calls of one object share the workspace: order them, or give concurrent
+    streams an object each, and keep an object until its calls, and the replays of a graph that holds one, have run."""
 
     def __init__(self, grads, out=None):
         """grads: contiguous bf16 and fp32 tensors on the current GPU, which may not overlap. out: where the scaled
@@ -584,7 +586,20 @@ class GradNorm:
         for (a, n, name), (b, _, other) in zip(spans, spans[1:]):
             if b < a + n:
                 raise ValueError(f"{name} and {other} overlap")
+        # The storages that the addresses lie in are kept, so that they stay memory of these tensors, and one tensor of
+        # each is asked for its address at every call: a storage that is resized has another.
+        self._storages, self._watched = {}, []
+        for t in self.grads + (self.out or []):
+            s = t.untyped_storage()
+            if t.numel() and s._cdata not in self._storages:
+                self._storages[s._cdata] = s
+                self._watched.append((t.data_ptr, t.data_ptr()))
         self.ws = _workspace(max(256, binding.query_norm_sizes(self._in, len(self.grads))), self.device)
+
+    def _in_place(self):
+        for address, was in self._watched:
+            if address() != was:
+                raise ValueError("a tensor's memory is another than when the object was made: make a new one")
 
     def _table(self, tensors, name):
         table = (binding.Tensor * len(tensors))()
@@ -598,6 +613,7 @@ class GradNorm:
     def norm(self, stream=None):
         """The norm, an fp32 tensor without dimensions on the device."""
         handle = _on(self.device, stream)
+        self._in_place()
         norm = _empty((), torch.float32, self.ws, stream)
         binding.moe_grad_norm(self._in, len(self.grads), norm, self.ws, self.ws.numel(), handle)
         return norm
@@ -606,6 +622,7 @@ class GradNorm:
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)) and returns the norm: their own, or the one given (an
         fp32 tensor of one element, such as a norm over all ranks' gradients)."""
         handle = _on(self.device, stream)
+        self._in_place()
         n = len(self.grads)
         if norm is None:
             norm = _empty((), torch.float32, self.ws, stream)

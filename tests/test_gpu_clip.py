@@ -163,6 +163,52 @@ def test_on_a_given_stream(kind):
     assert all(torch.equal(a, o) for a, o in zip(kept, plan.out))
 
 
+def other_storage(t):
+    t.untyped_storage().resize_(0)
+
+
+def other_data(t):
+    t.data = torch.ones(300, device=DEV)
+
+
+def other_set(t):
+    t.set_(torch.ones(300, device=DEV))
+
+
+def larger(t):
+    t.resize_(1 << 22)
+
+
+@pytest.mark.parametrize("change", [other_storage, other_data, other_set, larger])
+def test_tensors_with_other_memory_are_refused(change):
+    """Addresses are kept from the making on: a tensor whose memory is another by now is seen, and nothing is written."""
+    for which, into in ((i, o) for i in range(3) for o in (False, True)):
+        ts = [torch.full((n,), 2.0, device=DEV) for n in (300, 9000, 300)]
+        out = [torch.full_like(t, 3.0) for t in ts] if into else None
+        plan = GradNorm(ts, out)
+        plan.clip(1e9)
+        changed = out or ts
+        change(changed[which])
+        for call in (lambda: plan.norm(), lambda: plan.clip(1e-3), lambda: plan.clip(1e-3, norm=torch.ones((), device=DEV))):
+            with pytest.raises(ValueError, match="memory"):
+                call()
+        for i, t in enumerate(changed):
+            assert i == which or bool((t == 2).all())
+    # tensors behind one another in one storage
+    buf = torch.full((9600,), 2.0, device=DEV)
+    plan = GradNorm([buf[300:], buf[:300], buf[:0]])
+    norm = plan.clip(1.0)
+    buf.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="memory"):
+        plan.clip(1.0)
+    assert abs(float(norm) - 2 * 9600 ** 0.5) <= 2e-5
+    # a view that shares its storage with others and is given another: the old memory stays the object's
+    a, b = torch.full((600,), 2.0, device=DEV).split(300)
+    plan = GradNorm([a, b])
+    b.data = torch.ones(5, device=DEV)
+    assert abs(float(plan.norm()) - 2 * 600 ** 0.5) <= 1e-5
+
+
 def test_wrong_norms_and_bounds_are_refused():
     plan = GradNorm([torch.ones(4, device=DEV)])
     for norm in (1.0, torch.ones(2, device=DEV), torch.ones((), device=DEV, dtype=torch.float64), torch.ones(())):
