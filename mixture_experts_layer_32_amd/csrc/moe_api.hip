@@ -1297,8 +1297,9 @@ moe_status pairs_checks(int64_t T, int topk, int64_t H, int64_t nrows) {
     return fail(MOE_ERR_INVALID_ARG, "topk and H must be positive, T and nrows >= 0");
   if (topk > kMaxTopk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "topk must be <= 32");
   if (T > INT32_MAX / topk) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*topk must be < 2^31");
-  constexpr int64_t most = int64_t(1) << 40;
-  if (H >= most / std::max<int64_t>(T, 1) || H >= most / std::max<int64_t>(nrows, 1)) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*H and nrows*H must be < 2^40");
+  constexpr int64_t most = (int64_t(1) << 40) - 1;
+  if (H > most / std::max<int64_t>(T, 1) || H > most / std::max<int64_t>(nrows, 1))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T*H and nrows*H must be < 2^40");
   return MOE_OK;
 }
 }  // namespace

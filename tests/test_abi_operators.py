@@ -101,6 +101,17 @@ def test_pairs_arguments():
     refused(MODE, lambda: combine_bwd(rows_type=2))
 
 
+def test_pairs_sizes_up_to_the_limit():
+    """T*H and nrows*H just below 2^40 (3 divides 2^40 - 1), in calls that have nothing to do."""
+    H = (2 ** 40 - 1) // 3
+    dispatch(T=3, H=H, nrows=0, rows=None)
+    combine(T=0, H=H, nrows=3)
+    combine_bwd(T=0, H=H, nrows=3)
+    for call in (lambda h: dispatch(T=3, H=h, nrows=0, rows=None), lambda h: combine(T=0, H=h, nrows=3),
+                 lambda h: combine_bwd(T=0, H=h, nrows=3)):
+        refused(SHAPE, lambda: call(H + 1), "2\\^40")
+
+
 def test_without_tokens_or_rows_there_is_nothing_to_do():
     dispatch(T=0, x=None, pair_pos=None)
     dispatch(nrows=0, rows=None)
