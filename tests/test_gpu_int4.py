@@ -344,6 +344,161 @@ KERNELS = [pytest.param(3, 100, id="rows1_few"), pytest.param(60, 100, id="rows1
            pytest.param(2100, 4100, id="tile128"), pytest.param(8500, 2048, id="tile256")]
 
 
+GROUPED = [pytest.param(40, 9, 72, id="rows1"), pytest.param(100, 9, 4096, id="rows4"), pytest.param(700, 9, 1000, id="deep2"),
+           pytest.param(1000, 9, 1300, id="deep1"), pytest.param(3000, 100, 900, id="wide"),
+           pytest.param(3000, 20, 2080, id="tile128"), pytest.param(9000, 5, 2048, id="tile256")]
+# inputs of 5 and more times 128, an odd and an even number of them, whole ones and 32, 64 and 96 more; groups
+LONG = [(640, 128), (1120, 32), (1152, 64), (1184, 32), (1216, 64), (2048, 32), (2048, 64), (2048, 128)]
+
+
+@pytest.mark.parametrize("K,group", LONG)
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_long_rows_on_every_kernel(M, N, K, group):
+    g = gen(M + K)
+    x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
+    for low in (-8, -7):
+        v, s = rand_weight((N, K), group, g, exact=True, low=low)
+        want = x.double() @ real(v, s, group).T     # quarters below 2^19: exact in fp32
+        assert torch.equal(int4_matmul(x, *int4_pack(v, s), N=N, dtype=torch.float32), want.float())
+
+
+@pytest.mark.parametrize("K,group", [(640, 128), (1120, 32), (1216, 64), (2048, 128)])
+@pytest.mark.parametrize("M,G,N", GROUPED)
+def test_long_rows_in_groups(M, G, N, K, group):
+    g = gen(M + K)
+    off = offsets_of(M, G, g, 0.3, 3, 4)
+    v, s = rand_weight((G, N, K), group, g, exact=True)
+    v[::2].clamp_(min=-7)
+    x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
+    want = torch.full((M, N), 6.0, device=DEV)
+    y = want.clone()
+    bounds = off.tolist()
+    for e in range(G):
+        want[bounds[e]:bounds[e + 1]] = (x[bounds[e]:bounds[e + 1]].double() @ real(v[e], s[e], group).T).float()
+    int4_matmul(x, *int4_pack(v, s), offsets=off, y=y)
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("K", [256, 352])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_values_that_are_not_finite_on_every_kernel(M, N, K):
+    g = gen(M)
+    v, s = rand_weight((N, K), 32, g, exact=True)
+    x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
+    want = (x.double() @ real(v, s, 32).T).float()
+    bad = torch.zeros(M, dtype=torch.bool, device=DEV)
+    for r, k, value in ((M // 2, 77, float("nan")), (M - 1, K - 1, float("inf")), (0, 3, -float("inf"))):
+        x[r, k], bad[r] = value, True
+    y = int4_matmul(x, *int4_pack(v, s), N=N, dtype=torch.float32)
+    assert torch.equal(y[~bad], want[~bad]) and not bool(torch.isfinite(y[bad]).any())
+    s[5, 1], s[N - 1, K // 32 - 1] = float("nan"), float("inf")            # groups' scales: their channels alone
+    v[N - 1, K - 32:] = 1
+    x[:, K - 32:] = 1
+    want = (x.double() @ real(v, torch.where(torch.isfinite(s), s, 1), 32).T).float()
+    y = int4_matmul(x, *int4_pack(v, s), N=N, dtype=torch.float32)
+    keep = torch.ones(N, dtype=torch.bool, device=DEV)
+    keep[5] = keep[N - 1] = False
+    assert bool(y[:, 5].isnan().all()) and bool(torch.isinf(y[~bad][:, N - 1]).all())
+    bad[M - 1] = False                              # (that infinity stood among the last inputs)
+    assert torch.equal(y[~bad][:, keep], want[~bad][:, keep])
+
+
+@pytest.mark.parametrize("M,G,N", GROUPED)
+def test_rows_of_other_groups_that_are_not_finite(M, G, N):
+    """The rows at the groups' ends, and those outside of all groups, hold NaN: the rows beside them do not see it."""
+    g = gen(M)
+    K = 224
+    off = offsets_of(M, G, g, 0, 3, 4)
+    v, s = rand_weight((G, N, K), 32, g, exact=True)
+    x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(torch.bfloat16)
+    want = torch.full((M, N), 6.0, device=DEV)
+    bounds = off.tolist()
+    for e in range(G):
+        want[bounds[e]:bounds[e + 1]] = (x[bounds[e]:bounds[e + 1]].double() @ real(v[e], s[e], 32).T).float()
+    x[:3] = float("nan")
+    x[M - 4:] = float("inf")
+    bad = torch.zeros(M, dtype=torch.bool, device=DEV)
+    for e in range(0, G, 2):
+        if bounds[e + 1] > bounds[e]:
+            x[bounds[e + 1] - 1], bad[bounds[e + 1] - 1] = float("nan"), True
+    y = torch.full((M, N), 6.0, device=DEV)
+    int4_matmul(x, *int4_pack(v, s), offsets=off, y=y)
+    assert torch.equal(y[~bad], want[~bad]) and bool(y[bad].isnan().all())
+
+
+@pytest.mark.parametrize("M,G,N", GROUPED)
+def test_offsets_outside_the_rows_on_every_kernel(M, G, N):
+    g = gen(G)
+    v, s = rand_weight((G, N, 160), 32, g, exact=True)
+    w = int4_pack(v, s)
+    x = torch.randint(-4, 5, (M, 160), generator=g, device=DEV).to(torch.bfloat16)
+    off = offsets_of(M, G, g, 0)
+    off[-2] = M                                     # the last group is empty
+    good = int4_matmul(x, *w, N=N, offsets=off, dtype=torch.float32)
+    far = off.clone()
+    far[0], far[-2], far[-1] = -2 ** 31, M + 1, 2 ** 31 - 1
+    assert torch.equal(int4_matmul(x, *w, N=N, offsets=far, dtype=torch.float32), good)
+    off[:] = torch.where(torch.arange(G + 1, device=DEV) > G // 2, M, 0)     # one group has every row
+    want = (x.double() @ real(v[G // 2], s[G // 2], 32).T).float()
+    assert torch.equal(int4_matmul(x, *w, N=N, offsets=off, dtype=torch.float32), want)
+
+
+@pytest.mark.parametrize("M,G,N", GROUPED)
+def test_captured_and_replayed_on_every_kernel(M, G, N):
+    g = gen(N)
+    v, s = rand_weight((G, N, 384), 64, g, exact=True)
+    w = int4_pack(v, s)
+    x = torch.zeros((M, 384), dtype=torch.bfloat16, device=DEV)
+    off = torch.zeros(G + 1, dtype=torch.int32, device=DEV)
+    y = torch.zeros((M, N), device=DEV)
+    int4_matmul(x, *w, offsets=off, y=y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        int4_matmul(x, *w, offsets=off, y=y)
+    for i in range(4):
+        x.copy_(torch.randint(-4, 5, (M, 384), generator=g, device=DEV))
+        off.copy_(offsets_of(M, G, g, 0.5 * i))
+        y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        assert torch.equal(y, int4_matmul(x, *w, N=N, offsets=off, dtype=torch.float32))
+        bounds = off.tolist()
+        for e in range(G):
+            want = x[bounds[e]:bounds[e + 1]].double() @ real(v[e], s[e], 64).T
+            assert torch.equal(y[bounds[e]:bounds[e + 1]], want.float())
+
+
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_odd_addresses_of_y_on_every_kernel(M, N):
+    """N a multiple of 4 and y an element or two off: rows are stored element by element, or by two."""
+    g = gen(N)
+    v, s = rand_weight((N, 160), 32, g, exact=True)
+    w = int4_pack(v, s)
+    x = torch.randint(-4, 5, (M, 160), generator=g, device=DEV).to(torch.bfloat16)
+    want = x.double() @ real(v, s, 32).T
+    for out in (torch.bfloat16, torch.float32):
+        for lead in (1, 2):
+            buf = torch.full((M * N + 9,), 4.0, dtype=out, device=DEV)
+            y = buf[lead:lead + M * N].view(M, N)
+            int4_matmul(x, *w, y=y)
+            assert torch.equal(y, want.to(out))
+            assert bool((buf[:lead] == 4).all()) and bool((buf[lead + M * N:] == 4).all())
+
+
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_on_a_given_stream_on_every_kernel(M, N):
+    g = gen(M)
+    v, s = rand_weight((N, 256), 64, g, exact=True)
+    w = int4_pack(v, s)
+    x = torch.randint(-4, 5, (M, 256), generator=g, device=DEV).to(torch.bfloat16)
+    want = (x.double() @ real(v, s, 64).T).float()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = int4_matmul(x, *w, N=N, dtype=torch.float32, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("M,N", KERNELS)
 def test_another_width_than_the_weights_is_seen(M, N):
     """K within the same 128 inputs cannot be told from the tensors' shapes; the tiles say it, and y is NaN."""
