@@ -65,6 +65,27 @@ def test_sort_drops_strangers_and_repeats(T, k):
     check_sort(torch.full((T, k), 8).int(), 7, 2)                    # everything in the last expert
 
 
+@pytest.mark.parametrize("T,k,E,El,e0", [(70001, 8, 9, 5, 2), (140001, 8, 300, 300, 0), (262145, 8, 600, 512, 50),
+                                         (1048577, 1, 3, 3, 0)])
+def test_sort_of_many_blocks(T, k, E, El, e0):
+    """More than 256 and 512 blocks of 2048 pairs, whose counts are scanned 256 at a time; experts drawn unevenly, with
+    dropped ones."""
+    r = np.random.default_rng(T)
+    idx = (E * r.random((T, k)) ** 2).astype(np.int32)
+    idx[r.random((T, k)) < 0.1] = -1
+    flat = idx.reshape(-1).astype(np.int64) - e0
+    flat = np.where((flat >= 0) & (flat < El), flat, El)
+    order = np.argsort(flat, kind="stable")
+    P = int((flat < El).sum())
+    pos = np.empty_like(order)
+    pos[order] = np.arange(T * k)
+    offsets, perm, pair_pos = (t.cpu().numpy() for t in sort_pairs(torch.from_numpy(idx).to(DEV), El, e0))
+    np.testing.assert_array_equal(offsets, np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=El + 1)[:El])]))
+    np.testing.assert_array_equal(perm[:P], order[:P])
+    assert (perm[P:] == -1).all()
+    np.testing.assert_array_equal(pair_pos.reshape(-1), np.where(flat < El, pos, -1))
+
+
 def test_sort_agrees_with_the_layer():
     T, E, k = 1000, 32, 4
     layer = MoELayer(T, 256, 128, E, k, "bf16", E_local=12, expert_offset=8)
