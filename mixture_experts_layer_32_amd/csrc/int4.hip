@@ -117,7 +117,7 @@ struct Scales4<1> {
 // fourth column of it; with few channels y workgroups share them, and each wave takes every 4 y-th column (values of
 // 4096 x 4096 laid out in 16 us, by one workgroup to the channels in 42). Lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
 constexpr int kPackWaves = 16;
-constexpr int kPackGrid = 1 << 21;   // workgroups along the channels at most, the rest in their loops
+constexpr int kPackGrid = 1 << 21;   // workgroups along x at most, the rest along z
 
 // The words behind the channels, that of -8 still 0, ahead of y > 1 workgroups that may find one.
 __global__ __launch_bounds__(256) void k_int4_none(uint8_t* q, int64_t n, int K) {
@@ -133,92 +133,93 @@ __global__ __launch_bounds__(kPackWaves * 64) void k_int4_pack(const void* __res
   const int t = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int Kt = (K + kTileK - 1) / kTileK;
   const int per = group / 32, ng = 4 / per;     // steps of 32 inputs in a group, groups of a tile
-  for (int64_t row64 = blockIdx.x; row64 < rows; row64 += gridDim.x) {   // over the weights
-    const int64_t g = row64 / rows64(N);
-    const int n = (int)(row64 - g * rows64(N)) * 64 + 4 * c + t;
-    const int64_t row = g * N + n;
-    unsigned* flag = reinterpret_cast<unsigned*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4);
-    bool eights = false;
-    for (int kb = blockIdx.y * (kPackWaves / 4) + (threadIdx.x >> 8); kb < Kt; kb += gridDim.y * (kPackWaves / 4)) {
-      float v[4][8];
-      unsigned m[4];
-  #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = kb * kTileK + 32 * i + 8 * h;
-        const bool ok = n < N && k < K;
-        const size_t at = (size_t)row * K + k;
-        m[i] = 0u;
-        if constexpr (KIND == 0) {
-          uint4 r = make_uint4(0u, 0u, 0u, 0u);
-          if (ok) r = ld16(static_cast<const bf16*>(in) + at);
-          eng::unpack8(r, v[i]);
-        } else if constexpr (KIND == 1) {
-          uint4 r[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (ok) {
-            r[0] = ld16(static_cast<const float*>(in) + at);
-            r[1] = ld16(static_cast<const float*>(in) + at + 4);
-          }
-  #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = reinterpret_cast<const float*>(r)[j];
-        } else {
-          uint2 r = make_uint2(0u, 0u);
-          if (ok) r = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(in) + at);
-  #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[i][j] = (float)min(7, max(-8, (int)reinterpret_cast<const int8_t*>(&r)[j]));
+  // over the weights (a dimension of a grid holds less than 2^32 threads; a loop here costs registers and a quarter of the time)
+  const int64_t row64 = (int64_t)blockIdx.z * kPackGrid + blockIdx.x;
+  if (row64 >= rows) return;
+  const int64_t g = row64 / rows64(N);
+  const int n = (int)(row64 - g * rows64(N)) * 64 + 4 * c + t;
+  const int64_t row = g * N + n;
+  unsigned* flag = reinterpret_cast<unsigned*>(q + row64 * row_bytes(Kt) + (size_t)4 * Kt * kTileBytes4);
+  bool eights = false;
+  for (int kb = blockIdx.y * (kPackWaves / 4) + (threadIdx.x >> 8); kb < Kt; kb += gridDim.y * (kPackWaves / 4)) {
+    float v[4][8];
+    unsigned m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = kb * kTileK + 32 * i + 8 * h;
+      const bool ok = n < N && k < K;
+      const size_t at = (size_t)row * K + k;
+      m[i] = 0u;
+      if constexpr (KIND == 0) {
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) r = ld16(static_cast<const bf16*>(in) + at);
+        eng::unpack8(r, v[i]);
+      } else if constexpr (KIND == 1) {
+        uint4 r[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (ok) {
+          r[0] = ld16(static_cast<const float*>(in) + at);
+          r[1] = ld16(static_cast<const float*>(in) + at + 4);
         }
-        if constexpr (KIND != 2) {
-  #pragma unroll
-          for (int j = 0; j < 8; ++j) m[i] = max(m[i], __float_as_uint(v[i][j]) & 0x7fffffffu);
-          m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 16));
-          m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 32));
-        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = reinterpret_cast<const float*>(r)[j];
+      } else {
+        uint2 r = make_uint2(0u, 0u);
+        if (ok) r = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(in) + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = (float)min(7, max(-8, (int)reinterpret_cast<const int8_t*>(&r)[j]));
       }
-      unsigned w[4];
-  #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int i0 = i / per * per;
-        const bool ok = n < N && kb * kTileK + 32 * i0 < K;
-        uint16_t sb = 0;
-        if constexpr (KIND == 2) {
-          if (ok) sb = sin[row * (K / group) + (kb * kTileK + 32 * i0) / group];
+      if constexpr (KIND != 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[i] = max(m[i], __float_as_uint(v[i][j]) & 0x7fffffffu);
+        m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 16));
+        m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 32));
+      }
+    }
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int i0 = i / per * per;
+      const bool ok = n < N && kb * kTileK + 32 * i0 < K;
+      uint16_t sb = 0;
+      if constexpr (KIND == 2) {
+        if (ok) sb = sin[row * (K / group) + (kb * kTileK + 32 * i0) / group];
+      } else {
+        unsigned mg = 0u;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) mg = a / per == i / per ? max(mg, m[a]) : mg;
+        if (mg >= 0x7f800000u) {
+          sb = 0x7fc0;
         } else {
-          unsigned mg = 0u;
-  #pragma unroll
-          for (int a = 0; a < 4; ++a) mg = a / per == i / per ? max(mg, m[a]) : mg;
-          if (mg >= 0x7f800000u) {
-            sb = 0x7fc0;
-          } else {
-            const bf16 s = (bf16)fmaxf(__uint_as_float(mg) / 7.0f, 0x1p-126f);
-            sb = __builtin_bit_cast(uint16_t, s);
-          }
-          // v / s to the nearest whole number, ties to even. v and s have 24 and 8 significant bits, so that a quotient that is
-          // no tie lies 2^-25 or more from one; v times 1 / s, each rounded to 64 bits, is off by 2^-49 at most, and rounded
-          // to a multiple of 2^-32 (by adding a number with such a step) it is a tie where the quotient is one, and only there.
-          const double r = 1.0 / (double)bf16_bits(sb), step = 0x1.8p20;
-  #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const double x = fma((double)v[i][j], r, step) - step;
-            v[i][j] = mg >= 0x7f800000u ? 0.f : fminf(7.f, fmaxf(-7.f, (float)rint(x)));
-          }
-          if (!ok) sb = 0;
+          const bf16 s = (bf16)fmaxf(__uint_as_float(mg) / 7.0f, 0x1p-126f);
+          sb = __builtin_bit_cast(uint16_t, s);
         }
-        w[i] = 0u;
-  #pragma unroll
+        // v / s to the nearest whole number, ties to even. v and s have 24 and 8 significant bits, so that a quotient that is
+        // no tie lies 2^-25 or more from one; v times 1 / s, each rounded to 64 bits, is off by 2^-49 at most, and rounded
+        // to a multiple of 2^-32 (by adding a number with such a step) it is a tie where the quotient is one, and only there.
+        const double r = 1.0 / (double)bf16_bits(sb), step = 0x1.8p20;
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
-          w[i] |= pack4((int)v[i][j], j);
-          if constexpr (KIND == 2) eights |= v[i][j] == -8.f;
+          const double x = fma((double)v[i][j], r, step) - step;
+          v[i][j] = mg >= 0x7f800000u ? 0.f : fminf(7.f, fmaxf(-7.f, (float)rint(x)));
         }
-        if (h == 0 && i == i0) sout[scale_at(row64, Kt, kb, 4 * c + t, ng) + i / per] = sb;
+        if (!ok) sb = 0;
       }
-      st16(q + row64 * row_bytes(Kt) + ((size_t)t * Kt + kb) * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
+      w[i] = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[i] |= pack4((int)v[i][j], j);
+        if constexpr (KIND == 2) eights |= v[i][j] == -8.f;
+      }
+      if (h == 0 && i == i0) sout[scale_at(row64, Kt, kb, 4 * c + t, ng) + i / per] = sb;
     }
-    const int any = __syncthreads_or(eights);
-    if (KIND == 2 && gridDim.y > 1) {
-      if (threadIdx.x == 0 && any) atomicOr(flag, 1u);
-    } else if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) {
-      flag[threadIdx.x] = threadIdx.x == 0 ? any != 0 : threadIdx.x == 1 ? kSaysK | (unsigned)K : 0u;
-    }
+    st16(q + row64 * row_bytes(Kt) + ((size_t)t * Kt + kb) * kTileBytes4 + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  const int any = __syncthreads_or(eights);
+  if (KIND == 2 && gridDim.y > 1) {
+    if (threadIdx.x == 0 && any) atomicOr(flag, 1u);
+  } else if (blockIdx.y == 0 && threadIdx.x < kFlagBytes / 4) {
+    flag[threadIdx.x] = threadIdx.x == 0 ? any != 0 : threadIdx.x == 1 ? kSaysK | (unsigned)K : 0u;
   }
 }
 
@@ -914,9 +915,9 @@ hipError_t launch_int4_pack(const void* in, bool f32, const void* scales, int G,
   prof_mark_begin("int4_pack", s);
   const int64_t tiles = (int64_t)G * rows64(N);   // up to 2^23
   const int Kt = (K + kTileK - 1) / kTileK, columns = (Kt + kPackWaves / 4 - 1) / (kPackWaves / 4), few = 2 * persistent_grid(1);
-  // (a dimension of a grid holds less than 2^32 threads)
   const dim3 grid((unsigned)std::min<int64_t>(tiles, kPackGrid),
-                  (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)));
+                  (unsigned)std::min<int64_t>(columns, std::max<int64_t>(few / tiles, 1)),
+                  (unsigned)((tiles + kPackGrid - 1) / kPackGrid));
   if (scales && grid.y > 1) k_int4_none<<<(unsigned)((tiles + 255) / 256), 256, 0, s>>>(q, tiles, K);
   const uint16_t* si = static_cast<const uint16_t*>(scales);
   uint16_t* so = static_cast<uint16_t*>(out_scales);
