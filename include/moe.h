@@ -357,7 +357,8 @@ moe_status moe_combine_bwd(const void* dy, int type, const void* rows, int rows_
  * inputs of a channel: it stands for q[n, k] * s[n, k / group]. In memory 64 channels follow one another, and the weights
  * of [G, N, K] likewise; 64 channels hold four tiles a 128 inputs, [4][ceil(K/128)][1024] bytes in the order in which a
  * wavefront takes them, tile t holding the channels n with n % 4 = t, and then 16 bytes: a 32-bit word that is 0 if no
- * number is -8, one that is 0x4b000000 + K or (not telling) any with other high bits, and anything. Their scales are [ceil(K/128)][64][128 / group]. Padding has q = 0, s = 0.
+ * number is -8, one that is 0x4b000000 + K or (not telling) any with another high byte, and anything. Their scales are
+ * [ceil(K/128)][64][128 / group]. Padding has q = 0, s = 0.
  * With c = n % 64 / 4, i = k % 128 / 32, h = k % 32 / 8, j = k % 8, the number q[n, k] lies in the 32-bit word
  * (16 h + c) * 4 + i of its tile as a sign (1: q < 0) and m = |q| % 8: for j < 4, m in the three bits from bit 8 j and the
  * sign in bit 8 j + 7; for j >= 4, m from bit 8 (j - 4) + 4 and the sign in bit (8 (j - 4) + 11) % 32. */
@@ -388,11 +389,12 @@ moe_status moe_int4_matmul(const void* x, const uint8_t* q, const void* scales, 
  * moe_bwd and moe_router_bwd leave.
  *   norm = sqrt(sum over all tensors and elements g^2)             squares and sums in 64 bits, fp32 at the end
  *   c    = min(1, max_norm / (norm + 1e-6))                        in fp32; NaN if norm is NaN
- *   out  = c * g                                                   each element rounded once
+ *   out  = c * g                                                   in fp32, then rounded to out's type
  * The descriptions are read on the host during the call: count of them (0: the norm is 0), each a device pointer
  * (aligned to its elements), a number of elements (0: data may be null) and a type (FP32 or BF16). Together less than
  * 2^40 elements. out = null scales in place, and writes nothing where c = 1; otherwise out[i] has tensors[i]'s size, its
- * type may be the other one, and everything is written. Tensors may not overlap, but out[i] may be tensors[i].
+ * type may be the other one, and everything is written. Tensors may not overlap, nor hold norm, but out[i] may be
+ * tensors[i].
  * moe_grad_norm writes norm [1] fp32; moe_grad_clip scales by a norm given (other ranks' gradients may have
  * joined it); moe_clip_grad_norm does both, in a launch less where the tensors are few. ws: 256-byte aligned, of
  * moe_query_norm_sizes's size; contents need not be preserved, and calls that share one must be ordered by the caller.

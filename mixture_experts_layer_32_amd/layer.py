@@ -8,6 +8,7 @@ combine_backward; for training steps, GradNorm. No arithmetic happens here.
 """
 from __future__ import annotations
 
+import bisect
 import functools
 
 import torch
@@ -582,7 +583,7 @@ class GradNorm:
             spans.append((g.data_ptr(), g.numel() * g.element_size(), f"grads[{i}]"))
             if o.data_ptr() != g.data_ptr() or o.dtype != g.dtype:
                 spans.append((o.data_ptr(), o.numel() * o.element_size(), f"out[{i}]"))
-        spans = sorted(s for s in spans if s[1])
+        self._spans = spans = sorted(s for s in spans if s[1])
         for (a, n, name), (b, _, other) in zip(spans, spans[1:]):
             if b < a + n:
                 raise ValueError(f"{name} and {other} overlap")
@@ -620,7 +621,7 @@ class GradNorm:
 
     def clip(self, max_norm, norm=None, stream=None):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)) and returns the norm: their own, or the one given (an
-        fp32 tensor of one element, such as a norm over all ranks' gradients)."""
+        fp32 tensor of one element outside of the gradients, such as a norm over all ranks')."""
         handle = _on(self.device, stream)
         self._in_place()
         n = len(self.grads)
@@ -631,5 +632,9 @@ class GradNorm:
         if not isinstance(norm, torch.Tensor) or norm.numel() != 1:
             raise ValueError("norm: expected a tensor of one element")
         _expect(norm, "norm", norm.shape, torch.float32, self.device)
+        # (the scaling reads it while it writes the gradients)
+        i = bisect.bisect_right(self._spans, (norm.data_ptr() + 3,)) - 1
+        if i >= 0 and norm.data_ptr() < self._spans[i][0] + self._spans[i][1]:
+            raise ValueError(f"norm and {self._spans[i][2]} overlap")
         binding.moe_grad_clip(self._in, self._out, n, norm, max_norm, handle)
         return norm

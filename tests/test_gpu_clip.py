@@ -209,6 +209,24 @@ def test_tensors_with_other_memory_are_refused(change):
     assert abs(float(plan.norm()) - 2 * 600 ** 0.5) <= 1e-5
 
 
+def test_a_norm_inside_the_gradients_is_refused():
+    """The scaling would write it while others read it."""
+    buf = torch.ones(20000, device=DEV)
+    inside = GradNorm([buf[100:9000], buf[9000:19000]])
+    out = torch.zeros(300, device=DEV)
+    apart = GradNorm([buf[:100], buf[9000:9200]], [out[:100], out[100:]])
+    for plan, refused, taken in ((inside, (100, 5000, 8999, 9000, 18999), (0, 99, 19000, 19999)),
+                                 (apart, (0, 99, 9000, 9199), (100, 8999, 9200))):
+        for i in refused:
+            with pytest.raises(ValueError, match="norm and grads.* overlap"):
+                plan.clip(0.5, norm=buf[i])
+        for i in taken:
+            assert plan.clip(2.0, norm=buf[i]) is not None
+    with pytest.raises(ValueError, match="norm and out.0. overlap"):
+        apart.clip(0.5, norm=out[99])
+    assert bool((buf == 1).all())
+
+
 def test_wrong_norms_and_bounds_are_refused():
     plan = GradNorm([torch.ones(4, device=DEV)])
     for norm in (1.0, torch.ones(2, device=DEV), torch.ones((), device=DEV, dtype=torch.float64), torch.ones(())):
