@@ -2,7 +2,7 @@
 // the backward passes leave.
 //
 //   k_norm    each workgroup takes a contiguous run of the tensors' chunks and leaves one partial sum of squares.
-//             Squares and sums in 64 bits: no range is lost, and the order (fixed by the sizes alone) hardly shows.
+//             Squares and sums in 64 bits: no range is lost, and the order (fixed by the sizes and addresses) hardly shows.
 //             Bound by the reads, which go past the caches: 1.2 GB 183 us (6.6 TB/s; through them 231).
 //   k_root    norm = sqrt(sum of the partial sums).
 //   k_scale   out = c g, c = min(1, max_norm / (norm + 1e-6)); with the norm given, or from the partial sums, which
@@ -10,6 +10,8 @@
 //             us (6.0 TB/s), by kScaleBlocks workgroups whose chunks lie side by side, past the caches (plain stores 435;
 //             256 or 512 workgroups 757 and 489; a contiguous run of chunks for each workgroup 470 to 504; from the last
 //             chunk to the first, the norm's latest, no gain at any size and 12 MB 31 us a call where this takes 26).
+//             Outputs that are another number of elements off a 16-byte boundary than their tensors go element by element:
+//             600 M of bf16 1316 us for 414, 300 M of fp32 to bf16, both one element off, 674 for 338.
 // The tensors' addresses and sizes travel in the launch's arguments, kTable (with outputs kPair) tensors a launch: 150 tensors
 // of 400000 elements together 6 + 2 us.
 #include <algorithm>

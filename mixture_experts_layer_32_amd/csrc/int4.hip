@@ -2,8 +2,8 @@
 //
 //   k_int4_pack   a weight's tiles, from fp32 or bf16 (quantised here) or from whole numbers and scales.
 //   k_int4_rows   y = sum over groups of s (x q^T) for few rows: 16 at a time, the weight straight from memory into
-//                 registers, K split over a workgroup's waves. Bound by reading the weight (6.6 TB/s with 64 rows among 128
-//                 experts of 1536 x 4096, 31 us), and with one weight by the launch (one row of 1536 x 4096 5.1 us).
+//                 registers, K split over a workgroup's waves. Bound by reading the weight (5.2 TB/s with 64 rows among 128
+//                 experts of 1536 x 4096: 178 MB in 34 us), and with one weight by the launch (one row of 1536 x 4096 5.1 us).
 //   k_int4_deep   64 x 64 and 64 x 128 tiles for products of few: all operands come straight into LDS.
 //   k_int4_tile   256 x 128 and 128 x 128 tiles for products of many: x in LDS, the weight unpacked from registers.
 //                 16384 x 4096 x 2048 270 to 300 us (920 to 1020 TFLOP/s, box to box); a bf16 product of this size by the
@@ -112,7 +112,7 @@ struct Scales4<1> {
   __device__ __forceinline__ float operator[](int) const { return bf16_bits(v); }
 };
 
-// Once for a weight: 128 x 1536 x 4096 from bf16 576 us (3.5 TB/s), 4096 x 4096 17 us, laid out from bytes 475 and 16.
+// Once for a weight: 128 x 1536 x 4096 from bf16 530 us (3.8 TB/s), 4096 x 4096 17 us, laid out from bytes 486 and 16.
 // KIND 0: bf16, 1: fp32, 2: signed bytes with bf16 scales. A workgroup takes 64 channels, a wave one of their tiles, every
 // fourth column of it; with few channels y workgroups share them, and each wave takes every 4 y-th column (values of
 // 4096 x 4096 laid out in 16 us, by one workgroup to the channels in 42). Lane 16 h + c takes inputs 32 i + 8 h + j, i < 4, j < 8.
@@ -714,7 +714,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int4_tile(I4Params p) {
 // share a CU. WIDE: 64 rows by 128 channels, 4 waves of 4 x 2 blocks side by side, which unpack each number once instead of
 // twice, two workgroups a CU, where there are so many. Bound by the unpacking and the matrix instructions together, 0.35 us
 // a stage of 64 channels and CU (WIDE: 0.29). 256 rows of 4096 x 4096 17 us (KG = 1 21; in stages of 64 inputs with q and
-// scales in registers 33), 4096 rows in 64 groups of 1536 x 4096 82 us (64 channels 99, in registers 157). Three stages in
+// scales in registers 33), 4096 rows in 64 groups of 1536 x 4096 62 us with 64 rows
+// each and 82 with about 64 (64 channels 99, in registers 157). Three stages in
 // LDS, the next one's fragments in registers ahead of time, or 64 x 128 tiles of 2 x 4 blocks took as long or longer (256
 // rows 17.5, 18.2 and 24 to 28 us).
 template <int PER, int KG, bool WIDE>
@@ -867,6 +868,12 @@ int64_t tiles4(const I4Params& p, int bm, int bn) {
 //                            80: DW 61, 128 52           100: DW 63, 128 54
 //   16 groups, 768 x 2048    of 4 rows (240): 1 9.4, R 8.1   128: D 16, 128 25
 // One row of 32768 x 4096 (W 512): 1 17, R 14; 16384 rows of 2048 x 768 in 64 groups: 256 63, 128 69.
+// These are with groups of 128 inputs and of evenly drawn rows. Groups of 64 and of 32 inputs take 1.1 and 1.25 times as long
+// in all kernels alike (1024 rows of 4096 x 4096: DW 38, 42, 47), and the choice is within 10 % of the best kernel but for few
+// rows each (208 in 16 groups of 768 x 2048: DD 11, R 9; 1500 in 128: R 34, DW 30). The host knows the mean of the groups' rows
+// alone: where they differ much it chooses too large a tile. With groups drawn by odds 1 / e^1.1, of 1536 x 4096 in 64 groups
+// 4608 rows: DW 99, 128 139, 12288: DW 191, 256 266; of 768 x 2048 in 128 groups 24576: DW 96, 256 140; by 1 / e^2, 1500: R 27,
+// DW 22. Evenly drawn, 16384 rows of the first take DW 251, 256 273.
 template <int PER>
 void launch4(const I4Params& p, int grid, hipStream_t s) {
   const int64_t groups = std::min<int64_t>(p.M, p.G);

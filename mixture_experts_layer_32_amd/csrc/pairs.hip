@@ -5,15 +5,16 @@
 //   k_sort_small    up to kSortSmall pairs: one workgroup counts, scans and places them (64 pairs of 128 experts 4 us).
 //   k_sort_count, k_sort_place   beyond: counts per block of kSortPairs pairs and expert, positions. Up to kSortBlocks
 //                   blocks every workgroup of the second adds up all blocks' counts by itself, a launch less (131072 pairs
-//                   of 128 experts 5 + 7 us); for more, k_sort_scan makes their sums over the blocks.
+//                   of 128 experts 5 + 7 us); for more, k_sort_scan makes their sums over the blocks (1048576 pairs 18 us).
 //   k_dispatch      rows[pair_pos[t, j]] = x[t]: x is read once, each row written once. Bound by the writes: 131072 rows
-//                   of 4 KB 104 us (5.8 TB/s; a plain write reaches 6.8 here).
-//   k_pairs_combine y[t] = sum_j w_tj rows[pair_pos[t, j]]: each row read once. Bound by the reads: the same rows 108 us
-//                   (5.6 TB/s).
+//                   of 4 KB 98 to 106 us (5.7 to 6.2 TB/s; a plain write reaches 6.8 here).
+//   k_pairs_combine y[t] = sum_j w_tj rows[pair_pos[t, j]]: each row read once. Bound by the reads: the same rows 106 to
+//                   113 us (5.4 to 5.7 TB/s).
 //   k_pairs_combine_bwd  drows = w dy, dw = <dy, rows>, dlogits: each row read and written once, a copy at heart: the same
-//                   rows 214 us (5.3 TB/s; a copy reaches 4.9).
-// The last three have a form for short rows, several tokens to a wavefront (k_dispatch_short, k_pairs_combine_short; the
-// gradients' rows keep a wavefront each, for their sums).
+//                   rows 219 to 230 us (5.0 to 5.2 TB/s; a copy reaches 4.9). Beyond 256 chunks a row, where dy is read again for
+//                   each slot, 65536 rows of 8 KB 239 us (4.8 TB/s; by counter 0.99 GB read for 0.60) and of 14 KB 408 (4.9).
+// Dispatch and combine have a form for short rows, several tokens to a wavefront (k_dispatch_short, k_pairs_combine_short);
+// the gradients' rows keep a wavefront each, for their sums.
 // A pair's place within its block comes from the lanes below it that hold the same expert (ballots over the expert's bits),
 // so that the order is the pairs' own whatever the waves do; counts are LDS atomics of whole numbers, whose order is none.
 #include <algorithm>
