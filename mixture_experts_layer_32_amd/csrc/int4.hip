@@ -6,7 +6,7 @@
 //                 experts of 1536 x 4096: 178 MB in 34 us), and with one weight by the launch (one row of 1536 x 4096 5.1 us).
 //   k_int4_deep   64 x 64 and 64 x 128 tiles for products of few: all operands come straight into LDS.
 //   k_int4_tile   256 x 128 and 128 x 128 tiles for products of many: x in LDS, the weight unpacked from registers.
-//                 16384 x 4096 x 2048 270 to 300 us (920 to 1020 TFLOP/s, box to box); a bf16 product of this size by the
+//                 16384 x 4096 x 2048 270 to 300 us (920 to 1020 TFLOP/s, card to card); a bf16 product of this size by the
 //                 library takes 243, and a loop of this many matrix instructions on such numbers, with nothing else, reached
 //                 1120 to 1270 TFLOP/s (1415 on zeros): the clock falls with their load.
 // launch4 says which takes what, with times. A number q of a weight is held in four bits, a sign and m = |q| (sign 1 and

@@ -362,6 +362,18 @@ def test_long_rows_on_every_kernel(M, N, K, group):
         assert torch.equal(int4_matmul(x, *int4_pack(v, s), N=N, dtype=torch.float32), want.float())
 
 
+@pytest.mark.parametrize("K,group", [(1120, 32), (1216, 64), (2048, 128)])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_real_values_in_long_rows_on_every_kernel(M, N, K, group):
+    g = gen(M * K)
+    v, s = rand_weight((N, K), group, g)
+    x = (torch.randn(M, K, generator=g, device=DEV) * torch.exp(torch.randn(M, 1, generator=g, device=DEV))).to(torch.bfloat16)
+    want = x.double() @ real(v, s, group).T
+    for out in (torch.bfloat16, torch.float32):
+        y = int4_matmul(x, *int4_pack(v, s), N=N, dtype=out).double()
+        assert bool(((y - want).abs() <= HALF[out] * torch.maximum(y.abs(), want.abs()) + bound(x, v, s, group)).all())
+
+
 @pytest.mark.parametrize("K,group", [(640, 128), (1120, 32), (1216, 64), (2048, 128)])
 @pytest.mark.parametrize("M,G,N", GROUPED)
 def test_long_rows_in_groups(M, G, N, K, group):
